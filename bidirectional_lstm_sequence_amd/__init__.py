@@ -14,6 +14,9 @@ import os
 
 import numpy as np
 
+from . import sequence
+from .sequence import causal_conv, causal_conv_step  # noqa: F401
+
 HIDDEN = 128
 GATES = 512
 FEATURES = 60
@@ -33,7 +36,7 @@ EXPORTS = ["bilstm_plan_create", "bilstm_plan_create_ex", "bilstm_forward", "bil
            "bilstm_phase_times", "bilstm_destroy", "bilstm_last_error", "bilstm_pack_layer",
            "bilstm_schedule", "bilstm_probe_exchange", "bilstm_heads_create", "bilstm_heads_forward",
            "bilstm_heads_destroy", "bilstm_forward_noalloc", "bilstm_probe_fma_rate",
-           "bilstm_probe_mfma_rate"]
+           "bilstm_probe_mfma_rate", "bilstm_causal_conv", "bilstm_causal_conv_step"]
 HEAD_IN, HEAD_MID, HEAD_CLASSES = 256, 128, 7
 
 
@@ -134,6 +137,7 @@ def library():
         "bilstm_probe_mfma_rate": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int32,
                                     ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)], st),
     }
+    sig.update(sequence.signatures())
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args

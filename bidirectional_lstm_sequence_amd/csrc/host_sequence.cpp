@@ -1,0 +1,265 @@
+// C ABI of the causal sequence operators: checks of arguments, then one launcher call. These
+// entry points keep nothing between calls and allocate nothing.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "../../include/bilstm.h"
+#include "bilstm_host.h"
+#include "sequence_internal.h"
+
+using namespace bl;
+
+namespace {
+
+constexpr uint64_t kMostRows = 0x7FFFFFFFull;
+constexpr uint32_t kMostSequences = 1u << 30;
+
+// Byte range of a view, for overlap checks; strided views repeat `width` bytes every `stride`.
+struct Bytes {
+    uintptr_t first = 0;
+    uint64_t rows = 0, width = 0, stride = 0;
+    bool empty() const { return rows == 0 || width == 0 || first == 0; }
+    uintptr_t end() const { return first + (rows - 1) * stride + width; }
+};
+
+Bytes bytes_of(const bilstm_rows &r, uint64_t rows, uint64_t width, uint64_t size) {
+    return {reinterpret_cast<uintptr_t>(r.data), rows, width * size, r.stride * size};
+}
+
+Bytes bytes_of(const bilstm_buffer &b, uint64_t size) {
+    return {reinterpret_cast<uintptr_t>(b.data), b.data != nullptr ? 1ull : 0ull, b.len * size, b.len * size};
+}
+
+// Whether two views share a byte. Views of one wide buffer with the same stride may interleave:
+// they are apart if their columns are.
+bool overlap(const Bytes &a, const Bytes &b) {
+    if (a.empty() || b.empty()) return false;
+    if (a.end() <= b.first || b.end() <= a.first) return false;
+    if (a.stride == b.stride && a.rows > 1 && b.rows > 1) {
+        const uint64_t off = a.first <= b.first ? (b.first - a.first) % a.stride
+                                                : (a.stride - (a.first - b.first) % a.stride) % a.stride;
+        return off < a.width || off + b.width > a.stride;
+    }
+    return true;
+}
+
+bool same_view(const bilstm_rows &a, const bilstm_rows &b, uint64_t rows) {
+    return a.data == b.data && (rows <= 1 || a.stride == b.stride);
+}
+
+uint64_t size_of(int32_t type) { return type == BILSTM_FLOAT32 ? 4 : 2; }
+Elem elem_of(int32_t type) {
+    return type == BILSTM_FLOAT32 ? Elem::f32 : (type == BILSTM_BFLOAT16 ? Elem::bf16 : Elem::f16);
+}
+
+bilstm_status check_type(const char *call, int32_t type) {
+    if (type < BILSTM_FLOAT32 || type > BILSTM_FLOAT16) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: unknown element type %d", call, type);
+    }
+    return BILSTM_OK;
+}
+
+bilstm_status check_pointer(const char *call, const char *name, const void *p, uint64_t align) {
+    if (p == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: %s is NULL", call, name);
+    if (reinterpret_cast<uintptr_t>(p) % align != 0) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %s must be %llu-byte aligned", call, name,
+                    static_cast<unsigned long long>(align));
+    }
+    return BILSTM_OK;
+}
+
+bilstm_status check_rows(const char *call, const char *name, const bilstm_rows &r, uint64_t rows, uint64_t width,
+                         uint64_t size) {
+    bilstm_status st = check_pointer(call, name, r.data, size);
+    if (st != BILSTM_OK) return st;
+    if (r.stride < width && rows > 1) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %s has a row stride of %llu, less than its width %llu", call, name,
+                    static_cast<unsigned long long>(r.stride), static_cast<unsigned long long>(width));
+    }
+    uint64_t need = 0, bytes = 0;
+    if (__builtin_mul_overflow(rows - 1, r.stride, &need) || __builtin_add_overflow(need, width, &need) ||
+        __builtin_mul_overflow(need, size, &bytes) || bytes > (1ull << 56) || r.stride > (1ull << 56)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %s does not fit the address space", call, name);
+    }
+    if (r.len < need) {
+        return fail(BILSTM_BUFFER_LENGTH, "%s: %s: expected at least %llu elements, got %llu", call, name,
+                    static_cast<unsigned long long>(need), static_cast<unsigned long long>(r.len));
+    }
+    return BILSTM_OK;
+}
+
+// `expected` elements exactly; optional buffers may be NULL.
+bilstm_status check_buffer(const char *call, const char *name, const bilstm_buffer &b, uint64_t expected, uint64_t align,
+                           bool optional) {
+    if (b.data == nullptr && optional) return BILSTM_OK;
+    bilstm_status st = check_pointer(call, name, b.data, align);
+    if (st != BILSTM_OK) return st;
+    if (b.len != expected) {
+        return fail(BILSTM_BUFFER_LENGTH, "%s: %s: expected %llu elements, got %llu", call, name,
+                    static_cast<unsigned long long>(expected), static_cast<unsigned long long>(b.len));
+    }
+    return BILSTM_OK;
+}
+
+bilstm_status check_apart(const char *call, const char *out_name, const Bytes &out, const char *in_name, const Bytes &in) {
+    if (overlap(out, in)) return fail(BILSTM_INVALID_ARGUMENT, "%s: %s and %s overlap", call, out_name, in_name);
+    return BILSTM_OK;
+}
+
+#define BL_CHECK(expr)                          \
+    do {                                        \
+        const bilstm_status st_ = (expr);       \
+        if (st_ != BILSTM_OK) return st_;       \
+    } while (0)
+
+// Makes `device` current for a launch and the caller's device current again afterwards.
+class DeviceScope {
+  public:
+    explicit DeviceScope(int device) : device_(device) {}
+    bilstm_status enter(const char *call) {
+        constexpr int kKnown = 64;
+        static std::atomic<int> known[kKnown];  // 0 not looked at yet, 1 gfx950
+        hipError_t e = hipSuccess;
+        if (device_ < 0 || device_ >= kKnown || known[device_].load(std::memory_order_relaxed) == 0) {
+            int count = 0;
+            e = hipGetDeviceCount(&count);
+            if (e != hipSuccess || count == 0) {
+                return fail(BILSTM_UNSUPPORTED, "%s: no HIP device (%s)", call, hipGetErrorString(e));
+            }
+            if (device_ < 0 || device_ >= count) {
+                return fail(BILSTM_INVALID_ARGUMENT, "%s: device %d out of range (%d devices)", call, device_, count);
+            }
+            hipDeviceProp_t prop;
+            e = hipGetDeviceProperties(&prop, device_);
+            if (e != hipSuccess) return fail(BILSTM_HIP_ERROR, "%s: device properties: %s", call, hipGetErrorString(e));
+            if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) {
+                return fail(BILSTM_UNSUPPORTED, "%s: device %d is not a gfx950 (MI355X) GPU", call, device_);
+            }
+            if (device_ < kKnown) known[device_].store(1, std::memory_order_relaxed);
+        }
+        e = hipGetDevice(&saved_);
+        if (e == hipSuccess && saved_ != device_) {
+            e = hipSetDevice(device_);
+            switched_ = e == hipSuccess;
+        }
+        if (e != hipSuccess) return fail(BILSTM_HIP_ERROR, "%s: hipSetDevice: %s", call, hipGetErrorString(e));
+        return BILSTM_OK;
+    }
+    ~DeviceScope() {
+        if (switched_) (void)hipSetDevice(saved_);
+    }
+    DeviceScope(const DeviceScope &) = delete;
+    DeviceScope &operator=(const DeviceScope &) = delete;
+
+  private:
+    int device_;
+    int saved_ = 0;
+    bool switched_ = false;
+};
+
+bilstm_status launched(const char *call, hipError_t e) {
+    if (e == hipErrorInvalidConfiguration) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: more work than one launch's grid holds", call);
+    }
+    if (e != hipSuccess) return fail(BILSTM_HIP_ERROR, "%s: launch: %s", call, hipGetErrorString(e));
+    return BILSTM_OK;
+}
+
+// The sequences of a call: numbers, starts, slots, fresh.
+template <class Args>
+bilstm_status check_sequences(const char *call, const Args &a, bool step, SequenceArgs *s) {
+    if (a.rows > kMostRows) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows exceed 32-bit row numbers", call,
+                    static_cast<unsigned long long>(a.rows));
+    }
+    if (a.reserved != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
+    const uint64_t count = step ? a.rows : a.sequences;
+    if (count > kMostSequences || a.places > kMostRows) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: too many sequences or places", call);
+    }
+    if (!step && count > 0) BL_CHECK(check_buffer(call, "starts", a.starts, count + 1, 4, false));
+    if (count > 0) BL_CHECK(check_buffer(call, "slots", a.slots, count, 4, true));
+    if (!step && count > 0) BL_CHECK(check_buffer(call, "fresh", a.fresh, count, 1, true));
+    if (a.state.data == nullptr && (step || a.slots.data != nullptr || a.fresh.data != nullptr)) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %s", call,
+                    step ? "the single-token form needs a state" : "slots and fresh need a state");
+    }
+    if (a.state.data != nullptr && a.slots.data == nullptr && count > a.places) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %llu sequences without slots, but only %u places", call,
+                    static_cast<unsigned long long>(count), a.places);
+    }
+    s->starts = step ? nullptr : static_cast<const int *>(a.starts.data);
+    s->slots = static_cast<const int *>(a.slots.data);
+    s->fresh = step ? nullptr : static_cast<const unsigned char *>(a.fresh.data);
+    s->sequences = static_cast<int>(count);
+    s->places = static_cast<int>(a.places);
+    s->rows = static_cast<int>(a.rows);
+    return BILSTM_OK;
+}
+
+// ---- convolution -------------------------------------------------------------------------
+
+bilstm_status conv(const char *call, const bilstm_conv_args *args, bool step, void *stream) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    const bilstm_conv_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.channels == 0 || a.channels > kMostRows) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %u channels", call, a.channels);
+    }
+    if (a.taps < 2 || a.taps > 4) return fail(BILSTM_UNSUPPORTED, "%s: %u taps (2, 3 or 4 are built)", call, a.taps);
+    ConvArgs k;
+    BL_CHECK(check_sequences(call, a, step, &k.seq));
+    if (a.rows == 0 || k.seq.sequences == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type);
+    BL_CHECK(check_rows(call, "x", a.x, a.rows, a.channels, size));
+    BL_CHECK(check_rows(call, "y", a.y, a.rows, a.channels, size));
+    BL_CHECK(check_buffer(call, "weight", a.weight, static_cast<uint64_t>(a.channels) * a.taps, size, false));
+    BL_CHECK(check_buffer(call, "bias", a.bias, a.channels, size, true));
+    uint64_t state_len = 0;
+    if (__builtin_mul_overflow(static_cast<uint64_t>(a.places), static_cast<uint64_t>(a.channels) * (a.taps - 1),
+                               &state_len) || state_len > (1ull << 54)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: state does not fit the address space", call);
+    }
+    BL_CHECK(check_buffer(call, "state", a.state, state_len, size, true));
+    const Bytes x = bytes_of(a.x, a.rows, a.channels, size), y = bytes_of(a.y, a.rows, a.channels, size);
+    const Bytes state = bytes_of(a.state, size);
+    BL_CHECK(check_apart(call, "y", y, "x", x));
+    BL_CHECK(check_apart(call, "y", y, "state", state));
+    BL_CHECK(check_apart(call, "state", state, "x", x));
+    const Bytes inputs[] = {bytes_of(a.weight, size), bytes_of(a.bias, size), bytes_of(a.starts, 4), bytes_of(a.slots, 4),
+                            bytes_of(a.fresh, 1)};
+    for (const Bytes &in : inputs) {
+        BL_CHECK(check_apart(call, "y", y, "an input", in));
+        BL_CHECK(check_apart(call, "state", state, "an input", in));
+    }
+    k.x = a.x.data;
+    k.weight = a.weight.data;
+    k.bias = a.bias.data;
+    k.state = const_cast<void *>(a.state.data);
+    k.y = const_cast<void *>(a.y.data);
+    k.x_stride = a.x.stride;
+    k.y_stride = a.y.stride;
+    k.channels = static_cast<int>(a.channels);
+    k.taps = static_cast<int>(a.taps);
+    k.silu = a.silu != 0;
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return launched(call, step ? launch_conv_step(k, elem_of(a.type), s) : launch_conv(k, elem_of(a.type), s));
+}
+
+}  // namespace
+
+extern "C" {
+
+bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream) {
+    return conv("causal_conv", args, false, stream);
+}
+
+bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream) {
+    return conv("causal_conv_step", args, true, stream);
+}
+
+}  // extern "C"

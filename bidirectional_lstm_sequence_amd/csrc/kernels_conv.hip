@@ -1,0 +1,188 @@
+// Short causal convolution per channel over packed sequences and for single tokens.
+//
+//   v[t][c] = bias[c] + sum_k w[c][k] x[t - W + 1 + k][c],  W = 2, 3 or 4 taps
+//   y = v or v * sigmoid(v)
+//
+// 2W flops an element against 4 (16-bit) or 8 bytes: bound by memory. A thread takes one vector of
+// channels (16 bytes where alignment allows) and a run of kRun rows of one sequence, with the
+// run's rows and the W - 1 rows before it in registers, so x is read once apart from the W - 1
+// rows at each run's start, which the neighbouring run has in the L2. All of a run's loads are
+// issued before the first product. The thread with a sequence's first run also writes the
+// sequence's new state: it is the only one that reads the old one, so nothing has to wait.
+#include "sequence_device.h"
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[V][W], float (&bias)[V]) {
+    const T *wp = static_cast<const T *>(a.weight) + static_cast<size_t>(c) * W;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[i][k] = static_cast<float>(wp[i * W + k]);
+        bias[i] = a.bias != nullptr ? static_cast<float>(static_cast<const T *>(a.bias)[c + i]) : 0.0f;
+    }
+}
+
+template <typename T, int V, int W, int RUN>
+__global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
+    using X = Vec<T, V>;
+    const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
+    if (id >= threads) return;
+    const int run = static_cast<int>(id / vectors);
+    const int c = static_cast<int>(id % vectors) * V;
+    const int j = sequence_of_run(a.seq, run, RUN);
+    const Span span = span_of(a.seq, j);
+    const long long at = static_cast<long long>(run - run_base(a.seq, j, RUN)) * RUN;
+    if (at < 0 || at >= span.length) return;
+    const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
+    if (place < 0) return;
+    const int offset = static_cast<int>(at);
+    const int count = span.length - offset < RUN ? span.length - offset : RUN;
+
+    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(span.first) * a.x_stride + c;
+    T *y = static_cast<T *>(a.y) + static_cast<size_t>(span.first) * a.y_stride + c;
+    T *state = a.state != nullptr
+                   ? static_cast<T *>(a.state) + static_cast<size_t>(place) * (W - 1) * a.channels + c
+                   : nullptr;
+
+    X rows[RUN + W - 1];  // rows offset - (W - 1) .. offset + RUN - 1
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
+        rows[W - 1 + r] = X{};
+        if (r < count) rows[W - 1 + r] = *reinterpret_cast<const X *>(x + static_cast<size_t>(offset + r) * a.x_stride);
+    }
+    if (offset == 0) {
+        const bool kept = state != nullptr && !starts_fresh(a.seq, j);
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r) {
+            rows[r] = X{};
+            if (kept) rows[r] = *reinterpret_cast<const X *>(state + static_cast<size_t>(r) * a.channels);
+        }
+        if (state != nullptr) {
+            // the last W - 1 rows of (old state, x): old rows while the sequence is shorter
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r) {
+                const int from = span.length - (W - 1) + r;  // row of x; negative: kept row from + W - 1
+                X v{};
+                if (from >= 0) {
+                    v = *reinterpret_cast<const X *>(x + static_cast<size_t>(from) * a.x_stride);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k)
+                        if (k == from + W - 1) v = rows[k];
+                }
+                *reinterpret_cast<X *>(state + static_cast<size_t>(r) * a.channels) = v;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r) {
+            // a run starts at a multiple of RUN >= W - 1, so these rows are the sequence's own
+            rows[r] = *reinterpret_cast<const X *>(x + static_cast<size_t>(offset - (W - 1) + r) * a.x_stride);
+        }
+    }
+    static_assert(RUN >= W - 1, "a run's predecessors lie in the run before it");
+
+    float w[V][W], bias[V];
+    load_taps<T, V, W>(a, c, w, bias);
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
+        float out[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v = bias[i];
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = fmaf(w[i][k], static_cast<float>(rows[r + k][i]), v);
+            out[i] = a.silu ? silu<T>(v) : v;
+        }
+        if (r < count) store_floats<T, V>(y + static_cast<size_t>(offset + r) * a.y_stride, out);
+    }
+}
+
+template <typename T, int V, int W>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
+    using X = Vec<T, V>;
+    const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
+    if (id >= threads) return;
+    const int row = static_cast<int>(id / vectors);
+    const int c = static_cast<int>(id % vectors) * V;
+    const int place = place_of(a.seq, row);
+    if (place < 0) return;
+    T *state = static_cast<T *>(a.state) + static_cast<size_t>(place) * (W - 1) * a.channels + c;
+    X rows[W];
+    rows[W - 1] = *reinterpret_cast<const X *>(static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.x_stride + c);
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) rows[r] = *reinterpret_cast<const X *>(state + static_cast<size_t>(r) * a.channels);
+    float w[V][W], bias[V];
+    load_taps<T, V, W>(a, c, w, bias);
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) *reinterpret_cast<X *>(state + static_cast<size_t>(r) * a.channels) = rows[r + 1];
+    float out[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float v = bias[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) v = fmaf(w[i][k], static_cast<float>(rows[k][i]), v);
+        out[i] = a.silu ? silu<T>(v) : v;
+    }
+    store_floats<T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + c, out);
+}
+
+template <typename T, int V, int W>
+hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
+    constexpr int kRun = 16;
+    const unsigned vectors = static_cast<unsigned>(a.channels / V);
+    const unsigned long long runs =
+        step ? static_cast<unsigned long long>(a.seq.rows)
+             : static_cast<unsigned long long>(a.seq.rows) / kRun + static_cast<unsigned long long>(a.seq.sequences);
+    const unsigned long long threads = runs * vectors;
+    const unsigned long long blocks = (threads + kThreads - 1) / kThreads;
+    if (blocks == 0) return hipSuccess;
+    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (step) {
+        hipLaunchKernelGGL((conv_step_kernel<T, V, W>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+    } else {
+        hipLaunchKernelGGL((conv_kernel<T, V, W, kRun>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t by_taps(const ConvArgs &a, bool step, hipStream_t stream) {
+    switch (a.taps) {
+        case 2: return run_conv<T, V, 2>(a, step, stream);
+        case 3: return run_conv<T, V, 3>(a, step, stream);
+        case 4: return run_conv<T, V, 4>(a, step, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <typename T>
+hipError_t by_alignment(const ConvArgs &a, bool step, hipStream_t stream) {
+    constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
+                           reinterpret_cast<uintptr_t>(a.state);
+    const bool wide = bits % 16 == 0 && a.channels % kVec == 0 && a.x_stride % kVec == 0 && a.y_stride % kVec == 0;
+    return wide ? by_taps<T, kVec>(a, step, stream) : by_taps<T, 1>(a, step, stream);
+}
+
+hipError_t by_type(const ConvArgs &a, Elem type, bool step, hipStream_t stream) {
+    switch (type) {
+        case Elem::f32: return by_alignment<float>(a, step, stream);
+        case Elem::bf16: return by_alignment<__bf16>(a, step, stream);
+        default: return by_alignment<_Float16>(a, step, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_conv(const ConvArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, false, stream); }
+
+hipError_t launch_conv_step(const ConvArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, true, stream); }
+
+}  // namespace bl

@@ -1,0 +1,95 @@
+// Device helpers shared by the kernels of the causal sequence operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "sequence_internal.h"
+
+namespace bl {
+
+template <typename T, int N>
+using Vec = T __attribute__((ext_vector_type(N)));
+
+template <typename T, int N>
+__device__ __forceinline__ void load_floats(const T *p, float (&out)[N]) {
+    if constexpr (N == 1) {
+        out[0] = static_cast<float>(p[0]);
+    } else {
+        const Vec<T, N> v = *reinterpret_cast<const Vec<T, N> *>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = static_cast<float>(v[i]);
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_floats(T *p, const float (&in)[N]) {
+    if constexpr (N == 1) {
+        p[0] = static_cast<T>(in[0]);
+    } else {
+        Vec<T, N> v;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = static_cast<T>(in[i]);
+        *reinterpret_cast<Vec<T, N> *>(p) = v;
+    }
+}
+
+// v * sigmoid(v). 32-bit tensors take the correctly rounded division and the 1-ulp exponential;
+// for 16-bit ones v_exp_f32 and v_rcp_f32 (relative error below 2^-20) are far inside the output's
+// rounding of 2^-9 or 2^-12.
+template <typename T>
+__device__ __forceinline__ float silu(float v) {
+    if constexpr (sizeof(T) == 4) {
+        return v / (1.0f + expf(-v));
+    } else {
+        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * v));
+    }
+}
+
+// One sequence's rows in a packed batch, cut to 0..rows.
+struct Span {
+    int first;
+    int length;
+};
+
+__device__ __forceinline__ int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
+
+__device__ __forceinline__ Span span_of(const SequenceArgs &s, int j) {
+    if (s.starts == nullptr) return {j, 1};
+    const int first = clamp_row(s.starts[j], s.rows);
+    const int end = clamp_row(s.starts[j + 1], s.rows);
+    return {first, end > first ? end - first : 0};
+}
+
+// Runs of `size` rows that never cross a sequence: run r belongs to the last sequence j with
+// starts[j] / size + j <= r, as its run r - (starts[j] / size + j). Sequence j has
+// floor(starts[j + 1] / size) - floor(starts[j] / size) + 1 >= ceil(length / size) run numbers, so
+// rows / size + sequences numbers cover every batch without a table of lengths; numbers past a
+// sequence's end have no rows.
+__device__ __forceinline__ int run_base(const SequenceArgs &s, int j, int size) {
+    return clamp_row(s.starts[j], s.rows) / size + j;
+}
+
+__device__ __forceinline__ int sequence_of_run(const SequenceArgs &s, int run, int size) {
+    int low = 0, high = s.sequences - 1;  // the answer is in low..high (run_base(0) may exceed run: then 0)
+    while (low < high) {
+        const int mid = (low + high + 1) >> 1;
+        if (run_base(s, mid, size) <= run) {
+            low = mid;
+        } else {
+            high = mid - 1;
+        }
+    }
+    return low;
+}
+
+// The cache place of sequence j: -1 for one that is padding.
+__device__ __forceinline__ int place_of(const SequenceArgs &s, int j) {
+    const int p = s.slots != nullptr ? s.slots[j] : j;
+    return p >= 0 && p < s.places ? p : -1;
+}
+
+__device__ __forceinline__ bool starts_fresh(const SequenceArgs &s, int j) {
+    return s.fresh != nullptr && s.fresh[j] != 0;
+}
+
+}  // namespace bl

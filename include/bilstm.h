@@ -354,6 +354,92 @@ bilstm_status bilstm_heads_forward(bilstm_heads *heads, const float *y, size_t y
 /* Release the heads' device memory (waits for the device first). NULL is a no-op. */
 void bilstm_heads_destroy(bilstm_heads *heads);
 
+/* ---- operators of causal sequence layers -------------------------------------------- */
+
+/*
+ * What a causal layer beside the stack needs: a short causal convolution and a selective state
+ * space scan, each over packed sequences and for single tokens with a state carried from call
+ * to call; the root-mean-square norm that joins layers; and the log probabilities of given
+ * tokens (or classes) with entropy and top alternatives.
+ *
+ * Conventions of these calls, besides the shared ones above
+ *  - They are plain calls without a plan: `device` names the HIP device (gfx950 only) that all
+ *    pointers belong to and that `stream` was created on. They allocate nothing, so they can be
+ *    captured into a graph; a call that needs scratch memory takes it from the caller, and calls
+ *    that may run at the same time must not share it. The calling thread's current device is
+ *    the same after the call as before it.
+ *  - `type` is the element type of the tensors that are not said to be float or integers. Sums,
+ *    states of the scan and statistics are held in float32 (logarithms of decays in more);
+ *    outputs are rounded once.
+ *  - Matrices of rows come with a row stride in elements (>= the row's width): element (i, j) is
+ *    data[i * stride + j]. `len` is the number of elements from `data` on that belong to the
+ *    buffer; it must hold (rows - 1) * stride + width elements (BILSTM_BUFFER_LENGTH). Buffers
+ *    without a stride are contiguous and their `len` is checked exactly.
+ *  - Pointers must be aligned to their element; 16-byte aligned pointers, strides and widths are
+ *    faster. An output must not overlap an input unless a call says so.
+ *  - Packed sequences: `starts` holds `sequences` + 1 non-decreasing row numbers on the device;
+ *    sequence j is rows starts[j] .. starts[j + 1] - 1 and may be empty. Rows before the first and
+ *    behind the last sequence are not written. Values outside 0..rows are clamped.
+ *  - A state cache has `places` places; slots[j] (device; NULL = j) is the place of sequence or
+ *    row j. A slot outside the cache marks padding: that sequence or row is skipped, its output
+ *    rows are left as they were. Two sequences of one call must not share a place: which of them
+ *    is kept then is not defined. `fresh` (device, one byte a sequence; NULL = all 0): nonzero = the
+ *    sequence starts from zeros, whatever its place holds. A sequence without rows leaves its
+ *    place as it was.
+ */
+typedef enum {
+    BILSTM_FLOAT32 = 0,
+    BILSTM_BFLOAT16 = 1,
+    BILSTM_FLOAT16 = 2
+} bilstm_type;
+
+/* A matrix of rows in device memory (see the conventions above). */
+typedef struct {
+    const void *data;
+    uint64_t len;
+    uint64_t stride;
+} bilstm_rows;
+
+/* A contiguous device buffer; data may be NULL (with len 0) where it is optional. */
+typedef struct {
+    const void *data;
+    uint64_t len;
+} bilstm_buffer;
+
+/*
+ * Short causal convolution per channel:
+ *   v[t][c] = bias[c] + sum_k weight[c][k] * x[t - taps + 1 + k][c],  k = 0 .. taps - 1
+ *   y[t][c] = v, or v * sigmoid(v) with silu
+ * Rows before a sequence's first one come from its place in the state cache, which holds the
+ * last taps - 1 rows of x the sequence has seen, oldest first, and is updated by the call.
+ */
+typedef struct {
+    int32_t device;
+    int32_t type;       /* bilstm_type of x, weight, bias, state and y */
+    uint64_t rows;      /* rows of x and y, at most 2^31 - 1 */
+    uint32_t channels;  /* >= 1 */
+    uint32_t taps;      /* 2, 3 or 4 */
+    uint32_t sequences; /* bilstm_causal_conv: number of sequences; the step form ignores it */
+    uint32_t places;    /* places of the state cache */
+    int32_t silu;
+    int32_t reserved;     /* 0 */
+    bilstm_rows x;        /* [rows][channels] */
+    bilstm_buffer weight; /* [channels][taps] */
+    bilstm_buffer bias;   /* [channels], optional */
+    bilstm_buffer starts; /* int32 [sequences + 1]; the step form ignores it */
+    bilstm_buffer state;  /* [places][taps - 1][channels], updated; optional for bilstm_causal_conv:
+                             without it sequences start from zeros and nothing is kept */
+    bilstm_buffer slots;  /* int32 [sequences] or [rows], optional */
+    bilstm_buffer fresh;  /* uint8 [sequences], optional; the step form ignores it */
+    bilstm_rows y;        /* [rows][channels]; must not overlap x or state */
+} bilstm_conv_args;
+
+/* The convolution over packed sequences. Asynchronous on `stream`. */
+bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream);
+
+/* One new row per sequence: row i of x continues the sequence at place slots[i]. */
+bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream);
+
 /* ---- host-only helpers: no GPU call, usable without a device ---------------------- */
 
 /*

@@ -1,0 +1,120 @@
+"""Refusals of the causal sequence operators: the entry points check their arguments before they
+touch a device, so this runs without a GPU. Pointers are numbers that nothing reads."""
+
+import ctypes
+
+import pytest
+
+P = 1 << 20  # a 16-byte aligned address that no check follows
+
+
+@pytest.fixture(scope="module")
+def bl():
+    import os
+
+    import bidirectional_lstm_sequence_amd as bl
+    if not os.path.exists(bl.LIB_PATH):
+        from bidirectional_lstm_sequence_amd import _build
+        _build.build()
+    bl.library()
+    return bl
+
+
+def status(bl, name, packed):
+    return bl.STATUS[getattr(bl.library(), name)(packed, None)]
+
+
+def conv_args(**over):
+    """64 rows of 32 channels in 3 sequences, 4 taps, a cache of 5 places."""
+    f = dict(device=0, type=0, rows=64, channels=32, taps=4, sequences=3, places=5, silu=1, reserved=0,
+             x=(P, 64 * 32, 32), weight=(2 * P, 128), bias=(3 * P, 32), starts=(4 * P, 4), state=(5 * P, 5 * 96),
+             slots=(6 * P, 3), fresh=(7 * P, 3), y=(8 * P, 64 * 32, 32))
+    f.update(over)
+    return f
+
+
+def pack(form, f):
+    flat = []
+    for v in f.values():
+        flat.extend(v if isinstance(v, tuple) else (v,))
+    return form.pack(*flat)
+
+
+CONV_BAD = [
+    (dict(type=3), "BILSTM_INVALID_ARGUMENT"),
+    (dict(type=-1), "BILSTM_INVALID_ARGUMENT"),
+    (dict(channels=0), "BILSTM_INVALID_ARGUMENT"),
+    (dict(taps=1), "BILSTM_UNSUPPORTED"),
+    (dict(taps=5), "BILSTM_UNSUPPORTED"),
+    (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(sequences=(1 << 30) + 1), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(reserved=1), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(0, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P + 2, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P, 64 * 32 - 1, 32)), "BILSTM_BUFFER_LENGTH"),
+    (dict(x=(P, 1 << 62, 31)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P, 1 << 62, 1 << 60)), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(weight=(2 * P, 127)), "BILSTM_BUFFER_LENGTH"),
+    (dict(weight=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(bias=(3 * P, 31)), "BILSTM_BUFFER_LENGTH"),
+    (dict(starts=(4 * P, 3)), "BILSTM_BUFFER_LENGTH"),
+    (dict(starts=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(state=(5 * P, 4 * 96)), "BILSTM_BUFFER_LENGTH"),
+    (dict(state=(0, 0)), "BILSTM_INVALID_ARGUMENT"),  # slots without a state
+    (dict(slots=(6 * P, 2)), "BILSTM_BUFFER_LENGTH"),
+    (dict(slots=(0, 0), places=2, state=(5 * P, 2 * 96)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(fresh=(7 * P, 4)), "BILSTM_BUFFER_LENGTH"),
+    (dict(y=(P + 64 * 32 * 4 - 4, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # one element shared with x
+    (dict(y=(5 * P, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # the state
+    (dict(y=(2 * P, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # the weights
+    (dict(x=(P, 64 * 64, 64), y=(P + 124, 64 * 64, 64)), "BILSTM_INVALID_ARGUMENT"),  # columns 0..31 and 31..62
+]
+
+
+@pytest.mark.parametrize("over, expected", CONV_BAD, ids=lambda v: str(v)[:60])
+def test_conv_refuses(bl, over, expected):
+    assert status(bl, "bilstm_causal_conv", pack(bl.sequence._CONV, conv_args(**over))) == expected
+    assert bl.last_error().startswith("causal_conv:")
+
+
+def test_conv_step_refuses(bl):
+    step = dict(slots=(6 * P, 64), places=64, state=(5 * P, 64 * 96))
+    form = bl.sequence._CONV
+    assert status(bl, "bilstm_causal_conv_step", pack(form, conv_args(**step, taps=7))) == "BILSTM_UNSUPPORTED"
+    over = dict(step, state=(0, 0))
+    assert status(bl, "bilstm_causal_conv_step", pack(form, conv_args(**over))) == "BILSTM_INVALID_ARGUMENT"
+    over = dict(step, slots=(6 * P, 63))
+    assert status(bl, "bilstm_causal_conv_step", pack(form, conv_args(**over))) == "BILSTM_BUFFER_LENGTH"
+    assert bl.STATUS[bl.library().bilstm_causal_conv_step(None, None)] == "BILSTM_INVALID_ARGUMENT"
+
+
+def test_conv_accepts_what_the_header_allows(bl):
+    """Sound arguments pass every check: without a device the call then says so, and nothing was read."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are numbers: nothing may be launched")
+    form = bl.sequence._CONV
+    for over in (dict(), dict(bias=(0, 0)), dict(state=(0, 0), slots=(0, 0), fresh=(0, 0)),
+                 dict(x=(P, 64 * 64, 64), y=(P + 128, 64 * 64, 64)),  # columns side by side
+                 dict(x=(P, 63 * 100 + 32, 100))):
+        assert status(bl, "bilstm_causal_conv", pack(form, conv_args(**over))) == "BILSTM_UNSUPPORTED"
+        assert "no HIP device" in bl.last_error()
+    # nothing to do: no device is needed
+    assert status(bl, "bilstm_causal_conv", pack(form, conv_args(rows=0))) == "BILSTM_OK"
+    assert status(bl, "bilstm_causal_conv", pack(form, conv_args(sequences=0, starts=(0, 0)))) == "BILSTM_OK"
+
+
+def test_structures_have_the_header_sizes(bl):
+    """The packed layouts are the C structures of bilstm.h: 4- and 8-byte members without holes."""
+    assert ctypes.sizeof(ctypes.c_void_p) == 8
+    assert bl.sequence._CONV.size == 40 + 2 * 24 + 6 * 16
+
+
+def test_binding_refuses_before_the_library(bl):
+    import torch
+    x = torch.zeros(4, 8)
+    starts = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(TypeError):
+        bl.causal_conv(x, torch.zeros(8, 4), starts)
+    with pytest.raises(TypeError):
+        bl.causal_conv_step(x, torch.zeros(8, 4), torch.zeros(4, 3, 8))
