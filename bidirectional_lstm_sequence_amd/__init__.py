@@ -15,7 +15,8 @@ import os
 import numpy as np
 
 from . import sequence
-from .sequence import causal_conv, causal_conv_step  # noqa: F401
+from .sequence import (NormResult, TokenLogprobs, add_rms_norm, causal_conv, causal_conv_step,  # noqa: F401
+                       token_logprobs)
 
 HIDDEN = 128
 GATES = 512
@@ -36,7 +37,8 @@ EXPORTS = ["bilstm_plan_create", "bilstm_plan_create_ex", "bilstm_forward", "bil
            "bilstm_phase_times", "bilstm_destroy", "bilstm_last_error", "bilstm_pack_layer",
            "bilstm_schedule", "bilstm_probe_exchange", "bilstm_heads_create", "bilstm_heads_forward",
            "bilstm_heads_destroy", "bilstm_forward_noalloc", "bilstm_probe_fma_rate",
-           "bilstm_probe_mfma_rate", "bilstm_causal_conv", "bilstm_causal_conv_step"]
+           "bilstm_probe_mfma_rate", "bilstm_causal_conv", "bilstm_causal_conv_step",
+           "bilstm_add_rms_norm", "bilstm_token_logprobs", "bilstm_token_logprobs_scratch"]
 HEAD_IN, HEAD_MID, HEAD_CLASSES = 256, 128, 7
 
 

@@ -250,6 +250,157 @@ bilstm_status conv(const char *call, const bilstm_conv_args *args, bool step, vo
     return launched(call, step ? launch_conv_step(k, elem_of(a.type), s) : launch_conv(k, elem_of(a.type), s));
 }
 
+// ---- norm ----------------------------------------------------------------------------------
+
+bilstm_status norm(const char *call, const bilstm_norm_args *args, void *stream) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    const bilstm_norm_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.reserved != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
+    if (a.eight < BILSTM_EIGHT_NONE || a.eight > BILSTM_EIGHT_INT8) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: unknown 8-bit type %d", call, a.eight);
+    }
+    if (a.width == 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: width is 0", call);
+    if (!(a.eps >= 0.0f) || a.eps > 3.0e38f) return fail(BILSTM_INVALID_ARGUMENT, "%s: eps is not a number >= 0", call);
+    if (a.rows > kMostRows || a.width > (1u << 30)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u exceed the kernel's indexing", call,
+                    static_cast<unsigned long long>(a.rows), a.width);
+    }
+    const bool eight = a.eight != BILSTM_EIGHT_NONE;
+    if (!eight && (a.q.data != nullptr || a.scales.data != nullptr)) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: q and scales need an 8-bit type", call);
+    }
+    if (!eight && a.y.data == nullptr && a.rows > 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: y is NULL", call);
+    if (a.rows == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type);
+    BL_CHECK(check_rows(call, "x", a.x, a.rows, a.width, size));
+    if (a.residual.data != nullptr) BL_CHECK(check_rows(call, "residual", a.residual, a.rows, a.width, size));
+    BL_CHECK(check_buffer(call, "weight", a.weight, a.width, size, false));
+    if (a.residual_out.data != nullptr) BL_CHECK(check_rows(call, "residual_out", a.residual_out, a.rows, a.width, size));
+    if (a.y.data != nullptr) BL_CHECK(check_rows(call, "y", a.y, a.rows, a.width, size));
+    if (eight) {
+        BL_CHECK(check_rows(call, "q", a.q, a.rows, a.width, 1));
+        BL_CHECK(check_buffer(call, "scales", a.scales, a.rows, 4, false));
+    }
+    struct Out {
+        const char *name;
+        const bilstm_rows *view;  // may be an input itself; nullptr: may not
+        Bytes bytes;
+    };
+    const Out outs[] = {{"residual_out", &a.residual_out, bytes_of(a.residual_out, a.rows, a.width, size)},
+                        {"y", &a.y, bytes_of(a.y, a.rows, a.width, size)},
+                        {"q", nullptr, bytes_of(a.q, a.rows, a.width, 1)},
+                        {"scales", nullptr, bytes_of(a.scales, 4)}};
+    for (const Out &o : outs) {
+        BL_CHECK(check_apart(call, o.name, o.bytes, "weight", bytes_of(a.weight, size)));
+        for (const bilstm_rows *in : {&a.x, &a.residual}) {
+            if (o.view != nullptr && same_view(*o.view, *in, a.rows)) continue;
+            BL_CHECK(check_apart(call, o.name, o.bytes, in == &a.x ? "x" : "residual", bytes_of(*in, a.rows, a.width, size)));
+        }
+        for (const Out &other : outs) {
+            if (&other != &o) BL_CHECK(check_apart(call, o.name, o.bytes, other.name, other.bytes));
+        }
+    }
+    NormArgs k;
+    k.x = a.x.data;
+    k.residual = a.residual.data;
+    k.weight = a.weight.data;
+    k.residual_out = const_cast<void *>(a.residual_out.data);
+    k.y = const_cast<void *>(a.y.data);
+    k.q = static_cast<unsigned char *>(const_cast<void *>(a.q.data));
+    k.scales = static_cast<float *>(const_cast<void *>(a.scales.data));
+    k.x_stride = a.x.stride;
+    k.residual_stride = a.residual.data != nullptr ? a.residual.stride : 0;
+    k.residual_out_stride = a.residual_out.data != nullptr ? a.residual_out.stride : 0;
+    k.y_stride = a.y.data != nullptr ? a.y.stride : 0;
+    k.q_stride = eight ? a.q.stride : 0;
+    k.rows = static_cast<int>(a.rows);
+    k.width = static_cast<int>(a.width);
+    k.eps = a.eps;
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    return launched(call, launch_add_rms_norm(k, elem_of(a.type), static_cast<Eight>(a.eight),
+                                              static_cast<hipStream_t>(stream)));
+}
+
+// ---- token log probabilities ----------------------------------------------------------------
+
+bilstm_status logprob_sizes(const char *call, const bilstm_logprobs_args *args) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    if (args->vocabulary == 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: vocabulary is 0", call);
+    if (args->rows > kMostRows || args->vocabulary > (1u << 20)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u tokens exceed the kernel's indexing", call,
+                    static_cast<unsigned long long>(args->rows), args->vocabulary);
+    }
+    if (args->top > static_cast<uint32_t>(kMostTop) || args->top > args->vocabulary) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: top is %u: at most %d and the vocabulary", call, args->top, kMostTop);
+    }
+    return BILSTM_OK;
+}
+
+bilstm_status logprobs(const char *call, const bilstm_logprobs_args *args, void *stream) {
+    BL_CHECK(logprob_sizes(call, args));
+    const bilstm_logprobs_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.reserved != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
+    if (a.given > 1024) return fail(BILSTM_INVALID_ARGUMENT, "%s: %u given tokens a row: at most 1024", call, a.given);
+    if (a.rows == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type);
+    BL_CHECK(check_rows(call, "logits", a.logits, a.rows, a.vocabulary, size));
+    if (a.given > 0) {
+        BL_CHECK(check_buffer(call, "tokens", a.tokens, a.rows * a.given, 8, false));
+        BL_CHECK(check_buffer(call, "logprobs", a.logprobs, a.rows * a.given, 4, false));
+    }
+    BL_CHECK(check_buffer(call, "entropy", a.entropy, a.rows, 4, false));
+    if (a.top > 0) {
+        BL_CHECK(check_buffer(call, "top_tokens", a.top_tokens, a.rows * a.top, 8, false));
+        BL_CHECK(check_buffer(call, "top_logprobs", a.top_logprobs, a.rows * a.top, 4, false));
+    }
+    const uint64_t need = logprob_scratch_bytes(static_cast<int>(a.rows), static_cast<int>(a.vocabulary),
+                                                static_cast<int>(a.top));
+    if (need > 0) {
+        BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
+        if (a.scratch.len < need) {
+            return fail(BILSTM_BUFFER_LENGTH, "%s: scratch: expected at least %llu bytes, got %llu", call,
+                        static_cast<unsigned long long>(need), static_cast<unsigned long long>(a.scratch.len));
+        }
+    }
+    const bilstm_buffer none = {nullptr, 0};
+    struct Region {
+        const char *name;
+        Bytes bytes;
+    };
+    const Region ins[] = {{"logits", bytes_of(a.logits, a.rows, a.vocabulary, size)},
+                          {"tokens", bytes_of(a.given > 0 ? a.tokens : none, 8)}};
+    const Region outs[] = {{"logprobs", bytes_of(a.given > 0 ? a.logprobs : none, 4)},
+                           {"entropy", bytes_of(a.entropy, 4)},
+                           {"top_tokens", bytes_of(a.top > 0 ? a.top_tokens : none, 8)},
+                           {"top_logprobs", bytes_of(a.top > 0 ? a.top_logprobs : none, 4)},
+                           {"scratch", bytes_of(need > 0 ? a.scratch : none, 1)}};
+    for (const Region &o : outs) {
+        for (const Region &in : ins) BL_CHECK(check_apart(call, o.name, o.bytes, in.name, in.bytes));
+        for (const Region &other : outs) {
+            if (&other != &o) BL_CHECK(check_apart(call, o.name, o.bytes, other.name, other.bytes));
+        }
+    }
+    LogprobArgs k;
+    k.logits = a.logits.data;
+    k.stride = a.logits.stride;
+    k.tokens = static_cast<const long long *>(a.tokens.data);
+    k.logprobs = static_cast<float *>(const_cast<void *>(a.logprobs.data));
+    k.entropy = static_cast<float *>(const_cast<void *>(a.entropy.data));
+    k.top_tokens = static_cast<long long *>(const_cast<void *>(a.top_tokens.data));
+    k.top_logprobs = static_cast<float *>(const_cast<void *>(a.top_logprobs.data));
+    k.scratch = const_cast<void *>(a.scratch.data);
+    k.rows = static_cast<int>(a.rows);
+    k.vocabulary = static_cast<int>(a.vocabulary);
+    k.given = static_cast<int>(a.given);
+    k.top = static_cast<int>(a.top);
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    return launched(call, launch_token_logprobs(k, elem_of(a.type), static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -260,6 +411,22 @@ bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream) {
 
 bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream) {
     return conv("causal_conv_step", args, true, stream);
+}
+
+bilstm_status bilstm_add_rms_norm(const bilstm_norm_args *args, void *stream) {
+    return norm("add_rms_norm", args, stream);
+}
+
+bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, uint64_t *bytes) {
+    BL_CHECK(logprob_sizes("token_logprobs_scratch", args));
+    if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "token_logprobs_scratch: bytes is NULL");
+    *bytes = logprob_scratch_bytes(static_cast<int>(args->rows), static_cast<int>(args->vocabulary),
+                                   static_cast<int>(args->top));
+    return BILSTM_OK;
+}
+
+bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stream) {
+    return logprobs("token_logprobs", args, stream);
 }
 
 }  // extern "C"

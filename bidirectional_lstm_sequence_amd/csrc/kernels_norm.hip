@@ -1,0 +1,223 @@
+// Root-mean-square norm of rows with the residual's addition and an output in 8 bits.
+//
+//   s = x + residual;  r = 1 / sqrt(mean(s^2) + eps);  y = s r w;  scale = max|y| / top;  q = y / scale
+//
+// About 10 flops an element against 3 to 16 bytes: bound by memory. A group of lanes takes a row
+// and keeps it in registers, so every input is read once and every output written once. The sum of
+// squares and max|s w| come out of the same pass: max|y| = r max|s w| needs no second look at the
+// row. Rows that no register file holds (kBlocks) are read a second time for the outputs, from
+// the L2 where they fit. The sum s is not rounded to the tensor's type before it is normed.
+#include "sequence_device.h"
+
+namespace bl {
+namespace {
+
+constexpr float kLeastScale = 0x1p-100f;
+
+// Sum and maximum over the lanes of a group: 64 (a wave) or a whole workgroup.
+template <int GROUP>
+__device__ __forceinline__ void reduce(float &sum, float &most) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        sum += __shfl_xor(sum, o);
+        most = fmaxf(most, __shfl_xor(most, o));
+    }
+    if constexpr (GROUP > 64) {
+        __shared__ float sums[GROUP / 64], mosts[GROUP / 64];
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            sums[wave] = sum;
+            mosts[wave] = most;
+        }
+        __syncthreads();
+        sum = sums[0];
+        most = mosts[0];
+#pragma unroll
+        for (int w = 1; w < GROUP / 64; ++w) {
+            sum += sums[w];
+            most = fmaxf(most, mosts[w]);
+        }
+    }
+}
+
+// V values of y as 8-bit codes. e4m3: v_cvt_pk_fp8_f32 rounds to nearest even (OCP e4m3 on gfx950);
+// the clamp keeps a quotient that rounding left just above the top inside the range.
+template <int V, Eight E>
+__device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V], float inverse) {
+    unsigned char code[V];
+    if constexpr (E == Eight::e4m3) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float u = fminf(fmaxf(y[i] * inverse, -448.0f), 448.0f);
+            const float v = i + 1 < V ? fminf(fmaxf(y[i + 1 < V ? i + 1 : i] * inverse, -448.0f), 448.0f) : 0.0f;
+            const int two = __builtin_amdgcn_cvt_pk_fp8_f32(u, v, 0, false);
+            code[i] = static_cast<unsigned char>(two);
+            if (i + 1 < V) code[i + 1 < V ? i + 1 : i] = static_cast<unsigned char>(two >> 8);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            code[i] = static_cast<unsigned char>(
+                static_cast<int>(rintf(fminf(fmaxf(y[i] * inverse, -127.0f), 127.0f))));
+        }
+    }
+    if constexpr (V == 1) {
+        p[0] = code[0];
+    } else {
+        Vec<unsigned char, V> v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = code[i];
+        *reinterpret_cast<Vec<unsigned char, V> *>(p) = v;
+    }
+}
+
+// GROUP lanes a row, BLOCKS vectors of V elements a lane in registers; BLOCKS = 0: any width, the
+// row is read again for the outputs.
+template <typename T, int V, int GROUP, int BLOCKS, Eight E>
+__global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArgs a) {
+    constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
+    constexpr int kRows = kThreads / GROUP;
+    const int lane = threadIdx.x % GROUP;
+    const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / GROUP;
+    if (row >= a.rows) return;  // whole waves (GROUP = 64) or no workgroup at all: no barrier is left behind
+    const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+    const T *residual = a.residual != nullptr ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
+    const T *weight = static_cast<const T *>(a.weight);
+    T *residual_out = a.residual_out != nullptr ? static_cast<T *>(a.residual_out) + row * a.residual_out_stride : nullptr;
+    T *y = a.y != nullptr ? static_cast<T *>(a.y) + row * a.y_stride : nullptr;
+    unsigned char *q = a.q + row * a.q_stride;
+
+    auto load = [&](int c, float (&s)[V]) {
+        load_floats<T, V>(x + c, s);
+        if (residual != nullptr) {
+            float r[V];
+            load_floats<T, V>(residual + c, r);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] += r[i];
+        }
+    };
+    float sum = 0.0f, most = 0.0f;
+    auto measure = [&](int c, const float (&s)[V]) {
+        float w[V];
+        if constexpr (E != Eight::none) load_floats<T, V>(weight + c, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sum = fmaf(s[i], s[i], sum);
+            if constexpr (E != Eight::none) most = fmaxf(most, fabsf(s[i] * w[i]));
+        }
+    };
+    float r = 0.0f, inverse = 0.0f;
+    auto settle = [&] {
+        reduce<GROUP>(sum, most);
+        // correctly rounded square root and division: once a row
+        r = 1.0f / sqrtf(sum / static_cast<float>(a.width) + a.eps);
+        if constexpr (E != Eight::none) {
+            constexpr float kTop = E == Eight::e4m3 ? 448.0f : 127.0f;
+            // a NaN or an infinity is in `sum`, where the maximum may have dropped it
+            const float top = sum < __builtin_huge_valf() ? most * r : __builtin_nanf("");
+            float scale = top == 0.0f ? 1.0f : top / kTop;
+            if (scale < kLeastScale) scale = kLeastScale;  // its reciprocal stays finite
+            inverse = 1.0f / scale;
+            if (lane == 0) a.scales[row] = scale;
+        }
+    };
+    auto emit = [&](int c, const float (&s)[V]) {
+        float w[V], out[V];
+        load_floats<T, V>(weight + c, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = s[i] * r * w[i];
+        if (residual_out != nullptr) store_floats<T, V>(residual_out + c, s);
+        if (y != nullptr) store_floats<T, V>(y + c, out);
+        if constexpr (E != Eight::none) store_eight<V, E>(q + c, out, inverse);
+    };
+
+    if constexpr (BLOCKS > 0) {
+        float s[BLOCKS][V];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int c = (b * GROUP + lane) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[b][i] = 0.0f;
+            if (c < a.width) load(c, s[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int c = (b * GROUP + lane) * V;
+            if (c < a.width) measure(c, s[b]);
+        }
+        settle();
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int c = (b * GROUP + lane) * V;
+            if (c < a.width) emit(c, s[b]);
+        }
+    } else {
+        // outputs may be the inputs' own memory: nothing is written before a lane's second look,
+        // and a lane reads only what it writes itself
+        float s[V];
+        for (int c = lane * V; c < a.width; c += GROUP * V) {
+            load(c, s);
+            measure(c, s);
+        }
+        settle();
+        for (int c = lane * V; c < a.width; c += GROUP * V) {
+            load(c, s);
+            emit(c, s);
+        }
+    }
+}
+
+template <typename T, int V, int GROUP, int BLOCKS>
+hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
+    constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
+    constexpr int kRows = kThreads / GROUP;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.rows) + kRows - 1) / kRows));
+    switch (eight) {
+        case Eight::none:
+            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::none>), grid, dim3(kThreads), 0, stream, a);
+            break;
+        case Eight::e4m3:
+            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::e4m3>), grid, dim3(kThreads), 0, stream, a);
+            break;
+        default:
+            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::int8>), grid, dim3(kThreads), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+// A wave a row while a lane needs at most four vectors (no barrier, four rows a workgroup), then a
+// workgroup of 256, then one of 1024 lanes, then the form that reads the row twice.
+template <typename T, int V>
+hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
+    const int vectors = (a.width + V - 1) / V;
+    if (vectors <= 64) return run<T, V, 64, 1>(a, eight, stream);
+    if (vectors <= 4 * 64) return run<T, V, 64, 4>(a, eight, stream);
+    if (vectors <= 4 * 256) return run<T, V, 256, 4>(a, eight, stream);
+    if (vectors <= 4 * 1024) return run<T, V, 1024, 4>(a, eight, stream);
+    return run<T, V, 1024, 0>(a, eight, stream);
+}
+
+template <typename T>
+hipError_t by_alignment(const NormArgs &a, Eight eight, hipStream_t stream) {
+    constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
+                           reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
+                           reinterpret_cast<uintptr_t>(a.y);
+    const size_t strides = a.x_stride | a.residual_stride | a.residual_out_stride | a.y_stride | a.q_stride;
+    const bool wide = bits % 16 == 0 && reinterpret_cast<uintptr_t>(a.q) % kVec == 0 && a.width % kVec == 0 &&
+                      strides % kVec == 0;
+    return wide ? by_width<T, kVec>(a, eight, stream) : by_width<T, 1>(a, eight, stream);
+}
+
+}  // namespace
+
+hipError_t launch_add_rms_norm(const NormArgs &a, Elem type, Eight eight, hipStream_t stream) {
+    if (a.rows <= 0) return hipSuccess;
+    switch (type) {
+        case Elem::f32: return by_alignment<float>(a, eight, stream);
+        case Elem::bf16: return by_alignment<__bf16>(a, eight, stream);
+        default: return by_alignment<_Float16>(a, eight, stream);
+    }
+}
+
+}  // namespace bl

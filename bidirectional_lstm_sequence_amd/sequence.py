@@ -20,6 +20,9 @@ _VIEW = "3Q"
 _BUFFER = "2Q"
 _CONV = struct.Struct("<iiQIIIIii" + _VIEW + _BUFFER * 6 + _VIEW)
 
+_NORM = struct.Struct("<iiQIifi" + _VIEW * 2 + _BUFFER + _VIEW * 3 + _BUFFER)
+_LOGPROBS = struct.Struct("<iiQIIIi" + _VIEW + _BUFFER * 6)
+
 NO_BUFFER = (0, 0)
 NO_ROWS = (0, 0, 0)
 
@@ -27,7 +30,11 @@ NO_ROWS = (0, 0, 0)
 def signatures() -> dict:
     P = ctypes.c_void_p
     args = [ctypes.c_char_p, P]
-    return {name: (args, ctypes.c_int) for name in ("bilstm_causal_conv", "bilstm_causal_conv_step")}
+    sizes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint64)]
+    sig = {name: (args, ctypes.c_int) for name in ("bilstm_causal_conv", "bilstm_causal_conv_step",
+                                                   "bilstm_add_rms_norm", "bilstm_token_logprobs")}
+    sig["bilstm_token_logprobs_scratch"] = (sizes, ctypes.c_int)
+    return sig
 
 
 def _kinds():
@@ -105,6 +112,17 @@ class _Call:
         with contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=self.dtype if dtype is None else dtype, device=f"cuda:{self.device}")
 
+    def scratch(self, name: str, packed: bytes):
+        """(tensor, buffer) of the scratch memory the call needs by the library's own count."""
+        import torch
+        from . import _check, library
+        need = ctypes.c_uint64()
+        _check(getattr(library(), name)(packed, ctypes.byref(need)))
+        if need.value == 0:
+            return None, NO_BUFFER
+        t = self.empty((need.value,), torch.uint8)
+        return t, (t.data_ptr(), need.value)
+
     def run(self, name: str, packed: bytes) -> None:
         import torch
         from . import _check, library
@@ -176,3 +194,94 @@ def causal_conv_step(x, weight, state, bias=None, slots=None, silu: bool = True,
         *call.buffer(state, "state", (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), torch.int32),
         *NO_BUFFER, *yv))
     return out
+
+
+class NormResult(NamedTuple):
+    """``add_rms_norm``'s outputs; what was not asked for is None."""
+
+    y: object
+    q: object
+    scales: object
+    residual: object
+
+
+def _eight_bit():
+    import torch
+    return {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
+
+
+def add_rms_norm(x, weight, eps: float = 1e-5, residual=None, eight_bit=None, keep_y=None, out=None, residual_out=None,
+                 q=None, scales=None, stream=None) -> NormResult:
+    """Root-mean-square norm of the rows of ``x`` [rows, width] (with ``residual`` added first) times
+    ``weight`` [width].
+
+    Returns ``NormResult(y, q, scales, residual)``: ``residual`` is x + residual (None without one);
+    ``eight_bit`` "e4m3" or "int8" gives the rows in 8 bits, ``q``, and their ``scales`` [rows] float32
+    with y close to q * scales[:, None]; ``y`` itself comes with them if ``keep_y`` is true, without
+    ``eight_bit`` always. ``out`` and ``residual_out`` may be ``x`` or ``residual`` themselves.
+    """
+    import torch
+    call = _Call(x, "x", stream)
+    shape = _dims(x, "x", 2)
+    kinds = _eight_bit()
+    if eight_bit not in kinds:
+        raise ValueError(f"eight_bit must be None, 'e4m3' or 'int8', got {eight_bit!r}")
+    kind, code = kinds[eight_bit]
+    if kind == 0 and (q is not None or scales is not None or keep_y is False):
+        raise ValueError("without eight_bit the norm gives y only")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if out is None and (kind == 0 or keep_y):
+        out = call.empty(shape)
+    if residual is not None and residual_out is None:
+        residual_out = call.empty(shape)
+    if kind:
+        q = call.empty(shape, code) if q is None else q
+        scales = call.empty(shape[:1], torch.float32) if scales is None else scales
+    rows = lambda t, name, dtype=None: NO_ROWS if t is None else call.rows(t, name, shape, dtype)  # noqa: E731
+    call.run("bilstm_add_rms_norm", _NORM.pack(
+        call.device, call.kind, shape[0], shape[1], kind, eps, 0, *rows(x, "x"), *rows(residual, "residual"),
+        *call.buffer(weight, "weight", shape[1:]), *rows(residual_out, "residual_out"), *rows(out, "out"),
+        *rows(q, "q", code), *call.buffer(scales, "scales", shape[:1], torch.float32)))
+    return NormResult(out, q, scales, residual_out)
+
+
+class TokenLogprobs(NamedTuple):
+    """``token_logprobs``' outputs; ``top_tokens`` and ``top_logprobs`` are None without ``top``."""
+
+    logprobs: object
+    entropy: object
+    top_tokens: object
+    top_logprobs: object
+
+
+def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens under the softmax of each row of ``logits`` [rows, vocabulary]
+    (a vocabulary of at most 2^20; class scores or log probabilities, as ``Heads.forward`` gives, are taken too).
+
+    ``tokens`` int64 [rows] or [rows, given]; ``logprobs`` has its shape, float32, with NaN for a token
+    outside the vocabulary. ``entropy`` [rows] is in nats. ``top`` (at most 32) asks for that many of
+    each row's most likely tokens, int64, in falling order, of equally likely ones the lowest first,
+    and their log probabilities.
+    """
+    import torch
+    call = _Call(logits, "logits", stream)
+    rows, vocabulary = _dims(logits, "logits", 2)
+    shape = tuple(getattr(tokens, "shape", ()))
+    if len(shape) not in (1, 2) or shape[0] != rows:
+        raise ValueError(f"tokens must be [{rows}] or [{rows}, given], got {list(shape)}")
+    given = shape[1] if len(shape) == 2 else 1
+    if top < 0:
+        raise ValueError(f"top must be 0 or more, got {top}")
+    view = call.rows(logits, "logits", (rows, vocabulary))
+    ids = call.buffer(tokens, "tokens", shape, torch.int64)
+    head = (call.device, call.kind, rows, vocabulary, given, top, 0, *view, *ids)
+    hold, scratch = call.scratch("bilstm_token_logprobs_scratch", _LOGPROBS.pack(*head, *NO_BUFFER * 5))
+    logprobs, entropy = call.empty(shape, torch.float32), call.empty((rows,), torch.float32)
+    top_tokens = call.empty((rows, top), torch.int64) if top else None
+    top_logprobs = call.empty((rows, top), torch.float32) if top else None
+    place = lambda t: NO_BUFFER if t is None else (t.data_ptr(), t.numel())  # noqa: E731
+    call.run("bilstm_token_logprobs", _LOGPROBS.pack(
+        *head, *place(logprobs), *place(entropy), *place(top_tokens), *place(top_logprobs), *scratch))
+    del hold  # its memory goes back to the call's stream, behind the call's work
+    return TokenLogprobs(logprobs, entropy, top_tokens, top_logprobs)

@@ -440,6 +440,76 @@ bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream);
 /* One new row per sequence: row i of x continues the sequence at place slots[i]. */
 bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream);
 
+/*
+ * Root-mean-square norm of each row with the residual's addition, and an output in 8 bits:
+ *   s = x + residual (x alone without a residual), kept in float32 for what follows
+ *   residual_out = s;  y = s / sqrt(mean(s^2) + eps) * weight
+ *   scale = max|y| / 448 (e4m3) or / 127 (int8), at least 2^-100, and 1 where y is all zeros;
+ *   q = y / scale, rounded to nearest, ties to even
+ * A row with a NaN or an infinity, or whose sum of squares leaves float32's range, gets what the
+ * formulas give for y in float32, and a NaN scale.
+ */
+typedef enum {
+    BILSTM_EIGHT_NONE = 0,
+    BILSTM_EIGHT_E4M3 = 1, /* OCP e4m3, no infinities, largest value 448 */
+    BILSTM_EIGHT_INT8 = 2
+} bilstm_eight;
+
+typedef struct {
+    int32_t device;
+    int32_t type;             /* bilstm_type of x, residual, weight, y and residual_out */
+    uint64_t rows;            /* at most 2^31 - 1 */
+    uint32_t width;           /* >= 1 */
+    int32_t eight;            /* bilstm_eight of q */
+    float eps;                /* >= 0 */
+    int32_t reserved;         /* 0 */
+    bilstm_rows x;            /* [rows][width] */
+    bilstm_rows residual;     /* [rows][width], optional */
+    bilstm_buffer weight;     /* [width] */
+    bilstm_rows residual_out; /* [rows][width], optional; may be x or residual itself */
+    bilstm_rows y;            /* [rows][width], optional if q is given; may be x or residual itself */
+    bilstm_rows q;            /* 8-bit [rows][width], with eight */
+    bilstm_buffer scales;     /* float [rows], with eight */
+} bilstm_norm_args;
+
+bilstm_status bilstm_add_rms_norm(const bilstm_norm_args *args, void *stream);
+
+/*
+ * Log probabilities of given tokens under softmax(logits), with entropy and top alternatives.
+ * Per row, with lse = log sum_v exp(logits[v]):
+ *   logprobs[i] = logits[tokens[i]] - lse for each of `given` tokens; NaN for a token outside
+ *                 0 .. vocabulary - 1
+ *   entropy     = -sum_v p_v log p_v in nats (0 log 0 = 0)
+ *   top_tokens, top_logprobs: the `top` largest logits' tokens in falling order, of equal ones
+ *                 the lowest token first (NaN counts as the largest), and their log probabilities
+ * A logit of minus infinity is a masked token. A row with no other logits gives log probabilities
+ * of minus infinity, entropy 0 and the lowest tokens. A row with a NaN or plus infinity gives NaN.
+ * The input may be log probabilities already (the heads' output): normalising them again changes
+ * nothing.
+ */
+typedef struct {
+    int32_t device;
+    int32_t type;               /* bilstm_type of logits */
+    uint64_t rows;              /* at most 2^31 - 1 */
+    uint32_t vocabulary;        /* 1 .. 2^20 */
+    uint32_t given;             /* tokens asked for per row, 0 .. 1024 */
+    uint32_t top;               /* 0 .. 32, at most vocabulary */
+    int32_t reserved;           /* 0 */
+    bilstm_rows logits;         /* [rows][vocabulary] */
+    bilstm_buffer tokens;       /* int64 [rows][given] */
+    bilstm_buffer logprobs;     /* float [rows][given] */
+    bilstm_buffer entropy;      /* float [rows] */
+    bilstm_buffer top_tokens;   /* int64 [rows][top] */
+    bilstm_buffer top_logprobs; /* float [rows][top] */
+    bilstm_buffer scratch;      /* at least bilstm_token_logprobs_scratch() bytes (len in bytes), 16-byte aligned */
+} bilstm_logprobs_args;
+
+/* Bytes of scratch memory bilstm_token_logprobs needs for these sizes (reads device, rows,
+ * vocabulary and top of `args`; no pointer). */
+bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, uint64_t *bytes);
+
+bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stream);
+
 /* ---- host-only helpers: no GPU call, usable without a device ---------------------- */
 
 /*

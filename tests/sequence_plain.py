@@ -72,3 +72,49 @@ def conv(x, weight, starts, bias, state, slots, fresh, silu, y):
         if state is not None:
             state[place] = line[length:]
     return y, state, bound
+
+
+def norm(x, weight, eps, residual):
+    """y, s = x + residual, and the bound of y before its rounding."""
+    s = x.double() + (0 if residual is None else residual.double())
+    n = s.shape[1]
+    mean = s.pow(2).sum(1, keepdim=True) / n
+    y = s / torch.sqrt(mean + eps) * weight.double()
+    # s is rounded once (and enters the mean twice), the sum of squares has at most n / 64 + 16 roundings
+    # in a row (a lane's own terms, then lanes and waves), then division, sum, square root, reciprocal and
+    # the two products; half the relative error of the mean reaches the root
+    steps = 1 + (2 + n / 64 + 16) / 2 + 6
+    return y, s, steps * U32 * y.abs()
+
+
+def logprobs(logits, tokens, top):
+    """Per row: log probabilities of `tokens`, entropy, top tokens and their log probabilities, and the
+    bounds of the first two and the last. Masked tokens are minus infinity."""
+    z = logits.double()
+    rows, v = z.shape
+    masked = torch.isinf(z) & (z < 0)
+    empty = masked.all(1)
+    m = torch.where(empty, 0.0, z.amax(1))[:, None]
+    d = torch.where(masked, 0.0, z - m)
+    e = torch.where(masked, 0.0, torch.exp(d))
+    s = e.sum(1, keepdim=True)
+    safe = torch.where(s > 0, s, 1.0)
+    log_s = torch.log(safe)
+    lp = torch.where(masked | empty[:, None], -float("inf"), d - log_s)
+    entropy = (log_s - (e * d).sum(1, keepdim=True) / safe)[:, 0]
+    inside = (tokens >= 0) & (tokens < v)
+    given = torch.where(inside, torch.gather(lp, 1, tokens.clamp(0, v - 1)), float("nan"))
+    order = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top]
+    # Relative error of the sum: each term's exponential takes a rounded difference and a rounded product
+    # (|d| half steps each; the moves to larger maxima add up to at most |d| once more each) and up to 20
+    # exponentials and products of 3 half steps, and at most 32 + 8 + 20 additions in a row.
+    spread = (e * d.abs()).sum(1) / safe[:, 0]
+    square = (e * d * d).sum(1) / safe[:, 0]
+    rel = U32 * (6 * spread + 150)
+    big = torch.nan_to_num(given.abs(), nan=0.0, posinf=0.0)
+    given_bound = rel[:, None] + 4 * U32 * (2 * log_s.abs() + 2 * big)
+    top_lp = torch.gather(lp, 1, order)
+    size = torch.nan_to_num(top_lp.abs(), posinf=0.0)
+    top_bound = rel[:, None] + 4 * U32 * (2 * log_s.abs() + 2 * size)
+    entropy_bound = rel * (1 + spread) + U32 * (6 * square + 150 * spread + 4 * (log_s[:, 0].abs() + spread))
+    return (given, entropy, order, top_lp), (given_bound, entropy_bound, top_bound)

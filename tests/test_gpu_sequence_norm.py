@@ -1,0 +1,128 @@
+"""The root-mean-square norm with the residual's addition and 8-bit outputs, against 64 bits."""
+
+import pytest
+import torch
+
+from tests import sequence_plain as plain
+
+pytestmark = pytest.mark.gpu
+
+EIGHT = {"e4m3": (448.0, 2.0 ** -4, 2.0 ** -10), "int8": (127.0, 0.0, 0.5)}  # top, half step relative, half step
+
+
+@pytest.fixture(scope="module")
+def bl():
+    import bidirectional_lstm_sequence_amd as bl
+    return bl
+
+
+def _inputs(dtype, rows, width, seed, scale=3.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, width, generator=g).to(dtype)
+    r = (torch.randn(rows, width, generator=g) * scale).to(dtype)
+    return x, r, (torch.rand(width, generator=g) + 0.5).to(dtype)
+
+
+def _check(got, x, r, w, eps, eight):
+    y, s, error = plain.norm(x, w, eps, r)
+    dtype = x.dtype
+    if r is not None:
+        assert ((got.residual.cpu().double() - s).abs() <= plain.rounded(s, 0 * s, torch.float32) + plain.rounded(s, 0 * s, dtype)).all()
+    if got.y is not None:
+        off = (got.y.cpu().double() - y).abs()
+        assert (off <= plain.rounded(y, error, dtype)).all(), (off - plain.rounded(y, error, dtype)).max()
+    if eight:
+        top, relative, step = EIGHT[eight]
+        scale = got.scales.cpu().double()[:, None]
+        most = y.abs().amax(1, keepdim=True)
+        expect = torch.where(most > 0, most / top, 1.0)
+        # the scale carries y's relative error and two roundings
+        slack = (error / y.abs().clamp(min=1e-300)).max() + 4 * plain.U32
+        assert ((scale - expect).abs() <= slack * expect).all()
+        value = got.q.cpu().double() * scale
+        # half a step of the code at y's place, y's own error and the scale's (in y's size)
+        bound = relative * y.abs() + step * expect + error + 3 * slack * y.abs() + slack * expect
+        assert ((value - y).abs() <= bound).all(), ((value - y).abs() - bound).max()
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width", [1, 7, 64, 100, 256, 1000, 2048, 4097, 8200, 40000])
+@pytest.mark.parametrize("eight", [None, "e4m3", "int8"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_matches_the_definition(bl, dtype, width, eight, residual):
+    rows = 5
+    x, r, w = _inputs(dtype, rows, width, width)
+    r = r if residual else None
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), 1e-5, residual=None if r is None else r.cuda(), eight_bit=eight, keep_y=True)
+    assert (got.q is None) == (eight is None) and (got.residual is None) == (not residual)
+    _check(got, x, r, w, 1e-5, eight)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width", [33, 512, 2500, 40000])
+def test_in_place_and_strided(bl, dtype, width):
+    """Outputs in the inputs' own memory, rows of wider buffers, and the same bits as apart from it."""
+    x, r, w = _inputs(dtype, 6, width, 1)
+    apart = bl.add_rms_norm(x.cuda(), w.cuda(), residual=r.cuda())
+    wide = torch.zeros(6, 2 * width + 8, dtype=dtype, device="cuda")
+    xv, rv = wide[:, :width], wide[:, width + 8:]
+    xv.copy_(x)
+    rv.copy_(r)
+    got = bl.add_rms_norm(xv, w.cuda(), residual=rv, out=xv, residual_out=rv)
+    assert torch.equal(xv, apart.y) and torch.equal(rv, apart.residual) and got.y is xv
+    assert not wide[:, width: width + 8].any()
+    xv.copy_(x)
+    rv.copy_(r)
+    bl.add_rms_norm(xv, w.cuda(), residual=rv, out=rv, residual_out=xv)
+    assert torch.equal(rv, apart.y) and torch.equal(xv, apart.residual)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("eight", ["e4m3", "int8"])
+def test_edge_rows(bl, dtype, eight):
+    """Zeros, one large value, tiny values, and rows that are not numbers."""
+    x = torch.zeros(6, 96, dtype=dtype)
+    x[1, 17] = 100.0
+    x[2] = torch.finfo(dtype).smallest_normal
+    x[3, 5] = float("nan")
+    x[4, 5] = float("inf")
+    x[5] = 1.0
+    w = torch.ones(96, dtype=dtype)
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), 1e-5, eight_bit=eight, keep_y=True)
+    for i in (0, 1, 2, 5):
+        one = bl.NormResult(got.y[i: i + 1], got.q[i: i + 1], got.scales[i: i + 1], None)
+        if i == 2 and dtype != torch.float16:
+            # far below the least scale 2^-100: codes of zero
+            assert got.scales[2].item() == 2.0 ** -100 and not got.q[2].float().any()
+        else:
+            _check(one, x[i: i + 1], None, w, 1e-5, eight)
+    assert got.scales[0].item() == 1.0 and not got.q[0].float().any() and not got.y[0].any()
+    assert torch.isnan(got.scales[3:5]).all() and torch.isnan(got.y[3]).all() and torch.isnan(got.y[4, 5])
+
+
+def test_many_rows_and_none(bl):
+    x, r, w = _inputs(torch.float32, 18848, 256, 2)
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), residual=r.cuda())
+    _check(got, x, r, w, 1e-5, None)
+    none = bl.add_rms_norm(x[:0].cuda(), w.cuda(), residual=r[:0].cuda(), eight_bit="e4m3")
+    assert none.q.shape == (0, 256) and none.scales.shape == (0,)
+
+
+def test_captured_graph_and_stream(bl):
+    x, r, w = (t.cuda() for t in _inputs(torch.bfloat16, 40, 1024, 3))
+    expect = bl.add_rms_norm(x, w, residual=r, eight_bit="e4m3")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = bl.add_rms_norm(x, w, residual=r, eight_bit="e4m3", stream=side)
+    side.synchronize()
+    assert torch.equal(other.scales, expect.scales)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bl.add_rms_norm(x, w, residual=r, eight_bit="e4m3")
+    for k in range(3):
+        x.copy_(torch.randn(40, 1024, generator=torch.Generator().manual_seed(k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        again = bl.add_rms_norm(x, w, residual=r, eight_bit="e4m3")
+        assert torch.equal(got.q.view(torch.uint8), again.q.view(torch.uint8))
+        assert torch.equal(got.scales, again.scales) and torch.equal(got.residual, again.residual)

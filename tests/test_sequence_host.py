@@ -104,10 +104,118 @@ def test_conv_accepts_what_the_header_allows(bl):
     assert status(bl, "bilstm_causal_conv", pack(form, conv_args(sequences=0, starts=(0, 0)))) == "BILSTM_OK"
 
 
+def norm_args(**over):
+    """64 rows of 32 with a residual and an e4m3 output."""
+    f = dict(device=0, type=1, rows=64, width=32, eight=1, eps=1e-5, reserved=0, x=(P, 64 * 32, 32),
+             residual=(2 * P, 64 * 32, 32), weight=(3 * P, 32), residual_out=(4 * P, 64 * 32, 32), y=(0, 0, 0),
+             q=(5 * P, 64 * 32, 32), scales=(6 * P, 64))
+    f.update(over)
+    return f
+
+
+NORM_BAD = [
+    (dict(type=9), "BILSTM_INVALID_ARGUMENT"),
+    (dict(eight=3), "BILSTM_INVALID_ARGUMENT"),
+    (dict(width=0), "BILSTM_INVALID_ARGUMENT"),
+    (dict(eps=-1e-6), "BILSTM_INVALID_ARGUMENT"),
+    (dict(eps=float("nan")), "BILSTM_INVALID_ARGUMENT"),
+    (dict(eps=float("inf")), "BILSTM_INVALID_ARGUMENT"),
+    (dict(reserved=2), "BILSTM_INVALID_ARGUMENT"),
+    (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(x=(0, 0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P + 1, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(residual=(2 * P, 64 * 32 - 1, 32)), "BILSTM_BUFFER_LENGTH"),
+    (dict(weight=(3 * P, 33)), "BILSTM_BUFFER_LENGTH"),
+    (dict(scales=(6 * P, 63)), "BILSTM_BUFFER_LENGTH"),
+    (dict(scales=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(q=(0, 0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(eight=0), "BILSTM_INVALID_ARGUMENT"),  # q and scales without a type
+    (dict(eight=0, q=(0, 0, 0), scales=(0, 0)), "BILSTM_INVALID_ARGUMENT"),  # no output at all
+    (dict(q=(P, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # 8-bit rows over x
+    (dict(residual_out=(2 * P + 2, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # the residual, one element on
+    (dict(residual_out=(2 * P, 64 * 33, 33)), "BILSTM_INVALID_ARGUMENT"),  # the residual with another stride
+    (dict(y=(4 * P, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # two outputs in one place
+    (dict(y=(3 * P, 64 * 32, 32)), "BILSTM_INVALID_ARGUMENT"),  # the weights
+    (dict(scales=(5 * P + 64, 64)), "BILSTM_INVALID_ARGUMENT"),  # inside q
+]
+
+
+@pytest.mark.parametrize("over, expected", NORM_BAD, ids=lambda v: str(v)[:60])
+def test_norm_refuses(bl, over, expected):
+    assert status(bl, "bilstm_add_rms_norm", pack(bl.sequence._NORM, norm_args(**over))) == expected
+    assert bl.last_error().startswith("add_rms_norm:")
+
+
+def logprob_args(**over):
+    """16 rows of 20000 tokens, two given, top 4."""
+    f = dict(device=0, type=0, rows=16, vocabulary=20000, given=2, top=4, reserved=0, logits=(P, 16 * 20000, 20000),
+             tokens=(4 * P, 32), logprobs=(5 * P, 32), entropy=(6 * P, 16), top_tokens=(7 * P, 64),
+             top_logprobs=(8 * P, 64), scratch=(9 * P, 16 * 3 * 48))
+    f.update(over)
+    return f
+
+
+LOGPROB_BAD = [
+    (dict(type=4), "BILSTM_INVALID_ARGUMENT"),
+    (dict(vocabulary=0), "BILSTM_INVALID_ARGUMENT"),
+    (dict(vocabulary=(1 << 20) + 1), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(top=33), "BILSTM_INVALID_ARGUMENT"),
+    (dict(vocabulary=3), "BILSTM_INVALID_ARGUMENT"),  # top 4 of 3
+    (dict(given=1025), "BILSTM_INVALID_ARGUMENT"),
+    (dict(reserved=1), "BILSTM_INVALID_ARGUMENT"),
+    (dict(logits=(P + 2, 16 * 20000, 20000)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(logits=(P, 16 * 20000 - 1, 20000)), "BILSTM_BUFFER_LENGTH"),
+    (dict(tokens=(4 * P + 4, 32)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(tokens=(4 * P, 31)), "BILSTM_BUFFER_LENGTH"),
+    (dict(logprobs=(5 * P, 16)), "BILSTM_BUFFER_LENGTH"),
+    (dict(entropy=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(top_tokens=(7 * P, 63)), "BILSTM_BUFFER_LENGTH"),
+    (dict(top_logprobs=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(scratch=(9 * P, 16 * 3 * 48 - 1)), "BILSTM_BUFFER_LENGTH"),
+    (dict(scratch=(9 * P + 8, 1 << 20)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(scratch=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(entropy=(P, 16)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(top_logprobs=(7 * P, 64)), "BILSTM_INVALID_ARGUMENT"),
+]
+
+
+@pytest.mark.parametrize("over, expected", LOGPROB_BAD, ids=lambda v: str(v)[:60])
+def test_logprobs_refuse(bl, over, expected):
+    assert status(bl, "bilstm_token_logprobs", pack(bl.sequence._LOGPROBS, logprob_args(**over))) == expected
+    assert bl.last_error().startswith("token_logprobs")
+
+
+def test_logprobs_scratch(bl):
+    """Tiles of 8192 logits whose rows may start up to 7 tokens into a vector; 16 bytes and a key of 8
+    for each top token a tile; none where one launch is enough."""
+    need = ctypes.c_uint64()
+    for vocabulary, tiles in ((1024, 0), (1025, 0), (8185, 0), (8186, 2), (20000, 3), (1 << 20, 129)):
+        f = logprob_args(vocabulary=vocabulary)
+        packed = pack(bl.sequence._LOGPROBS, f)
+        assert bl.library().bilstm_token_logprobs_scratch(packed, ctypes.byref(need)) == 0
+        assert need.value == 16 * tiles * (16 + 8 * 4)
+
+
+def test_sound_arguments_reach_the_device(bl):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are numbers: nothing may be launched")
+    for over in (dict(), dict(residual_out=(2 * P, 64 * 32, 32)), dict(y=(P, 64 * 32, 32)),
+                 dict(residual=(0, 0, 0), residual_out=(0, 0, 0))):
+        assert status(bl, "bilstm_add_rms_norm", pack(bl.sequence._NORM, norm_args(**over))) == "BILSTM_UNSUPPORTED"
+    for over in (dict(), dict(given=0, tokens=(0, 0), logprobs=(0, 0)), dict(vocabulary=500, scratch=(0, 0))):
+        assert status(bl, "bilstm_token_logprobs", pack(bl.sequence._LOGPROBS, logprob_args(**over))) == "BILSTM_UNSUPPORTED"
+    assert status(bl, "bilstm_add_rms_norm", pack(bl.sequence._NORM, norm_args(rows=0))) == "BILSTM_OK"
+    assert status(bl, "bilstm_token_logprobs", pack(bl.sequence._LOGPROBS, logprob_args(rows=0))) == "BILSTM_OK"
+
+
 def test_structures_have_the_header_sizes(bl):
     """The packed layouts are the C structures of bilstm.h: 4- and 8-byte members without holes."""
     assert ctypes.sizeof(ctypes.c_void_p) == 8
     assert bl.sequence._CONV.size == 40 + 2 * 24 + 6 * 16
+    assert bl.sequence._NORM.size == 32 + 5 * 24 + 2 * 16
+    assert bl.sequence._LOGPROBS.size == 32 + 24 + 6 * 16
 
 
 def test_binding_refuses_before_the_library(bl):
@@ -118,3 +226,7 @@ def test_binding_refuses_before_the_library(bl):
         bl.causal_conv(x, torch.zeros(8, 4), starts)
     with pytest.raises(TypeError):
         bl.causal_conv_step(x, torch.zeros(8, 4), torch.zeros(4, 3, 8))
+    with pytest.raises(TypeError):
+        bl.add_rms_norm(x, torch.ones(8))
+    with pytest.raises(TypeError):
+        bl.token_logprobs(x, torch.zeros(4, dtype=torch.int64))
