@@ -16,7 +16,7 @@ import numpy as np
 
 from . import sequence
 from .sequence import (NormResult, TokenLogprobs, add_rms_norm, causal_conv, causal_conv_step,  # noqa: F401
-                       token_logprobs)
+                       selective_scan, selective_scan_step, token_logprobs)
 
 HIDDEN = 128
 GATES = 512
@@ -38,6 +38,7 @@ EXPORTS = ["bilstm_plan_create", "bilstm_plan_create_ex", "bilstm_forward", "bil
            "bilstm_schedule", "bilstm_probe_exchange", "bilstm_heads_create", "bilstm_heads_forward",
            "bilstm_heads_destroy", "bilstm_forward_noalloc", "bilstm_probe_fma_rate",
            "bilstm_probe_mfma_rate", "bilstm_causal_conv", "bilstm_causal_conv_step",
+           "bilstm_scan", "bilstm_scan_step", "bilstm_scan_scratch",
            "bilstm_add_rms_norm", "bilstm_token_logprobs", "bilstm_token_logprobs_scratch"]
 HEAD_IN, HEAD_MID, HEAD_CLASSES = 256, 128, 7
 

@@ -250,6 +250,115 @@ bilstm_status conv(const char *call, const bilstm_conv_args *args, bool step, vo
     return launched(call, step ? launch_conv_step(k, elem_of(a.type), s) : launch_conv(k, elem_of(a.type), s));
 }
 
+// ---- scan ----------------------------------------------------------------------------------
+
+// The sizes of a scan, without its pointers.
+bilstm_status scan_sizes(const char *call, const bilstm_scan_args *args, bool step, ScanArgs *k) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    const bilstm_scan_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.heads == 0 || a.groups == 0 || a.heads % a.groups != 0) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %u heads in %u groups", call, a.heads, a.groups);
+    }
+    if (a.width != 32 && a.width != 64 && a.width != 128) {
+        return fail(BILSTM_UNSUPPORTED, "%s: heads of %u channels (32, 64 and 128 are built)", call, a.width);
+    }
+    if (a.states != 16 && a.states != 32 && a.states != 64 && a.states != 128 && a.states != 256) {
+        return fail(BILSTM_UNSUPPORTED, "%s: %u states (16, 32, 64, 128 and 256 are built)", call, a.states);
+    }
+    if (a.heads > (1u << 20) || a.rows > kMostRows || a.sequences > kMostSequences) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u heads exceed the kernels' indexing", call,
+                    static_cast<unsigned long long>(a.rows), a.heads);
+    }
+    k->heads = static_cast<int>(a.heads);
+    k->width = static_cast<int>(a.width);
+    k->groups = static_cast<int>(a.groups);
+    k->states = static_cast<int>(a.states);
+    k->seq.rows = static_cast<int>(a.rows);
+    k->seq.sequences = static_cast<int>(step ? a.rows : a.sequences);
+    return BILSTM_OK;
+}
+
+bilstm_status scan(const char *call, const bilstm_scan_args *args, bool step, void *stream) {
+    ScanArgs k;
+    BL_CHECK(scan_sizes(call, args, step, &k));
+    const bilstm_scan_args &a = *args;
+    BL_CHECK(check_sequences(call, a, step, &k.seq));
+    if (a.rows == 0 || k.seq.sequences == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type);
+    const uint64_t inner = static_cast<uint64_t>(a.heads) * a.width, shared = static_cast<uint64_t>(a.groups) * a.states;
+    BL_CHECK(check_rows(call, "x", a.x, a.rows, inner, size));
+    BL_CHECK(check_rows(call, "dt", a.dt, a.rows, a.heads, size));
+    BL_CHECK(check_rows(call, "b", a.b, a.rows, shared, size));
+    BL_CHECK(check_rows(call, "c", a.c, a.rows, shared, size));
+    if (a.z.data != nullptr) BL_CHECK(check_rows(call, "z", a.z, a.rows, inner, size));
+    BL_CHECK(check_rows(call, "y", a.y, a.rows, inner, size));
+    BL_CHECK(check_buffer(call, "a", a.a, a.heads, 4, false));
+    BL_CHECK(check_buffer(call, "d", a.d, a.heads, 4, true));
+    BL_CHECK(check_buffer(call, "dt_bias", a.dt_bias, a.heads, 4, true));
+    uint64_t state_len = 0;
+    if (__builtin_mul_overflow(static_cast<uint64_t>(a.places), inner * a.states, &state_len) || state_len > (1ull << 54)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: state does not fit the address space", call);
+    }
+    BL_CHECK(check_buffer(call, "state", a.state, state_len, 16, true));
+    const uint64_t need = step ? 0 : scan_scratch_bytes(k, elem_of(a.type));
+    if (need > 0) {
+        BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
+        if (a.scratch.len < need) {
+            return fail(BILSTM_BUFFER_LENGTH, "%s: scratch: expected at least %llu bytes, got %llu", call,
+                        static_cast<unsigned long long>(need), static_cast<unsigned long long>(a.scratch.len));
+        }
+    }
+    struct Region {
+        const char *name;
+        Bytes bytes;
+    };
+    const bilstm_rows no_rows = {nullptr, 0, 0};
+    const bilstm_buffer none = {nullptr, 0};
+    const Region ins[] = {{"x", bytes_of(a.x, a.rows, inner, size)},
+                          {"dt", bytes_of(a.dt, a.rows, a.heads, size)},
+                          {"b", bytes_of(a.b, a.rows, shared, size)},
+                          {"c", bytes_of(a.c, a.rows, shared, size)},
+                          {"z", bytes_of(a.z.data != nullptr ? a.z : no_rows, a.rows, inner, size)},
+                          {"a", bytes_of(a.a, 4)},
+                          {"d", bytes_of(a.d, 4)},
+                          {"dt_bias", bytes_of(a.dt_bias, 4)},
+                          {"starts", bytes_of(step ? none : a.starts, 4)},
+                          {"slots", bytes_of(a.slots, 4)},
+                          {"fresh", bytes_of(step ? none : a.fresh, 1)}};
+    const Region outs[] = {{"y", bytes_of(a.y, a.rows, inner, size)},
+                           {"state", bytes_of(a.state, 4)},
+                           {"scratch", bytes_of(need > 0 ? a.scratch : none, 1)}};
+    for (const Region &o : outs) {
+        for (const Region &in : ins) BL_CHECK(check_apart(call, o.name, o.bytes, in.name, in.bytes));
+        for (const Region &other : outs) {
+            if (&other != &o) BL_CHECK(check_apart(call, o.name, o.bytes, other.name, other.bytes));
+        }
+    }
+    k.x = a.x.data;
+    k.dt = a.dt.data;
+    k.b = a.b.data;
+    k.c = a.c.data;
+    k.z = a.z.data;
+    k.a = static_cast<const float *>(a.a.data);
+    k.d = static_cast<const float *>(a.d.data);
+    k.dt_bias = static_cast<const float *>(a.dt_bias.data);
+    k.state = static_cast<float *>(const_cast<void *>(a.state.data));
+    k.y = const_cast<void *>(a.y.data);
+    k.x_stride = a.x.stride;
+    k.dt_stride = a.dt.stride;
+    k.b_stride = a.b.stride;
+    k.c_stride = a.c.stride;
+    k.z_stride = a.z.data != nullptr ? a.z.stride : 0;
+    k.y_stride = a.y.stride;
+    k.softplus = a.softplus != 0;
+    k.scratch = const_cast<void *>(a.scratch.data);
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return launched(call, step ? launch_scan_step(k, elem_of(a.type), s) : launch_scan(k, elem_of(a.type), s));
+}
+
 // ---- norm ----------------------------------------------------------------------------------
 
 bilstm_status norm(const char *call, const bilstm_norm_args *args, void *stream) {
@@ -412,6 +521,18 @@ bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream) {
 bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream) {
     return conv("causal_conv_step", args, true, stream);
 }
+
+bilstm_status bilstm_scan_scratch(const bilstm_scan_args *args, uint64_t *bytes) {
+    ScanArgs k;
+    BL_CHECK(scan_sizes("scan_scratch", args, false, &k));
+    if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "scan_scratch: bytes is NULL");
+    *bytes = scan_scratch_bytes(k, elem_of(args->type));
+    return BILSTM_OK;
+}
+
+bilstm_status bilstm_scan(const bilstm_scan_args *args, void *stream) { return scan("scan", args, false, stream); }
+
+bilstm_status bilstm_scan_step(const bilstm_scan_args *args, void *stream) { return scan("scan_step", args, true, stream); }
 
 bilstm_status bilstm_add_rms_norm(const bilstm_norm_args *args, void *stream) {
     return norm("add_rms_norm", args, stream);

@@ -1,0 +1,147 @@
+// Selective state space scan over packed sequences and for single tokens.
+//
+//   D_t = softplus(dt_t + bias);  S_t = exp(D_t a) S_{t-1} + D_t x_t (x) b_t;  y_t = S_t c_t + d x_t
+//
+// per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z).
+#include "sequence_device.h"
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
+
+// The step D of row `row`, head `h`.
+template <typename T>
+__device__ __forceinline__ float step_of(const ScanArgs &a, long long row, int h) {
+    float v = static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]);
+    if (a.dt_bias != nullptr) v += a.dt_bias[h];
+    return a.softplus ? softplus(v) : v;
+}
+
+// A workgroup takes kThreads / (N / 4) * PASSES state rows of one head of one sequence and walks
+// over its rows, four states of a state row a lane. The single-token form is a sequence of one
+// row, bound by the state's bytes: all of a lane's state is loaded before it is used.
+template <typename T, int N, int PASSES>
+__global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int parts) {
+    constexpr int kLanes = N / 4;
+    constexpr int kStep = kThreads / kLanes;  // state rows of one pass
+    const int lane = threadIdx.x % kLanes;
+    const int part = static_cast<int>(blockIdx.x) % parts;
+    const int h = static_cast<int>(blockIdx.x) / parts % a.heads;
+    const int j = static_cast<int>(blockIdx.x) / parts / a.heads;
+    const Span span = span_of(a.seq, j);
+    if (span.length == 0) return;
+    const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
+    if (place < 0) return;
+    const int g = h / (a.heads / a.groups);
+    const int p0 = part * kStep * PASSES + threadIdx.x / kLanes;
+    float *state = a.state != nullptr
+                       ? a.state + (static_cast<size_t>(place) * a.heads + h) * a.width * N + lane * 4
+                       : nullptr;
+    const bool kept = state != nullptr && !starts_fresh(a.seq, j);
+    float s[PASSES][4];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int p = p0 + i * kStep;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
+        if (kept && p < a.width) load_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
+    }
+    const float decay = a.a[h];
+    const float skip = a.d != nullptr ? a.d[h] : 0.0f;
+    for (int t = 0; t < span.length; ++t) {
+        const long long row = static_cast<long long>(span.first) + t;
+        float b[4], c[4];
+        const T *bp = static_cast<const T *>(a.b) + row * a.b_stride + g * N + lane * 4;
+        const T *cp = static_cast<const T *>(a.c) + row * a.c_stride + g * N + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            b[e] = static_cast<float>(bp[e]);
+            c[e] = static_cast<float>(cp[e]);
+        }
+        const float step = step_of<T>(a, row, h);
+        const float keep = expf(step * decay);
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int p = p0 + i * kStep;
+            const bool live = p < a.width;
+            const float x = live ? static_cast<float>(static_cast<const T *>(a.x)[row * a.x_stride + h * a.width + p]) : 0.0f;
+            const float in = step * x;
+            float y = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[i][e] = fmaf(s[i][e], keep, in * b[e]);
+                y = fmaf(s[i][e], c[e], y);
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) y += __shfl_xor(y, o);
+            if (lane == 0 && live) {
+                y = fmaf(skip, x, y);
+                if (a.z != nullptr) {
+                    y *= silu<T>(static_cast<float>(static_cast<const T *>(a.z)[row * a.z_stride + h * a.width + p]));
+                }
+                static_cast<T *>(a.y)[row * a.y_stride + h * a.width + p] = static_cast<T>(y);
+            }
+        }
+    }
+    if (state == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int p = p0 + i * kStep;
+        if (p < a.width) store_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
+    }
+}
+
+template <typename T, int N, int PASSES>
+hipError_t run_rows(const ScanArgs &a, hipStream_t stream) {
+    constexpr int kStep = kThreads / (N / 4) * PASSES;
+    const int parts = (a.width + kStep - 1) / kStep;
+    const unsigned long long blocks =
+        static_cast<unsigned long long>(a.seq.sequences) * static_cast<unsigned>(a.heads) * static_cast<unsigned>(parts);
+    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((scan_rows_kernel<T, N, PASSES>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a,
+                       parts);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+hipError_t by_passes(const ScanArgs &a, hipStream_t stream) {
+    constexpr int kStep = kThreads / (N / 4);
+    const int passes = (a.width + kStep - 1) / kStep;
+    if (passes >= 8) return run_rows<T, N, 8>(a, stream);
+    if (passes >= 4) return run_rows<T, N, 4>(a, stream);
+    if (passes >= 2) return run_rows<T, N, 2>(a, stream);
+    return run_rows<T, N, 1>(a, stream);
+}
+
+template <typename T>
+hipError_t by_states(const ScanArgs &a, hipStream_t stream) {
+    switch (a.states) {
+        case 16: return by_passes<T, 16>(a, stream);
+        case 32: return by_passes<T, 32>(a, stream);
+        case 64: return by_passes<T, 64>(a, stream);
+        case 128: return by_passes<T, 128>(a, stream);
+        case 256: return by_passes<T, 256>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
+    switch (type) {
+        case Elem::f32: return by_states<float>(a, stream);
+        case Elem::bf16: return by_states<__bf16>(a, stream);
+        default: return by_states<_Float16>(a, stream);
+    }
+}
+
+}  // namespace
+
+size_t scan_scratch_bytes(const ScanArgs &, Elem) { return 0; }
+
+hipError_t launch_scan(const ScanArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, stream); }
+
+hipError_t launch_scan_step(const ScanArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, stream); }
+
+}  // namespace bl

@@ -20,6 +20,7 @@ _VIEW = "3Q"
 _BUFFER = "2Q"
 _CONV = struct.Struct("<iiQIIIIii" + _VIEW + _BUFFER * 6 + _VIEW)
 
+_SCAN = struct.Struct("<iiQIIIIIIii" + _VIEW * 5 + _BUFFER * 7 + _VIEW + _BUFFER)
 _NORM = struct.Struct("<iiQIifi" + _VIEW * 2 + _BUFFER + _VIEW * 3 + _BUFFER)
 _LOGPROBS = struct.Struct("<iiQIIIi" + _VIEW + _BUFFER * 6)
 
@@ -31,9 +32,10 @@ def signatures() -> dict:
     P = ctypes.c_void_p
     args = [ctypes.c_char_p, P]
     sizes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint64)]
-    sig = {name: (args, ctypes.c_int) for name in ("bilstm_causal_conv", "bilstm_causal_conv_step",
-                                                   "bilstm_add_rms_norm", "bilstm_token_logprobs")}
-    sig["bilstm_token_logprobs_scratch"] = (sizes, ctypes.c_int)
+    sig = {name: (args, ctypes.c_int) for name in ("bilstm_causal_conv", "bilstm_causal_conv_step", "bilstm_scan",
+                                                   "bilstm_scan_step", "bilstm_add_rms_norm", "bilstm_token_logprobs")}
+    for name in ("bilstm_scan_scratch", "bilstm_token_logprobs_scratch"):
+        sig[name] = (sizes, ctypes.c_int)
     return sig
 
 
@@ -194,6 +196,55 @@ def causal_conv_step(x, weight, state, bias=None, slots=None, silu: bool = True,
         *call.buffer(state, "state", (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), torch.int32),
         *NO_BUFFER, *yv))
     return out
+
+
+def _scan(name: str, x, dt, a, b, c, seq_starts, d, z, dt_bias, softplus, state, slots, fresh, out, stream):
+    import torch
+    call = _Call(x, "x", stream)
+    rows, heads, width = shape = _dims(x, "x", 3)
+    _, groups, states = _dims(b, "b", 3)
+    if seq_starts is None:
+        count, starts, begin = 0, NO_BUFFER, NO_BUFFER
+        places = call.buffer(slots, "slots", (rows,), torch.int32)
+    else:
+        count, starts, places, begin = _sequences(call, seq_starts, state, slots, fresh)
+    cache = _dims(state, "state", 4)[0] if state is not None else 0
+    if out is None:
+        out = call.empty(shape)
+    head = (call.device, call.kind, rows, heads, width, groups, states, count, cache, 1 if softplus else 0, 0,
+            *call.rows(x, "x", shape), *call.rows(dt, "dt", (rows, heads)), *call.rows(b, "b", (rows, groups, states)),
+            *call.rows(c, "c", (rows, groups, states)), *(NO_ROWS if z is None else call.rows(z, "z", shape)),
+            *call.buffer(a, "a", (heads,), torch.float32), *call.buffer(d, "d", (heads,), torch.float32),
+            *call.buffer(dt_bias, "dt_bias", (heads,), torch.float32), *starts,
+            *call.buffer(state, "state", (cache, heads, width, states), torch.float32), *places, *begin,
+            *call.rows(out, "out", shape))
+    hold, scratch = None, NO_BUFFER
+    if seq_starts is not None:
+        hold, scratch = call.scratch("bilstm_scan_scratch", _SCAN.pack(*head, *NO_BUFFER))
+    call.run(name, _SCAN.pack(*head, *scratch))
+    del hold  # its memory goes back to the call's stream, behind the call's work
+    return out
+
+
+def selective_scan(x, dt, a, b, c, seq_starts, d=None, z=None, dt_bias=None, softplus: bool = True, state=None, slots=None,
+                   fresh=None, out=None, stream=None):
+    """Selective state space scan over packed sequences; returns y like ``x``.
+
+    ``x`` and the optional gate ``z`` [rows, heads, width] (width 32, 64 or 128); ``dt`` [rows, heads];
+    ``b`` and ``c`` [rows, groups, states] (16, 32, 64, 128 or 256 states; head h belongs to group
+    h * groups // heads); ``a``, ``d`` (optional) and ``dt_bias`` (optional) float32 [heads]; with
+    ``softplus`` the step is log(1 + exp(dt + dt_bias)). ``seq_starts``, ``slots`` and ``fresh`` as in
+    ``causal_conv``; ``state`` float32 [places, heads, width, states] holds each sequence's state and is
+    updated in place. Rows of no sequence are not written: pass ``out`` to keep what they hold.
+    """
+    return _scan("bilstm_scan", x, dt, a, b, c, seq_starts, d, z, dt_bias, softplus, state, slots, fresh, out, stream)
+
+
+def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, softplus: bool = True, slots=None, out=None,
+                        stream=None):
+    """One new row per sequence of ``selective_scan``: row i continues the state at place ``slots[i]``
+    (i if None) of ``state``, which is updated in place."""
+    return _scan("bilstm_scan_step", x, dt, a, b, c, None, d, z, dt_bias, softplus, state, slots, None, out, stream)
 
 
 class NormResult(NamedTuple):

@@ -441,6 +441,53 @@ bilstm_status bilstm_causal_conv(const bilstm_conv_args *args, void *stream);
 bilstm_status bilstm_causal_conv_step(const bilstm_conv_args *args, void *stream);
 
 /*
+ * Selective state space scan. Per head h of group g = h * groups / heads, with a state S of
+ * [width][states] float32 per sequence and head:
+ *   D_t = dt[t][h] + dt_bias[h], through softplus(v) = log(1 + e^v) if asked
+ *   S_t = exp(D_t * a[h]) * S_{t-1} + D_t * x[t][h] (outer product) b[t][g]
+ *   y[t][h] = S_t c[t][g] + d[h] * x[t][h], times z[t][h] * sigmoid(z[t][h]) if z is given
+ */
+typedef struct {
+    int32_t device;
+    int32_t type;       /* bilstm_type of x, dt, b, c, z and y */
+    uint64_t rows;      /* rows of x, dt, b, c, z and y, at most 2^31 - 1 */
+    uint32_t heads;     /* >= 1, a multiple of groups */
+    uint32_t width;     /* 32, 64 or 128 channels a head */
+    uint32_t groups;    /* groups of heads that share b and c */
+    uint32_t states;    /* 16, 32, 64, 128 or 256 */
+    uint32_t sequences; /* bilstm_scan: number of sequences; the step form ignores it */
+    uint32_t places;    /* places of the state cache */
+    int32_t softplus;
+    int32_t reserved;      /* 0 */
+    bilstm_rows x;         /* [rows][heads * width] */
+    bilstm_rows dt;        /* [rows][heads] */
+    bilstm_rows b;         /* [rows][groups * states] */
+    bilstm_rows c;         /* [rows][groups * states] */
+    bilstm_rows z;         /* [rows][heads * width], optional */
+    bilstm_buffer a;       /* float [heads] */
+    bilstm_buffer d;       /* float [heads], optional */
+    bilstm_buffer dt_bias; /* float [heads], optional */
+    bilstm_buffer starts;  /* int32 [sequences + 1]; the step form ignores it */
+    bilstm_buffer state;   /* float [places][heads][width][states], updated, 16-byte aligned; optional for
+                              bilstm_scan: without it sequences start from zeros and nothing is kept */
+    bilstm_buffer slots;   /* int32 [sequences] or [rows], optional */
+    bilstm_buffer fresh;   /* uint8 [sequences], optional; the step form ignores it */
+    bilstm_rows y;         /* [rows][heads * width]; must not overlap any input */
+    bilstm_buffer scratch; /* at least bilstm_scan_scratch() bytes (len in bytes), 16-byte aligned; the step
+                              form needs none */
+} bilstm_scan_args;
+
+/* Bytes of scratch memory bilstm_scan needs for these sizes (reads device, rows, heads, width,
+ * groups, states, sequences and type of `args`; no pointer). */
+bilstm_status bilstm_scan_scratch(const bilstm_scan_args *args, uint64_t *bytes);
+
+/* The scan over packed sequences. Asynchronous on `stream`. */
+bilstm_status bilstm_scan(const bilstm_scan_args *args, void *stream);
+
+/* One new row per sequence: row i continues the state at place slots[i]. */
+bilstm_status bilstm_scan_step(const bilstm_scan_args *args, void *stream);
+
+/*
  * Root-mean-square norm of each row with the residual's addition, and an output in 8 bits:
  *   s = x + residual (x alone without a residual), kept in float32 for what follows
  *   residual_out = s;  y = s / sqrt(mean(s^2) + eps) * weight

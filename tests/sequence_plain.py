@@ -118,3 +118,61 @@ def logprobs(logits, tokens, top):
     top_bound = rel[:, None] + 4 * U32 * (2 * log_s.abs() + 2 * size)
     entropy_bound = rel * (1 + spread) + U32 * (6 * square + 150 * spread + 4 * (log_s[:, 0].abs() + spread))
     return (given, entropy, order, top_lp), (given_bound, entropy_bound, top_bound)
+
+
+def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y):
+    """The recurrence step by step. Returns y, state, and the bounds of both (y's after its rounding).
+
+    ``state`` may be None; all tensors on the CPU, y holds what rows of no sequence keep.
+    """
+    dtype = x.dtype
+    rows, heads, width = x.shape
+    groups, n = b.shape[1], b.shape[2]
+    per = heads // groups
+    xs, bs, cs, a = x.double(), b.double(), c.double(), a.double()
+    v = dt.double() + (0 if dt_bias is None else dt_bias.double())
+    # dt + bias is rounded; softplus' slope over its value is at most 1, so |v| half steps carry over;
+    # its exponential, logarithm and sum take 8 more
+    step, step_rel = (torch.nn.functional.softplus(v, threshold=1000), U32 * (v.abs() + 8)) if softplus else (v, U32 + 0 * v)
+    # Products of 16-bit tensors may be taken in two bf16 parts of each float32 operand: 2^-9 * 2^-9 of it is left
+    # out; an fp16 input is itself two parts, and the product of the two small parts is left out: 2^-18 again.
+    parts = 0.0 if dtype == torch.float32 else 2.0 ** -17
+    y, bound = y.double().clone(), torch.zeros(y.shape, dtype=torch.float64)
+    state = None if state is None else state.double().clone()
+    state_bound = None if state is None else torch.zeros_like(state)
+    for j, (first, length) in enumerate(spans(starts, rows)):
+        place = (slots[j] if slots is not None else j) if state is not None else 0
+        if length == 0 or place < 0 or (state is not None and place >= state.shape[0]):
+            continue
+        s = torch.zeros(heads, width, n, dtype=torch.float64)
+        if state is not None and not (fresh is not None and fresh[j]):
+            s = state[place].clone()
+        size, error = s.abs(), torch.zeros_like(s)
+        for t in range(first, first + length):
+            arg = step[t] * a
+            keep = torch.exp(arg)[:, None, None]
+            bt, ct = bs[t].repeat_interleave(per, 0)[:, None], cs[t].repeat_interleave(per, 0)[:, None]
+            term = (step[t][:, None] * xs[t])[:, :, None] * bt
+            # the decay's exponent carries the step's error, two roundings and the exponential's 1 ulp
+            off = (arg.abs() * (step_rel[t] + 3 * U32) + 4 * U32)[:, None, None]
+            s = keep * s + term
+            error = keep * (error + off * size) + (step_rel[t][:, None, None] + parts + 8 * U32) * term.abs()
+            size = keep * size + term.abs()
+            error = error + 2 * U32 * size  # one more addition, in sums of any order
+            out = (s * ct).sum(2)
+            weight = (size * ct.abs()).sum(2)
+            off_y = (error * ct.abs()).sum(2) + (2 * parts + 2 * U32 * (n + 80)) * weight
+            if d is not None:
+                skip = d.double()[:, None] * xs[t]
+                out, off_y = out + skip, off_y + 2 * U32 * (skip.abs() + weight)
+            if z is not None:
+                zt = z[t].double()
+                gate = zt * sigmoid(zt)
+                off_y = off_y * gate.abs() + (8 + zt.abs()) * U32 * gate.abs() * (out.abs() + off_y)
+                out = out * gate
+            y[t] = out
+            bound[t] = rounded(out, off_y, dtype)
+        if state is not None:
+            state[place] = s
+            state_bound[place] = rounded(s, error, torch.float32)
+    return y, state, bound, state_bound

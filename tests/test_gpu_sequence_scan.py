@@ -1,0 +1,243 @@
+"""The selective state space scan on the GPU against its recurrence in 64 bits."""
+
+import pytest
+import torch
+
+from tests import sequence_plain as plain
+
+pytestmark = pytest.mark.gpu
+
+LENGTHS = {
+    "one": [1],
+    "edges": [31, 32, 33, 0, 1, 63, 64, 65],
+    "chunks": [130, 2, 257],
+    "ones": [1] * 20,
+}
+
+
+@pytest.fixture(scope="module")
+def bl():
+    import bidirectional_lstm_sequence_amd as bl
+    return bl
+
+
+def _starts(lengths, before=0):
+    out = [before]
+    for n in lengths:
+        out.append(out[-1] + n)
+    return out
+
+
+class Case:
+    """Inputs on the CPU; x, b and c as columns of one buffer."""
+
+    def __init__(self, dtype, rows, heads, width, groups, states, sequences, seed, pad=0):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *shape: torch.randn(*shape, generator=g)  # noqa: E731
+        self.dtype, self.rows, self.heads, self.width, self.groups, self.states = dtype, rows, heads, width, groups, states
+        inner = heads * width
+        self.wide = (r(rows, inner + 2 * groups * states + pad) * 0.7).to(dtype)
+        self.dt = (r(rows, heads) * 0.5).to(dtype)
+        self.dt_bias = r(heads) - 2.0
+        self.a = -(torch.rand(heads, generator=g) * 8 + 0.5)
+        self.d = r(heads)
+        self.z = r(rows, heads, width).to(dtype)
+        self.state = r(sequences + 2, heads, width, states)
+        self.slots = torch.randperm(sequences + 2, generator=g)[:sequences].to(torch.int32)
+        self.fresh = torch.rand(sequences, generator=g) < 0.5
+
+    def views(self, wide):
+        inner, gn = self.heads * self.width, self.groups * self.states
+        rows = wide.shape[0]
+        return (wide[:, :inner].view(rows, self.heads, self.width),
+                wide[:, inner: inner + gn].view(rows, self.groups, self.states),
+                wide[:, inner + gn: inner + 2 * gn].view(rows, self.groups, self.states))
+
+
+def _compare(got, ref, bound, what):
+    got = got.cpu().double()
+    assert torch.isfinite(got).all(), what
+    off = (got - ref).abs()
+    assert (off <= bound).all(), f"{what}: {(off - bound).max():.3e} over the bound, at most {(off / bound.clamp(min=1e-300)).max():.2f} of it"
+
+
+def _run_and_check(bl, k, starts, stateful=True, extras=True, softplus=True, slots=None, fresh=None):
+    x, b, c = k.views(k.wide)
+    gx, gb, gc = k.views(k.wide.cuda())
+    d, z, bias = (k.d, k.z, k.dt_bias) if extras else (None, None, None)
+    cu = lambda t: None if t is None else t.cuda()  # noqa: E731
+    slots = k.slots if slots is None else slots
+    fresh = k.fresh if fresh is None else fresh
+    out = torch.full((k.rows, k.heads, k.width), 3.0, dtype=k.dtype)
+    state = k.state.cuda() if stateful else None
+    y = bl.selective_scan(gx, k.dt.cuda(), k.a.cuda(), gb, gc, torch.tensor(starts, dtype=torch.int32).cuda(), d=cu(d),
+                          z=cu(z), dt_bias=cu(bias), softplus=softplus, state=state, slots=slots.cuda() if stateful else None,
+                          fresh=fresh.cuda() if stateful else None, out=out.cuda())
+    ref, ref_state, bound, state_bound = plain.scan(
+        x, k.dt, k.a, b, c, starts, d, z, bias, softplus, k.state if stateful else None,
+        slots.tolist() if stateful else None, fresh.tolist() if stateful else None, out)
+    _compare(y, ref, bound, "y")
+    if stateful:
+        _compare(state, ref_state, state_bound, "state")
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width", [32, 64, 128])
+@pytest.mark.parametrize("states", [16, 32, 64, 128, 256])
+def test_every_shape_matches_the_recurrence(bl, dtype, width, states):
+    starts = _starts(LENGTHS["edges"], before=2)
+    k = Case(dtype, starts[-1] + 3, 2, width, 1, states, 8, width + states)
+    _run_and_check(bl, k, starts)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+@pytest.mark.parametrize("heads, groups", [(1, 1), (6, 2), (4, 4)])
+def test_packed_sequences_and_groups(bl, dtype, lengths, heads, groups):
+    lens = LENGTHS[lengths]
+    starts = _starts(lens)
+    k = Case(dtype, starts[-1], heads, 64, groups, 32, len(lens), 7)
+    slots = k.slots.clone()
+    if len(lens) > 2:
+        slots[1] = -1  # padding: its rows and every place stay as they were
+        slots[2] = 1000
+    _run_and_check(bl, k, starts, slots=slots)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_one_long_sequence(bl, dtype):
+    """Few sequences and heads: the time axis is split and joined."""
+    for rows, before in ((700, 0), (1500, 5)):
+        k = Case(dtype, rows + before, 1, 64, 1, 64, 1, rows)
+        _run_and_check(bl, k, [before, before + rows], fresh=torch.tensor([rows == 700]))
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_without_options(bl, dtype):
+    """No state, bias, skip, gate or softplus; steps as they are, all positive."""
+    k = Case(dtype, 100, 2, 64, 1, 16, 2, 3)
+    k.dt = k.dt.abs() * 0.2
+    _run_and_check(bl, k, [0, 37, 100], stateful=False, extras=False, softplus=False)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_rows_without_alignment(bl, dtype):
+    """An odd row stride: no row is aligned to more than an element."""
+    k = Case(dtype, 150, 2, 32, 2, 16, 2, 4, pad=3)
+    _run_and_check(bl, k, [0, 70, 150])
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_far_decays(bl, dtype):
+    """Decays from hardly any to a state that is gone within a row, for hundreds of rows."""
+    k = Case(dtype, 400, 4, 32, 1, 32, 1, 5)
+    k.a = -torch.tensor([1e-4, 0.3, 16.0, 300.0])
+    k.dt_bias = torch.tensor([-6.0, 0.0, 1.0, 2.0])
+    _run_and_check(bl, k, [0, 400], fresh=torch.tensor([False]))
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width, states", [(32, 16), (64, 128), (128, 256), (64, 64)])
+def test_steps_match_the_recurrence(bl, dtype, width, states):
+    rows = 5
+    k = Case(dtype, rows, 6, width, 3, states, rows, 6)
+    slots = k.slots.clone()
+    slots[3] = -5
+    x, b, c = k.views(k.wide)
+    gx, gb, gc = k.views(k.wide.cuda())
+    state, out = k.state.cuda(), torch.full((rows, 6, width), 2.0, dtype=dtype)
+    y = bl.selective_scan_step(gx, k.dt.cuda(), k.a.cuda(), gb, gc, state, d=k.d.cuda(), z=k.z.cuda(),
+                               dt_bias=k.dt_bias.cuda(), slots=slots.cuda(), out=out.cuda())
+    ref, ref_state, bound, state_bound = plain.scan(x, k.dt, k.a, b, c, list(range(rows + 1)), k.d, k.z, k.dt_bias, True,
+                                                    k.state, slots.tolist(), None, out)
+    _compare(y, ref, bound, "y")
+    _compare(state, ref_state, state_bound, "state")
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_a_prompt_and_steps_match_one_longer_prompt(bl, dtype):
+    rows, more = 90, 6
+    k = Case(dtype, rows + more, 4, 64, 1, 128, 1, 8)
+    x, b, c = k.views(k.wide)
+    gx, gb, gc = k.views(k.wide.cuda())
+    ref, ref_state, bound, state_bound = plain.scan(x, k.dt, k.a, b, c, [0, rows + more], k.d, k.z, k.dt_bias, True,
+                                                    k.state, [1], [False], torch.zeros_like(x))
+    dt, a, d, z, bias, state = (t.cuda() for t in (k.dt, k.a, k.d, k.z, k.dt_bias, k.state))
+    one = torch.tensor([1], dtype=torch.int32).cuda()
+    y = [bl.selective_scan(gx[:rows], dt[:rows], a, gb[:rows], gc[:rows], torch.tensor([0, rows], dtype=torch.int32).cuda(),
+                           d=d, z=z[:rows], dt_bias=bias, state=state, slots=one)]
+    for t in range(rows, rows + more):
+        s = slice(t, t + 1)
+        y.append(bl.selective_scan_step(gx[s], dt[s], a, gb[s], gc[s], state, d=d, z=z[s], dt_bias=bias, slots=one))
+    _compare(torch.cat(y), ref, bound, "y")
+    _compare(state, ref_state, state_bound, "state")
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_not_a_number_stays_behind_its_row(bl, dtype, bad):
+    """Rows before one that is not a number, other channels and other sequences are as without it."""
+    k = Case(dtype, 200, 2, 64, 1, 64, 2, 9)
+    x, b, c = k.views(k.wide)
+    run = lambda wide: bl.selective_scan(*(k.views(wide)[0], k.dt.cuda(), k.a.cuda()), *k.views(wide)[1:],  # noqa: E731
+                                         torch.tensor([0, 120, 200], dtype=torch.int32).cuda(), d=k.d.cuda(), z=k.z.cuda(),
+                                         dt_bias=k.dt_bias.cuda())
+    sound = run(k.wide.cuda())
+    wide = k.wide.cuda()
+    wide[75, 64 + 9] = bad  # head 1, channel 9
+    got = run(wide)
+    ref, _, bound, _ = plain.scan(x, k.dt, k.a, b, c, [0, 120, 200], k.d, k.z, k.dt_bias, True, None, None, None,
+                                  torch.zeros_like(x))
+    assert not torch.isfinite(got[75:120, 1, 9]).any()
+    got[75:120, 1, 9] = sound[75:120, 1, 9]
+    _compare(got, ref, bound, "y")
+
+
+def test_state_offsets_past_32_bits(bl):
+    """A cache of more than 2^31 floats, the last place used."""
+    heads, width, states = 64, 128, 256
+    places = (1 << 31) // (heads * width * states) + 2
+    state = torch.zeros(places, heads, width, states, device="cuda")
+    k = Case(torch.bfloat16, 3, heads, width, 1, states, 1, 10)
+    state[places - 1] = k.state[0].cuda()
+    x, b, c = k.views(k.wide)
+    gx, gb, gc = k.views(k.wide.cuda())
+    place = torch.tensor([places - 1], dtype=torch.int32).cuda()
+    y = bl.selective_scan(gx, k.dt.cuda(), k.a.cuda(), gb, gc, torch.tensor([0, 3], dtype=torch.int32).cuda(),
+                          dt_bias=k.dt_bias.cuda(), state=state, slots=place)
+    ref, ref_state, bound, state_bound = plain.scan(x, k.dt, k.a, b, c, [0, 3], None, None, k.dt_bias, True, k.state[:1],
+                                                    None, None, torch.zeros_like(x))
+    _compare(y, ref, bound, "y")
+    _compare(state[places - 1], ref_state[0], state_bound[0], "state")
+    assert not state[: places - 1].any()
+
+
+def test_starts_outside_the_rows_are_clamped(bl):
+    k = Case(torch.float32, 90, 2, 32, 1, 32, 4, 11)
+    slots = torch.arange(4, dtype=torch.int32)
+    _run_and_check(bl, k, [-9, 40, 40, 1000, 2 ** 31 - 1], slots=slots)
+
+
+def test_captured_graph_stream_and_repeated_calls(bl):
+    """Replays continue the state as eager calls do, bit for bit; so does a call on another stream."""
+    k = Case(torch.bfloat16, 600, 2, 64, 1, 128, 1, 12)
+    gx, gb, gc = k.views(k.wide.cuda())
+    starts = torch.tensor([0, 600], dtype=torch.int32).cuda()
+    dt, a, d, z, bias = (t.cuda() for t in (k.dt, k.a, k.d, k.z, k.dt_bias))
+    run = lambda state, **kw: bl.selective_scan(gx, dt, a, gb, gc, starts, d=d, z=z, dt_bias=bias, state=state, **kw)  # noqa: E731
+    eager = k.state.cuda()
+    expect = [run(eager) for _ in range(4)]
+    side, state = torch.cuda.Stream(), k.state.cuda()
+    torch.cuda.synchronize()
+    first = run(state, stream=side)
+    side.synchronize()
+    assert torch.equal(first, expect[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run(state)
+    for i in range(1, 4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect[i])
+        torch.zeros(1000, device="cuda").sum().item()
+    assert torch.equal(state, eager)

@@ -104,6 +104,66 @@ def test_conv_accepts_what_the_header_allows(bl):
     assert status(bl, "bilstm_causal_conv", pack(form, conv_args(sequences=0, starts=(0, 0)))) == "BILSTM_OK"
 
 
+def scan_args(**over):
+    """64 rows of 4 heads of 64 channels and 32 states in 3 sequences, a cache of 5 places."""
+    f = dict(device=0, type=1, rows=64, heads=4, width=64, groups=2, states=32, sequences=3, places=5, softplus=1,
+             reserved=0, x=(P, 64 * 256, 256), dt=(2 * P, 64 * 4, 4), b=(3 * P, 64 * 64, 64), c=(4 * P, 64 * 64, 64),
+             z=(5 * P, 64 * 256, 256), a=(6 * P, 4), d=(7 * P, 4), dt_bias=(8 * P, 4), starts=(9 * P, 4),
+             state=(10 * P, 5 * 4 * 64 * 32), slots=(12 * P, 3), fresh=(13 * P, 3), y=(14 * P, 64 * 256, 256),
+             scratch=(20 * P, 1 << 30))
+    f.update(over)
+    return f
+
+
+SCAN_BAD = [
+    (dict(type=3), "BILSTM_INVALID_ARGUMENT"),
+    (dict(heads=0), "BILSTM_INVALID_ARGUMENT"),
+    (dict(groups=3), "BILSTM_INVALID_ARGUMENT"),
+    (dict(groups=0), "BILSTM_INVALID_ARGUMENT"),
+    (dict(width=48), "BILSTM_UNSUPPORTED"),
+    (dict(states=8), "BILSTM_UNSUPPORTED"),
+    (dict(states=512), "BILSTM_UNSUPPORTED"),
+    (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(sequences=(1 << 30) + 1), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(reserved=1), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P + 1, 64 * 256, 256)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(x=(P, 64 * 256 - 1, 256)), "BILSTM_BUFFER_LENGTH"),
+    (dict(dt=(2 * P, 64 * 4, 3)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(dt=(0, 0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(b=(3 * P, 64 * 63, 63)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(c=(4 * P, 100, 64)), "BILSTM_BUFFER_LENGTH"),
+    (dict(z=(5 * P, 100, 256)), "BILSTM_BUFFER_LENGTH"),
+    (dict(a=(6 * P, 3)), "BILSTM_BUFFER_LENGTH"),
+    (dict(a=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(d=(7 * P, 5)), "BILSTM_BUFFER_LENGTH"),
+    (dict(dt_bias=(8 * P + 2, 4)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(starts=(9 * P, 3)), "BILSTM_BUFFER_LENGTH"),
+    (dict(state=(10 * P, 5 * 4 * 64 * 32 - 1)), "BILSTM_BUFFER_LENGTH"),
+    (dict(state=(10 * P + 4, 5 * 4 * 64 * 32)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(state=(0, 0)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(slots=(12 * P, 4)), "BILSTM_BUFFER_LENGTH"),
+    (dict(fresh=(13 * P, 2)), "BILSTM_BUFFER_LENGTH"),
+    (dict(y=(P, 64 * 256, 256)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(y=(5 * P, 64 * 256, 256)), "BILSTM_INVALID_ARGUMENT"),
+    (dict(state=(P, 5 * 4 * 64 * 32)), "BILSTM_INVALID_ARGUMENT"),
+]
+
+
+@pytest.mark.parametrize("over, expected", SCAN_BAD, ids=lambda v: str(v)[:60])
+def test_scan_refuses(bl, over, expected):
+    assert status(bl, "bilstm_scan", pack(bl.sequence._SCAN, scan_args(**over))) == expected
+    assert bl.last_error().startswith("scan:")
+
+
+def test_scan_step_refuses(bl):
+    step = dict(slots=(12 * P, 64))
+    form = bl.sequence._SCAN
+    assert status(bl, "bilstm_scan_step", pack(form, scan_args(**step, state=(0, 0)))) == "BILSTM_INVALID_ARGUMENT"
+    assert status(bl, "bilstm_scan_step", pack(form, scan_args(slots=(12 * P, 3)))) == "BILSTM_BUFFER_LENGTH"
+    assert status(bl, "bilstm_scan_step", pack(form, scan_args(slots=(0, 0)))) == "BILSTM_INVALID_ARGUMENT"
+    assert status(bl, "bilstm_scan_step", pack(form, scan_args(**step, width=16))) == "BILSTM_UNSUPPORTED"
+
+
 def norm_args(**over):
     """64 rows of 32 with a residual and an e4m3 output."""
     f = dict(device=0, type=1, rows=64, width=32, eight=1, eps=1e-5, reserved=0, x=(P, 64 * 32, 32),
@@ -206,6 +266,10 @@ def test_sound_arguments_reach_the_device(bl):
         assert status(bl, "bilstm_add_rms_norm", pack(bl.sequence._NORM, norm_args(**over))) == "BILSTM_UNSUPPORTED"
     for over in (dict(), dict(given=0, tokens=(0, 0), logprobs=(0, 0)), dict(vocabulary=500, scratch=(0, 0))):
         assert status(bl, "bilstm_token_logprobs", pack(bl.sequence._LOGPROBS, logprob_args(**over))) == "BILSTM_UNSUPPORTED"
+    for over in (dict(), dict(z=(0, 0, 0), d=(0, 0), dt_bias=(0, 0)), dict(state=(0, 0), slots=(0, 0), fresh=(0, 0))):
+        assert status(bl, "bilstm_scan", pack(bl.sequence._SCAN, scan_args(**over))) == "BILSTM_UNSUPPORTED"
+        assert "no HIP device" in bl.last_error()
+    assert status(bl, "bilstm_scan", pack(bl.sequence._SCAN, scan_args(rows=0))) == "BILSTM_OK"
     assert status(bl, "bilstm_add_rms_norm", pack(bl.sequence._NORM, norm_args(rows=0))) == "BILSTM_OK"
     assert status(bl, "bilstm_token_logprobs", pack(bl.sequence._LOGPROBS, logprob_args(rows=0))) == "BILSTM_OK"
 
@@ -214,6 +278,7 @@ def test_structures_have_the_header_sizes(bl):
     """The packed layouts are the C structures of bilstm.h: 4- and 8-byte members without holes."""
     assert ctypes.sizeof(ctypes.c_void_p) == 8
     assert bl.sequence._CONV.size == 40 + 2 * 24 + 6 * 16
+    assert bl.sequence._SCAN.size == 48 + 6 * 24 + 8 * 16
     assert bl.sequence._NORM.size == 32 + 5 * 24 + 2 * 16
     assert bl.sequence._LOGPROBS.size == 32 + 24 + 6 * 16
 
