@@ -2,23 +2,14 @@
 //
 //   D_t = softplus(dt_t + bias);  S_t = exp(D_t a) S_{t-1} + D_t x_t (x) b_t;  y_t = S_t c_t + d x_t
 //
-// per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z).
-#include "sequence_device.h"
+// per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z). Two forms: row
+// by row (here: single tokens and short sequences) and in chunks of rows (scan_chunks.h).
+#include "scan_device.h"
 
 namespace bl {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
-
-// The step D of row `row`, head `h`.
-template <typename T>
-__device__ __forceinline__ float step_of(const ScanArgs &a, long long row, int h) {
-    float v = static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]);
-    if (a.dt_bias != nullptr) v += a.dt_bias[h];
-    return a.softplus ? softplus(v) : v;
-}
 
 // A workgroup takes kThreads / (N / 4) * PASSES state rows of one head of one sequence and walks
 // over its rows, four states of a state row a lane. The single-token form is a sequence of one
@@ -61,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int par
             b[e] = static_cast<float>(bp[e]);
             c[e] = static_cast<float>(cp[e]);
         }
-        const float step = step_of<T>(a, row, h);
+        const float step = step_from(a, load_dt<T>(a, row, h), h);
         const float keep = expf(step * decay);
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
@@ -136,11 +127,38 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
     }
 }
 
+// Rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences.
+int run_rows_of(const ScanArgs &a) {
+    constexpr long long kShort = 8;      // rows a sequence, on average
+    constexpr long long kWhole = 512;    // workgroups that fill the chip without splitting
+    constexpr long long kSplit = 768;
+    const long long rows = a.seq.rows, sequences = a.seq.sequences;
+    if (rows <= kShort * sequences) return 0;
+    if (sequences * a.heads >= kWhole) return 0x7FFFFFFF;
+    long long run = (rows * a.heads + kSplit - 1) / kSplit;
+    run = (run + 63) / 64 * 64;
+    if (run < 256) run = 256;
+    return run >= rows ? 0x7FFFFFFF : static_cast<int>(run);
+}
+
 }  // namespace
 
-size_t scan_scratch_bytes(const ScanArgs &, Elem) { return 0; }
+size_t scan_scratch_bytes(const ScanArgs &a, Elem) {
+    const int run = run_rows_of(a);
+    if (run == 0 || run > a.seq.rows) return 0;
+    const size_t parts = (static_cast<size_t>(a.seq.rows / run) + a.seq.sequences) * a.heads;
+    return parts * (static_cast<size_t>(a.width) * a.states + 1) * sizeof(float);
+}
 
-hipError_t launch_scan(const ScanArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, stream); }
+hipError_t launch_scan(const ScanArgs &a, Elem type, hipStream_t stream) {
+    const int run = run_rows_of(a);
+    if (run == 0) return by_type(a, type, stream);
+    switch (type) {
+        case Elem::f32: return launch_scan_chunks<float>(a, run, stream);
+        case Elem::bf16: return launch_scan_chunks<__bf16>(a, run, stream);
+        default: return launch_scan_chunks<_Float16>(a, run, stream);
+    }
+}
 
 hipError_t launch_scan_step(const ScanArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, stream); }
 

@@ -134,9 +134,12 @@ def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y
     # dt + bias is rounded; softplus' slope over its value is at most 1, so |v| half steps carry over;
     # its exponential, logarithm and sum take 8 more
     step, step_rel = (torch.nn.functional.softplus(v, threshold=1000), U32 * (v.abs() + 8)) if softplus else (v, U32 + 0 * v)
-    # Products of 16-bit tensors may be taken in two bf16 parts of each float32 operand: 2^-9 * 2^-9 of it is left
-    # out; an fp16 input is itself two parts, and the product of the two small parts is left out: 2^-18 again.
-    parts = 0.0 if dtype == torch.float32 else 2.0 ** -17
+    # Products of 16-bit tensors are taken in bf16 parts of each float32 operand, a part leaving at most bf16's half
+    # step, 2^-8, of what it rounds. Two parts in products that only meet an output leave 2^-16; an fp16 input is
+    # two parts itself (exactly, 16 bits hold its 11), and the product of the two small ones, 2^-8 * 2^-8, is left
+    # out too: 2^-15. Three parts in products that meet the state leave 2^-24, and as much for fp16 inputs.
+    parts = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -15}[dtype]
+    kept = 0.0 if dtype == torch.float32 else 2.0 ** -23
     y, bound = y.double().clone(), torch.zeros(y.shape, dtype=torch.float64)
     state = None if state is None else state.double().clone()
     state_bound = None if state is None else torch.zeros_like(state)
@@ -156,12 +159,12 @@ def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y
             # the decay's exponent carries the step's error, two roundings and the exponential's 1 ulp
             off = (arg.abs() * (step_rel[t] + 3 * U32) + 4 * U32)[:, None, None]
             s = keep * s + term
-            error = keep * (error + off * size) + (step_rel[t][:, None, None] + parts + 8 * U32) * term.abs()
+            error = keep * (error + off * size) + (step_rel[t][:, None, None] + kept + 8 * U32) * term.abs()
             size = keep * size + term.abs()
             error = error + 2 * U32 * size  # one more addition, in sums of any order
             out = (s * ct).sum(2)
             weight = (size * ct.abs()).sum(2)
-            off_y = (error * ct.abs()).sum(2) + (2 * parts + 2 * U32 * (n + 80)) * weight
+            off_y = (error * ct.abs()).sum(2) + (parts + 2 * U32 * (n + 80)) * weight
             if d is not None:
                 skip = d.double()[:, None] * xs[t]
                 out, off_y = out + skip, off_y + 2 * U32 * (skip.abs() + weight)
