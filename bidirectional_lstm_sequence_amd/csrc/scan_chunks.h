@@ -4,26 +4,29 @@
 // before the chunk,
 //   y_t = exp(cum_t) S c_t + sum_{s <= t} (c_t . b_s) exp(cum_t - cum_s) D_s x_s
 //   S'  = exp(cum_L) S + sum_s exp(cum_L - cum_s) D_s x_s (x) b_s
-// are four matrix products. One workgroup takes a head of a run of rows (a whole sequence, or a
-// part of it where there are few) and walks over its chunks with the state in registers, so x, z, b
-// and c are read once and y is written once. P / 16 waves; wave w owns channels 16 w .. 16 w + 15:
-//   1. M[t][s] = (c_t . b_s) exp(cum_t - cum_s) D_s for s <= t: 16 x 16 blocks on and below the
-//      diagonal, spread over the waves, into LDS. The others read as zeros.
-//   2. y = (S C^T) exp(cum) + X^T M^T, the wave's 16 channels by L rows. The state is the left
-//      operand straight from the registers that step 3 leaves it in: its accumulator layout (channel
-//      = lane % 16, state 16 i + 4 (lane / 16) + r) is the operand layout of K steps whose K order
-//      is (tile parity, r) within a lane group, and c is read in that order.
-//   3. S' = exp(cum_L) S + B^T (w X) with w_s = exp(cum_L - cum_s) D_s; b and x are read from LDS by
-//      columns (ds_read_b64_tr_b16 for 16-bit elements).
-// The next chunk's rows travel from memory to registers meanwhile.
+// are four matrix products. A workgroup of four waves takes 64 CT neighbouring channels of one group
+// of heads (a head or a part of one or several heads: they share b and c) over a run of rows (a whole
+// sequence, or a part of it where there are few) and walks over its chunks with the state in
+// registers, so x and z are read once and y is written once. Per chunk the rows of b, c and x go
+// through registers, a chunk ahead, into LDS; from there each wave works alone on its 16 CT channels:
+//   1. y = (S C^T) exp(cum), channels by rows.
+//   2. S' = exp(cum_L) S + B^T (w X) with w_s = exp(cum_L - cum_s) D_s.
+//   3. per 16 rows t: G = B C^T for the 16-row blocks s up to t's, M = G exp(cum_t - cum_s) D_s for
+//      s <= t, y += X^T M, then the skip, the gate and the store.
+// Every product reads its operands in the layout that another one's result has: an accumulator
+// holds rows 4 q + r of column lane % 16 (q = lane / 16), and a K step of 32 takes within lane group q
+// the K values {16 e + 4 q + r, e < 2, r < 4}, on both sides. So S is the left operand of 1 as 2 leaves
+// it, and G that of 3 without a pass through LDS. b and x are read by columns with
+// ds_read_b64_tr_b16 (16-bit types).
 //
 // Precision. Exponents are summed in float64 and kept as two floats, so a difference of two of
 // them carries no more than the rounding of the difference. 16-bit inputs enter products as they
 // are (fp16 as two bf16 parts, exactly). Float32 operands enter as bf16 parts, each rounding leaving
 // at most 2^-8 of what it rounds: w x, whose products a state sums up over a whole sequence, in
 // three parts (2^-24 left, as float32 itself), M and S, whose products only meet a 16-bit output, in
-// two (2^-16 left). float32 inputs take the FP32 matrix instructions. Sums and the state are float32. Non-finite x must not reach the rows before it through a zero of
-// M: where a wave's outputs hold one, it takes the products with M again, row by row.
+// two (2^-16 left). float32 inputs take the FP32 matrix instructions. Sums and the state are float32.
+// A non-finite x must not reach the rows before it through a zero of M: where a wave's outputs hold
+// one, it takes step 3 again without such x and sets what follows them in their channel to NaN.
 #pragma once
 
 #include "scan_device.h"
@@ -32,6 +35,8 @@ namespace bl {
 namespace scan_chunks {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
 typedef short h4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
@@ -76,44 +81,42 @@ __device__ __forceinline__ Vec<T, 4> column4(const T *p) {
     return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
 }
 
-// Operands of the products for one input type. A fragment holds 8 values of K for row (or column)
-// lane % 16, K = 8 (lane / 16) + j unless read otherwise on both sides. In: values of an input tensor;
-// Made: float32 values on their way to an output; Kept: to the state.
+// Operands of the products for one input type: fragments of 8 values of K for row (or column)
+// lane % 16, K = 16 e + 4 (lane / 16) + r in place 4 e + r. In: values of an input tensor; Made: float32
+// values on their way to an output; Kept: to the state.
 template <typename T>
 struct Operand;
+
+// Fragments from rows of LDS (p: the lane's row and its first value) and from columns (p: the first
+// row's first column).
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> row_values(const T *p) {
+    return __builtin_shufflevector(*reinterpret_cast<const Vec<T, 4> *>(p), *reinterpret_cast<const Vec<T, 4> *>(p + 16), 0,
+                                   1, 2, 3, 4, 5, 6, 7);
+}
+
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> column_values(const T *p, int stride, int lane) {
+    const T *at = p + (4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + (lane & 3) * 4;
+    return __builtin_shufflevector(column4(at), column4(at + 16 * stride), 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 template <>
 struct Operand<__bf16> {
     typedef b8 In;
     typedef Parts Made;
     typedef Parts3 Kept;
-    typedef __bf16 Stored;
-    static constexpr int kPlanes = 2;
-    static __device__ __forceinline__ In rows(const __bf16 *p) { return *reinterpret_cast<const b8 *>(p); }
-    static __device__ __forceinline__ In halves(const __bf16 *p, const __bf16 *q) {
-        return __builtin_shufflevector(*reinterpret_cast<const b4 *>(p), *reinterpret_cast<const b4 *>(q), 0, 1, 2, 3, 4, 5,
-                                       6, 7);
-    }
+    static __device__ __forceinline__ In rows(const __bf16 *p) { return row_values(p); }
     static __device__ __forceinline__ In columns(const __bf16 *p, int stride, int lane) {
-        const __bf16 *at = p + (8 * (lane >> 4) + ((lane & 15) >> 2)) * stride + (lane & 3) * 4;
-        return __builtin_shufflevector(column4(at), column4(at + 4 * stride), 0, 1, 2, 3, 4, 5, 6, 7);
+        return column_values(p, stride, lane);
     }
     static __device__ __forceinline__ float value(const In &a, int j) { return static_cast<float>(a[j]); }
+    static __device__ __forceinline__ In zero_at(In a, int j) {
+        a[j] = static_cast<__bf16>(0.0f);
+        return a;
+    }
     static __device__ __forceinline__ Made make(const float (&v)[8]) { return split(v); }
     static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return split3(v); }
-    static __device__ __forceinline__ Made stored(const __bf16 *p, int plane) {
-        return {*reinterpret_cast<const b8 *>(p), *reinterpret_cast<const b8 *>(p + plane)};
-    }
-    static __device__ __forceinline__ void store4(__bf16 *p, int plane, const float (&v)[4]) {
-        b4 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            hi[j] = static_cast<__bf16>(v[j]);
-            lo[j] = static_cast<__bf16>(v[j] - static_cast<float>(hi[j]));
-        }
-        *reinterpret_cast<b4 *>(p) = hi;
-        *reinterpret_cast<b4 *>(p + plane) = lo;
-    }
     static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) { return mfma(a, b, c); }
     static __device__ __forceinline__ f4 mul(const Made &a, const In &b, f4 c) { return mfma(a.hi, b, mfma(a.lo, b, c)); }
     static __device__ __forceinline__ f4 mul(const In &a, const Made &b, f4 c) { return mfma(a, b.hi, mfma(a, b.lo, c)); }
@@ -127,32 +130,25 @@ struct Operand<_Float16> {
     typedef Parts In;  // exact: 8 + 8 bits hold the 11 of an fp16
     typedef Parts Made;
     typedef Parts3 Kept;
-    typedef __bf16 Stored;
-    static constexpr int kPlanes = 2;
     static __device__ __forceinline__ In widen(const Vec<_Float16, 8> &h) {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(h[j]);
         return split(v);
     }
-    static __device__ __forceinline__ In rows(const _Float16 *p) { return widen(*reinterpret_cast<const Vec<_Float16, 8> *>(p)); }
-    static __device__ __forceinline__ In halves(const _Float16 *p, const _Float16 *q) {
-        return widen(__builtin_shufflevector(*reinterpret_cast<const Vec<_Float16, 4> *>(p),
-                                             *reinterpret_cast<const Vec<_Float16, 4> *>(q), 0, 1, 2, 3, 4, 5, 6, 7));
-    }
+    static __device__ __forceinline__ In rows(const _Float16 *p) { return widen(row_values(p)); }
     static __device__ __forceinline__ In columns(const _Float16 *p, int stride, int lane) {
-        const _Float16 *at = p + (8 * (lane >> 4) + ((lane & 15) >> 2)) * stride + (lane & 3) * 4;
-        return widen(__builtin_shufflevector(column4(at), column4(at + 4 * stride), 0, 1, 2, 3, 4, 5, 6, 7));
+        return widen(column_values(p, stride, lane));
     }
     static __device__ __forceinline__ float value(const In &a, int j) {
         return static_cast<float>(a.hi[j]) + static_cast<float>(a.lo[j]);
     }
+    static __device__ __forceinline__ In zero_at(In a, int j) {
+        a.hi[j] = a.lo[j] = static_cast<__bf16>(0.0f);
+        return a;
+    }
     static __device__ __forceinline__ Made make(const float (&v)[8]) { return split(v); }
     static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return split3(v); }
-    static __device__ __forceinline__ Made stored(const __bf16 *p, int plane) { return Operand<__bf16>::stored(p, plane); }
-    static __device__ __forceinline__ void store4(__bf16 *p, int plane, const float (&v)[4]) {
-        Operand<__bf16>::store4(p, plane, v);
-    }
     // products of parts that make at most 2^-24 of the whole are left out
     static __device__ __forceinline__ f4 mul(const In &a, const Kept &b, f4 c) {
         return mfma(a.hi, b.hi, mfma(a.hi, b.mid, mfma(a.lo, b.hi, mfma(a.lo, b.mid, mfma(a.hi, b.lo, c)))));
@@ -170,11 +166,9 @@ struct Operand<float> {
     };
     typedef In Made;
     typedef In Kept;
-    typedef float Stored;
-    static constexpr int kPlanes = 1;
-    static __device__ __forceinline__ In halves(const float *p, const float *q) {
+    static __device__ __forceinline__ In rows(const float *p) {
         In r;
-        const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(q);
+        const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(p + 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             r.v[j] = a[j];
@@ -182,15 +176,18 @@ struct Operand<float> {
         }
         return r;
     }
-    static __device__ __forceinline__ In rows(const float *p) { return halves(p, p + 4); }
     static __device__ __forceinline__ In columns(const float *p, int stride, int lane) {
         In r;
-        const float *at = p + 8 * (lane >> 4) * stride + (lane & 15);
+        const float *at = p + 4 * (lane >> 4) * stride + (lane & 15);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r.v[j] = at[j * stride];
+        for (int j = 0; j < 8; ++j) r.v[j] = at[((j >> 2) * 16 + (j & 3)) * stride];
         return r;
     }
     static __device__ __forceinline__ float value(const In &a, int j) { return a.v[j]; }
+    static __device__ __forceinline__ In zero_at(In a, int j) {
+        a.v[j] = 0.0f;
+        return a;
+    }
     static __device__ __forceinline__ Made make(const float (&v)[8]) {
         In r;
 #pragma unroll
@@ -198,8 +195,6 @@ struct Operand<float> {
         return r;
     }
     static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return make(v); }
-    static __device__ __forceinline__ Made stored(const float *p, int) { return rows(p); }
-    static __device__ __forceinline__ void store4(float *p, int, const float (&v)[4]) { store_floats<float, 4>(p, v); }
     static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
@@ -207,69 +202,106 @@ struct Operand<float> {
     }
 };
 
-// 16 bytes of a row; element by element where rows are not aligned to them.
-template <typename T>
-__device__ __forceinline__ uint4 load16(const T *p, bool wide) {
-    if (wide) return *reinterpret_cast<const uint4 *>(p);
-    Vec<T, 16 / sizeof(T)> v;
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) v[i] = p[i];
-    return __builtin_bit_cast(uint4, v);
-}
+// The rows of a chunk in memory: n rows from `base` on. WIDE: 16-byte aligned rows through a buffer
+// resource that ends with the last row, so that rows behind it read as zeros and are not written,
+// without a branch (the caller's stride keeps 64 rows below 2^31 bytes). Else element by element.
+template <typename T, bool WIDE>
+struct ChunkRows {
+    T *base;
+    size_t stride;
+    int n;
+    __amdgpu_buffer_rsrc_t rsrc;
 
-template <typename T>
-__device__ __forceinline__ void load4(const T *p, bool wide, float (&out)[4]) {
-    if (wide) {
-        load_floats<T, 4>(p, out);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = static_cast<float>(p[i]);
+    __device__ __forceinline__ ChunkRows(const T *rows, size_t row_stride, int count, int width)
+        : base(const_cast<T *>(rows)), stride(row_stride), n(count) {
+        if constexpr (WIDE) {
+            const unsigned bytes = static_cast<unsigned>(((count - 1) * row_stride + width) * sizeof(T));
+            rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, static_cast<int>(bytes), 0x00027000);
+        }
     }
-}
+    __device__ __forceinline__ int offset(int t, int v, bool live) const {
+        return live ? static_cast<int>((t * static_cast<unsigned>(stride) + v) * sizeof(T)) : 0x7FFFFFF0;
+    }
+    __device__ __forceinline__ u4 load16(int t, int v, bool live) const {
+        if constexpr (WIDE) {
+            return __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(t, v, live), 0, 0);
+        } else {
+            Vec<T, 16 / sizeof(T)> out = {};
+            if (live && t < n) {
+#pragma unroll
+                for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) out[i] = base[t * stride + v + i];
+            }
+            return __builtin_bit_cast(u4, out);
+        }
+    }
+    __device__ __forceinline__ Vec<T, 4> load4(int t, int v) const {
+        if constexpr (WIDE && sizeof(T) == 4) {
+            return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(t, v, true), 0, 0));
+        } else if constexpr (WIDE) {
+            return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_raw_buffer_load_b64(rsrc, offset(t, v, true), 0, 0));
+        } else {
+            Vec<T, 4> out = {};
+            if (t < n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[i] = base[t * stride + v + i];
+            }
+            return out;
+        }
+    }
+    __device__ __forceinline__ void store4(int t, int v, Vec<T, 4> value) const {
+        if constexpr (WIDE && sizeof(T) == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, value), rsrc, offset(t, v, true), 0, 0);
+        } else if constexpr (WIDE) {
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, value), rsrc, offset(t, v, true), 0, 0);
+        } else if (t < n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) base[t * stride + v + i] = value[i];
+        }
+    }
+};
+
+constexpr int kThreads = 256;
 
 // Rows of a chunk: 64, or 32 where the tiles of b and c would leave a CU one workgroup.
 template <typename T, int N>
-constexpr int chunk_rows() { return sizeof(T) == 4 || N > 128 ? 32 : 64; }
+constexpr int chunk_rows() { return 32; }
 
 // The parts of a split sequence: run r's own end state (from a zero start; run 0 of a sequence from
-// the sequence's own), [runs][heads][P][N] floats, then the log2 of its decay, [runs][heads].
+// the sequence's own), [runs][heads * width][N] floats, then the log2 of its decay, [runs][heads].
 // phase 0: a sequence's first run whole, and the end states of the others but the last;
 // phase 1: the other runs whole, from the states that phase 0 left.
-template <typename T, int P, int N>
-__global__ __launch_bounds__(4 * P, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int phase, bool wide) {
+template <typename T, int N, int CT, bool WIDE>
+__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int blocks, int phase) {
     using F = Operand<T>;
-    typedef typename F::Stored Stored;
-    constexpr int kWaves = P / 16;
-    constexpr int kThreads = 64 * kWaves;
+    using Rows = ChunkRows<T, WIDE>;
     constexpr int L = chunk_rows<T, N>();
-    constexpr int kBlocks = L / 16;           // row blocks
+    constexpr int kBlocks = L / 16;           // 16-row blocks
     constexpr int kSteps = L / 32;            // K steps over a chunk's rows
     constexpr int NP = N < 32 ? 32 : N;       // states, padded with zeros to a K step
-    constexpr int kTiles = NP / 16;
+    constexpr int kTiles = N / 16;
+    constexpr int kStates = NP / 32;          // K steps over the states
+    constexpr int kChannels = 64 * CT;        // of a workgroup
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
-    // rows padded by 16 bytes: 16 rows' 16-byte reads then cover all banks
-    constexpr int CS = NP + VE, XS = P + VE;
-    constexpr int MS = L + 16 / static_cast<int>(sizeof(Stored));
-    constexpr int kPlane = L * MS;
-    constexpr int NV = NP / VE, PV = P / VE;
+    // rows padded by 16 bytes, so that the same columns of 16 rows lie in different banks
+    constexpr int CS = NP + VE, XS = kChannels + VE;
+    constexpr int NV = NP / VE, XV = kChannels / VE;
     constexpr int kBcEach = (L * NV + kThreads - 1) / kThreads;
-    constexpr int kXEach = (L * PV + kThreads - 1) / kThreads;
+    constexpr int kXEach = L * XV / kThreads;
+    static_assert(L * XV % kThreads == 0, "x tile");
     __shared__ __attribute__((aligned(16))) T cs[L * CS];
     __shared__ __attribute__((aligned(16))) T bs[L * CS];
     __shared__ __attribute__((aligned(16))) T xs[L * XS];
-    __shared__ __attribute__((aligned(16))) Stored ms[F::kPlanes * kPlane];
-    // of the chunk at hand and the next: log2 of the decay since the chunk's start (two parts), the
-    // step, the decay itself, and the step times the decay to the chunk's end
-    __shared__ __attribute__((aligned(16))) float cum_hi[2][L], cum_lo[2][L], steps[2][L], since[2][L], to_end[2][L];
-    __shared__ float through[2];
+    // each wave's own: log2 of the decay since the chunk's start (two parts), the step, the decay
+    // itself, and the step times the decay to the chunk's end
+    __shared__ __attribute__((aligned(16))) float decay_tables[4][5][L];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = tid >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15;
     const int quad = lane >> 4;
-    const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.heads));
-    const int run = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.heads));
+    const int block = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
+    const int run = static_cast<int>(blockIdx.x / static_cast<unsigned>(blocks));
     const int j = sequence_of_run(a.seq, run, run_rows);
     const Span span = span_of(a.seq, j);
     const int first_run = run_base(a.seq, j, run_rows);
@@ -283,79 +315,108 @@ __global__ __launch_bounds__(4 * P, 2) void scan_chunk_kernel(ScanArgs a, int ru
     if (phase == 0 ? !first && last : first) return;
     const bool whole = phase == 1 || first;
 
-    const int g = h / (a.heads / a.groups);
+    // channels: of the group, of the workgroup in it, of the wave in the workgroup
+    const int group_channels = a.heads / a.groups * a.width;
+    const int per_group = blocks / a.groups;
+    const int g = block / per_group;
+    const int in_group = block % per_group * kChannels;
+    const int live_channels = group_channels - in_group < kChannels ? group_channels - in_group : kChannels;
+    const int wave_channel = wave * 16 * CT;
+    const bool active = wave_channel < live_channels;
+    const int channel0 = g * group_channels + in_group;
+    const int h = active ? (channel0 + wave_channel) / a.width : 0;
     const long long row0 = span.first + offset;
-    const int p_lane = 16 * wave + col;  // this lane's channel in the state
-    float *cache = a.state != nullptr ? a.state + ((static_cast<size_t>(place) * a.heads + h) * P + p_lane) * N : nullptr;
+    const size_t all_channels = static_cast<size_t>(a.heads) * a.width;
+    // this lane's first channel in the state; the next ct's is 16 on
+    const size_t state_channel = static_cast<size_t>(channel0) + wave_channel + col;
+    float *cache = a.state != nullptr ? a.state + (place * all_channels + state_channel) * N + 4 * quad : nullptr;
     float *parts = static_cast<float *>(a.scratch);
-    auto part = [&](int r) { return parts + ((static_cast<size_t>(r) * a.heads + h) * P + p_lane) * N; };
-    float *totals = parts + static_cast<size_t>(runs) * a.heads * P * N;
+    auto part = [&](int r) { return parts + (r * all_channels + state_channel) * N + 4 * quad; };
+    float *totals = parts + runs * all_channels * N;
 
-    f4 s[kTiles];
+    f4 s[CT][kTiles];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) s[i] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) s[ct][i] = f4{0.f, 0.f, 0.f, 0.f};
+    }
     auto load_state = [&](const float *from, float keep) {
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) s[i] = s[i] * keep + *reinterpret_cast<const f4 *>(from + 16 * i + 4 * quad);
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                s[ct][i] = s[ct][i] * keep + *reinterpret_cast<const f4 *>(from + 16 * ct * N + 16 * i);
+            }
+        }
     };
     auto store_state = [&](float *to) {
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) *reinterpret_cast<f4 *>(to + 16 * i + 4 * quad) = s[i];
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) *reinterpret_cast<f4 *>(to + 16 * ct * N + 16 * i) = s[ct][i];
+        }
     };
-    if (first) {
-        if (cache != nullptr && !starts_fresh(a.seq, j)) load_state(cache, 0.0f);
-    } else if (whole) {
-        for (int r = first_run; r < run; ++r) {
-            load_state(part(r), __builtin_amdgcn_exp2f(totals[static_cast<size_t>(r) * a.heads + h]));
+    if (active) {
+        if (first) {
+            if (cache != nullptr && !starts_fresh(a.seq, j)) load_state(cache, 0.0f);
+        } else if (whole) {
+            for (int r = first_run; r < run; ++r) {
+                load_state(part(r), __builtin_amdgcn_exp2f(totals[static_cast<size_t>(r) * a.heads + h]));
+            }
         }
     }
 
-    const T *xg = static_cast<const T *>(a.x) + row0 * a.x_stride + h * P;
+    const T *xg = static_cast<const T *>(a.x) + row0 * a.x_stride + channel0;
     const T *bg = static_cast<const T *>(a.b) + row0 * a.b_stride + g * N;
     const T *cg = static_cast<const T *>(a.c) + row0 * a.c_stride + g * N;
-    const T *zg = a.z != nullptr ? static_cast<const T *>(a.z) + row0 * a.z_stride + h * P : nullptr;
-    T *yg = static_cast<T *>(a.y) + row0 * a.y_stride + h * P;
+    const T *zg = a.z != nullptr ? static_cast<const T *>(a.z) + row0 * a.z_stride + channel0 : nullptr;
+    T *yg = static_cast<T *>(a.y) + row0 * a.y_stride + channel0;
     const int chunks = (rows + L - 1) / L;
 
     // a chunk's rows on their way through registers; rows behind the run's end are zeros
-    uint4 rc[kBcEach], rb[kBcEach], rx[kXEach];
+    u4 rc[kBcEach], rb[kBcEach], rx[kXEach];
     float dt_next = 0.0f;
     auto fetch = [&](int chunk) {
-        const int t0 = chunk * L, n = rows - t0 < L ? rows - t0 : L;
+        const size_t t0 = static_cast<size_t>(chunk) * L;
+        const int n = rows - chunk * L < L ? rows - chunk * L : L;
+        const Rows b_rows(bg + t0 * a.b_stride, a.b_stride, n, N), c_rows(cg + t0 * a.c_stride, a.c_stride, n, N);
+        const Rows x_rows(xg + t0 * a.x_stride, a.x_stride, n, live_channels);
 #pragma unroll
         for (int u = 0; u < kBcEach; ++u) {
             const int at = tid + u * kThreads, t = at / NV, v = at % NV * VE;
-            const bool live = t < n && v < N;  // at < L NV follows from t < n <= L
-            rb[u] = live ? load16(bg + static_cast<size_t>(t0 + t) * a.b_stride + v, wide) : uint4{0, 0, 0, 0};
-            if (whole) rc[u] = live ? load16(cg + static_cast<size_t>(t0 + t) * a.c_stride + v, wide) : uint4{0, 0, 0, 0};
+            const bool live = (NP == N || v < N) && (L * NV % kThreads == 0 || t < L);
+            rb[u] = b_rows.load16(t, v, live);
+            if (whole) rc[u] = c_rows.load16(t, v, live);
         }
 #pragma unroll
         for (int u = 0; u < kXEach; ++u) {
-            const int at = tid + u * kThreads, t = at / PV, v = at % PV * VE;
-            rx[u] = t < n ? load16(xg + static_cast<size_t>(t0 + t) * a.x_stride + v, wide) : uint4{0, 0, 0, 0};
+            const int at = tid + u * kThreads, t = at / XV, v = at % XV * VE;
+            rx[u] = x_rows.load16(t, v, v < live_channels);
         }
-        if (wave == 0 && lane < n) dt_next = load_dt<T>(a, row0 + t0 + lane, h);
+        if (active && lane < n) dt_next = load_dt<T>(a, row0 + t0 + lane, h);
     };
     auto stage = [&] {
 #pragma unroll
         for (int u = 0; u < kBcEach; ++u) {
             const int at = tid + u * kThreads, t = at / NV, v = at % NV * VE;
-            if (L * NV % kThreads != 0 && at >= L * NV) continue;
-            *reinterpret_cast<uint4 *>(bs + t * CS + v) = rb[u];
-            if (whole) *reinterpret_cast<uint4 *>(cs + t * CS + v) = rc[u];
+            if (L * NV % kThreads != 0 && t >= L) continue;
+            *reinterpret_cast<u4 *>(bs + t * CS + v) = rb[u];
+            if (whole) *reinterpret_cast<u4 *>(cs + t * CS + v) = rc[u];
         }
 #pragma unroll
         for (int u = 0; u < kXEach; ++u) {
-            const int at = tid + u * kThreads, t = at / PV, v = at % PV * VE;
-            if (L * PV % kThreads != 0 && at >= L * PV) continue;
-            *reinterpret_cast<uint4 *>(xs + t * XS + v) = rx[u];
+            const int at = tid + u * kThreads, t = at / XV, v = at % XV * VE;
+            *reinterpret_cast<u4 *>(xs + t * XS + v) = rx[u];
         }
     };
     const double exponent = static_cast<double>(a.a[h]) * 1.4426950408889634074;
     double run_total = 0.0;
-    // wave 0: steps and decays of the rows fetched last; a row behind the end has step 0 and decay 1
+    float keep = 0.0f;  // the decay over the chunk at hand
+    float(&cum_hi)[L] = decay_tables[wave][0], (&cum_lo)[L] = decay_tables[wave][1], (&steps)[L] = decay_tables[wave][2],
+    (&since)[L] = decay_tables[wave][3], (&to_end)[L] = decay_tables[wave][4];
+    // steps and decays of the rows fetched last; a row behind the end has step 0 and decay 1
     auto decays = [&](int chunk) {
-        const int buf = chunk & 1, n = rows - chunk * L;
+        const int n = rows - chunk * L;
         const float step = lane < n && lane < L ? step_from(a, dt_next, h) : 0.0f;
         double cum = static_cast<double>(step) * exponent;
 #pragma unroll
@@ -365,194 +426,235 @@ __global__ __launch_bounds__(4 * P, 2) void scan_chunk_kernel(ScanArgs a, int ru
         }
         const double total = __shfl(cum, L - 1);
         run_total += total;
+        keep = __builtin_amdgcn_exp2f(static_cast<float>(total));
         if (lane < L) {
             const float hi = static_cast<float>(cum);
-            cum_hi[buf][lane] = hi;
-            cum_lo[buf][lane] = static_cast<float>(cum - static_cast<double>(hi));
-            steps[buf][lane] = step;
-            since[buf][lane] = __builtin_amdgcn_exp2f(hi);
-            to_end[buf][lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
+            cum_hi[lane] = hi;
+            cum_lo[lane] = static_cast<float>(cum - static_cast<double>(hi));
+            steps[lane] = step;
+            since[lane] = __builtin_amdgcn_exp2f(hi);
+            to_end[lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
         }
-        if (lane == 0) through[buf] = __builtin_amdgcn_exp2f(static_cast<float>(total));
     };
 
-    // blocks of M above the diagonal that a K step of 32 rows still reads
-    for (int i = tid; i < F::kPlanes * kPlane; i += kThreads) ms[i] = static_cast<Stored>(0.0f);
     fetch(0);
-    if (wave == 0) decays(0);
+    if (active) decays(0);
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
-    const int p_quad = 16 * wave + 4 * quad;  // first of this lane's four channels in y
+    const int y_channel = wave_channel + 4 * quad;  // of this lane's four in y, for ct 0
 
     for (int chunk = 0; chunk < chunks; ++chunk) {
-        const int buf = chunk & 1;
         const int n = rows - chunk * L < L ? rows - chunk * L : L;
         __syncthreads();  // the chunk before has been read
         stage();
         __syncthreads();
         if (chunk + 1 < chunks) fetch(chunk + 1);
+        if (!active) continue;
+        const size_t t0 = static_cast<size_t>(chunk) * L;
+        Vec<T, 4> z[kBlocks][CT];
+        f4 y[kBlocks][CT];
         if (whole) {
-            float z[kBlocks][4];
             if (zg != nullptr) {
+                const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
 #pragma unroll
                 for (int tb = 0; tb < kBlocks; ++tb) {
-                    const int t = 16 * tb + col;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[tb][e] = 0.0f;
-                    if (t < n) load4(zg + static_cast<size_t>(chunk * L + t) * a.z_stride + p_quad, wide, z[tb]);
+                    for (int ct = 0; ct < CT; ++ct) z[tb][ct] = z_rows.load4(16 * tb + col, y_channel + 16 * ct);
                 }
             }
-            // 1. M
-            for (int block = wave; block < kBlocks * (kBlocks + 1) / 2; block += kWaves) {
-                const int tb = block < 1 ? 0 : (block < 3 ? 1 : (block < 6 ? 2 : 3));
-                const int sb = block - tb * (tb + 1) / 2;
-                f4 acc = {0.f, 0.f, 0.f, 0.f};
+            // 1. from the state
 #pragma unroll
-                for (int i = 0; i < NP / 32; ++i) {
-                    acc = F::mul(F::rows(bs + (16 * sb + col) * CS + 32 * i + 8 * quad),
-                                 F::rows(cs + (16 * tb + col) * CS + 32 * i + 8 * quad), acc);
-                }
-                const int t = 16 * tb + col;
-                const float hi = cum_hi[buf][t], lo = cum_lo[buf][t];
-                float m[4];
+            for (int tb = 0; tb < kBlocks; ++tb) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int sr = 16 * sb + 4 * quad + r;
-                    const float d = (hi - cum_hi[buf][sr]) + (lo - cum_lo[buf][sr]);
-                    m[r] = sr <= t ? acc[r] * (__builtin_amdgcn_exp2f(d) * steps[buf][sr]) : 0.0f;
-                }
-                F::store4(ms + t * MS + 16 * sb + 4 * quad, kPlane, m);
+                for (int ct = 0; ct < CT; ++ct) y[tb][ct] = f4{0.f, 0.f, 0.f, 0.f};
             }
-            // 2. from the state
-            f4 y[kBlocks];
-            auto from_state = [&] {
 #pragma unroll
-                for (int tb = 0; tb < kBlocks; ++tb) y[tb] = f4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < kStates; ++i) {
+                typename F::In right[kBlocks];
 #pragma unroll
-                for (int i = 0; i < NP / 32; ++i) {
-                    const float v[8] = {s[2 * i][0], s[2 * i][1], s[2 * i][2], s[2 * i][3],
-                                        s[2 * i + 1][0], s[2 * i + 1][1], s[2 * i + 1][2], s[2 * i + 1][3]};
+                for (int tb = 0; tb < kBlocks; ++tb) right[tb] = F::rows(cs + (16 * tb + col) * CS + 32 * i + 4 * quad);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
                     const typename F::Made left = F::make(v);
 #pragma unroll
-                    for (int tb = 0; tb < kBlocks; ++tb) {
-                        const T *at = cs + (16 * tb + col) * CS + 32 * i + 4 * quad;
-                        y[tb] = F::mul(left, F::halves(at, at + 16), y[tb]);
-                    }
-                }
-#pragma unroll
-                for (int tb = 0; tb < kBlocks; ++tb) y[tb] *= since[buf][16 * tb + col];
-            };
-            from_state();
-            __syncthreads();  // M is whole
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const typename F::In left = F::columns(xs + 32 * k * XS + 16 * wave, XS, lane);
-#pragma unroll
-                for (int tb = 2 * k; tb < kBlocks; ++tb) {
-                    y[tb] = F::mul(left, F::stored(ms + (16 * tb + col) * MS + 32 * k + 8 * quad, kPlane), y[tb]);
-                }
-            }
-            float check = 0.0f;
-#pragma unroll
-            for (int tb = 0; tb < kBlocks; ++tb) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) check = fmaf(y[tb][r], 0.0f, check);
-            }
-            if (__any(check != 0.0f)) {
-                from_state();
-#pragma unroll
-                for (int tb = 0; tb < kBlocks; ++tb) {
-                    const int t = 16 * tb + col;
-                    for (int sr = 0; sr <= t; ++sr) {
-                        float m = static_cast<float>(ms[t * MS + sr]);
-                        if constexpr (F::kPlanes == 2) m += static_cast<float>(ms[kPlane + t * MS + sr]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) y[tb][r] = fmaf(m, static_cast<float>(xs[sr * XS + p_quad + r]), y[tb][r]);
-                    }
+                    for (int tb = 0; tb < kBlocks; ++tb) y[tb][ct] = F::mul(left, right[tb], y[tb][ct]);
                 }
             }
 #pragma unroll
             for (int tb = 0; tb < kBlocks; ++tb) {
-                const int t = 16 * tb + col;
-                float x[4], out[4];
-                load_floats<T, 4>(xs + t * XS + p_quad, x);
+                const float decay = since[16 * tb + col];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    out[r] = a.d != nullptr ? fmaf(skip, x[r], y[tb][r]) : y[tb][r];
-                    if (zg != nullptr) out[r] *= silu<T>(z[tb][r]);
-                }
-                if (t < n) {
-                    T *to = yg + static_cast<size_t>(chunk * L + t) * a.y_stride + p_quad;
-                    if (wide) {
-                        store_floats<T, 4>(to, out);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) to[r] = static_cast<T>(out[r]);
-                    }
-                }
+                for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
             }
         }
-        // 3. the state behind the chunk
-        const float keep = through[buf];
+        typename F::In x[CT][kSteps];
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) s[i] *= keep;
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) x[ct][k] = F::columns(xs + 32 * k * XS + wave_channel + 16 * ct, XS, lane);
+        }
+        // 2. the state behind the chunk
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) s[ct][i] *= keep;
+        }
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            const typename F::In x = F::columns(xs + 32 * k * XS + 16 * wave, XS, lane);
-            float w[8];
+            typename F::Kept right[CT];
+            float weight[8];
+            load_floats<float, 4>(to_end + 32 * k + 4 * quad, reinterpret_cast<float(&)[4]>(weight[0]));
+            load_floats<float, 4>(to_end + 32 * k + 16 + 4 * quad, reinterpret_cast<float(&)[4]>(weight[4]));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = F::value(x, e) * to_end[buf][32 * k + 8 * quad + e];
-            const typename F::Kept right = F::keep(w);
+            for (int ct = 0; ct < CT; ++ct) {
+                float w[8];
 #pragma unroll
-            for (int i = 0; i < N / 16; ++i) s[i] = F::mul(F::columns(bs + 32 * k * CS + 16 * i, CS, lane), right, s[i]);
+                for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct][k], e) * weight[e];
+                right[ct] = F::keep(w);
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const typename F::In left = F::columns(bs + 32 * k * CS + 16 * i, CS, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i]);
+            }
         }
-        if (wave == 0 && chunk + 1 < chunks) decays(chunk + 1);
+        // 3. from the chunk's own rows
+        if (whole) {
+            const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+#pragma unroll
+            for (int tb = 0; tb < kBlocks; ++tb) {
+                typename F::In c[kStates];
+#pragma unroll
+                for (int i = 0; i < kStates; ++i) c[i] = F::rows(cs + (16 * tb + col) * CS + 32 * i + 4 * quad);
+                const int t = 16 * tb + col;
+                const float hi = cum_hi[t], lo = cum_lo[t];
+                typename F::Made m[kSteps];
+#pragma unroll
+                for (int k = 0; k <= tb / 2; ++k) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int sb = 2 * k + e;
+                        if (sb > tb) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[4 * e + r] = 0.0f;
+                            continue;
+                        }
+                        f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < kStates; ++i) {
+                            acc = F::mul(F::rows(bs + (16 * sb + col) * CS + 32 * i + 4 * quad), c[i], acc);
+                        }
+                        float s_hi[4], s_lo[4], s_step[4];
+                        load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi);
+                        load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo);
+                        load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float d = (hi - s_hi[r]) + (lo - s_lo[r]);
+                            const float full = acc[r] * (__builtin_amdgcn_exp2f(d) * s_step[r]);
+                            v[4 * e + r] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
+                        }
+                    }
+                    m[k] = F::make(v);
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    f4 inside = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k <= tb / 2; ++k) inside = F::mul(x[ct][k], m[k], inside);
+                    const float check = inside[0] * 0.0f + inside[1] * 0.0f + inside[2] * 0.0f + inside[3] * 0.0f;
+                    if (__any(check != 0.0f)) {
+                        // the first row of this lane's channel (16 ct + col) whose x is not finite
+                        int bad = L;
+                        inside = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k <= tb / 2; ++k) {
+                            typename F::In sound = x[ct][k];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (F::value(sound, e) * 0.0f == 0.0f) continue;
+                                const int row = 32 * k + 16 * (e >> 2) + 4 * quad + (e & 3);
+                                bad = row < bad ? row : bad;
+                                sound = F::zero_at(sound, e);
+                            }
+                            inside = F::mul(sound, m[k], inside);
+                        }
+                        bad = min(bad, __shfl_xor(bad, 16));
+                        bad = min(bad, __shfl_xor(bad, 32));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (t >= __shfl(bad, 4 * quad + r)) inside[r] = __builtin_nanf("");
+                        }
+                    }
+                    const Vec<T, 4> xv = *reinterpret_cast<const Vec<T, 4> *>(xs + t * XS + y_channel + 16 * ct);
+                    Vec<T, 4> out;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v = y[tb][ct][r] + inside[r];
+                        if (a.d != nullptr) v = fmaf(skip, static_cast<float>(xv[r]), v);
+                        if (zg != nullptr) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
+                        out[r] = static_cast<T>(v);
+                    }
+                    y_rows.store4(t, y_channel + 16 * ct, out);
+                }
+            }
+        }
+        if (chunk + 1 < chunks) decays(chunk + 1);
     }
+    if (!active) return;
     if (last) {
         if (cache != nullptr) store_state(cache);
     } else if (phase == 0) {
         store_state(part(run));
-        if (tid == 0) totals[static_cast<size_t>(run) * a.heads + h] = static_cast<float>(run_total);
+        if (lane == 0 && (channel0 + wave_channel) % a.width == 0) {
+            totals[static_cast<size_t>(run) * a.heads + h] = static_cast<float>(run_total);
+        }
     }
 }
 
-template <typename T, int P, int N>
+template <typename T, int N, int CT, bool WIDE>
 hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
+    const int group_channels = a.heads / a.groups * a.width;
+    const int blocks = a.groups * ((group_channels + 64 * CT - 1) / (64 * CT));
     const long long runs = static_cast<long long>(a.seq.rows / run_rows) + a.seq.sequences;
-    const long long blocks = runs * a.heads;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.b) |
-                           reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.y);
-    const size_t strides = a.x_stride | a.b_stride | a.c_stride | a.z_stride | a.y_stride;
-    const bool wide = bits % 16 == 0 && strides % (16 / sizeof(T)) == 0;
+    if (runs * blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
     for (int phase = 0; phase < (run_rows <= a.seq.rows ? 2 : 1); ++phase) {
-        hipLaunchKernelGGL((scan_chunk_kernel<T, P, N>), dim3(static_cast<unsigned>(blocks)), dim3(4 * P), 0, stream, a,
-                           run_rows, static_cast<int>(runs), phase, wide);
+        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), dim3(static_cast<unsigned>(runs * blocks)), dim3(kThreads), 0,
+                           stream, a, run_rows, static_cast<int>(runs), blocks, phase);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-template <typename T, int P>
-hipError_t by_states(const ScanArgs &a, int run_rows, hipStream_t stream) {
-    switch (a.states) {
-        case 16: return run_chunks<T, P, 16>(a, run_rows, stream);
-        case 32: return run_chunks<T, P, 32>(a, run_rows, stream);
-        case 64: return run_chunks<T, P, 64>(a, run_rows, stream);
-        case 128: return run_chunks<T, P, 128>(a, run_rows, stream);
-        case 256: return run_chunks<T, P, 256>(a, run_rows, stream);
-        default: return hipErrorInvalidValue;
+template <typename T, int N>
+hipError_t by_alignment(ScanArgs a, int run_rows, hipStream_t stream) {
+    constexpr int CT = N > 128 ? 1 : 2;
+    if (a.seq.rows == 1) {  // a single row's strides say nothing
+        a.x_stride = a.y_stride = a.z_stride = static_cast<size_t>(a.heads) * a.width;
+        a.b_stride = a.c_stride = static_cast<size_t>(a.groups) * a.states;
     }
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.b) |
+                           reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.y);
+    const size_t strides = a.x_stride | a.b_stride | a.c_stride | a.z_stride | a.y_stride;
+    const bool wide = bits % 16 == 0 && strides % (16 / sizeof(T)) == 0 && strides < (1u << 22);
+    return wide ? run_chunks<T, N, CT, true>(a, run_rows, stream) : run_chunks<T, N, CT, false>(a, run_rows, stream);
 }
 
 }  // namespace scan_chunks
 
 template <typename T>
 hipError_t launch_scan_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
-    switch (a.width) {
-        case 32: return scan_chunks::by_states<T, 32>(a, run_rows, stream);
-        case 64: return scan_chunks::by_states<T, 64>(a, run_rows, stream);
-        case 128: return scan_chunks::by_states<T, 128>(a, run_rows, stream);
+    switch (a.states) {
+        case 16: return scan_chunks::by_alignment<T, 16>(a, run_rows, stream);
+        case 32: return scan_chunks::by_alignment<T, 32>(a, run_rows, stream);
+        case 64: return scan_chunks::by_alignment<T, 64>(a, run_rows, stream);
+        case 128: return scan_chunks::by_alignment<T, 128>(a, run_rows, stream);
+        case 256: return scan_chunks::by_alignment<T, 256>(a, run_rows, stream);
         default: return hipErrorInvalidValue;
     }
 }
