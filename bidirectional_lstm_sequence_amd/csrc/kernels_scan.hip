@@ -127,17 +127,27 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
     }
 }
 
-// Rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences.
+// Rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences. The lengths
+// of the sequences are on the device, so the rule goes by their sum and number.
+//  * Row by row up to kShort rows a sequence on average.
+//  * Splitting costs the end states of most runs (the products with x and b a second time) and two
+//    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
+//    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
+//    sequence of 4096 rows 117, 112, 106, 135 and 142 us in runs of 128, 192, 256, 384 and 512 rows,
+//    495 us whole; 24 unequal ones of 16384 rows together 343, 326, 323 and 370 us in runs of 256, 384,
+//    512 and 1024, 487 us whole. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589 rows:
+//    69, 80, 87 and 101 us in runs of 96, 128, 256 and 512, 94 us whole.
+//  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {
-    constexpr long long kShort = 8;      // rows a sequence, on average
-    constexpr long long kWhole = 512;    // workgroups that fill the chip without splitting
-    constexpr long long kSplit = 768;
+    constexpr long long kShort = 8, kPlaces = 512, kLeast = 96, kMost = 512;
+    constexpr int kChannels = 128;  // of a workgroup
     const long long rows = a.seq.rows, sequences = a.seq.sequences;
     if (rows <= kShort * sequences) return 0;
-    if (sequences * a.heads >= kWhole) return 0x7FFFFFFF;
-    long long run = (rows * a.heads + kSplit - 1) / kSplit;
-    run = (run + 63) / 64 * 64;
-    if (run < 256) run = 256;
+    const long long blocks = a.groups * ((a.heads / a.groups * static_cast<long long>(a.width) + kChannels - 1) / kChannels);
+    long long run = rows * blocks / kPlaces;
+    run = run < kLeast ? kLeast : (run > kMost ? kMost : run);
+    if (sequences * blocks >= 4 * kPlaces && run < 2 * rows / sequences) run = 2 * rows / sequences;
+    run = (run + 31) / 32 * 32;
     return run >= rows ? 0x7FFFFFFF : static_cast<int>(run);
 }
 

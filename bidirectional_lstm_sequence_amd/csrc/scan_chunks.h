@@ -9,10 +9,10 @@
 // sequence, or a part of it where there are few) and walks over its chunks with the state in
 // registers, so x and z are read once and y is written once. Per chunk the rows of b, c and x go
 // through registers, a chunk ahead, into LDS; from there each wave works alone on its 16 CT channels:
-//   1. y = (S C^T) exp(cum), channels by rows.
+//   1. y = (S C^T) exp(cum), channels by rows, and G = B C^T for the three 16 x 16 blocks s <= t, from
+//      the same fragments of c; M = G exp(cum_t - cum_s) D_s for s <= t.
 //   2. S' = exp(cum_L) S + B^T (w X) with w_s = exp(cum_L - cum_s) D_s.
-//   3. per 16 rows t: G = B C^T for the 16-row blocks s up to t's, M = G exp(cum_t - cum_s) D_s for
-//      s <= t, y += X^T M, then the skip, the gate and the store.
+//   3. y += X^T M, then the skip, the gate and the store.
 // Every product reads its operands in the layout that another one's result has: an accumulator
 // holds rows 4 q + r of column lane % 16 (q = lane / 16), and a K step of 32 takes within lane group q
 // the K values {16 e + 4 q + r, e < 2, r < 4}, on both sides. So S is the left operand of 1 as 2 leaves
@@ -28,6 +28,8 @@
 // A non-finite x must not reach the rows before it through a zero of M: where a wave's outputs hold
 // one, it takes step 3 again without such x and sets what follows them in their channel to NaN.
 #pragma once
+
+#include <type_traits>
 
 #include "scan_device.h"
 
@@ -262,28 +264,42 @@ struct ChunkRows {
 
 constexpr int kThreads = 256;
 
-// Rows of a chunk: 64, or 32 where the tiles of b and c would leave a CU one workgroup.
-template <typename T, int N>
-constexpr int chunk_rows() { return 32; }
+constexpr int L = 32;  // rows of a chunk: one K step of the products over rows
 
-// The parts of a split sequence: run r's own end state (from a zero start; run 0 of a sequence from
-// the sequence's own), [runs][heads * width][N] floats, then the log2 of its decay, [runs][heads].
-// phase 0: a sequence's first run whole, and the end states of the others but the last;
-// phase 1: the other runs whole, from the states that phase 0 left.
+// Sums over each half wave of 32 lanes, up to and with each lane.
+__device__ __forceinline__ double running_sum(double v) {
+    auto from = [](double u, auto control) {
+        const int2 w = __builtin_bit_cast(int2, u);
+        return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, w.x, decltype(control)::value, 0xF, 0xF, true),
+                                                    __builtin_amdgcn_update_dpp(0, w.y, decltype(control)::value, 0xF, 0xF, true)));
+    };
+    v += from(v, std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8: zero from outside the 16 lanes
+    v += from(v, std::integral_constant<int, 0x112>{});
+    v += from(v, std::integral_constant<int, 0x114>{});
+    v += from(v, std::integral_constant<int, 0x118>{});
+    const double other = __shfl(v, (threadIdx.x & 32) + 15);
+    return (threadIdx.x & 16) != 0 ? v + other : v;
+}
+
+// A split sequence takes three launches. Scratch holds run r's end state, [runs][heads * width][N]
+// floats, then the log2 of its decay, [runs][heads].
+// phase 0: a sequence's first run whole, and the end states of the others but the last from a zero start;
+// scan_join_kernel: end states from the sequence's start;
+// phase 1: the other runs whole, each from the end state of the run before it.
 template <typename T, int N, int CT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int blocks, int phase) {
     using F = Operand<T>;
     using Rows = ChunkRows<T, WIDE>;
-    constexpr int L = chunk_rows<T, N>();
-    constexpr int kBlocks = L / 16;           // 16-row blocks
-    constexpr int kSteps = L / 32;            // K steps over a chunk's rows
     constexpr int NP = N < 32 ? 32 : N;       // states, padded with zeros to a K step
     constexpr int kTiles = N / 16;
     constexpr int kStates = NP / 32;          // K steps over the states
     constexpr int kChannels = 64 * CT;        // of a workgroup
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
-    // rows padded by 16 bytes, so that the same columns of 16 rows lie in different banks
-    constexpr int CS = NP + VE, XS = kChannels + VE;
+    // Rows are padded, by 32 bytes for 16-bit types: reads of four values from 16 rows and reads by
+    // columns then meet every bank equally often; by 16 bytes for float32, whose columns are read value
+    // by value.
+    constexpr int kPad = sizeof(T) == 4 ? VE : 2 * VE;
+    constexpr int CS = NP + kPad, XS = kChannels + kPad;
     constexpr int NV = NP / VE, XV = kChannels / VE;
     constexpr int kBcEach = (L * NV + kThreads - 1) / kThreads;
     constexpr int kXEach = L * XV / kThreads;
@@ -291,9 +307,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     __shared__ __attribute__((aligned(16))) T cs[L * CS];
     __shared__ __attribute__((aligned(16))) T bs[L * CS];
     __shared__ __attribute__((aligned(16))) T xs[L * XS];
-    // each wave's own: log2 of the decay since the chunk's start (two parts), the step, the decay
-    // itself, and the step times the decay to the chunk's end
-    __shared__ __attribute__((aligned(16))) float decay_tables[4][5][L];
+    // each wave's own, of two chunks at hand and the next two: log2 of the decay since the chunk's start
+    // (two parts), the step, the decay itself, and the step times the decay to the chunk's end
+    __shared__ __attribute__((aligned(16))) float decay_tables[4][2][5][2 * L];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -340,12 +356,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) s[ct][i] = f4{0.f, 0.f, 0.f, 0.f};
     }
-    auto load_state = [&](const float *from, float keep) {
+    auto load_state = [&](const float *from) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
-                s[ct][i] = s[ct][i] * keep + *reinterpret_cast<const f4 *>(from + 16 * ct * N + 16 * i);
+                s[ct][i] = *reinterpret_cast<const f4 *>(from + 16 * ct * N + 16 * i);
             }
         }
     };
@@ -358,11 +374,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     };
     if (active) {
         if (first) {
-            if (cache != nullptr && !starts_fresh(a.seq, j)) load_state(cache, 0.0f);
+            if (cache != nullptr && !starts_fresh(a.seq, j)) load_state(cache);
         } else if (whole) {
-            for (int r = first_run; r < run; ++r) {
-                load_state(part(r), __builtin_amdgcn_exp2f(totals[static_cast<size_t>(r) * a.heads + h]));
-            }
+            load_state(part(run - 1));
         }
     }
 
@@ -393,7 +407,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             const int at = tid + u * kThreads, t = at / XV, v = at % XV * VE;
             rx[u] = x_rows.load16(t, v, v < live_channels);
         }
-        if (active && lane < n) dt_next = load_dt<T>(a, row0 + t0 + lane, h);
+    };
+    // one element of dt a lane, for two chunks
+    auto fetch_dt = [&](int chunk) {
+        const unsigned t = static_cast<unsigned>(chunk) * L + lane;
+        if (t < static_cast<unsigned>(rows)) dt_next = load_dt<T>(a, row0 + t, h);
     };
     auto stage = [&] {
 #pragma unroll
@@ -411,34 +429,30 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     };
     const double exponent = static_cast<double>(a.a[h]) * 1.4426950408889634074;
     double run_total = 0.0;
-    float keep = 0.0f;  // the decay over the chunk at hand
-    float(&cum_hi)[L] = decay_tables[wave][0], (&cum_lo)[L] = decay_tables[wave][1], (&steps)[L] = decay_tables[wave][2],
-    (&since)[L] = decay_tables[wave][3], (&to_end)[L] = decay_tables[wave][4];
-    // steps and decays of the rows fetched last; a row behind the end has step 0 and decay 1
+    float keeps = 0.0f, next_keep = 0.0f;  // the decay over a chunk: lanes 0..31 of the even one, then of the odd one
+    // steps and decays of the two chunks whose dt came last; a row behind the end has step 0 and decay 1
     auto decays = [&](int chunk) {
-        const int n = rows - chunk * L;
-        const float step = lane < n && lane < L ? step_from(a, dt_next, h) : 0.0f;
-        double cum = static_cast<double>(step) * exponent;
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) {
-            const double before = __shfl_up(cum, o);
-            if (lane >= o) cum += before;
-        }
-        const double total = __shfl(cum, L - 1);
-        run_total += total;
-        keep = __builtin_amdgcn_exp2f(static_cast<float>(total));
-        if (lane < L) {
-            const float hi = static_cast<float>(cum);
-            cum_hi[lane] = hi;
-            cum_lo[lane] = static_cast<float>(cum - static_cast<double>(hi));
-            steps[lane] = step;
-            since[lane] = __builtin_amdgcn_exp2f(hi);
-            to_end[lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
-        }
+        float *table = &decay_tables[wave][chunk >> 1 & 1][0][0];
+        const float step = static_cast<unsigned>(chunk) * L + lane < static_cast<unsigned>(rows) ? step_from(a, dt_next, h) : 0.0f;
+        const double cum = running_sum(static_cast<double>(step) * exponent);
+        const double total = __shfl(cum, lane | 31);
+        const float over = static_cast<float>(total);
+        const float hi = static_cast<float>(cum);
+        table[lane] = hi;
+        table[2 * L + lane] = static_cast<float>(cum - static_cast<double>(hi));
+        table[4 * L + lane] = step;
+        table[6 * L + lane] = __builtin_amdgcn_exp2f(hi);
+        table[8 * L + lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
+        run_total += total;  // lane 0: of even chunks, lane 32: of odd ones
+        return __builtin_amdgcn_exp2f(over);
     };
 
     fetch(0);
-    if (active) decays(0);
+    if (active) {
+        fetch_dt(0);
+        next_keep = decays(0);
+        fetch_dt(2);
+    }
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
     const int y_channel = wave_channel + 4 * quad;  // of this lane's four in y, for ct 0
 
@@ -447,154 +461,151 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         __syncthreads();  // the chunk before has been read
         stage();
         __syncthreads();
+        if (active && (chunk & 1) == 0) {
+            // before the next rows are asked for: dt came before the rows just staged, and a wait for it
+            // must not become one for them
+            keeps = next_keep;
+            next_keep = decays(chunk + 2);
+            fetch_dt(chunk + 4);
+        }
         if (chunk + 1 < chunks) fetch(chunk + 1);
         if (!active) continue;
+        const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
+                    *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
+        const float keep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(keeps), (chunk & 1) * 32));
         const size_t t0 = static_cast<size_t>(chunk) * L;
-        Vec<T, 4> z[kBlocks][CT];
-        f4 y[kBlocks][CT];
+        Vec<T, 4> z[2][CT];
+        f4 y[2][CT];
+        typename F::Made m[2];
         if (whole) {
             if (zg != nullptr) {
                 const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
 #pragma unroll
-                for (int tb = 0; tb < kBlocks; ++tb) {
+                for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) z[tb][ct] = z_rows.load4(16 * tb + col, y_channel + 16 * ct);
                 }
             }
-            // 1. from the state
+            // 1. from the state, and M
+            f4 gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
 #pragma unroll
-            for (int tb = 0; tb < kBlocks; ++tb) {
+            for (int k = 0; k < 3; ++k) gram[k] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[tb][ct] = f4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
-                typename F::In right[kBlocks];
-#pragma unroll
-                for (int tb = 0; tb < kBlocks; ++tb) right[tb] = F::rows(cs + (16 * tb + col) * CS + 32 * i + 4 * quad);
+                const int at = col * CS + 32 * i + 4 * quad;
+                const typename F::In c0 = F::rows(cs + at), c1 = F::rows(cs + 16 * CS + at);
+                const typename F::In b0 = F::rows(bs + at), b1 = F::rows(bs + 16 * CS + at);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
                     const typename F::Made left = F::make(v);
-#pragma unroll
-                    for (int tb = 0; tb < kBlocks; ++tb) y[tb][ct] = F::mul(left, right[tb], y[tb][ct]);
+                    y[0][ct] = F::mul(left, c0, y[0][ct]);
+                    y[1][ct] = F::mul(left, c1, y[1][ct]);
                 }
+                gram[0] = F::mul(b0, c0, gram[0]);
+                gram[1] = F::mul(b0, c1, gram[1]);
+                gram[2] = F::mul(b1, c1, gram[2]);
+            }
+            float s_hi[2][4], s_lo[2][4], s_step[2][4];
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+                load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi[sb]);
+                load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo[sb]);
+                load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step[sb]);
             }
 #pragma unroll
-            for (int tb = 0; tb < kBlocks; ++tb) {
-                const float decay = since[16 * tb + col];
+            for (int tb = 0; tb < 2; ++tb) {
+                const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col];
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int sb = e >> 2, r = e & 3;
+                    v[e] = 0.0f;
+                    if (sb > tb) continue;
+                    const float d = (hi - s_hi[sb][r]) + (lo - s_lo[sb][r]);
+                    const float full = gram[sb + tb][r] * (__builtin_amdgcn_exp2f(d) * s_step[sb][r]);
+                    v[e] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
+                }
+                m[tb] = F::make(v);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
             }
         }
-        typename F::In x[CT][kSteps];
+        typename F::In x[CT];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) x[ct][k] = F::columns(xs + 32 * k * XS + wave_channel + 16 * ct, XS, lane);
-        }
+        for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
         // 2. the state behind the chunk
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) s[ct][i] *= keep;
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        {
             typename F::Kept right[CT];
-            float weight[8];
-            load_floats<float, 4>(to_end + 32 * k + 4 * quad, reinterpret_cast<float(&)[4]>(weight[0]));
-            load_floats<float, 4>(to_end + 32 * k + 16 + 4 * quad, reinterpret_cast<float(&)[4]>(weight[4]));
+            float weight[2][4];
+            load_floats<float, 4>(to_end + 4 * quad, weight[0]);
+            load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct][k], e) * weight[e];
+                for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
                 right[ct] = F::keep(w);
             }
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
-                const typename F::In left = F::columns(bs + 32 * k * CS + 16 * i, CS, lane);
+                const typename F::In left = F::columns(bs + 16 * i, CS, lane);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i]);
+                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i] * keep);
             }
         }
         // 3. from the chunk's own rows
         if (whole) {
-            const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+            f4 sums[2][CT];
+            float check = 0.0f;
 #pragma unroll
-            for (int tb = 0; tb < kBlocks; ++tb) {
-                typename F::In c[kStates];
-#pragma unroll
-                for (int i = 0; i < kStates; ++i) c[i] = F::rows(cs + (16 * tb + col) * CS + 32 * i + 4 * quad);
-                const int t = 16 * tb + col;
-                const float hi = cum_hi[t], lo = cum_lo[t];
-                typename F::Made m[kSteps];
-#pragma unroll
-                for (int k = 0; k <= tb / 2; ++k) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int sb = 2 * k + e;
-                        if (sb > tb) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) v[4 * e + r] = 0.0f;
-                            continue;
-                        }
-                        f4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < kStates; ++i) {
-                            acc = F::mul(F::rows(bs + (16 * sb + col) * CS + 32 * i + 4 * quad), c[i], acc);
-                        }
-                        float s_hi[4], s_lo[4], s_step[4];
-                        load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi);
-                        load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo);
-                        load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float d = (hi - s_hi[r]) + (lo - s_lo[r]);
-                            const float full = acc[r] * (__builtin_amdgcn_exp2f(d) * s_step[r]);
-                            v[4 * e + r] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
-                        }
-                    }
-                    m[k] = F::make(v);
-                }
+            for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    f4 inside = {0.f, 0.f, 0.f, 0.f};
+                    const f4 &v = sums[tb][ct] = F::mul(x[ct], m[tb], y[tb][ct]);
+                    check += (v[0] + v[1]) + (v[2] + v[3]);
+                }
+            }
+            if (__any(check * 0.0f != 0.0f)) {
 #pragma unroll
-                    for (int k = 0; k <= tb / 2; ++k) inside = F::mul(x[ct][k], m[k], inside);
-                    const float check = inside[0] * 0.0f + inside[1] * 0.0f + inside[2] * 0.0f + inside[3] * 0.0f;
-                    if (__any(check != 0.0f)) {
-                        // the first row of this lane's channel (16 ct + col) whose x is not finite
-                        int bad = L;
-                        inside = f4{0.f, 0.f, 0.f, 0.f};
+                for (int ct = 0; ct < CT; ++ct) {
+                    // the first row of this lane's channel (16 ct + col) whose x is not finite
+                    int bad = L;
+                    typename F::In sound = x[ct];
 #pragma unroll
-                        for (int k = 0; k <= tb / 2; ++k) {
-                            typename F::In sound = x[ct][k];
+                    for (int e = 0; e < 8; ++e) {
+                        if (F::value(x[ct], e) * 0.0f == 0.0f) continue;
+                        const int row = 16 * (e >> 2) + 4 * quad + (e & 3);
+                        bad = row < bad ? row : bad;
+                        sound = F::zero_at(sound, e);
+                    }
+                    bad = min(bad, __shfl_xor(bad, 16));
+                    bad = min(bad, __shfl_xor(bad, 32));
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (F::value(sound, e) * 0.0f == 0.0f) continue;
-                                const int row = 32 * k + 16 * (e >> 2) + 4 * quad + (e & 3);
-                                bad = row < bad ? row : bad;
-                                sound = F::zero_at(sound, e);
-                            }
-                            inside = F::mul(sound, m[k], inside);
-                        }
-                        bad = min(bad, __shfl_xor(bad, 16));
-                        bad = min(bad, __shfl_xor(bad, 32));
+                    for (int tb = 0; tb < 2; ++tb) {
+                        sums[tb][ct] = F::mul(sound, m[tb], y[tb][ct]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            if (t >= __shfl(bad, 4 * quad + r)) inside[r] = __builtin_nanf("");
+                            if (16 * tb + col >= __shfl(bad, 4 * quad + r)) sums[tb][ct][r] = __builtin_nanf("");
                         }
                     }
+                }
+            }
+            const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                const int t = 16 * tb + col;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
                     const Vec<T, 4> xv = *reinterpret_cast<const Vec<T, 4> *>(xs + t * XS + y_channel + 16 * ct);
                     Vec<T, 4> out;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float v = y[tb][ct][r] + inside[r];
+                        float v = sums[tb][ct][r];
                         if (a.d != nullptr) v = fmaf(skip, static_cast<float>(xv[r]), v);
                         if (zg != nullptr) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
                         out[r] = static_cast<T>(v);
@@ -603,15 +614,49 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                 }
             }
         }
-        if (chunk + 1 < chunks) decays(chunk + 1);
     }
     if (!active) return;
     if (last) {
         if (cache != nullptr) store_state(cache);
     } else if (phase == 0) {
         store_state(part(run));
+        run_total += __shfl_xor(run_total, 32);
         if (lane == 0 && (channel0 + wave_channel) % a.width == 0) {
             totals[static_cast<size_t>(run) * a.heads + h] = static_cast<float>(run_total);
+        }
+    }
+}
+
+// One lane a channel and four states of a sequence: part r += decay of run r * part r - 1, in order. The
+// parts of kAhead runs are on their way at once.
+inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int runs, int lanes) {
+    constexpr int kAhead = 8;
+    const int each = static_cast<int>((static_cast<long long>(lanes) + kThreads - 1) / kThreads);
+    const int j = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
+    const int at = static_cast<int>(blockIdx.x % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
+    const Span span = span_of(a.seq, j);
+    if (at >= lanes || (a.state != nullptr && place_of(a.seq, j) < 0)) return;
+    const int first = run_base(a.seq, j, run_rows);
+    const int count = (span.length - 1) / run_rows;  // runs before the last one
+    const size_t run_floats = static_cast<size_t>(lanes) * 4;
+    f4 *parts = reinterpret_cast<f4 *>(static_cast<float *>(a.scratch) + first * run_floats) + at;
+    const float *totals = static_cast<const float *>(a.scratch) + runs * run_floats +
+                          static_cast<size_t>(first) * a.heads + at / (a.width * a.states / 4);
+    f4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < count; r0 += kAhead) {
+        f4 own[kAhead];
+        float decay[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i < count ? r0 + i : count - 1;
+            own[i] = parts[static_cast<size_t>(r) * lanes];
+            decay[i] = totals[static_cast<size_t>(r) * a.heads];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (r0 + i >= count) break;
+            s = r0 + i == 0 ? own[i] : s * __builtin_amdgcn_exp2f(decay[i]) + own[i];
+            parts[static_cast<size_t>(r0 + i) * lanes] = s;
         }
     }
 }
@@ -621,14 +666,19 @@ hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
     const int group_channels = a.heads / a.groups * a.width;
     const int blocks = a.groups * ((group_channels + 64 * CT - 1) / (64 * CT));
     const long long runs = static_cast<long long>(a.seq.rows / run_rows) + a.seq.sequences;
-    if (runs * blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    for (int phase = 0; phase < (run_rows <= a.seq.rows ? 2 : 1); ++phase) {
-        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), dim3(static_cast<unsigned>(runs * blocks)), dim3(kThreads), 0,
-                           stream, a, run_rows, static_cast<int>(runs), blocks, phase);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const int lanes = a.heads * a.width * (N / 4);
+    const long long joins = static_cast<long long>(a.seq.sequences) * ((lanes + kThreads - 1) / kThreads);
+    if (runs * blocks > 0x7FFFFFFFll || joins > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(runs * blocks)), threads(kThreads);
+    const int count = static_cast<int>(runs);
+    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), grid, threads, 0, stream, a, run_rows, count, blocks, 0);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || run_rows > a.seq.rows) return e;
+    hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, count, lanes);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), grid, threads, 0, stream, a, run_rows, count, blocks, 1);
+    return hipGetLastError();
 }
 
 template <typename T, int N>

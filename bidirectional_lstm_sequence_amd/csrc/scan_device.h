@@ -5,7 +5,21 @@
 
 namespace bl {
 
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
+// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], and log1p(e) = 2 artanh(r) with
+// r = e / (2 + e) <= 1/3: the series r + r^3/3 + ... to r^13/13 leaves 2^-26 of it.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(v));
+    const float r = e * __builtin_amdgcn_rcpf(2.0f + e);
+    const float q = r * r;
+    float p = 1.0f / 13.0f;
+    p = fmaf(p, q, 1.0f / 11.0f);
+    p = fmaf(p, q, 1.0f / 9.0f);
+    p = fmaf(p, q, 1.0f / 7.0f);
+    p = fmaf(p, q, 1.0f / 5.0f);
+    p = fmaf(p, q, 1.0f / 3.0f);
+    p = fmaf(p, q, 1.0f);
+    return fmaf(2.0f * r, p, fmaxf(v, 0.0f));
+}
 
 // The step D of a head from its element of dt.
 __device__ __forceinline__ float step_from(const ScanArgs &a, float dt, int h) {
