@@ -11,8 +11,8 @@ gradient is refused while gradients are enabled.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import struct
 from typing import NamedTuple
 
@@ -39,63 +39,84 @@ def signatures() -> dict:
     return sig
 
 
-def _kinds():
-    import torch
-    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+class _Torch:
+    """What the calls need of torch and the library, looked up at the first call."""
+
+    def __init__(self):
+        import torch
+        from . import _check, library
+        self.Tensor, self.empty = torch.Tensor, torch.empty
+        self.kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        self.float32, self.int32, self.int64 = torch.float32, torch.int32, torch.int64
+        self.uint8, self.bool = torch.uint8, torch.bool
+        self.eight = {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
+        self.grad = torch.is_grad_enabled
+        self.on_stream = torch.cuda.stream
+        # the handle alone, without a Stream object around it
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        self.check, self.library = _check, library()
 
 
-_TYPES: dict = {}
+_torch = None
 
 
-def _type_of(t, name: str) -> int:
-    if not _TYPES:
-        _TYPES.update(_kinds())
-    kind = _TYPES.get(getattr(t, "dtype", None))
-    if kind is None:
-        raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor")
-    return kind
+def _get_torch() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
 
 
 class _Call:
     """What the tensors of one call have in common: the device, and the element type of most."""
 
-    __slots__ = ("device", "dtype", "kind", "grad", "stream")
+    __slots__ = ("torch", "like", "device", "dtype", "kind", "grad", "stream")
 
     def __init__(self, first, name: str, stream):
-        import torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        self.torch = t = _torch or _get_torch()
+        if not isinstance(first, t.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-        self.kind = _type_of(first, name)
+        self.like = first
         self.dtype = first.dtype
+        self.kind = t.kinds.get(self.dtype)
+        if self.kind is None:
+            raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor, got {self.dtype}")
         self.device = first.get_device()
-        self.grad = torch.is_grad_enabled()
+        self.grad = t.grad()
         if stream is not None and stream.device_index != self.device:
             raise ValueError(f"stream belongs to device {stream.device_index}, {name} to device {self.device}")
         self.stream = stream
 
     def _check(self, t, name: str, dtype, shape) -> None:
-        import torch
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
+        try:
+            if (t.get_device() == self.device and t.dtype == dtype and t.shape == shape
+                    and not (self.grad and t.requires_grad)):
+                return
+        except AttributeError:
+            pass
+        if not isinstance(t, self.torch.Tensor) or t.get_device() != self.device:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor on device {self.device}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if self.grad and t.requires_grad:
+        if t.requires_grad:
             raise TypeError(f"{name} requires a gradient; these operators have none (use torch.no_grad())")
 
     def rows(self, t, name: str, shape: tuple, dtype=None) -> tuple:
         """(pointer, elements, row stride) of a tensor of rows: [rows, width] or [rows, parts, width]."""
-        self._check(t, name, self.dtype if dtype is None else dtype, shape)
+        self._check(t, name, dtype or self.dtype, shape)
+        count, width = shape[0], shape[-1]
+        if t.is_contiguous():
+            if len(shape) == 3:
+                width *= shape[1]
+            return (t.data_ptr(), count * width, width) if count and width else NO_ROWS
         strides = t.stride()
-        width = shape[-1]
         if (width > 1 and strides[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and strides[1] != width):
             raise ValueError(f"{name} must be contiguous within a row, got strides {strides}")
         if len(shape) == 3:
             width *= shape[1]
-        count = shape[0]
-        if count == 0 or width == 0:
-            return NO_ROWS
         stride = strides[0] if count > 1 else width
         return t.data_ptr(), (count - 1) * stride + width, stride
 
@@ -103,33 +124,40 @@ class _Call:
         """(pointer, elements) of a contiguous tensor; None is no buffer."""
         if t is None:
             return NO_BUFFER
-        self._check(t, name, self.dtype if dtype is None else dtype, shape)
+        self._check(t, name, dtype or self.dtype, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
         return t.data_ptr(), t.numel()
 
     def empty(self, shape, dtype=None):
         """A new tensor that belongs to the call's stream."""
-        import torch
-        with contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=self.dtype if dtype is None else dtype, device=f"cuda:{self.device}")
+        if self.stream is None:
+            return self.like.new_empty(shape, dtype=dtype)
+        with self.torch.on_stream(self.stream):
+            return self.like.new_empty(shape, dtype=dtype)
 
-    def scratch(self, name: str, packed: bytes):
-        """(tensor, buffer) of the scratch memory the call needs by the library's own count."""
-        import torch
-        from . import _check, library
-        need = ctypes.c_uint64()
-        _check(getattr(library(), name)(packed, ctypes.byref(need)))
-        if need.value == 0:
+    def scratch(self, bytes_needed: int):
+        """(tensor, buffer) of the call's scratch memory."""
+        if bytes_needed == 0:
             return None, NO_BUFFER
-        t = self.empty((need.value,), torch.uint8)
-        return t, (t.data_ptr(), need.value)
+        t = self.empty((bytes_needed,), self.torch.uint8)
+        return t, (t.data_ptr(), bytes_needed)
 
     def run(self, name: str, packed: bytes) -> None:
-        import torch
-        from . import _check, library
-        stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        _check(getattr(library(), name)(packed, stream.cuda_stream))
+        t = self.torch
+        stream = t.stream(self.device) if self.stream is None else self.stream.cuda_stream
+        status = getattr(t.library, name)(packed, stream)
+        if status != 0:
+            t.check(status)
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_bytes(name: str, packed: bytes) -> int:
+    """Bytes of scratch memory by the library's own count: a function of the sizes in ``packed``."""
+    t = _get_torch()
+    need = ctypes.c_uint64()
+    t.check(getattr(t.library, name)(packed, ctypes.byref(need)))
+    return need.value
 
 
 def _dims(t, name: str, count: int) -> tuple:
@@ -141,16 +169,15 @@ def _dims(t, name: str, count: int) -> tuple:
 
 def _sequences(call: _Call, seq_starts, state, slots, fresh) -> tuple:
     """(sequences, starts, slots, fresh) of a packed batch, the last three as buffers."""
-    import torch
+    torch = call.torch
     count = _dims(seq_starts, "seq_starts", 1)[0] - 1
     if count < 0:
         raise ValueError("seq_starts must hold one row number more than there are sequences")
     if state is None and (slots is not None or fresh is not None):
         raise ValueError("slots and fresh need a state")
-    if fresh is not None and fresh.dtype == torch.bool:
-        fresh = fresh.view(torch.uint8)
+    flag = torch.bool if getattr(fresh, "dtype", None) == torch.bool else torch.uint8
     return (count, call.buffer(seq_starts, "seq_starts", (count + 1,), torch.int32),
-            call.buffer(slots, "slots", (count,), torch.int32), call.buffer(fresh, "fresh", (count,), torch.uint8))
+            call.buffer(slots, "slots", (count,), torch.int32), call.buffer(fresh, "fresh", (count,), flag))
 
 
 def causal_conv(x, weight, seq_starts, bias=None, state=None, slots=None, fresh=None, silu: bool = True, out=None,
@@ -182,7 +209,6 @@ def causal_conv(x, weight, seq_starts, bias=None, state=None, slots=None, fresh=
 def causal_conv_step(x, weight, state, bias=None, slots=None, silu: bool = True, out=None, stream=None):
     """One new row per sequence of ``causal_conv``: row i of ``x`` [rows, channels] continues the
     sequence at place ``slots[i]`` (i if None) of ``state``, which is updated in place."""
-    import torch
     call = _Call(x, "x", stream)
     rows, channels = _dims(x, "x", 2)
     taps = _dims(weight, "weight", 2)[1]
@@ -193,14 +219,14 @@ def causal_conv_step(x, weight, state, bias=None, slots=None, silu: bool = True,
     call.run("bilstm_causal_conv_step", _CONV.pack(
         call.device, call.kind, rows, channels, taps, 0, cache, 1 if silu else 0, 0, *xv,
         *call.buffer(weight, "weight", (channels, taps)), *call.buffer(bias, "bias", (channels,)), *NO_BUFFER,
-        *call.buffer(state, "state", (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), torch.int32),
+        *call.buffer(state, "state", (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), call.torch.int32),
         *NO_BUFFER, *yv))
     return out
 
 
 def _scan(name: str, x, dt, a, b, c, seq_starts, d, z, dt_bias, softplus, state, slots, fresh, out, stream):
-    import torch
     call = _Call(x, "x", stream)
+    torch = call.torch
     rows, heads, width = shape = _dims(x, "x", 3)
     _, groups, states = _dims(b, "b", 3)
     if seq_starts is None:
@@ -211,16 +237,16 @@ def _scan(name: str, x, dt, a, b, c, seq_starts, d, z, dt_bias, softplus, state,
     cache = _dims(state, "state", 4)[0] if state is not None else 0
     if out is None:
         out = call.empty(shape)
-    head = (call.device, call.kind, rows, heads, width, groups, states, count, cache, 1 if softplus else 0, 0,
-            *call.rows(x, "x", shape), *call.rows(dt, "dt", (rows, heads)), *call.rows(b, "b", (rows, groups, states)),
-            *call.rows(c, "c", (rows, groups, states)), *(NO_ROWS if z is None else call.rows(z, "z", shape)),
+    sizes = (call.device, call.kind, rows, heads, width, groups, states, count)
+    head = (*sizes, cache, 1 if softplus else 0, 0, *call.rows(x, "x", shape), *call.rows(dt, "dt", (rows, heads)),
+            *call.rows(b, "b", (rows, groups, states)), *call.rows(c, "c", (rows, groups, states)), *(NO_ROWS if z is None else call.rows(z, "z", shape)),
             *call.buffer(a, "a", (heads,), torch.float32), *call.buffer(d, "d", (heads,), torch.float32),
             *call.buffer(dt_bias, "dt_bias", (heads,), torch.float32), *starts,
             *call.buffer(state, "state", (cache, heads, width, states), torch.float32), *places, *begin,
             *call.rows(out, "out", shape))
     hold, scratch = None, NO_BUFFER
     if seq_starts is not None:
-        hold, scratch = call.scratch("bilstm_scan_scratch", _SCAN.pack(*head, *NO_BUFFER))
+        hold, scratch = call.scratch(_scratch_bytes("bilstm_scan_scratch", _SCAN.pack(*sizes, *(0,) * 37)))
     call.run(name, _SCAN.pack(*head, *scratch))
     del hold  # its memory goes back to the call's stream, behind the call's work
     return out
@@ -256,11 +282,6 @@ class NormResult(NamedTuple):
     residual: object
 
 
-def _eight_bit():
-    import torch
-    return {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
-
-
 def add_rms_norm(x, weight, eps: float = 1e-5, residual=None, eight_bit=None, keep_y=None, out=None, residual_out=None,
                  q=None, scales=None, stream=None) -> NormResult:
     """Root-mean-square norm of the rows of ``x`` [rows, width] (with ``residual`` added first) times
@@ -271,13 +292,12 @@ def add_rms_norm(x, weight, eps: float = 1e-5, residual=None, eight_bit=None, ke
     with y close to q * scales[:, None]; ``y`` itself comes with them if ``keep_y`` is true, without
     ``eight_bit`` always. ``out`` and ``residual_out`` may be ``x`` or ``residual`` themselves.
     """
-    import torch
     call = _Call(x, "x", stream)
+    torch = call.torch
     shape = _dims(x, "x", 2)
-    kinds = _eight_bit()
-    if eight_bit not in kinds:
+    if eight_bit not in torch.eight:
         raise ValueError(f"eight_bit must be None, 'e4m3' or 'int8', got {eight_bit!r}")
-    kind, code = kinds[eight_bit]
+    kind, code = torch.eight[eight_bit]
     if kind == 0 and (q is not None or scales is not None or keep_y is False):
         raise ValueError("without eight_bit the norm gives y only")
     if residual is None and residual_out is not None:
@@ -315,8 +335,8 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
     each row's most likely tokens, int64, in falling order, of equally likely ones the lowest first,
     and their log probabilities.
     """
-    import torch
     call = _Call(logits, "logits", stream)
+    torch = call.torch
     rows, vocabulary = _dims(logits, "logits", 2)
     shape = tuple(getattr(tokens, "shape", ()))
     if len(shape) not in (1, 2) or shape[0] != rows:
@@ -326,13 +346,13 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
         raise ValueError(f"top must be 0 or more, got {top}")
     view = call.rows(logits, "logits", (rows, vocabulary))
     ids = call.buffer(tokens, "tokens", shape, torch.int64)
-    head = (call.device, call.kind, rows, vocabulary, given, top, 0, *view, *ids)
-    hold, scratch = call.scratch("bilstm_token_logprobs_scratch", _LOGPROBS.pack(*head, *NO_BUFFER * 5))
+    sizes = (call.device, call.kind, rows, vocabulary, given, top)
+    hold, scratch = call.scratch(_scratch_bytes("bilstm_token_logprobs_scratch", _LOGPROBS.pack(*sizes, *(0,) * 16)))
     logprobs, entropy = call.empty(shape, torch.float32), call.empty((rows,), torch.float32)
     top_tokens = call.empty((rows, top), torch.int64) if top else None
     top_logprobs = call.empty((rows, top), torch.float32) if top else None
     place = lambda t: NO_BUFFER if t is None else (t.data_ptr(), t.numel())  # noqa: E731
     call.run("bilstm_token_logprobs", _LOGPROBS.pack(
-        *head, *place(logprobs), *place(entropy), *place(top_tokens), *place(top_logprobs), *scratch))
+        *sizes, 0, *view, *ids, *place(logprobs), *place(entropy), *place(top_tokens), *place(top_logprobs), *scratch))
     del hold  # its memory goes back to the call's stream, behind the call's work
     return TokenLogprobs(logprobs, entropy, top_tokens, top_logprobs)

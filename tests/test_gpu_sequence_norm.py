@@ -126,3 +126,28 @@ def test_captured_graph_and_stream(bl):
         again = bl.add_rms_norm(x, w, residual=r, eight_bit="e4m3")
         assert torch.equal(got.q.view(torch.uint8), again.q.view(torch.uint8))
         assert torch.equal(got.scales, again.scales) and torch.equal(got.residual, again.residual)
+
+
+def test_the_binding_refuses_what_the_operators_do_not_take(bl):
+    """Types, shapes, devices, strides within a row, gradients: said before anything runs."""
+    x, r, w = (t.cuda() for t in _inputs(torch.float32, 4, 64, 5))
+    for error, call in (
+            (TypeError, lambda: bl.add_rms_norm(x.cpu(), w)),
+            (TypeError, lambda: bl.add_rms_norm(x, w.cpu())),
+            (TypeError, lambda: bl.add_rms_norm(x, w.double())),
+            (TypeError, lambda: bl.add_rms_norm(x.double(), w.double())),
+            (TypeError, lambda: bl.add_rms_norm(x, [1.0] * 64)),
+            (ValueError, lambda: bl.add_rms_norm(x, w[:63])),
+            (ValueError, lambda: bl.add_rms_norm(x[0], w)),
+            (ValueError, lambda: bl.add_rms_norm(x.t().contiguous().t(), w)),
+            (ValueError, lambda: bl.add_rms_norm(x, w, eight_bit="int4")),
+            (ValueError, lambda: bl.add_rms_norm(x, w, residual_out=r)),
+            (ValueError, lambda: bl.add_rms_norm(x, w, keep_y=False)),
+            (TypeError, lambda: bl.add_rms_norm(x, w.clone().requires_grad_())),
+            (bl.BilstmError, lambda: bl.add_rms_norm(x, w, eps=-1.0)),
+            (bl.BilstmError, lambda: bl.add_rms_norm(x, w, residual=r, out=r[:, :], residual_out=r)),
+            (bl.BilstmError, lambda: bl.add_rms_norm(x[:1].expand(4, 64), w, out=x))):
+        with pytest.raises(error):
+            call()
+    with torch.no_grad():
+        assert bl.add_rms_norm(x, w.clone().requires_grad_()).y.shape == x.shape
