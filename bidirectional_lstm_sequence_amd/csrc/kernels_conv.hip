@@ -4,7 +4,7 @@
 //   y = v or v * sigmoid(v)
 //
 // 2W flops an element against 4 (16-bit) or 8 bytes: bound by memory. A thread takes one vector of
-// channels (16 bytes where alignment allows) and a run of kRun rows of one sequence, with the
+// channels (16 bytes where alignment allows) and a run of 8 or 16 rows of one sequence, with the
 // run's rows and the W - 1 rows before it in registers, so x is read once apart from the W - 1
 // rows at each run's start, which the neighbouring run has in the L2. All of a run's loads are
 // issued before the first product. The thread with a sequence's first run also writes the
@@ -132,13 +132,12 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigne
     store_floats<T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + c, out);
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, int RUN>
 hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
-    constexpr int kRun = 16;
     const unsigned vectors = static_cast<unsigned>(a.channels / V);
     const unsigned long long runs =
         step ? static_cast<unsigned long long>(a.seq.rows)
-             : static_cast<unsigned long long>(a.seq.rows) / kRun + static_cast<unsigned long long>(a.seq.sequences);
+             : static_cast<unsigned long long>(a.seq.rows) / RUN + static_cast<unsigned long long>(a.seq.sequences);
     const unsigned long long threads = runs * vectors;
     const unsigned long long blocks = (threads + kThreads - 1) / kThreads;
     if (blocks == 0) return hipSuccess;
@@ -147,17 +146,27 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     if (step) {
         hipLaunchKernelGGL((conv_step_kernel<T, V, W>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     } else {
-        hipLaunchKernelGGL((conv_kernel<T, V, W, kRun>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+        hipLaunchKernelGGL((conv_kernel<T, V, W, RUN>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     }
     return hipGetLastError();
+}
+
+// Long runs read fewer rows twice, short ones put more loads in flight where there is little work:
+// 18848 x 384 float32 takes 16.3, 15.1, 17.2 and 21.5 us in runs of 4, 8, 16 and 32 rows (1810 threads
+// a CU in runs of 4), 16384 x 4352 bfloat16 108, 77, 70 and 76 us (8700 a CU). So runs of 16 where they
+// leave every CU 1024 threads or more, else of 8.
+template <typename T, int V, int W>
+hipError_t by_run(const ConvArgs &a, bool step, hipStream_t stream) {
+    const double long_runs = static_cast<double>(a.seq.rows) / 16 * (a.channels / V);
+    return long_runs >= 256.0 * 1024.0 ? run_conv<T, V, W, 16>(a, step, stream) : run_conv<T, V, W, 8>(a, step, stream);
 }
 
 template <typename T, int V>
 hipError_t by_taps(const ConvArgs &a, bool step, hipStream_t stream) {
     switch (a.taps) {
-        case 2: return run_conv<T, V, 2>(a, step, stream);
-        case 3: return run_conv<T, V, 3>(a, step, stream);
-        case 4: return run_conv<T, V, 4>(a, step, stream);
+        case 2: return by_run<T, V, 2>(a, step, stream);
+        case 3: return by_run<T, V, 3>(a, step, stream);
+        case 4: return by_run<T, V, 4>(a, step, stream);
         default: return hipErrorInvalidValue;
     }
 }

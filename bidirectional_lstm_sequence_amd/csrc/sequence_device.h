@@ -33,16 +33,19 @@ __device__ __forceinline__ void store_floats(T *p, const float (&in)[N]) {
     }
 }
 
-// v * sigmoid(v). 32-bit tensors take the correctly rounded division and the 1-ulp exponential;
-// for 16-bit ones v_exp_f32 and v_rcp_f32 (relative error below 2^-20) are far inside the output's
-// rounding of 2^-9 or 2^-12.
+// v * sigmoid(v) on v_exp_f32 and v_rcp_f32 (1 ulp each). For 32-bit tensors the exponent's rounding
+// is carried along: t + rest = -v log2 e, e^-v = 2^t (1 + rest ln 2). For 16-bit ones it is dropped:
+// |v| 2^-24 of the value, far inside the output's rounding.
 template <typename T>
 __device__ __forceinline__ float silu(float v) {
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911266175e-8f, kLn2 = 0.6931471805599453f;
+    const float t = -kLog2e * v;
+    float e = __builtin_amdgcn_exp2f(t);
     if constexpr (sizeof(T) == 4) {
-        return v / (1.0f + expf(-v));
-    } else {
-        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * v));
+        const float rest = fmaf(-kLog2e, v, -t) - kLog2eLow * v;
+        e = e < __builtin_huge_valf() ? fmaf(e, rest * kLn2, e) : e;
     }
+    return v * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // One sequence's rows in a packed batch, cut to 0..rows.
