@@ -436,6 +436,7 @@ bilstm_status norm(const char *call, const bilstm_norm_args *args, void *stream)
 
 bilstm_status logprob_sizes(const char *call, const bilstm_logprobs_args *args) {
     if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    BL_CHECK(check_type(call, args->type));
     if (args->vocabulary == 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: vocabulary is 0", call);
     if (args->rows > kMostRows || args->vocabulary > (1u << 20)) {
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u tokens exceed the kernel's indexing", call,
@@ -450,7 +451,6 @@ bilstm_status logprob_sizes(const char *call, const bilstm_logprobs_args *args) 
 bilstm_status logprobs(const char *call, const bilstm_logprobs_args *args, void *stream) {
     BL_CHECK(logprob_sizes(call, args));
     const bilstm_logprobs_args &a = *args;
-    BL_CHECK(check_type(call, a.type));
     if (a.reserved != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
     if (a.given > 1024) return fail(BILSTM_INVALID_ARGUMENT, "%s: %u given tokens a row: at most 1024", call, a.given);
     if (a.rows == 0) return BILSTM_OK;
@@ -466,7 +466,7 @@ bilstm_status logprobs(const char *call, const bilstm_logprobs_args *args, void 
         BL_CHECK(check_buffer(call, "top_logprobs", a.top_logprobs, a.rows * a.top, 4, false));
     }
     const uint64_t need = logprob_scratch_bytes(static_cast<int>(a.rows), static_cast<int>(a.vocabulary),
-                                                static_cast<int>(a.top));
+                                                static_cast<int>(a.top), elem_of(a.type));
     if (need > 0) {
         BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
         if (a.scratch.len < need) {
@@ -542,7 +542,7 @@ bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, ui
     BL_CHECK(logprob_sizes("token_logprobs_scratch", args));
     if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "token_logprobs_scratch: bytes is NULL");
     *bytes = logprob_scratch_bytes(static_cast<int>(args->rows), static_cast<int>(args->vocabulary),
-                                   static_cast<int>(args->top));
+                                   static_cast<int>(args->top), elem_of(args->type));
     return BILSTM_OK;
 }
 

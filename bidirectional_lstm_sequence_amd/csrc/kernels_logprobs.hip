@@ -15,13 +15,14 @@
 // Two forms:
 //  * small vocabularies (up to kSmall): a group of 8 to 64 lanes a row, several rows a wave, the
 //    row in registers, `top` rounds of a maximum over the group;
-//  * others: a workgroup takes a tile of 8192 logits into registers with 16-byte loads (rows need
-//    no alignment: a row's first and last vector are read element by element). A lower bound of
-//    the tile's top-th logit comes from the lanes' maxima: per wave the largest 16-bit prefix
-//    that `top` lanes reach, found by halving with ballots, and of those the largest of the four
-//    waves. The few logits that reach it go to a list in LDS and are ranked by counting. More
+//  * others: a workgroup takes a tile of 16384 16-bit or 8192 float32 logits into registers with
+//    16-byte loads (rows need no alignment: a row's first and last vector are read element by
+//    element). A wave finds its maximum first, so that every logit takes one exponential. A lower
+//    bound of the tile's top-th logit comes from the lanes' maxima: per wave the largest 16-bit
+//    prefix that `top` lanes reach, found by halving with ballots, and of those the largest of the
+//    four waves. The few logits that reach it go to a list in LDS and are ranked by counting. More
 //    than the list holds (a tile of equal logits) are taken by `top` rounds of a maximum. A second
-//    launch joins the tiles of a row, a wave each; a row of one tile needs no second launch.
+//    launch joins the tiles of a row, a workgroup each; a row of one tile needs no second launch.
 #include "sequence_device.h"
 
 namespace bl {
@@ -31,48 +32,82 @@ typedef unsigned long long Key;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kEach = 32;                     // logits a lane of a tile
-constexpr int kTile = kThreads * kEach;       // logits of a tile
 constexpr int kList = 256;                    // candidates ranked by counting
+constexpr int kMostTiles = 129;               // 2^20 float32 logits and a vector's skew
 constexpr int kSmall = 1024;                  // vocabularies a group of lanes takes
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
+// Logits of a tile, and of it those of a lane: 128 bytes a lane.
+template <typename T>
+constexpr int tile_each() { return 128 / static_cast<int>(sizeof(T)); }
+
+// Sums over logits relative to m, in powers of 2: s = sum 2^u, w = sum 2^u u, u = (z - m) log2 e.
 struct Part {
     float m, s, w;
 };
 
-// A logit below every finite one, or so far below the maximum that its weight is 0, must not
-// multiply that 0 by an infinity; a NaN passes.
-__device__ __forceinline__ float bounded(float d) { return d < -1e30f ? -1e30f : d; }
+// (z - m) log2 e. A logit below every finite one, or so far below the maximum that its weight is 0,
+// must not multiply that 0 by an infinity; a NaN passes (v_maximum3_f32).
+__device__ __forceinline__ float relative(float z, float m) {
+    return __builtin_elementwise_maximum((z - m) * kLog2e, -1000.0f);
+}
 
 __device__ __forceinline__ void add_logit(Part &p, float z) {
-    const float d = bounded(z - p.m);
-    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+    const float u = relative(z, p.m);
+    const float e = __builtin_amdgcn_exp2f(u);
     p.s += e;
-    p.w = fmaf(e, d, p.w);
+    p.w = fmaf(e, u, p.w);
 }
 
+// The part's sums relative to another m.
 __device__ __forceinline__ Part moved(const Part &p, float m) {
-    const float d = bounded(p.m - m);
-    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-    return {m, p.s * e, e * fmaf(d, p.s, p.w)};
+    const float u = relative(p.m, m);
+    const float e = __builtin_amdgcn_exp2f(u);
+    return {m, p.s * e, e * fmaf(u, p.s, p.w)};
 }
 
-__device__ __forceinline__ Part join(const Part &a, const Part &b) {
-    const float m = fmaxf(a.m, b.m);
-    const Part x = moved(a, m), y = moved(b, m);
-    return {m, x.s + y.s, x.w + y.w};
+// Maximum and sum over groups of lanes, 8 to 64; both lanes of a pair combine the same two numbers.
+template <int CONTROL>
+__device__ __forceinline__ float lane_pair(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CONTROL, 0xF, 0xF, true));
+}
+
+template <int GROUP, class Op>
+__device__ __forceinline__ float over_lanes(float v, Op op) {
+    v = op(v, lane_pair<0xB1>(v));   // quad_perm 1,0,3,2
+    v = op(v, lane_pair<0x4E>(v));   // quad_perm 2,3,0,1
+    v = op(v, lane_pair<0x141>(v));  // row_half_mirror: the other quad of eight
+    if constexpr (GROUP > 8) v = op(v, lane_pair<0x140>(v));  // row_mirror: the other eight of sixteen
+    if constexpr (GROUP > 16) v = op(v, __shfl_xor(v, 16));
+    if constexpr (GROUP > 32) v = op(v, __shfl_xor(v, 32));
+    return v;
 }
 
 template <int GROUP>
-__device__ __forceinline__ Part join_lanes(Part p) {
+__device__ __forceinline__ float most_over_lanes(float v) {
+    return over_lanes<GROUP>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int GROUP>
+__device__ __forceinline__ float sum_over_lanes(float v) {
+    return over_lanes<GROUP>(v, [](float a, float b) { return a + b; });
+}
+
+// Four waves' parts as one; every thread of the workgroup gets it. Ends with the sums read.
+__device__ __forceinline__ Part join_waves(const Part &p, Part (&parts)[kWaves]) {
+    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = p;
+    __syncthreads();
+    const float m = fmaxf(fmaxf(parts[0].m, parts[1].m), fmaxf(parts[2].m, parts[3].m));
+    Part all = {m, 0.0f, 0.0f};
 #pragma unroll
-    for (int o = 1; o < GROUP; o <<= 1) {
-        const Part other = {__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.w, o)};
-        p = join(p, other);  // both sides of a pair add the same two numbers
+    for (int i = 0; i < kWaves; ++i) {
+        const Part one = moved(parts[i], m);
+        all.s += one.s;
+        all.w += one.w;
     }
-    return p;
+    return all;
 }
 
 // Ordered bits of a logit: larger logits have larger ones, both zeros the same, NaN the largest.
@@ -105,6 +140,18 @@ __device__ __forceinline__ Key most_of_lanes(Key k) {
         const Key other = (static_cast<Key>(high) << 32) | low;
         k = other > k ? other : k;
     }
+    return k;
+}
+
+// The largest key of the workgroup. Called in turns: the barriers keep one turn's keys from the next's.
+__device__ __forceinline__ Key most_of_waves(Key k, Key (&round)[kWaves]) {
+    k = most_of_lanes<64>(k);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) round[threadIdx.x >> 6] = k;
+    __syncthreads();
+    k = round[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) k = round[w] > k ? round[w] : k;
     return k;
 }
 
@@ -153,7 +200,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, long long row, 
         }
         a.logprobs[row * a.given + i] = v;
     }
-    if (lane == 0) a.entropy[row] = empty ? 0.0f : log_s - p.w / p.s;
+    if (lane == 0) a.entropy[row] = empty ? 0.0f : log_s - p.w / p.s * kLn2;
     for (int r = lane; r < a.top; r += lanes) write_top(a, row, r, keys, p.m, log_s, empty);
 }
 
@@ -175,9 +222,11 @@ __global__ __launch_bounds__(kThreads) void small_kernel(LogprobArgs a) {
         z[i] = v < a.vocabulary ? static_cast<float>(x[v]) : -__builtin_huge_valf();
         p.m = fmaxf(p.m, z[i]);
     }
+    p.m = most_over_lanes<GROUP>(p.m);
 #pragma unroll
     for (int i = 0; i < EACH; ++i) add_logit(p, z[i]);
-    p = join_lanes<GROUP>(p);
+    p.s = sum_over_lanes<GROUP>(p.s);
+    p.w = sum_over_lanes<GROUP>(p.w);
     Key last = ~static_cast<Key>(0);
     for (int r = 0; r < a.top; ++r) {
         Key best = 0;
@@ -199,8 +248,9 @@ __global__ __launch_bounds__(kThreads) void small_kernel(LogprobArgs a) {
 __host__ __device__ inline size_t part_words(int top) { return 2 + static_cast<size_t>(top); }  // 64-bit words of a tile
 
 template <typename T, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void tile_kernel(LogprobArgs a, int tiles) {
+__global__ __launch_bounds__(kThreads, 4) void tile_kernel(LogprobArgs a, int tiles) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
+    constexpr int kEach = tile_each<T>();
     constexpr int kVectors = kEach / V;
     __shared__ Part parts[kWaves];
     __shared__ unsigned reach[kWaves];
@@ -216,33 +266,46 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(LogprobArgs a, int tiles
     const T *x = static_cast<const T *>(a.logits) + row * a.stride;
     // vector n of the row holds tokens n V - skew .. n V - skew + V - 1, 16-byte aligned
     const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    float z[kEach];
+    const int first = (tile * kVectors * kThreads + tid) * V - skew;  // of this lane's first vector
+    const T masked_out = static_cast<T>(-__builtin_huge_valf());
+    typedef unsigned int Raw __attribute__((ext_vector_type(4)));
+    Raw raw[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
-        const int first = ((tile * kVectors + i) * kThreads + tid) * V - skew;
-        if (first >= 0 && first + V <= a.vocabulary) {
-            const Vec<T, V> v = *reinterpret_cast<const Vec<T, V> *>(x + first);
-#pragma unroll
-            for (int e = 0; e < V; ++e) z[i * V + e] = static_cast<float>(v[e]);
+        const int t = first + i * kThreads * V;
+        if (t >= 0 && t + V <= a.vocabulary) {
+            raw[i] = *reinterpret_cast<const Raw *>(x + t);
         } else {
+            Vec<T, V> v;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int t = first + e;
-                z[i * V + e] = t >= 0 && t < a.vocabulary ? static_cast<float>(x[t]) : -__builtin_huge_valf();
-            }
+            for (int e = 0; e < V; ++e) v[e] = t + e >= 0 && t + e < a.vocabulary ? x[t + e] : masked_out;
+            raw[i] = __builtin_bit_cast(Raw, v);
         }
     }
-    auto token = [&](int i) { return ((tile * kVectors + i / V) * kThreads + tid) * V - skew + i % V; };
-
-    Part p = {kLowest, 0.0f, 0.0f};
+    auto logit = [&](int i) { return static_cast<float>(__builtin_bit_cast(Vec<T, V>, raw[i / V])[i % V]); };
+    // The logits stay as they came, 32 registers; widened ones are not kept from one pass over them to the
+    // next (the compiler would).
+    auto forget_widened = [&] {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) p.m = fmaxf(p.m, z[i]);
-    const float lane_most = p.m;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) add_logit(p, z[i]);
-    p = join_lanes<64>(p);
+            for (int i = 0; i < kVectors; ++i) asm volatile("" : "+v"(raw[i]));
+        }
+    };
+    auto token = [&](int i) { return first + i / V * kThreads * V + i % V; };
     if (tid == 0) listed = 0;
     if (tid < kMostTop) top[tid] = 0;
+
+    float lane_most = kLowest;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) lane_most = fmaxf(lane_most, logit(i));
+    Part p = {most_over_lanes<64>(lane_most), 0.0f, 0.0f};
+    forget_widened();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) add_logit(p, logit(i));
+    forget_widened();
+    const bool lane_nan = p.s != p.s;  // or infinite: then its maximum is
+    p.s = sum_over_lanes<64>(p.s);
+    p.w = sum_over_lanes<64>(p.w);
     if (a.top > 0) {
         // the largest prefix (sign, exponent, 7 bits) that at least `top` lanes' maxima reach
         const unsigned mine = ordered(lane_most);
@@ -253,19 +316,22 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(LogprobArgs a, int tiles
         }
         if ((tid & 63) == 0) reach[wave] = bound;
     }
-    if ((tid & 63) == 0) parts[wave] = p;
-    __syncthreads();
-    p = join(join(parts[0], parts[1]), join(parts[2], parts[3]));
+    p = join_waves(p, parts);
     if (a.top > 0) {
         unsigned bound = reach[0];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) bound = reach[w] > bound ? reach[w] : bound;
-        const float least = from_ordered(bound);  // at least kLowest: every lane's maximum is
+        const float least = from_ordered(bound);  // at least kLowest, as every lane's maximum is: nothing masked reaches it
+        if (__any(lane_nan || lane_most >= least)) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (!(z[i] < least) && !masked(z[i])) {
-                const int at = atomicAdd(&listed, 1);
-                if (at < kList) list[at] = key_of(z[i], token(i));
+            for (int i = 0; i < kEach; ++i) {
+                const bool found = !(logit(i) < least);  // a NaN too
+                if (__any(found)) {
+                    if (found) {
+                        const int at = atomicAdd(&listed, 1);
+                        if (at < kList) list[at] = key_of(logit(i), token(i));
+                    }
+                }
             }
         }
         __syncthreads();
@@ -281,21 +347,21 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(LogprobArgs a, int tiles
         } else {
             Key last = ~static_cast<Key>(0);
             for (int r = 0; r < a.top; ++r) {
+                // from the caches again: 64 keys a lane at once would not fit the registers
                 Key best = 0;
+#pragma unroll 1
+                for (int i = 0; i < kVectors; ++i) {
 #pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const Key k = key_of(z[i], token(i));
-                    best = k < last && k > best ? k : best;
+                    for (int e = 0; e < V; ++e) {
+                        const int t = first + i * kThreads * V + e;
+                        const Key k = t >= 0 && t < a.vocabulary ? key_of(static_cast<float>(x[t]), t) : 0;
+                        best = k < last && k > best ? k : best;
+                    }
                 }
-                best = most_of_lanes<64>(best);
-                if ((tid & 63) == 0) round[wave] = best;
-                __syncthreads();
-                last = round[0];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w) last = round[w] > last ? round[w] : last;
+                last = most_of_waves(best, round);
                 if (tid == 0) top[r] = last;
-                __syncthreads();
             }
+            __syncthreads();
         }
     }
     if constexpr (WHOLE) {
@@ -310,48 +376,60 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(LogprobArgs a, int tiles
     }
 }
 
-// One wave a row joins its tiles: lane l the parts of tiles l, l + 64, ..., and in each round of
-// the top list it offers the best of its tiles' first keys that are not taken yet.
+// A workgroup joins the tiles of a row: thread t takes tile t's part; the tiles' top keys, all
+// different, are ranked by counting, or, where there are many, taken by `top` rounds of a maximum.
 template <typename T>
-__global__ __launch_bounds__(64) void join_kernel(LogprobArgs a, int tiles) {
+__global__ __launch_bounds__(kThreads) void join_kernel(LogprobArgs a, int tiles) {
+    constexpr int kRanked = 512;
+    __shared__ Part parts[kWaves];
+    __shared__ Key keys[kMostTiles * kMostTop];
     __shared__ Key top[kMostTop];
-    const int lane = threadIdx.x;
+    __shared__ Key round[kWaves];
+    static_assert(kMostTiles <= kThreads, "a tile a thread");
+    const int tid = threadIdx.x;
     const long long row = blockIdx.x;
-    const size_t words = part_words(a.top);
+    const int words = static_cast<int>(part_words(a.top));
     const Key *in = static_cast<const Key *>(a.scratch) + static_cast<size_t>(row) * tiles * words;
+    const int n = tiles * a.top;
+    for (int i = tid; i < n; i += kThreads) keys[i] = in[i / a.top * words + 2 + i % a.top];
     Part p = {kLowest, 0.0f, 0.0f};
-    for (int t = lane; t < tiles; t += 64) {
-        const Key first = in[t * words], second = in[t * words + 1];
-        p = join(p, {__uint_as_float(static_cast<unsigned>(first)), __uint_as_float(static_cast<unsigned>(first >> 32)),
-                     __uint_as_float(static_cast<unsigned>(second))});
+    if (tid < tiles) {
+        const Key one = in[tid * words], two = in[tid * words + 1];
+        p = {__uint_as_float(static_cast<unsigned>(one)), __uint_as_float(static_cast<unsigned>(one >> 32)),
+             __uint_as_float(static_cast<unsigned>(two))};
     }
-    p = join_lanes<64>(p);
-    Key last = ~static_cast<Key>(0);
-    for (int r = 0; r < a.top; ++r) {
-        Key best = 0;
-        for (int t = lane; t < tiles; t += 64) {
-            // a tile's keys fall, so its first one below `last` is its offer
-            for (int i = 0; i < a.top; ++i) {
-                const Key k = in[t * words + 2 + i];
-                if (k < last) {
-                    best = k > best ? k : best;
-                    break;
-                }
-            }
+    if (tid < kMostTop) top[tid] = 0;
+    p = moved(p, most_over_lanes<64>(p.m));
+    p.s = sum_over_lanes<64>(p.s);
+    p.w = sum_over_lanes<64>(p.w);
+    p = join_waves(p, parts);
+    if (n <= kRanked) {
+        for (int i = tid; i < n; i += kThreads) {
+            const Key mine = keys[i];
+            if (mine == 0) continue;
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += keys[j] > mine ? 1 : 0;
+            if (rank < a.top) top[rank] = mine;
         }
-        last = most_of_lanes<64>(best);
-        if (lane == 0) top[r] = last;
-        if (last == 0) {
-            if (lane > r && lane < a.top) top[lane] = 0;
-            break;
+    } else {
+        Key last = ~static_cast<Key>(0);
+        for (int r = 0; r < a.top; ++r) {
+            Key best = 0;
+            for (int i = tid; i < n; i += kThreads) best = keys[i] < last && keys[i] > best ? keys[i] : best;
+            last = most_of_waves(best, round);
+            if (tid == 0) top[r] = last;
         }
     }
     __syncthreads();
-    finish_row<T>(a, row, p, lane, 64, [&](int r) { return top[r]; });
+    finish_row<T>(a, row, p, tid, kThreads, [&](int r) { return top[r]; });
 }
 
-// Tiles of a row, whatever its alignment: at most 7 tokens are skipped in front.
-int tiles_of(int vocabulary) { return (vocabulary + 7 + kTile - 1) / kTile; }
+// Tiles of a row, whatever its alignment: a vector's first tokens may belong to the row before.
+template <typename T>
+int tiles_of(int vocabulary) {
+    constexpr int kTile = kThreads * tile_each<T>(), kSkew = 16 / static_cast<int>(sizeof(T)) - 1;
+    return (vocabulary + kSkew + kTile - 1) / kTile;
+}
 
 template <typename T, int GROUP, int EACH>
 hipError_t run_small(const LogprobArgs &a, hipStream_t stream) {
@@ -368,7 +446,7 @@ hipError_t run(const LogprobArgs &a, hipStream_t stream) {
     if (a.vocabulary <= 128) return run_small<T, 32, 4>(a, stream);
     if (a.vocabulary <= 256) return run_small<T, 64, 4>(a, stream);
     if (a.vocabulary <= kSmall) return run_small<T, 64, kSmall / 64>(a, stream);
-    const int tiles = tiles_of(a.vocabulary);
+    const int tiles = tiles_of<T>(a.vocabulary);
     const long long blocks = static_cast<long long>(a.rows) * tiles;
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
     if (tiles == 1) {
@@ -378,15 +456,16 @@ hipError_t run(const LogprobArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((tile_kernel<T, false>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, tiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<T>), dim3(static_cast<unsigned>(a.rows)), dim3(64), 0, stream, a, tiles);
+    hipLaunchKernelGGL((join_kernel<T>), dim3(static_cast<unsigned>(a.rows)), dim3(kThreads), 0, stream, a, tiles);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t logprob_scratch_bytes(int rows, int vocabulary, int top) {
-    if (vocabulary <= kSmall || tiles_of(vocabulary) == 1) return 0;
-    return static_cast<size_t>(rows) * tiles_of(vocabulary) * part_words(top) * sizeof(Key);
+size_t logprob_scratch_bytes(int rows, int vocabulary, int top, Elem type) {
+    const int tiles = type == Elem::f32 ? tiles_of<float>(vocabulary) : tiles_of<__bf16>(vocabulary);
+    if (vocabulary <= kSmall || tiles == 1) return 0;
+    return static_cast<size_t>(rows) * tiles * part_words(top) * sizeof(Key);
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs &a, Elem type, hipStream_t stream) {

@@ -85,7 +85,7 @@ struct LogprobArgs {
 };
 
 constexpr int kMostTop = 32;
-size_t logprob_scratch_bytes(int rows, int vocabulary, int top);
+size_t logprob_scratch_bytes(int rows, int vocabulary, int top, Elem type);
 hipError_t launch_token_logprobs(const LogprobArgs &args, Elem type, hipStream_t stream);
 
 }  // namespace bl

@@ -551,7 +551,7 @@ typedef struct {
     bilstm_buffer scratch;      /* at least bilstm_token_logprobs_scratch() bytes (len in bytes), 16-byte aligned */
 } bilstm_logprobs_args;
 
-/* Bytes of scratch memory bilstm_token_logprobs needs for these sizes (reads device, rows,
+/* Bytes of scratch memory bilstm_token_logprobs needs for these sizes (reads device, type, rows,
  * vocabulary and top of `args`; no pointer). */
 bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, uint64_t *bytes);
 

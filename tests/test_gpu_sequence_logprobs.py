@@ -8,7 +8,7 @@ from tests import sequence_plain as plain
 pytestmark = pytest.mark.gpu
 
 # groups of lanes (up to 1024), one tile, several tiles, odd sizes around their borders
-VOCABULARIES = [1, 2, 7, 8, 9, 31, 33, 129, 255, 257, 1024, 1025, 5000, 8185, 8186, 8193, 40001]
+VOCABULARIES = [1, 2, 7, 8, 9, 31, 33, 129, 255, 257, 1024, 1025, 5000, 8185, 8186, 8189, 8190, 8193, 16377, 16378, 16390, 40001]
 
 
 @pytest.fixture(scope="module")

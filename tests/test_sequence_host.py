@@ -247,14 +247,15 @@ def test_logprobs_refuse(bl, over, expected):
 
 
 def test_logprobs_scratch(bl):
-    """Tiles of 8192 logits whose rows may start up to 7 tokens into a vector; 16 bytes and a key of 8
-    for each top token a tile; none where one launch is enough."""
+    """Tiles of 8192 float32 or 16384 16-bit logits whose rows may start up to 3 or 7 tokens into a
+    vector; 16 bytes and a key of 8 for each top token a tile; none where one launch is enough."""
     need = ctypes.c_uint64()
-    for vocabulary, tiles in ((1024, 0), (1025, 0), (8185, 0), (8186, 2), (20000, 3), (1 << 20, 129)):
-        f = logprob_args(vocabulary=vocabulary)
-        packed = pack(bl.sequence._LOGPROBS, f)
-        assert bl.library().bilstm_token_logprobs_scratch(packed, ctypes.byref(need)) == 0
-        assert need.value == 16 * tiles * (16 + 8 * 4)
+    for kind, sizes in ((0, ((1024, 0), (1025, 0), (8189, 0), (8190, 2), (20000, 3), (1 << 20, 129))),
+                        (1, ((1024, 0), (8190, 0), (16377, 0), (16378, 2), (20000, 2), (1 << 20, 65)))):
+        for vocabulary, tiles in sizes:
+            packed = pack(bl.sequence._LOGPROBS, logprob_args(type=kind, vocabulary=vocabulary))
+            assert bl.library().bilstm_token_logprobs_scratch(packed, ctypes.byref(need)) == 0
+            assert need.value == 16 * tiles * (16 + 8 * 4)
 
 
 def test_sound_arguments_reach_the_device(bl):
