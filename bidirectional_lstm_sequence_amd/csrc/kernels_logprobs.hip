@@ -61,6 +61,31 @@ __device__ __forceinline__ void add_logit(Part &p, float z) {
     p.w = fmaf(e, u, p.w);
 }
 
+// As add_logit for every one of a lane's logits, in one fused operation from z to the exponent: with
+// c = m log2 e rounded and r what the rounding left, fma(z, log2 e, -c) is u + r. r, up to 2^-25 of c,
+// has to stay small beside u: below 2^-8 up to the bound taken here, which fp16's lowest value is
+// inside of. Beyond it the difference is taken first.
+template <int EACH, class Logit>
+__device__ __forceinline__ void add_logits(Part &p, const Logit &logit) {
+    if (fabsf(p.m) <= 65536.0f) {
+        const float c = p.m * kLog2e;
+        const float r = fmaf(p.m, kLog2e, -c);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const float u = __builtin_elementwise_maximum(fmaf(logit(i), kLog2e, -c), -1000.0f);
+            const float e = __builtin_amdgcn_exp2f(u);
+            p.s += e;
+            p.w = fmaf(e, u, p.w);
+        }
+        const float back = __builtin_amdgcn_exp2f(-r);
+        p.w = back * fmaf(-r, p.s, p.w);
+        p.s *= back;
+    } else {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) add_logit(p, logit(i));
+    }
+}
+
 // The part's sums relative to another m.
 __device__ __forceinline__ Part moved(const Part &p, float m) {
     const float u = relative(p.m, m);
@@ -223,8 +248,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(LogprobArgs a) {
         p.m = fmaxf(p.m, z[i]);
     }
     p.m = most_over_lanes<GROUP>(p.m);
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) add_logit(p, z[i]);
+    add_logits<EACH>(p, [&](int i) { return z[i]; });
     p.s = sum_over_lanes<GROUP>(p.s);
     p.w = sum_over_lanes<GROUP>(p.w);
     Key last = ~static_cast<Key>(0);
@@ -270,16 +294,21 @@ __global__ __launch_bounds__(kThreads, 4) void tile_kernel(LogprobArgs a, int ti
     const T masked_out = static_cast<T>(-__builtin_huge_valf());
     typedef unsigned int Raw __attribute__((ext_vector_type(4)));
     Raw raw[kVectors];
+    if (tile * kEach * kThreads >= skew && (tile + 1) * kEach * kThreads - skew <= a.vocabulary) {
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) {
-        const int t = first + i * kThreads * V;
-        if (t >= 0 && t + V <= a.vocabulary) {
-            raw[i] = *reinterpret_cast<const Raw *>(x + t);
-        } else {
-            Vec<T, V> v;
+        for (int i = 0; i < kVectors; ++i) raw[i] = *reinterpret_cast<const Raw *>(x + first + i * kThreads * V);
+    } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = t + e >= 0 && t + e < a.vocabulary ? x[t + e] : masked_out;
-            raw[i] = __builtin_bit_cast(Raw, v);
+        for (int i = 0; i < kVectors; ++i) {
+            const int t = first + i * kThreads * V;
+            if (t >= 0 && t + V <= a.vocabulary) {
+                raw[i] = *reinterpret_cast<const Raw *>(x + t);
+            } else {
+                Vec<T, V> v;
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] = t + e >= 0 && t + e < a.vocabulary ? x[t + e] : masked_out;
+                raw[i] = __builtin_bit_cast(Raw, v);
+            }
         }
     }
     auto logit = [&](int i) { return static_cast<float>(__builtin_bit_cast(Vec<T, V>, raw[i / V])[i % V]); };
@@ -295,13 +324,17 @@ __global__ __launch_bounds__(kThreads, 4) void tile_kernel(LogprobArgs a, int ti
     if (tid == 0) listed = 0;
     if (tid < kMostTop) top[tid] = 0;
 
-    float lane_most = kLowest;
+    float lane_most = kLowest, vector_most[kVectors];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) lane_most = fmaxf(lane_most, logit(i));
+    for (int i = 0; i < kVectors; ++i) {
+        vector_most[i] = kLowest;
+#pragma unroll
+        for (int e = 0; e < V; ++e) vector_most[i] = fmaxf(vector_most[i], logit(i * V + e));
+        lane_most = fmaxf(lane_most, vector_most[i]);
+    }
     Part p = {most_over_lanes<64>(lane_most), 0.0f, 0.0f};
     forget_widened();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) add_logit(p, logit(i));
+    add_logits<kEach>(p, logit);
     forget_widened();
     const bool lane_nan = p.s != p.s;  // or infinite: then its maximum is
     p.s = sum_over_lanes<64>(p.s);
@@ -322,15 +355,15 @@ __global__ __launch_bounds__(kThreads, 4) void tile_kernel(LogprobArgs a, int ti
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) bound = reach[w] > bound ? reach[w] : bound;
         const float least = from_ordered(bound);  // at least kLowest, as every lane's maximum is: nothing masked reaches it
-        if (__any(lane_nan || lane_most >= least)) {
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const bool found = !(logit(i) < least);  // a NaN too
-                if (__any(found)) {
-                    if (found) {
-                        const int at = atomicAdd(&listed, 1);
-                        if (at < kList) list[at] = key_of(logit(i), token(i));
-                    }
+        for (int i = 0; i < kVectors; ++i) {
+            if (!__any(lane_nan || vector_most[i] >= least)) continue;
+#pragma unroll
+            for (int e = i * V; e < (i + 1) * V; ++e) {
+                const bool found = !(logit(e) < least);  // a NaN too
+                if (found) {
+                    const int at = atomicAdd(&listed, 1);
+                    if (at < kList) list[at] = key_of(logit(e), token(e));
                 }
             }
         }

@@ -100,6 +100,18 @@ def test_ties_fall_to_the_lowest_token(bl, dtype):
         assert torch.equal(r.top_tokens.cpu(), torch.sort(logits.float(), dim=1, descending=True, stable=True).indices[:, :32])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e8, 1e20, 1e37])
+@pytest.mark.parametrize("vocabulary", [100, 20000])
+def test_logits_of_any_size(bl, dtype, size, vocabulary):
+    """Far from zero, alone and with the spread of ordinary logits, on both sides."""
+    logits, tokens = _logits(dtype, 6, vocabulary, 21, scale=1.0)
+    logits[:2] = logits[:2] * size
+    logits[2:4] = logits[2:4] - size
+    logits[4:] = logits[4:] + size
+    _check(bl.token_logprobs(logits.cuda(), tokens.cuda(), top=5), logits, tokens, 5)
+
+
 def test_rising_logits(bl):
     """Every tile beats the one before it."""
     logits = torch.arange(50000, dtype=torch.float32).repeat(3, 1) * 1e-3
