@@ -53,26 +53,32 @@ struct Parts3 {
 
 __device__ __forceinline__ f4 mfma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-__device__ __forceinline__ Parts split(const float (&v)[8]) {
-    Parts p;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        p.hi[j] = static_cast<__bf16>(v[j]);
-        p.lo[j] = static_cast<__bf16>(v[j] - static_cast<float>(p.hi[j]));
-    }
-    return p;
+// Pairs of values in bf16 (one v_cvt_pk_bf16_f32), and what the rounding left of them.
+__device__ __forceinline__ unsigned int round_pair(float &a, float &b) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 pair = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    const unsigned int bits = __builtin_bit_cast(unsigned int, pair);
+    a -= __uint_as_float(bits << 16);
+    b -= __uint_as_float(bits & 0xFFFF0000u);
+    return bits;
 }
 
-__device__ __forceinline__ Parts3 split3(const float (&v)[8]) {
-    Parts3 p;
+__device__ __forceinline__ b8 round_all(float (&v)[8]) {
+    u4 bits;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        p.hi[j] = static_cast<__bf16>(v[j]);
-        const float rest = v[j] - static_cast<float>(p.hi[j]);
-        p.mid[j] = static_cast<__bf16>(rest);
-        p.lo[j] = static_cast<__bf16>(rest - static_cast<float>(p.mid[j]));
-    }
-    return p;
+    for (int j = 0; j < 4; ++j) bits[j] = round_pair(v[2 * j], v[2 * j + 1]);
+    return __builtin_bit_cast(b8, bits);
+}
+
+__device__ __forceinline__ Parts split(float (&v)[8]) {
+    const b8 hi = round_all(v);
+    return {hi, round_all(v)};
+}
+
+__device__ __forceinline__ Parts3 split3(float (&v)[8]) {
+    const b8 hi = round_all(v);
+    const b8 mid = round_all(v);
+    return {hi, mid, round_all(v)};
 }
 
 // 4 rows x 16 columns of 16-bit elements a group of 16 lanes: lane i of the group names four
@@ -83,6 +89,15 @@ __device__ __forceinline__ Vec<T, 4> column4(const T *p) {
     return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
 }
 
+// Place of a tile's row within its 16 rows of LDS. Rows of 16-bit elements are read in two ways: four
+// values of 16 rows at a time, and four rows at a time by columns. With rows padded by 16 bytes (4 of 64
+// banks), neighbouring places are 4 banks apart, right for the first; the second wants the rows of
+// half a block 8 banks apart, so even places take rows 0..7 and odd ones rows 8..15.
+template <typename T>
+__device__ __forceinline__ constexpr int place_of_row(int t) {
+    return sizeof(T) == 4 ? t : (t & ~15) | (t & 7) << 1 | (t >> 3 & 1);
+}
+
 // Operands of the products for one input type: fragments of 8 values of K for row (or column)
 // lane % 16, K = 16 e + 4 (lane / 16) + r in place 4 e + r. In: values of an input tensor; Made: float32
 // values on their way to an output; Kept: to the state.
@@ -90,7 +105,7 @@ template <typename T>
 struct Operand;
 
 // Fragments from rows of LDS (p: the lane's row and its first value) and from columns (p: the first
-// row's first column).
+// column of the tile's first row; rows lie at place_of_row).
 template <typename T>
 __device__ __forceinline__ Vec<T, 8> row_values(const T *p) {
     return __builtin_shufflevector(*reinterpret_cast<const Vec<T, 4> *>(p), *reinterpret_cast<const Vec<T, 4> *>(p + 16), 0,
@@ -99,7 +114,7 @@ __device__ __forceinline__ Vec<T, 8> row_values(const T *p) {
 
 template <typename T>
 __device__ __forceinline__ Vec<T, 8> column_values(const T *p, int stride, int lane) {
-    const T *at = p + (4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + (lane & 3) * 4;
+    const T *at = p + place_of_row<T>(4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + (lane & 3) * 4;
     return __builtin_shufflevector(column4(at), column4(at + 16 * stride), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -117,8 +132,8 @@ struct Operand<__bf16> {
         a[j] = static_cast<__bf16>(0.0f);
         return a;
     }
-    static __device__ __forceinline__ Made make(const float (&v)[8]) { return split(v); }
-    static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return split3(v); }
+    static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
+    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
     static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) { return mfma(a, b, c); }
     static __device__ __forceinline__ f4 mul(const Made &a, const In &b, f4 c) { return mfma(a.hi, b, mfma(a.lo, b, c)); }
     static __device__ __forceinline__ f4 mul(const In &a, const Made &b, f4 c) { return mfma(a, b.hi, mfma(a, b.lo, c)); }
@@ -149,8 +164,8 @@ struct Operand<_Float16> {
         a.hi[j] = a.lo[j] = static_cast<__bf16>(0.0f);
         return a;
     }
-    static __device__ __forceinline__ Made make(const float (&v)[8]) { return split(v); }
-    static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return split3(v); }
+    static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
+    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
     // products of parts that make at most 2^-24 of the whole are left out
     static __device__ __forceinline__ f4 mul(const In &a, const Kept &b, f4 c) {
         return mfma(a.hi, b.hi, mfma(a.hi, b.mid, mfma(a.lo, b.hi, mfma(a.lo, b.mid, mfma(a.hi, b.lo, c)))));
@@ -190,13 +205,13 @@ struct Operand<float> {
         a.v[j] = 0.0f;
         return a;
     }
-    static __device__ __forceinline__ Made make(const float (&v)[8]) {
+    static __device__ __forceinline__ Made make(float (&v)[8]) {
         In r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) r.v[j] = v[j];
         return r;
     }
-    static __device__ __forceinline__ Kept keep(const float (&v)[8]) { return make(v); }
+    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return make(v); }
     static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
@@ -295,11 +310,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     constexpr int kStates = NP / 32;          // K steps over the states
     constexpr int kChannels = 64 * CT;        // of a workgroup
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
-    // Rows are padded, by 32 bytes for 16-bit types: reads of four values from 16 rows and reads by
-    // columns then meet every bank equally often; by 16 bytes for float32, whose columns are read value
-    // by value.
-    constexpr int kPad = sizeof(T) == 4 ? VE : 2 * VE;
-    constexpr int CS = NP + kPad, XS = kChannels + kPad;
+    constexpr int CS = NP + VE, XS = kChannels + VE;  // rows padded by 16 bytes (place_of_row)
     constexpr int NV = NP / VE, XV = kChannels / VE;
     constexpr int kBcEach = (L * NV + kThreads - 1) / kThreads;
     constexpr int kXEach = L * XV / kThreads;
@@ -418,25 +429,37 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         for (int u = 0; u < kBcEach; ++u) {
             const int at = tid + u * kThreads, t = at / NV, v = at % NV * VE;
             if (L * NV % kThreads != 0 && t >= L) continue;
-            *reinterpret_cast<u4 *>(bs + t * CS + v) = rb[u];
-            if (whole) *reinterpret_cast<u4 *>(cs + t * CS + v) = rc[u];
+            *reinterpret_cast<u4 *>(bs + place_of_row<T>(t) * CS + v) = rb[u];
+            if (whole) *reinterpret_cast<u4 *>(cs + place_of_row<T>(t) * CS + v) = rc[u];
         }
 #pragma unroll
         for (int u = 0; u < kXEach; ++u) {
             const int at = tid + u * kThreads, t = at / XV, v = at % XV * VE;
-            *reinterpret_cast<u4 *>(xs + t * XS + v) = rx[u];
+            *reinterpret_cast<u4 *>(xs + place_of_row<T>(t) * XS + v) = rx[u];
         }
     };
     const double exponent = static_cast<double>(a.a[h]) * 1.4426950408889634074;
     double run_total = 0.0;
-    float keeps = 0.0f, next_keep = 0.0f;  // the decay over a chunk: lanes 0..31 of the even one, then of the odd one
+    // log2 of the decay over a chunk: lanes 0..31 of the even one, 32..63 of the odd one
+    float totals_now = 0.0f, totals_next = 0.0f;
+    // The state is held without the decay of the last chunks, 2^scale, until that leaves 2^-20..2^20:
+    // its registers are then multiplied once for several chunks.
+    float scale = 0.0f;
+    auto settle_scale = [&] {
+        const float by = __builtin_amdgcn_exp2f(scale);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) s[ct][i] *= by;
+        }
+        scale = 0.0f;
+    };
     // steps and decays of the two chunks whose dt came last; a row behind the end has step 0 and decay 1
     auto decays = [&](int chunk) {
         float *table = &decay_tables[wave][chunk >> 1 & 1][0][0];
         const float step = static_cast<unsigned>(chunk) * L + lane < static_cast<unsigned>(rows) ? step_from(a, dt_next, h) : 0.0f;
         const double cum = running_sum(static_cast<double>(step) * exponent);
         const double total = __shfl(cum, lane | 31);
-        const float over = static_cast<float>(total);
         const float hi = static_cast<float>(cum);
         table[lane] = hi;
         table[2 * L + lane] = static_cast<float>(cum - static_cast<double>(hi));
@@ -444,13 +467,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         table[6 * L + lane] = __builtin_amdgcn_exp2f(hi);
         table[8 * L + lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
         run_total += total;  // lane 0: of even chunks, lane 32: of odd ones
-        return __builtin_amdgcn_exp2f(over);
+        return static_cast<float>(total);
     };
 
     fetch(0);
     if (active) {
         fetch_dt(0);
-        next_keep = decays(0);
+        totals_next = decays(0);
         fetch_dt(2);
     }
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
@@ -464,19 +487,20 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         if (active && (chunk & 1) == 0) {
             // before the next rows are asked for: dt came before the rows just staged, and a wait for it
             // must not become one for them
-            keeps = next_keep;
-            next_keep = decays(chunk + 2);
+            totals_now = totals_next;
+            totals_next = decays(chunk + 2);
             fetch_dt(chunk + 4);
         }
         if (chunk + 1 < chunks) fetch(chunk + 1);
         if (!active) continue;
         const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
                     *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
-        const float keep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(keeps), (chunk & 1) * 32));
+        const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
         const size_t t0 = static_cast<size_t>(chunk) * L;
         Vec<T, 4> z[2][CT];
         f4 y[2][CT];
         typename F::Made m[2];
+        const float state_decay = __builtin_amdgcn_exp2f(scale);
         if (whole) {
             if (zg != nullptr) {
                 const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
@@ -494,7 +518,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
-                const int at = col * CS + 32 * i + 4 * quad;
+                const int at = place_of_row<T>(col) * CS + 32 * i + 4 * quad;
                 const typename F::In c0 = F::rows(cs + at), c1 = F::rows(cs + 16 * CS + at);
                 const typename F::In b0 = F::rows(bs + at), b1 = F::rows(bs + 16 * CS + at);
 #pragma unroll
@@ -519,7 +543,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             }
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
-                const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col];
+                const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col] * state_decay;
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -539,11 +563,16 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
         // 2. the state behind the chunk
+        scale += total;
+        if (!(fabsf(scale) < 20.0f)) settle_scale();
         {
             typename F::Kept right[CT];
             float weight[2][4];
             load_floats<float, 4>(to_end + 4 * quad, weight[0]);
             load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
+            const float unscaled = __builtin_amdgcn_exp2f(-scale);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float w[8];
@@ -555,7 +584,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             for (int i = 0; i < kTiles; ++i) {
                 const typename F::In left = F::columns(bs + 16 * i, CS, lane);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i] * keep);
+                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i]);
             }
         }
         // 3. from the chunk's own rows
@@ -601,7 +630,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                 const int t = 16 * tb + col;
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    const Vec<T, 4> xv = *reinterpret_cast<const Vec<T, 4> *>(xs + t * XS + y_channel + 16 * ct);
+                    const Vec<T, 4> xv = *reinterpret_cast<const Vec<T, 4> *>(xs + place_of_row<T>(t) * XS + y_channel + 16 * ct);
                     Vec<T, 4> out;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -616,6 +645,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         }
     }
     if (!active) return;
+    settle_scale();
     if (last) {
         if (cache != nullptr) store_state(cache);
     } else if (phase == 0) {
