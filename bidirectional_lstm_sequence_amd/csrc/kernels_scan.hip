@@ -42,6 +42,7 @@ __global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int par
     }
     const float decay = a.a[h];
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
+    const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
     for (int t = 0; t < span.length; ++t) {
         const long long row = static_cast<long long>(span.first) + t;
         float b[4], c[4];
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int par
             b[e] = static_cast<float>(bp[e]);
             c[e] = static_cast<float>(cp[e]);
         }
-        const float step = step_from(a, load_dt<T>(a, row, h), h);
+        const float step = step_from(static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]), bias, a.softplus);
         const float keep = expf(step * decay);
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {

@@ -398,9 +398,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     T *yg = static_cast<T *>(a.y) + row0 * a.y_stride + channel0;
     const int chunks = (rows + L - 1) / L;
 
+    const T *dt_rows = static_cast<const T *>(a.dt) + row0 * a.dt_stride + h;
+    const float dt_bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
     // a chunk's rows on their way through registers; rows behind the run's end are zeros
     u4 rc[kBcEach], rb[kBcEach], rx[kXEach];
-    float dt_next = 0.0f;
+    T dt_next = static_cast<T>(0.0f);  // as it comes: widening it would wait for it
     auto fetch = [&](int chunk) {
         const size_t t0 = static_cast<size_t>(chunk) * L;
         const int n = rows - chunk * L < L ? rows - chunk * L : L;
@@ -422,7 +424,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     // one element of dt a lane, for two chunks
     auto fetch_dt = [&](int chunk) {
         const unsigned t = static_cast<unsigned>(chunk) * L + lane;
-        if (t < static_cast<unsigned>(rows)) dt_next = load_dt<T>(a, row0 + t, h);
+        if (t < static_cast<unsigned>(rows)) dt_next = dt_rows[static_cast<size_t>(t) * a.dt_stride];
     };
     auto stage = [&] {
 #pragma unroll
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     // steps and decays of the two chunks whose dt came last; a row behind the end has step 0 and decay 1
     auto decays = [&](int chunk) {
         float *table = &decay_tables[wave][chunk >> 1 & 1][0][0];
-        const float step = static_cast<unsigned>(chunk) * L + lane < static_cast<unsigned>(rows) ? step_from(a, dt_next, h) : 0.0f;
+        const float step = static_cast<unsigned>(chunk) * L + lane < static_cast<unsigned>(rows) ? step_from(static_cast<float>(dt_next), dt_bias, a.softplus) : 0.0f;
         const double cum = running_sum(static_cast<double>(step) * exponent);
         const double total = __shfl(cum, lane | 31);
         const float hi = static_cast<float>(cum);

@@ -21,15 +21,9 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(2.0f * r, p, fmaxf(v, 0.0f));
 }
 
-// The step D of a head from its element of dt.
-__device__ __forceinline__ float step_from(const ScanArgs &a, float dt, int h) {
-    if (a.dt_bias != nullptr) dt += a.dt_bias[h];
-    return a.softplus ? softplus(dt) : dt;
-}
-
-template <typename T>
-__device__ __forceinline__ float load_dt(const ScanArgs &a, long long row, int h) {
-    return static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]);
+// The step D of a head from its element of dt and its bias.
+__device__ __forceinline__ float step_from(float dt, float bias, bool through_softplus) {
+    return through_softplus ? softplus(dt + bias) : dt + bias;
 }
 
 // The chunked form for element type T (scan_chunks.h); one source file instantiates each type.
