@@ -100,7 +100,9 @@ __device__ __forceinline__ constexpr int place_of_row(int t) {
 
 // Operands of the products for one input type: fragments of 8 values of K for row (or column)
 // lane % 16, K = 16 e + 4 (lane / 16) + r in place 4 e + r. In: values of an input tensor; Made: float32
-// values on their way to an output; Kept: to the state.
+// values on their way to an output; Kept: to the state. A product is a sum of terms, a matrix
+// instruction each; callers take one term of several products before the next, as instructions on one
+// accumulator wait for each other.
 template <typename T>
 struct Operand;
 
@@ -134,11 +136,16 @@ struct Operand<__bf16> {
     }
     static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
     static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
-    static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) { return mfma(a, b, c); }
-    static __device__ __forceinline__ f4 mul(const Made &a, const In &b, f4 c) { return mfma(a.hi, b, mfma(a.lo, b, c)); }
-    static __device__ __forceinline__ f4 mul(const In &a, const Made &b, f4 c) { return mfma(a, b.hi, mfma(a, b.lo, c)); }
-    static __device__ __forceinline__ f4 mul(const In &a, const Kept &b, f4 c) {
-        return mfma(a, b.hi, mfma(a, b.mid, mfma(a, b.lo, c)));
+    static constexpr int kInTerms = 1, kMadeTerms = 2, kKeptTerms = 3;
+    static __device__ __forceinline__ f4 in_term(int, const In &a, const In &b, f4 c) { return mfma(a, b, c); }
+    static __device__ __forceinline__ f4 made_term(int k, const Made &a, const In &b, f4 c) {
+        return mfma(k == 0 ? a.lo : a.hi, b, c);
+    }
+    static __device__ __forceinline__ f4 made_term(int k, const In &a, const Made &b, f4 c) {
+        return mfma(a, k == 0 ? b.lo : b.hi, c);
+    }
+    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const Kept &b, f4 c) {
+        return mfma(a, k == 0 ? b.lo : (k == 1 ? b.mid : b.hi), c);
     }
 };
 
@@ -166,13 +173,15 @@ struct Operand<_Float16> {
     }
     static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
     static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
-    // products of parts that make at most 2^-24 of the whole are left out
-    static __device__ __forceinline__ f4 mul(const In &a, const Kept &b, f4 c) {
-        return mfma(a.hi, b.hi, mfma(a.hi, b.mid, mfma(a.lo, b.hi, mfma(a.lo, b.mid, mfma(a.hi, b.lo, c)))));
-    }
+    static constexpr int kInTerms = 3, kMadeTerms = 3, kKeptTerms = 5;
     // the product of the two small parts, at most 2^-16 of the whole, is left out
-    static __device__ __forceinline__ f4 mul(const Parts &a, const Parts &b, f4 c) {
-        return mfma(a.hi, b.hi, mfma(a.hi, b.lo, mfma(a.lo, b.hi, c)));
+    static __device__ __forceinline__ f4 in_term(int k, const Parts &a, const Parts &b, f4 c) {
+        return mfma(k == 0 ? a.lo : a.hi, k == 1 ? b.lo : b.hi, c);
+    }
+    static __device__ __forceinline__ f4 made_term(int k, const Parts &a, const Parts &b, f4 c) { return in_term(k, a, b, c); }
+    // products of parts that make at most 2^-24 of the whole are left out
+    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const Kept &b, f4 c) {
+        return mfma(k == 1 || k == 3 ? a.lo : a.hi, k == 0 ? b.lo : (k == 1 || k == 2 ? b.mid : b.hi), c);
     }
 };
 
@@ -212,11 +221,12 @@ struct Operand<float> {
         return r;
     }
     static __device__ __forceinline__ Kept keep(float (&v)[8]) { return make(v); }
-    static __device__ __forceinline__ f4 mul(const In &a, const In &b, f4 c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
-        return c;
+    static constexpr int kInTerms = 8, kMadeTerms = 8, kKeptTerms = 8;
+    static __device__ __forceinline__ f4 in_term(int k, const In &a, const In &b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[k], b.v[k], c, 0, 0, 0);
     }
+    static __device__ __forceinline__ f4 made_term(int k, const In &a, const In &b, f4 c) { return in_term(k, a, b, c); }
+    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const In &b, f4 c) { return in_term(k, a, b, c); }
 };
 
 // The rows of a chunk in memory: n rows from `base` on. WIDE: 16-byte aligned rows through a buffer
@@ -481,30 +491,30 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
     const int y_channel = wave_channel + 4 * quad;  // of this lane's four in y, for ct 0
 
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-        const int n = rows - chunk * L < L ? rows - chunk * L : L;
-        __syncthreads();  // the chunk before has been read
-        stage();
-        __syncthreads();
-        if (active && (chunk & 1) == 0) {
-            // before the next rows are asked for: dt came before the rows just staged, and a wait for it
-            // must not become one for them
-            totals_now = totals_next;
-            totals_next = decays(chunk + 2);
-            fetch_dt(chunk + 4);
-        }
-        if (chunk + 1 < chunks) fetch(chunk + 1);
-        if (!active) continue;
-        const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
-                    *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
-        const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
-        const size_t t0 = static_cast<size_t>(chunk) * L;
-        Vec<T, 4> z[2][CT];
-        f4 y[2][CT];
-        typename F::Made m[2];
-        const float state_decay = __builtin_amdgcn_exp2f(scale);
-        if (whole) {
-            if (zg != nullptr) {
+    {
+        const bool gated = whole && zg != nullptr;
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            const int n = rows - chunk * L < L ? rows - chunk * L : L;
+            __syncthreads();  // the chunk before has been read
+            stage();
+            __syncthreads();
+            if (active && (chunk & 1) == 0) {
+                // before the next rows are asked for: dt came before the rows just staged, and a wait for it
+                // must not become one for them
+                totals_now = totals_next;
+                totals_next = decays(chunk + 2);
+                fetch_dt(chunk + 4);
+            }
+            if (chunk + 1 < chunks) fetch(chunk + 1);
+            if (!active) continue;
+            const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
+                        *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
+            const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
+            const size_t t0 = static_cast<size_t>(chunk) * L;
+            Vec<T, 4> z[2][CT];
+            f4 y[2][CT], gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
+            const float state_decay = __builtin_amdgcn_exp2f(scale);
+            if (gated) {
                 const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
@@ -512,136 +522,190 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                     for (int ct = 0; ct < CT; ++ct) z[tb][ct] = z_rows.load4(16 * tb + col, y_channel + 16 * ct);
                 }
             }
-            // 1. from the state, and M
-            f4 gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
+            // 1. from the state, and G
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) gram[k] = f4{0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < 3; ++k) gram[k] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
+                for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
+                const T *at = cs + place_of_row<T>(col) * CS + 4 * quad, *bt = bs + place_of_row<T>(col) * CS + 4 * quad;
+                typename F::In c[2][2], b[2][2];  // of this K step and the next, on their way early
 #pragma unroll
-            for (int i = 0; i < kStates; ++i) {
-                const int at = place_of_row<T>(col) * CS + 32 * i + 4 * quad;
-                const typename F::In c0 = F::rows(cs + at), c1 = F::rows(cs + 16 * CS + at);
-                const typename F::In b0 = F::rows(bs + at), b1 = F::rows(bs + 16 * CS + at);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
-                    const typename F::Made left = F::make(v);
-                    y[0][ct] = F::mul(left, c0, y[0][ct]);
-                    y[1][ct] = F::mul(left, c1, y[1][ct]);
+                for (int k = 0; k < 2; ++k) {
+                    c[0][k] = F::rows(at + 16 * k * CS);
+                    b[0][k] = F::rows(bt + 16 * k * CS);
                 }
-                gram[0] = F::mul(b0, c0, gram[0]);
-                gram[1] = F::mul(b0, c1, gram[1]);
-                gram[2] = F::mul(b1, c1, gram[2]);
-            }
-            float s_hi[2][4], s_lo[2][4], s_step[2][4];
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
-                load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi[sb]);
-                load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo[sb]);
-                load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step[sb]);
-            }
+                for (int i = 0; i < kStates; ++i) {
+                    if (i + 1 < kStates) {
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col] * state_decay;
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int sb = e >> 2, r = e & 3;
-                    v[e] = 0.0f;
-                    if (sb > tb) continue;
-                    const float d = (hi - s_hi[sb][r]) + (lo - s_lo[sb][r]);
-                    const float full = gram[sb + tb][r] * (__builtin_amdgcn_exp2f(d) * s_step[sb][r]);
-                    v[e] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
-                }
-                m[tb] = F::make(v);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
-            }
-        }
-        typename F::In x[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
-        // 2. the state behind the chunk
-        scale += total;
-        if (!(fabsf(scale) < 20.0f)) settle_scale();
-        {
-            typename F::Kept right[CT];
-            float weight[2][4];
-            load_floats<float, 4>(to_end + 4 * quad, weight[0]);
-            load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
-            const float unscaled = __builtin_amdgcn_exp2f(-scale);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                float w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
-                right[ct] = F::keep(w);
-            }
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                const typename F::In left = F::columns(bs + 16 * i, CS, lane);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) s[ct][i] = F::mul(left, right[ct], s[ct][i]);
-            }
-        }
-        // 3. from the chunk's own rows
-        if (whole) {
-            f4 sums[2][CT];
-            float check = 0.0f;
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const f4 &v = sums[tb][ct] = F::mul(x[ct], m[tb], y[tb][ct]);
-                    check += (v[0] + v[1]) + (v[2] + v[3]);
-                }
-            }
-            if (__any(check * 0.0f != 0.0f)) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    // the first row of this lane's channel (16 ct + col) whose x is not finite
-                    int bad = L;
-                    typename F::In sound = x[ct];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (F::value(x[ct], e) * 0.0f == 0.0f) continue;
-                        const int row = 16 * (e >> 2) + 4 * quad + (e & 3);
-                        bad = row < bad ? row : bad;
-                        sound = F::zero_at(sound, e);
+                        for (int k = 0; k < 2; ++k) {
+                            c[(i + 1) & 1][k] = F::rows(at + 16 * k * CS + 32 * (i + 1));
+                            b[(i + 1) & 1][k] = F::rows(bt + 16 * k * CS + 32 * (i + 1));
+                        }
                     }
-                    bad = min(bad, __shfl_xor(bad, 16));
-                    bad = min(bad, __shfl_xor(bad, 32));
+                    const typename F::In(&cn)[2] = c[i & 1], (&bn)[2] = b[i & 1];
+                    typename F::Made left[CT];
 #pragma unroll
-                    for (int tb = 0; tb < 2; ++tb) {
-                        sums[tb][ct] = F::mul(sound, m[tb], y[tb][ct]);
+                    for (int ct = 0; ct < CT; ++ct) {
+                        float v[8];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if (16 * tb + col >= __shfl(bad, 4 * quad + r)) sums[tb][ct][r] = __builtin_nanf("");
+                        for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
+                        left[ct] = F::make(v);
+                    }
+#pragma unroll
+                    for (int k = 0; k < F::kInTerms; ++k) {
+                        gram[0] = F::in_term(k, bn[0], cn[0], gram[0]);
+                        gram[1] = F::in_term(k, bn[0], cn[1], gram[1]);
+                        gram[2] = F::in_term(k, bn[1], cn[1], gram[2]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < F::kMadeTerms; ++k) {
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                            for (int tb = 0; tb < 2; ++tb) y[tb][ct] = F::made_term(k, left[ct], cn[tb], y[tb][ct]);
                         }
                     }
                 }
             }
-            const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+            typename F::Made m[2];
+            if (whole) {
+                float s_hi[2][4], s_lo[2][4], s_step[2][4];
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                const int t = 16 * tb + col;
+                for (int sb = 0; sb < 2; ++sb) {
+                    load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi[sb]);
+                    load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo[sb]);
+                    load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step[sb]);
+                }
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col] * state_decay;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int sb = e >> 2, r = e & 3;
+                        v[e] = 0.0f;
+                        if (sb > tb) continue;
+                        const float d = (hi - s_hi[sb][r]) + (lo - s_lo[sb][r]);
+                        const float full = gram[sb + tb][r] * (__builtin_amdgcn_exp2f(d) * s_step[sb][r]);
+                        v[e] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
+                    }
+                    m[tb] = F::make(v);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
+                }
+            }
+            scale += total;
+            if (!(fabsf(scale) < 20.0f)) settle_scale();
+            __builtin_amdgcn_sched_barrier(0);  // the registers do not hold more at once
+            // 2. the state behind the chunk
+            typename F::In x[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
+            {
+                typename F::Kept right[CT];
+                float weight[2][4];
+                load_floats<float, 4>(to_end + 4 * quad, weight[0]);
+                load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
+                const float unscaled = __builtin_amdgcn_exp2f(-scale);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    const Vec<T, 4> xv = *reinterpret_cast<const Vec<T, 4> *>(xs + place_of_row<T>(t) * XS + y_channel + 16 * ct);
-                    Vec<T, 4> out;
+                    float w[8];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = sums[tb][ct][r];
-                        if (a.d != nullptr) v = fmaf(skip, static_cast<float>(xv[r]), v);
-                        if (zg != nullptr) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
-                        out[r] = static_cast<T>(v);
+                    for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
+                    right[ct] = F::keep(w);
+                }
+                constexpr int kPair = kTiles < 2 ? 1 : 2;
+                typename F::In left[2][kPair];
+#pragma unroll
+                for (int k = 0; k < kPair; ++k) left[0][k] = F::columns(bs + 16 * k, CS, lane);
+#pragma unroll
+                for (int i = 0; i < kTiles / kPair; ++i) {
+                    if (i + 1 < kTiles / kPair) {
+#pragma unroll
+                        for (int k = 0; k < kPair; ++k) left[(i + 1) & 1][k] = F::columns(bs + 16 * (kPair * (i + 1) + k), CS, lane);
                     }
-                    y_rows.store4(t, y_channel + 16 * ct, out);
+#pragma unroll
+                    for (int term = 0; term < F::kKeptTerms; ++term) {
+#pragma unroll
+                        for (int k = 0; k < kPair; ++k) {
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) {
+                                s[ct][kPair * i + k] = F::kept_term(term, left[i & 1][k], right[ct], s[ct][kPair * i + k]);
+                            }
+                        }
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // 3. from the chunk's own rows
+            if (whole) {
+                f4 sums[2][CT];
+                float check = 0.0f;
+#pragma unroll
+                for (int k = 0; k < F::kMadeTerms; ++k) {
+#pragma unroll
+                    for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) sums[tb][ct] = F::made_term(k, x[ct], m[tb], k == 0 ? y[tb][ct] : sums[tb][ct]);
+                    }
+                }
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const f4 &v = sums[tb][ct];
+                        check += (v[0] + v[1]) + (v[2] + v[3]);
+                    }
+                }
+                if (__any(check * 0.0f != 0.0f)) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        // the first row of this lane's channel (16 ct + col) whose x is not finite
+                        int bad = L;
+                        typename F::In sound = x[ct];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            if (F::value(x[ct], e) * 0.0f == 0.0f) continue;
+                            const int row = 16 * (e >> 2) + 4 * quad + (e & 3);
+                            bad = row < bad ? row : bad;
+                            sound = F::zero_at(sound, e);
+                        }
+                        bad = min(bad, __shfl_xor(bad, 16));
+                        bad = min(bad, __shfl_xor(bad, 32));
+#pragma unroll
+                        for (int tb = 0; tb < 2; ++tb) {
+                            sums[tb][ct] = y[tb][ct];
+#pragma unroll
+                            for (int k = 0; k < F::kMadeTerms; ++k) sums[tb][ct] = F::made_term(k, sound, m[tb], sums[tb][ct]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                if (16 * tb + col >= __shfl(bad, 4 * quad + r)) sums[tb][ct][r] = __builtin_nanf("");
+                            }
+                        }
+                    }
+                }
+                const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    const int t = 16 * tb + col;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const Vec<T, 4> xv =
+                            *reinterpret_cast<const Vec<T, 4> *>(xs + place_of_row<T>(t) * XS + y_channel + 16 * ct);
+                        Vec<T, 4> out;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            // without d the skip is 0 x, which is 0: rows whose x is not finite are not either
+                            float v = fmaf(skip, static_cast<float>(xv[r]), sums[tb][ct][r]);
+                            if (gated) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
+                            out[r] = static_cast<T>(v);
+                        }
+                        y_rows.store4(t, y_channel + 16 * ct, out);
+                    }
                 }
             }
         }
