@@ -134,10 +134,10 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
 //  * Splitting costs the end states of most runs (the products with x and b a second time) and two
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
-//    sequence of 4096 rows 117, 112, 106, 135 and 142 us in runs of 128, 192, 256, 384 and 512 rows,
-//    495 us whole; 24 unequal ones of 16384 rows together 343, 326, 323 and 370 us in runs of 256, 384,
-//    512 and 1024, 487 us whole. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589 rows:
-//    69, 80, 87 and 101 us in runs of 96, 128, 256 and 512, 94 us whole.
+//    sequence of 4096 rows 124, 98, 84, 101, 92 and 120 us in runs of 96, 192, 256, 384, 512 and 768 rows,
+//    over 400 us whole; 24 unequal ones of 16384 rows together 350, 310, 299, 273 and 294 us in runs of
+//    192, 256, 384, 512 and 768. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589
+//    rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256, 384 and 512, 94 us whole.
 //  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {
     constexpr long long kShort = 8, kPlaces = 512, kLeast = 96, kMost = 512;

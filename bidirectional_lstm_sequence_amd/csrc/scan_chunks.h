@@ -306,13 +306,16 @@ __device__ __forceinline__ double running_sum(double v) {
     return (threadIdx.x & 16) != 0 ? v + other : v;
 }
 
-// A split sequence takes three launches. Scratch holds run r's end state, [runs][heads * width][N]
+// A split sequence takes three launches. Scratch holds run r's first state, [runs][heads * width][N]
 // floats, then the log2 of its decay, [runs][heads].
-// phase 0: a sequence's first run whole, and the end states of the others but the last from a zero start;
-// scan_join_kernel: end states from the sequence's start;
-// phase 1: the other runs whole, each from the end state of the run before it.
-template <typename T, int N, int CT, bool WIDE>
-__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int blocks, int phase) {
+//  * scan_chunk_kernel without WHOLE: the end state of every run but a sequence's last from a zero start,
+//    as the first state of the next run;
+//  * scan_join_kernel: first states from the sequence's own;
+//  * scan_chunk_kernel with WHOLE: all runs. Only it writes the cache, whose old states the join has
+//    copied: a sequence's first and last run work at the same time.
+// Sequences of one run need only the last launch.
+template <typename T, int N, int CT, bool WIDE, bool WHOLE>
+__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int blocks) {
     using F = Operand<T>;
     using Rows = ChunkRows<T, WIDE>;
     constexpr int NP = N < 32 ? 32 : N;       // states, padded with zeros to a K step
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const int quad = lane >> 4;
     const int block = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
     const int run = static_cast<int>(blockIdx.x / static_cast<unsigned>(blocks));
-    const int j = sequence_of_run(a.seq, run, run_rows);
+    const int j = sequence_of_run_wave(a.seq, run, run_rows);
     const Span span = span_of(a.seq, j);
     const int first_run = run_base(a.seq, j, run_rows);
     const long long offset = static_cast<long long>(run - first_run) * run_rows;
@@ -349,8 +352,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const int rows = static_cast<int>(span.length - offset < run_rows ? span.length - offset : run_rows);
     const bool last = offset + rows == span.length;
     const bool first = offset == 0;
-    if (phase == 0 ? !first && last : first) return;
-    const bool whole = phase == 1 || first;
+    if (!WHOLE && last) return;
 
     // channels: of the group, of the workgroup in it, of the wave in the workgroup
     const int group_channels = a.heads / a.groups * a.width;
@@ -393,11 +395,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             for (int i = 0; i < kTiles; ++i) *reinterpret_cast<f4 *>(to + 16 * ct * N + 16 * i) = s[ct][i];
         }
     };
-    if (active) {
-        if (first) {
-            if (cache != nullptr && !starts_fresh(a.seq, j)) load_state(cache);
-        } else if (whole) {
-            load_state(part(run - 1));
+    if (WHOLE && active) {
+        if (!first) {
+            load_state(part(run));
+        } else if (cache != nullptr && !starts_fresh(a.seq, j)) {
+            load_state(last ? cache : part(run));
         }
     }
 
@@ -423,7 +425,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             const int at = tid + u * kThreads, t = at / NV, v = at % NV * VE;
             const bool live = (NP == N || v < N) && (L * NV % kThreads == 0 || t < L);
             rb[u] = b_rows.load16(t, v, live);
-            if (whole) rc[u] = c_rows.load16(t, v, live);
+            if (WHOLE) rc[u] = c_rows.load16(t, v, live);
         }
 #pragma unroll
         for (int u = 0; u < kXEach; ++u) {
@@ -442,7 +444,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             const int at = tid + u * kThreads, t = at / NV, v = at % NV * VE;
             if (L * NV % kThreads != 0 && t >= L) continue;
             *reinterpret_cast<u4 *>(bs + place_of_row<T>(t) * CS + v) = rb[u];
-            if (whole) *reinterpret_cast<u4 *>(cs + place_of_row<T>(t) * CS + v) = rc[u];
+            if (WHOLE) *reinterpret_cast<u4 *>(cs + place_of_row<T>(t) * CS + v) = rc[u];
         }
 #pragma unroll
         for (int u = 0; u < kXEach; ++u) {
@@ -491,231 +493,229 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
     const int y_channel = wave_channel + 4 * quad;  // of this lane's four in y, for ct 0
 
-    {
-        const bool gated = whole && zg != nullptr;
-        for (int chunk = 0; chunk < chunks; ++chunk) {
-            const int n = rows - chunk * L < L ? rows - chunk * L : L;
-            __syncthreads();  // the chunk before has been read
-            stage();
-            __syncthreads();
-            if (active && (chunk & 1) == 0) {
-                // before the next rows are asked for: dt came before the rows just staged, and a wait for it
-                // must not become one for them
-                totals_now = totals_next;
-                totals_next = decays(chunk + 2);
-                fetch_dt(chunk + 4);
+    const bool gated = WHOLE && zg != nullptr;
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int n = rows - chunk * L < L ? rows - chunk * L : L;
+        __syncthreads();  // the chunk before has been read
+        stage();
+        __syncthreads();
+        if (active && (chunk & 1) == 0) {
+            // before the next rows are asked for: dt came before the rows just staged, and a wait for it
+            // must not become one for them
+            totals_now = totals_next;
+            totals_next = decays(chunk + 2);
+            fetch_dt(chunk + 4);
+        }
+        if (chunk + 1 < chunks) fetch(chunk + 1);
+        if (!active) continue;
+        const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
+                    *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
+        const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
+        const size_t t0 = static_cast<size_t>(chunk) * L;
+        Vec<T, 4> z[2][CT];
+        f4 y[2][CT], gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
+        const float state_decay = __builtin_amdgcn_exp2f(scale);
+        if (gated) {
+            const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) z[tb][ct] = z_rows.load4(16 * tb + col, y_channel + 16 * ct);
             }
-            if (chunk + 1 < chunks) fetch(chunk + 1);
-            if (!active) continue;
-            const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
-                        *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
-            const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
-            const size_t t0 = static_cast<size_t>(chunk) * L;
-            Vec<T, 4> z[2][CT];
-            f4 y[2][CT], gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
-            const float state_decay = __builtin_amdgcn_exp2f(scale);
-            if (gated) {
-                const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
+        }
+        // 1. from the state, and G
+        if constexpr (WHOLE) {
 #pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
+            for (int k = 0; k < 3; ++k) gram[k] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) z[tb][ct] = z_rows.load4(16 * tb + col, y_channel + 16 * ct);
-                }
+            for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
+            const T *at = cs + place_of_row<T>(col) * CS + 4 * quad, *bt = bs + place_of_row<T>(col) * CS + 4 * quad;
+            typename F::In c[2][2], b[2][2];  // of this K step and the next, on their way early
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                c[0][k] = F::rows(at + 16 * k * CS);
+                b[0][k] = F::rows(bt + 16 * k * CS);
             }
-            // 1. from the state, and G
-            if (whole) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) gram[k] = f4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < kStates; ++i) {
+                if (i + 1 < kStates) {
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[0][ct] = y[1][ct] = f4{0.f, 0.f, 0.f, 0.f};
-                const T *at = cs + place_of_row<T>(col) * CS + 4 * quad, *bt = bs + place_of_row<T>(col) * CS + 4 * quad;
-                typename F::In c[2][2], b[2][2];  // of this K step and the next, on their way early
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    c[0][k] = F::rows(at + 16 * k * CS);
-                    b[0][k] = F::rows(bt + 16 * k * CS);
-                }
-#pragma unroll
-                for (int i = 0; i < kStates; ++i) {
-                    if (i + 1 < kStates) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            c[(i + 1) & 1][k] = F::rows(at + 16 * k * CS + 32 * (i + 1));
-                            b[(i + 1) & 1][k] = F::rows(bt + 16 * k * CS + 32 * (i + 1));
-                        }
-                    }
-                    const typename F::In(&cn)[2] = c[i & 1], (&bn)[2] = b[i & 1];
-                    typename F::Made left[CT];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
-                        left[ct] = F::make(v);
-                    }
-#pragma unroll
-                    for (int k = 0; k < F::kInTerms; ++k) {
-                        gram[0] = F::in_term(k, bn[0], cn[0], gram[0]);
-                        gram[1] = F::in_term(k, bn[0], cn[1], gram[1]);
-                        gram[2] = F::in_term(k, bn[1], cn[1], gram[2]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < F::kMadeTerms; ++k) {
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-                            for (int tb = 0; tb < 2; ++tb) y[tb][ct] = F::made_term(k, left[ct], cn[tb], y[tb][ct]);
-                        }
+                    for (int k = 0; k < 2; ++k) {
+                        c[(i + 1) & 1][k] = F::rows(at + 16 * k * CS + 32 * (i + 1));
+                        b[(i + 1) & 1][k] = F::rows(bt + 16 * k * CS + 32 * (i + 1));
                     }
                 }
-            }
-            typename F::Made m[2];
-            if (whole) {
-                float s_hi[2][4], s_lo[2][4], s_step[2][4];
-#pragma unroll
-                for (int sb = 0; sb < 2; ++sb) {
-                    load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi[sb]);
-                    load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo[sb]);
-                    load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step[sb]);
-                }
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col] * state_decay;
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int sb = e >> 2, r = e & 3;
-                        v[e] = 0.0f;
-                        if (sb > tb) continue;
-                        const float d = (hi - s_hi[sb][r]) + (lo - s_lo[sb][r]);
-                        const float full = gram[sb + tb][r] * (__builtin_amdgcn_exp2f(d) * s_step[sb][r]);
-                        v[e] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
-                    }
-                    m[tb] = F::make(v);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
-                }
-            }
-            scale += total;
-            if (!(fabsf(scale) < 20.0f)) settle_scale();
-            __builtin_amdgcn_sched_barrier(0);  // the registers do not hold more at once
-            // 2. the state behind the chunk
-            typename F::In x[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
-            {
-                typename F::Kept right[CT];
-                float weight[2][4];
-                load_floats<float, 4>(to_end + 4 * quad, weight[0]);
-                load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
-                const float unscaled = __builtin_amdgcn_exp2f(-scale);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
+                const typename F::In(&cn)[2] = c[i & 1], (&bn)[2] = b[i & 1];
+                typename F::Made left[CT];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    float w[8];
+                    float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
-                    right[ct] = F::keep(w);
+                    for (int e = 0; e < 8; ++e) v[e] = e < 4 || kTiles > 1 ? s[ct][(2 * i + (e >> 2)) % kTiles][e & 3] : 0.0f;
+                    left[ct] = F::make(v);
                 }
-                constexpr int kPair = kTiles < 2 ? 1 : 2;
-                typename F::In left[2][kPair];
 #pragma unroll
-                for (int k = 0; k < kPair; ++k) left[0][k] = F::columns(bs + 16 * k, CS, lane);
-#pragma unroll
-                for (int i = 0; i < kTiles / kPair; ++i) {
-                    if (i + 1 < kTiles / kPair) {
-#pragma unroll
-                        for (int k = 0; k < kPair; ++k) left[(i + 1) & 1][k] = F::columns(bs + 16 * (kPair * (i + 1) + k), CS, lane);
-                    }
-#pragma unroll
-                    for (int term = 0; term < F::kKeptTerms; ++term) {
-#pragma unroll
-                        for (int k = 0; k < kPair; ++k) {
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) {
-                                s[ct][kPair * i + k] = F::kept_term(term, left[i & 1][k], right[ct], s[ct][kPair * i + k]);
-                            }
-                        }
-                    }
+                for (int k = 0; k < F::kInTerms; ++k) {
+                    gram[0] = F::in_term(k, bn[0], cn[0], gram[0]);
+                    gram[1] = F::in_term(k, bn[0], cn[1], gram[1]);
+                    gram[2] = F::in_term(k, bn[1], cn[1], gram[2]);
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            // 3. from the chunk's own rows
-            if (whole) {
-                f4 sums[2][CT];
-                float check = 0.0f;
 #pragma unroll
                 for (int k = 0; k < F::kMadeTerms; ++k) {
 #pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                        for (int tb = 0; tb < 2; ++tb) y[tb][ct] = F::made_term(k, left[ct], cn[tb], y[tb][ct]);
+                    }
+                }
+            }
+        }
+        typename F::Made m[2];
+        if constexpr (WHOLE) {
+            float s_hi[2][4], s_lo[2][4], s_step[2][4];
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+                load_floats<float, 4>(cum_hi + 16 * sb + 4 * quad, s_hi[sb]);
+                load_floats<float, 4>(cum_lo + 16 * sb + 4 * quad, s_lo[sb]);
+                load_floats<float, 4>(steps + 16 * sb + 4 * quad, s_step[sb]);
+            }
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                const float hi = cum_hi[16 * tb + col], lo = cum_lo[16 * tb + col], decay = since[16 * tb + col] * state_decay;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int sb = e >> 2, r = e & 3;
+                    v[e] = 0.0f;
+                    if (sb > tb) continue;
+                    const float d = (hi - s_hi[sb][r]) + (lo - s_lo[sb][r]);
+                    const float full = gram[sb + tb][r] * (__builtin_amdgcn_exp2f(d) * s_step[sb][r]);
+                    v[e] = sb < tb || 4 * quad + r <= col ? full : 0.0f;
+                }
+                m[tb] = F::make(v);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
+            }
+        }
+        scale += total;
+        if (!(fabsf(scale) < 20.0f)) settle_scale();
+        __builtin_amdgcn_sched_barrier(0);  // the registers do not hold more at once
+        // 2. the state behind the chunk
+        typename F::In x[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
+        {
+            typename F::Kept right[CT];
+            float weight[2][4];
+            load_floats<float, 4>(to_end + 4 * quad, weight[0]);
+            load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
+            const float unscaled = __builtin_amdgcn_exp2f(-scale);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                float w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
+                right[ct] = F::keep(w);
+            }
+            constexpr int kPair = kTiles < 2 ? 1 : 2;
+            typename F::In left[2][kPair];
+#pragma unroll
+            for (int k = 0; k < kPair; ++k) left[0][k] = F::columns(bs + 16 * k, CS, lane);
+#pragma unroll
+            for (int i = 0; i < kTiles / kPair; ++i) {
+                if (i + 1 < kTiles / kPair) {
+#pragma unroll
+                    for (int k = 0; k < kPair; ++k) left[(i + 1) & 1][k] = F::columns(bs + 16 * (kPair * (i + 1) + k), CS, lane);
+                }
+#pragma unroll
+                for (int term = 0; term < F::kKeptTerms; ++term) {
+#pragma unroll
+                    for (int k = 0; k < kPair; ++k) {
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            s[ct][kPair * i + k] = F::kept_term(term, left[i & 1][k], right[ct], s[ct][kPair * i + k]);
+                        }
+                    }
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // 3. from the chunk's own rows
+        if constexpr (WHOLE) {
+            f4 sums[2][CT];
+            float check = 0.0f;
+#pragma unroll
+            for (int k = 0; k < F::kMadeTerms; ++k) {
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) sums[tb][ct] = F::made_term(k, x[ct], m[tb], k == 0 ? y[tb][ct] : sums[tb][ct]);
+                }
+            }
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f4 &v = sums[tb][ct];
+                    check += (v[0] + v[1]) + (v[2] + v[3]);
+                }
+            }
+            if (__any(check * 0.0f != 0.0f)) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    // the first row of this lane's channel (16 ct + col) whose x is not finite
+                    int bad = L;
+                    typename F::In sound = x[ct];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (F::value(x[ct], e) * 0.0f == 0.0f) continue;
+                        const int row = 16 * (e >> 2) + 4 * quad + (e & 3);
+                        bad = row < bad ? row : bad;
+                        sound = F::zero_at(sound, e);
+                    }
+                    bad = min(bad, __shfl_xor(bad, 16));
+                    bad = min(bad, __shfl_xor(bad, 32));
+#pragma unroll
                     for (int tb = 0; tb < 2; ++tb) {
+                        sums[tb][ct] = y[tb][ct];
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) sums[tb][ct] = F::made_term(k, x[ct], m[tb], k == 0 ? y[tb][ct] : sums[tb][ct]);
-                    }
-                }
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const f4 &v = sums[tb][ct];
-                        check += (v[0] + v[1]) + (v[2] + v[3]);
-                    }
-                }
-                if (__any(check * 0.0f != 0.0f)) {
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        // the first row of this lane's channel (16 ct + col) whose x is not finite
-                        int bad = L;
-                        typename F::In sound = x[ct];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (F::value(x[ct], e) * 0.0f == 0.0f) continue;
-                            const int row = 16 * (e >> 2) + 4 * quad + (e & 3);
-                            bad = row < bad ? row : bad;
-                            sound = F::zero_at(sound, e);
-                        }
-                        bad = min(bad, __shfl_xor(bad, 16));
-                        bad = min(bad, __shfl_xor(bad, 32));
-#pragma unroll
-                        for (int tb = 0; tb < 2; ++tb) {
-                            sums[tb][ct] = y[tb][ct];
-#pragma unroll
-                            for (int k = 0; k < F::kMadeTerms; ++k) sums[tb][ct] = F::made_term(k, sound, m[tb], sums[tb][ct]);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                if (16 * tb + col >= __shfl(bad, 4 * quad + r)) sums[tb][ct][r] = __builtin_nanf("");
-                            }
-                        }
-                    }
-                }
-                const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    const int t = 16 * tb + col;
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const Vec<T, 4> xv =
-                            *reinterpret_cast<const Vec<T, 4> *>(xs + place_of_row<T>(t) * XS + y_channel + 16 * ct);
-                        Vec<T, 4> out;
+                        for (int k = 0; k < F::kMadeTerms; ++k) sums[tb][ct] = F::made_term(k, sound, m[tb], sums[tb][ct]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            // without d the skip is 0 x, which is 0: rows whose x is not finite are not either
-                            float v = fmaf(skip, static_cast<float>(xv[r]), sums[tb][ct][r]);
-                            if (gated) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
-                            out[r] = static_cast<T>(v);
+                            if (16 * tb + col >= __shfl(bad, 4 * quad + r)) sums[tb][ct][r] = __builtin_nanf("");
                         }
-                        y_rows.store4(t, y_channel + 16 * ct, out);
                     }
+                }
+            }
+            const Rows y_rows(yg + t0 * a.y_stride, a.y_stride, n, live_channels);
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                const int t = 16 * tb + col;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const Vec<T, 4> xv =
+                        *reinterpret_cast<const Vec<T, 4> *>(xs + place_of_row<T>(t) * XS + y_channel + 16 * ct);
+                    Vec<T, 4> out;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        // without d the skip is 0 x, which is 0: rows whose x is not finite are not either
+                        float v = fmaf(skip, static_cast<float>(xv[r]), sums[tb][ct][r]);
+                        if (gated) v *= silu<T>(static_cast<float>(z[tb][ct][r]));
+                        out[r] = static_cast<T>(v);
+                    }
+                    y_rows.store4(t, y_channel + 16 * ct, out);
                 }
             }
         }
     }
     if (!active) return;
     settle_scale();
-    if (last) {
-        if (cache != nullptr) store_state(cache);
-    } else if (phase == 0) {
-        store_state(part(run));
+    if constexpr (WHOLE) {
+        if (last && cache != nullptr) store_state(cache);
+    } else {
+        store_state(part(run + 1));
         run_total += __shfl_xor(run_total, 32);
         if (lane == 0 && (channel0 + wave_channel) % a.width == 0) {
             totals[static_cast<size_t>(run) * a.heads + h] = static_cast<float>(run_total);
@@ -723,36 +723,44 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     }
 }
 
-// One lane a channel and four states of a sequence: part r += decay of run r * part r - 1, in order. The
-// parts of kAhead runs are on their way at once.
+// One lane a channel and four states of a sequence: its state, then for each run but the last
+// s = decay * s + the run's own end state, each the next run's first state. The parts of kAhead runs are on
+// their way at once. From a zero start nothing changes up to the second run.
 inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int runs, int lanes) {
     constexpr int kAhead = 8;
     const int each = static_cast<int>((static_cast<long long>(lanes) + kThreads - 1) / kThreads);
     const int j = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
     const int at = static_cast<int>(blockIdx.x % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
     const Span span = span_of(a.seq, j);
-    if (at >= lanes || (a.state != nullptr && place_of(a.seq, j) < 0)) return;
-    const int first = run_base(a.seq, j, run_rows);
     const int count = (span.length - 1) / run_rows;  // runs before the last one
+    const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
+    if (at >= lanes || count < 1 || place < 0) return;
+    const bool kept = a.state != nullptr && !starts_fresh(a.seq, j);
+    const int first = run_base(a.seq, j, run_rows);
     const size_t run_floats = static_cast<size_t>(lanes) * 4;
     f4 *parts = reinterpret_cast<f4 *>(static_cast<float *>(a.scratch) + first * run_floats) + at;
     const float *totals = static_cast<const float *>(a.scratch) + runs * run_floats +
                           static_cast<size_t>(first) * a.heads + at / (a.width * a.states / 4);
     f4 s = {0.f, 0.f, 0.f, 0.f};
+    if (kept) parts[0] = s = reinterpret_cast<const f4 *>(a.state + place * run_floats)[at];
     for (int r0 = 0; r0 < count; r0 += kAhead) {
         f4 own[kAhead];
         float decay[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = r0 + i < count ? r0 + i : count - 1;
-            own[i] = parts[static_cast<size_t>(r) * lanes];
+            own[i] = parts[static_cast<size_t>(r + 1) * lanes];
             decay[i] = totals[static_cast<size_t>(r) * a.heads];
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (r0 + i >= count) break;
-            s = r0 + i == 0 ? own[i] : s * __builtin_amdgcn_exp2f(decay[i]) + own[i];
-            parts[static_cast<size_t>(r0 + i) * lanes] = s;
+            if (!kept && r0 + i == 0) {
+                s = own[i];
+            } else {
+                s = s * __builtin_amdgcn_exp2f(decay[i]) + own[i];
+                parts[static_cast<size_t>(r0 + i + 1) * lanes] = s;
+            }
         }
     }
 }
@@ -767,13 +775,15 @@ hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
     if (runs * blocks > 0x7FFFFFFFll || joins > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(runs * blocks)), threads(kThreads);
     const int count = static_cast<int>(runs);
-    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), grid, threads, 0, stream, a, run_rows, count, blocks, 0);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || run_rows > a.seq.rows) return e;
-    hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, count, lanes);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE>), grid, threads, 0, stream, a, run_rows, count, blocks, 1);
+    if (run_rows <= a.seq.rows) {
+        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, false>), grid, threads, 0, stream, a, run_rows, count, blocks);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, count, lanes);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, true>), grid, threads, 0, stream, a, run_rows, count, blocks);
     return hipGetLastError();
 }
 

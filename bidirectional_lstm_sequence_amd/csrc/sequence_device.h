@@ -85,6 +85,22 @@ __device__ __forceinline__ int sequence_of_run(const SequenceArgs &s, int run, i
     return low;
 }
 
+// The same for a whole wave with one run: 64 places of the table at a time, so that 64 sequences take
+// one load's time and 4096 take two.
+__device__ __forceinline__ int sequence_of_run_wave(const SequenceArgs &s, int run, int size) {
+    const int lane = threadIdx.x & 63;
+    int low = 0, count = s.sequences;  // the answer is in low .. low + count - 1
+    while (count > 1) {
+        const int step = (count + 63) / 64;
+        const int at = lane * step;  // lane 0 always passes: the answer is at low or behind it
+        const bool passes = at < count && (lane == 0 || run_base(s, low + at, size) <= run);
+        const int ahead = (__popcll(__ballot(passes)) - 1) * step;
+        low += ahead;
+        count = count - ahead < step ? count - ahead : step;
+    }
+    return __builtin_amdgcn_readfirstlane(low);
+}
+
 // The cache place of sequence j: -1 for one that is padding.
 __device__ __forceinline__ int place_of(const SequenceArgs &s, int j) {
     const int p = s.slots != nullptr ? s.slots[j] : j;
