@@ -3,8 +3,8 @@
 //   v[t][c] = bias[c] + sum_k w[c][k] x[t - W + 1 + k][c],  W = 2, 3 or 4 taps
 //   y = v or v * sigmoid(v)
 //
-// 2W flops an element against 4 (16-bit) or 8 bytes: bound by memory. A thread takes one vector of
-// channels (16 bytes where alignment allows) and a run of 8 or 16 rows of one sequence, with the
+// 2W flops an element against 4 (16-bit) or 8 bytes: bound by memory. A thread takes 16 bytes of
+// channels (at any alignment; a row's last ones may be fewer) and a run of 8 or 16 rows of one sequence, with the
 // run's rows and the W - 1 rows before it in registers, so x is read once apart from the W - 1
 // rows at each run's start, which the neighbouring run has in the L2. All of a run's loads are
 // issued before the first product. The thread with a sequence's first run also writes the
@@ -17,23 +17,33 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[V][W], float (&bias)[V]) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int count, float (&w)[V][W], float (&bias)[V]) {
     const T *wp = static_cast<const T *>(a.weight) + static_cast<size_t>(c) * W;
+    Vec<T, V> raw[W];  // the channels' taps as they lie, W after W
+#pragma unroll
+    for (int k = 0; k < W; ++k) raw[k] = load_vector<false, T, V>(wp + k * V, count * W - k * V);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[i][k] = static_cast<float>(wp[i * W + k]);
-        bias[i] = a.bias != nullptr ? static_cast<float>(static_cast<const T *>(a.bias)[c + i]) : 0.0f;
+        for (int k = 0; k < W; ++k) w[i][k] = static_cast<float>(raw[(i * W + k) / V][(i * W + k) % V]);
+        bias[i] = 0.0f;
+    }
+    if (a.bias != nullptr) {
+        const Vec<T, V> b = load_vector<false, T, V>(static_cast<const T *>(a.bias) + c, count);
+#pragma unroll
+        for (int i = 0; i < V; ++i) bias[i] = static_cast<float>(b[i]);
     }
 }
 
-template <typename T, int V, int W, int RUN>
+template <typename T, int V, int W, int RUN, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
     using X = Vec<T, V>;
     const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
     if (id >= threads) return;
     const int run = static_cast<int>(id / vectors);
     const int c = static_cast<int>(id % vectors) * V;
+    const int channels = a.channels - c;  // of this vector, at least V but for a row's last one
+    auto load = [&](const T *p) { return load_vector<ALIGNED, T, V>(p, channels); };
     const int j = sequence_of_run(a.seq, run, RUN);
     const Span span = span_of(a.seq, j);
     const long long at = static_cast<long long>(run - run_base(a.seq, j, RUN)) * RUN;
@@ -53,14 +63,14 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
 #pragma unroll
     for (int r = 0; r < RUN; ++r) {
         rows[W - 1 + r] = X{};
-        if (r < count) rows[W - 1 + r] = *reinterpret_cast<const X *>(x + static_cast<size_t>(offset + r) * a.x_stride);
+        if (r < count) rows[W - 1 + r] = load(x + static_cast<size_t>(offset + r) * a.x_stride);
     }
     if (offset == 0) {
         const bool kept = state != nullptr && !starts_fresh(a.seq, j);
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
             rows[r] = X{};
-            if (kept) rows[r] = *reinterpret_cast<const X *>(state + static_cast<size_t>(r) * a.channels);
+            if (kept) rows[r] = load(state + static_cast<size_t>(r) * a.channels);
         }
         if (state != nullptr) {
             // the last W - 1 rows of (old state, x): old rows while the sequence is shorter
@@ -69,72 +79,77 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
                 const int from = span.length - (W - 1) + r;  // row of x; negative: kept row from + W - 1
                 X v{};
                 if (from >= 0) {
-                    v = *reinterpret_cast<const X *>(x + static_cast<size_t>(from) * a.x_stride);
+                    v = load(x + static_cast<size_t>(from) * a.x_stride);
                 } else {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k)
                         if (k == from + W - 1) v = rows[k];
                 }
-                *reinterpret_cast<X *>(state + static_cast<size_t>(r) * a.channels) = v;
+                store_vector<ALIGNED, T, V>(state + static_cast<size_t>(r) * a.channels, v, channels);
             }
         }
     } else {
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
             // a run starts at a multiple of RUN >= W - 1, so these rows are the sequence's own
-            rows[r] = *reinterpret_cast<const X *>(x + static_cast<size_t>(offset - (W - 1) + r) * a.x_stride);
+            rows[r] = load(x + static_cast<size_t>(offset - (W - 1) + r) * a.x_stride);
         }
     }
     static_assert(RUN >= W - 1, "a run's predecessors lie in the run before it");
 
     float w[V][W], bias[V];
-    load_taps<T, V, W>(a, c, w, bias);
+    load_taps<T, V, W>(a, c, channels, w, bias);
 #pragma unroll
     for (int r = 0; r < RUN; ++r) {
-        float out[V];
+        X out;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float v = bias[i];
 #pragma unroll
             for (int k = 0; k < W; ++k) v = fmaf(w[i][k], static_cast<float>(rows[r + k][i]), v);
-            out[i] = a.silu ? silu<T>(v) : v;
+            out[i] = static_cast<T>(a.silu ? silu<T>(v) : v);
         }
-        if (r < count) store_floats<T, V>(y + static_cast<size_t>(offset + r) * a.y_stride, out);
+        if (r < count) store_vector<ALIGNED, T, V>(y + static_cast<size_t>(offset + r) * a.y_stride, out, channels);
     }
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
     using X = Vec<T, V>;
     const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
     if (id >= threads) return;
     const int row = static_cast<int>(id / vectors);
     const int c = static_cast<int>(id % vectors) * V;
+    const int channels = a.channels - c;
+    auto load = [&](const T *p) { return load_vector<ALIGNED, T, V>(p, channels); };
     const int place = place_of(a.seq, row);
     if (place < 0) return;
     T *state = static_cast<T *>(a.state) + static_cast<size_t>(place) * (W - 1) * a.channels + c;
     X rows[W];
-    rows[W - 1] = *reinterpret_cast<const X *>(static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.x_stride + c);
+    rows[W - 1] = load(static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.x_stride + c);
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) rows[r] = *reinterpret_cast<const X *>(state + static_cast<size_t>(r) * a.channels);
+    for (int r = 0; r < W - 1; ++r) rows[r] = load(state + static_cast<size_t>(r) * a.channels);
     float w[V][W], bias[V];
-    load_taps<T, V, W>(a, c, w, bias);
+    load_taps<T, V, W>(a, c, channels, w, bias);
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) *reinterpret_cast<X *>(state + static_cast<size_t>(r) * a.channels) = rows[r + 1];
-    float out[V];
+    for (int r = 0; r < W - 1; ++r) {
+        store_vector<ALIGNED, T, V>(state + static_cast<size_t>(r) * a.channels, rows[r + 1], channels);
+    }
+    X out;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float v = bias[i];
 #pragma unroll
         for (int k = 0; k < W; ++k) v = fmaf(w[i][k], static_cast<float>(rows[k][i]), v);
-        out[i] = a.silu ? silu<T>(v) : v;
+        out[i] = static_cast<T>(a.silu ? silu<T>(v) : v);
     }
-    store_floats<T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + c, out);
+    store_vector<ALIGNED, T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + c, out, channels);
 }
 
-template <typename T, int V, int W, int RUN>
+template <typename T, int W, int RUN, bool ALIGNED>
 hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
-    const unsigned vectors = static_cast<unsigned>(a.channels / V);
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const unsigned vectors = static_cast<unsigned>((a.channels + V - 1) / V);
     const unsigned long long runs =
         step ? static_cast<unsigned long long>(a.seq.rows)
              : static_cast<unsigned long long>(a.seq.rows) / RUN + static_cast<unsigned long long>(a.seq.sequences);
@@ -144,9 +159,9 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks));
     if (step) {
-        hipLaunchKernelGGL((conv_step_kernel<T, V, W>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+        hipLaunchKernelGGL((conv_step_kernel<T, V, W, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     } else {
-        hipLaunchKernelGGL((conv_kernel<T, V, W, RUN>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+        hipLaunchKernelGGL((conv_kernel<T, V, W, RUN, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     }
     return hipGetLastError();
 }
@@ -155,18 +170,19 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
 // 18848 x 384 float32 takes 16.3, 15.1, 17.2 and 21.5 us in runs of 4, 8, 16 and 32 rows (1810 threads
 // a CU in runs of 4), 16384 x 4352 bfloat16 108, 77, 70 and 76 us (8700 a CU). So runs of 16 where they
 // leave every CU 1024 threads or more, else of 8.
-template <typename T, int V, int W>
+template <typename T, int W, bool ALIGNED>
 hipError_t by_run(const ConvArgs &a, bool step, hipStream_t stream) {
-    const double long_runs = static_cast<double>(a.seq.rows) / 16 * (a.channels / V);
-    return long_runs >= 256.0 * 1024.0 ? run_conv<T, V, W, 16>(a, step, stream) : run_conv<T, V, W, 8>(a, step, stream);
+    const double long_runs = static_cast<double>(a.seq.rows) / 16 * a.channels / (16 / sizeof(T));
+    return long_runs >= 256.0 * 1024.0 ? run_conv<T, W, 16, ALIGNED>(a, step, stream)
+                                       : run_conv<T, W, 8, ALIGNED>(a, step, stream);
 }
 
-template <typename T, int V>
+template <typename T, bool ALIGNED>
 hipError_t by_taps(const ConvArgs &a, bool step, hipStream_t stream) {
     switch (a.taps) {
-        case 2: return by_run<T, V, 2>(a, step, stream);
-        case 3: return by_run<T, V, 3>(a, step, stream);
-        case 4: return by_run<T, V, 4>(a, step, stream);
+        case 2: return by_run<T, 2, ALIGNED>(a, step, stream);
+        case 3: return by_run<T, 3, ALIGNED>(a, step, stream);
+        case 4: return by_run<T, 4, ALIGNED>(a, step, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -177,7 +193,7 @@ hipError_t by_alignment(const ConvArgs &a, bool step, hipStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
                            reinterpret_cast<uintptr_t>(a.state);
     const bool wide = bits % 16 == 0 && a.channels % kVec == 0 && a.x_stride % kVec == 0 && a.y_stride % kVec == 0;
-    return wide ? by_taps<T, kVec>(a, step, stream) : by_taps<T, 1>(a, step, stream);
+    return wide ? by_taps<T, true>(a, step, stream) : by_taps<T, false>(a, step, stream);
 }
 
 hipError_t by_type(const ConvArgs &a, Elem type, bool step, hipStream_t stream) {

@@ -42,17 +42,17 @@ __device__ __forceinline__ void reduce(float &sum, float &most) {
 
 // V values of y as 8-bit codes. e4m3: v_cvt_pk_fp8_f32 rounds to nearest even (OCP e4m3 on gfx950);
 // the clamp keeps a quotient that rounding left just above the top inside the range.
-template <int V, Eight E>
-__device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V], float inverse) {
+template <bool ALIGNED, int V, Eight E>
+__device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V], float inverse, int count) {
     unsigned char code[V];
     if constexpr (E == Eight::e4m3) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
             const float u = fminf(fmaxf(y[i] * inverse, -448.0f), 448.0f);
-            const float v = i + 1 < V ? fminf(fmaxf(y[i + 1 < V ? i + 1 : i] * inverse, -448.0f), 448.0f) : 0.0f;
+            const float v = fminf(fmaxf(y[i + 1] * inverse, -448.0f), 448.0f);
             const int two = __builtin_amdgcn_cvt_pk_fp8_f32(u, v, 0, false);
             code[i] = static_cast<unsigned char>(two);
-            if (i + 1 < V) code[i + 1 < V ? i + 1 : i] = static_cast<unsigned char>(two >> 8);
+            code[i + 1] = static_cast<unsigned char>(two >> 8);
         }
     } else {
 #pragma unroll
@@ -61,20 +61,18 @@ __device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V
                 static_cast<int>(rintf(fminf(fmaxf(y[i] * inverse, -127.0f), 127.0f))));
         }
     }
-    if constexpr (V == 1) {
-        p[0] = code[0];
-    } else {
-        Vec<unsigned char, V> v;
+    Vec<unsigned char, V> v;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = code[i];
-        *reinterpret_cast<Vec<unsigned char, V> *>(p) = v;
-    }
+    for (int i = 0; i < V; ++i) v[i] = code[i];
+    store_vector<ALIGNED, unsigned char, V>(p, v, count);
 }
 
-// GROUP lanes a row, BLOCKS vectors of V elements a lane in registers; BLOCKS = 0: any width, the
-// row is read again for the outputs.
-template <typename T, int V, int GROUP, int BLOCKS, Eight E>
+// GROUP lanes a row, BLOCKS vectors of 16 bytes a lane in registers; BLOCKS = 0: any width, the row is
+// read again for the outputs. ALIGNED: rows and width are multiples of a vector; else vectors lie at
+// any element and a row's last one may be short.
+template <typename T, bool ALIGNED, int GROUP, int BLOCKS, Eight E>
 __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArgs a) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
     constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
     constexpr int kRows = kThreads / GROUP;
     const int lane = threadIdx.x % GROUP;
@@ -87,11 +85,22 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
     T *y = a.y != nullptr ? static_cast<T *>(a.y) + row * a.y_stride : nullptr;
     unsigned char *q = a.q + row * a.q_stride;
 
+    auto floats = [&](const T *p, int c, float (&out)[V]) {
+        const Vec<T, V> v = load_vector<ALIGNED, T, V>(p + c, a.width - c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = static_cast<float>(v[i]);
+    };
+    auto store = [&](T *p, int c, const float (&in)[V]) {
+        Vec<T, V> v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = static_cast<T>(in[i]);
+        store_vector<ALIGNED, T, V>(p + c, v, a.width - c);
+    };
     auto load = [&](int c, float (&s)[V]) {
-        load_floats<T, V>(x + c, s);
+        floats(x, c, s);
         if (residual != nullptr) {
             float r[V];
-            load_floats<T, V>(residual + c, r);
+            floats(residual, c, r);
 #pragma unroll
             for (int i = 0; i < V; ++i) s[i] += r[i];
         }
@@ -99,7 +108,7 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
     float sum = 0.0f, most = 0.0f;
     auto measure = [&](int c, const float (&s)[V]) {
         float w[V];
-        if constexpr (E != Eight::none) load_floats<T, V>(weight + c, w);
+        if constexpr (E != Eight::none) floats(weight, c, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             sum = fmaf(s[i], s[i], sum);
@@ -123,12 +132,12 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
     };
     auto emit = [&](int c, const float (&s)[V]) {
         float w[V], out[V];
-        load_floats<T, V>(weight + c, w);
+        floats(weight, c, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = s[i] * r * w[i];
-        if (residual_out != nullptr) store_floats<T, V>(residual_out + c, s);
-        if (y != nullptr) store_floats<T, V>(y + c, out);
-        if constexpr (E != Eight::none) store_eight<V, E>(q + c, out, inverse);
+        if (residual_out != nullptr) store(residual_out, c, s);
+        if (y != nullptr) store(y, c, out);
+        if constexpr (E != Eight::none) store_eight<ALIGNED, V, E>(q + c, out, inverse, a.width - c);
     };
 
     if constexpr (BLOCKS > 0) {
@@ -167,34 +176,35 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
     }
 }
 
-template <typename T, int V, int GROUP, int BLOCKS>
+template <typename T, bool ALIGNED, int GROUP, int BLOCKS>
 hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
     constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
     constexpr int kRows = kThreads / GROUP;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.rows) + kRows - 1) / kRows));
     switch (eight) {
         case Eight::none:
-            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::none>), grid, dim3(kThreads), 0, stream, a);
+            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::none>), grid, dim3(kThreads), 0, stream, a);
             break;
         case Eight::e4m3:
-            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::e4m3>), grid, dim3(kThreads), 0, stream, a);
+            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::e4m3>), grid, dim3(kThreads), 0, stream, a);
             break;
         default:
-            hipLaunchKernelGGL((norm_kernel<T, V, GROUP, BLOCKS, Eight::int8>), grid, dim3(kThreads), 0, stream, a);
+            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::int8>), grid, dim3(kThreads), 0, stream, a);
     }
     return hipGetLastError();
 }
 
 // A wave a row while a lane needs at most four vectors (no barrier, four rows a workgroup), then a
 // workgroup of 256, then one of 1024 lanes, then the form that reads the row twice.
-template <typename T, int V>
+template <typename T, bool ALIGNED>
 hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
     const int vectors = (a.width + V - 1) / V;
-    if (vectors <= 64) return run<T, V, 64, 1>(a, eight, stream);
-    if (vectors <= 4 * 64) return run<T, V, 64, 4>(a, eight, stream);
-    if (vectors <= 4 * 256) return run<T, V, 256, 4>(a, eight, stream);
-    if (vectors <= 4 * 1024) return run<T, V, 1024, 4>(a, eight, stream);
-    return run<T, V, 1024, 0>(a, eight, stream);
+    if (vectors <= 64) return run<T, ALIGNED, 64, 1>(a, eight, stream);
+    if (vectors <= 4 * 64) return run<T, ALIGNED, 64, 4>(a, eight, stream);
+    if (vectors <= 4 * 256) return run<T, ALIGNED, 256, 4>(a, eight, stream);
+    if (vectors <= 4 * 1024) return run<T, ALIGNED, 1024, 4>(a, eight, stream);
+    return run<T, ALIGNED, 1024, 0>(a, eight, stream);
 }
 
 template <typename T>
@@ -206,7 +216,7 @@ hipError_t by_alignment(const NormArgs &a, Eight eight, hipStream_t stream) {
     const size_t strides = a.x_stride | a.residual_stride | a.residual_out_stride | a.y_stride | a.q_stride;
     const bool wide = bits % 16 == 0 && reinterpret_cast<uintptr_t>(a.q) % kVec == 0 && a.width % kVec == 0 &&
                       strides % kVec == 0;
-    return wide ? by_width<T, kVec>(a, eight, stream) : by_width<T, 1>(a, eight, stream);
+    return wide ? by_width<T, true>(a, eight, stream) : by_width<T, false>(a, eight, stream);
 }
 
 }  // namespace

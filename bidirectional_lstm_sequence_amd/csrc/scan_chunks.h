@@ -231,7 +231,7 @@ struct Operand<float> {
 
 // The rows of a chunk in memory: n rows from `base` on. WIDE: 16-byte aligned rows through a buffer
 // resource that ends with the last row, so that rows behind it read as zeros and are not written,
-// without a branch (the caller's stride keeps 64 rows below 2^31 bytes). Else element by element.
+// without a branch (the caller's stride keeps 64 rows below 2^31 bytes). Else rows of any alignment.
 template <typename T, bool WIDE>
 struct ChunkRows {
     T *base;
@@ -253,12 +253,8 @@ struct ChunkRows {
         if constexpr (WIDE) {
             return __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(t, v, live), 0, 0);
         } else {
-            Vec<T, 16 / sizeof(T)> out = {};
-            if (live && t < n) {
-#pragma unroll
-                for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) out[i] = base[t * stride + v + i];
-            }
-            return __builtin_bit_cast(u4, out);
+            if (!live || t >= n) return u4{0, 0, 0, 0};
+            return __builtin_bit_cast(u4, load_vector<false, T, 16 / sizeof(T)>(base + t * stride + v, 16 / sizeof(T)));
         }
     }
     __device__ __forceinline__ Vec<T, 4> load4(int t, int v) const {
@@ -267,12 +263,8 @@ struct ChunkRows {
         } else if constexpr (WIDE) {
             return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_raw_buffer_load_b64(rsrc, offset(t, v, true), 0, 0));
         } else {
-            Vec<T, 4> out = {};
-            if (t < n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[i] = base[t * stride + v + i];
-            }
-            return out;
+            if (t >= n) return Vec<T, 4>{};
+            return load_vector<false, T, 4>(base + t * stride + v, 4);
         }
     }
     __device__ __forceinline__ void store4(int t, int v, Vec<T, 4> value) const {
@@ -281,8 +273,7 @@ struct ChunkRows {
         } else if constexpr (WIDE) {
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, value), rsrc, offset(t, v, true), 0, 0);
         } else if (t < n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) base[t * stride + v + i] = value[i];
+            store_vector<false, T, 4>(base + t * stride + v, value, 4);
         }
     }
 };

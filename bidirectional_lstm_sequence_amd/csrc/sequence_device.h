@@ -10,6 +10,38 @@ namespace bl {
 template <typename T, int N>
 using Vec = T __attribute__((ext_vector_type(N)));
 
+// Global memory takes 16-byte accesses at any element's address; the compiler has to be told.
+template <typename T, int N>
+using AnyVec __attribute__((aligned(sizeof(T)))) = T __attribute__((ext_vector_type(N)));
+
+// The N elements at p of which `count` exist. ALIGNED: all do, at a multiple of the vector's size.
+template <bool ALIGNED, typename T, int N>
+__device__ __forceinline__ Vec<T, N> load_vector(const T *p, int count) {
+    if constexpr (ALIGNED) {
+        return *reinterpret_cast<const Vec<T, N> *>(p);
+    } else {
+        if (count >= N) return *reinterpret_cast<const AnyVec<T, N> *>(p);
+        Vec<T, N> v = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < count) v[i] = p[i];
+        return v;
+    }
+}
+
+template <bool ALIGNED, typename T, int N>
+__device__ __forceinline__ void store_vector(T *p, const Vec<T, N> &v, int count) {
+    if constexpr (ALIGNED) {
+        *reinterpret_cast<Vec<T, N> *>(p) = v;
+    } else if (count >= N) {
+        *reinterpret_cast<AnyVec<T, N> *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < count) p[i] = v[i];
+    }
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void load_floats(const T *p, float (&out)[N]) {
     if constexpr (N == 1) {
