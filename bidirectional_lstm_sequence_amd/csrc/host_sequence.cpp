@@ -266,7 +266,8 @@ bilstm_status scan_sizes(const char *call, const bilstm_scan_args *args, bool st
     if (a.states != 16 && a.states != 32 && a.states != 64 && a.states != 128 && a.states != 256) {
         return fail(BILSTM_UNSUPPORTED, "%s: %u states (16, 32, 64, 128 and 256 are built)", call, a.states);
     }
-    if (a.heads > (1u << 20) || a.rows > kMostRows || a.sequences > kMostSequences) {
+    if (static_cast<uint64_t>(a.heads) * a.width * a.states > (1u << 30) || a.rows > kMostRows ||
+        a.sequences > kMostSequences) {
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u heads exceed the kernels' indexing", call,
                     static_cast<unsigned long long>(a.rows), a.heads);
     }

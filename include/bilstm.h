@@ -382,8 +382,8 @@ void bilstm_heads_destroy(bilstm_heads *heads);
  *    behind the last sequence are not written. Values outside 0..rows are clamped.
  *  - A state cache has `places` places; slots[j] (device; NULL = j) is the place of sequence or
  *    row j. A slot outside the cache marks padding: that sequence or row is skipped, its output
- *    rows are left as they were. Two sequences of one call must not share a place: which of them
- *    is kept then is not defined. `fresh` (device, one byte a sequence; NULL = all 0): nonzero = the
+ *    rows are left as they were. Two sequences of one call must not share a place: what it holds
+ *    afterwards is then not defined. `fresh` (device, one byte a sequence; NULL = all 0): nonzero = the
  *    sequence starts from zeros, whatever its place holds. A sequence without rows leaves its
  *    place as it was.
  */
@@ -451,7 +451,7 @@ typedef struct {
     int32_t device;
     int32_t type;       /* bilstm_type of x, dt, b, c, z and y */
     uint64_t rows;      /* rows of x, dt, b, c, z and y, at most 2^31 - 1 */
-    uint32_t heads;     /* >= 1, a multiple of groups */
+    uint32_t heads;     /* >= 1, a multiple of groups; heads * width * states at most 2^30 */
     uint32_t width;     /* 32, 64 or 128 channels a head */
     uint32_t groups;    /* groups of heads that share b and c */
     uint32_t states;    /* 16, 32, 64, 128 or 256 */
@@ -464,7 +464,8 @@ typedef struct {
     bilstm_rows b;         /* [rows][groups * states] */
     bilstm_rows c;         /* [rows][groups * states] */
     bilstm_rows z;         /* [rows][heads * width], optional */
-    bilstm_buffer a;       /* float [heads] */
+    bilstm_buffer a;       /* float [heads], finite; D_t * a[h] <= 0 in earnest: a state that grows out of
+                              float32's range within 32 rows is not a number */
     bilstm_buffer d;       /* float [heads], optional */
     bilstm_buffer dt_bias; /* float [heads], optional */
     bilstm_buffer starts;  /* int32 [sequences + 1]; the step form ignores it */

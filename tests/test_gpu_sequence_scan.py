@@ -137,6 +137,30 @@ def test_far_decays(bl, dtype):
 
 
 @pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_growing_states_and_negative_steps(bl, dtype):
+    """Exponents of either sign: states that grow by powers of ten, and steps below zero."""
+    k = Case(dtype, 300, 3, 32, 1, 32, 2, 13)
+    k.a = torch.tensor([0.3, 2.0, -1.0])
+    k.dt_bias = torch.tensor([-2.0, -4.0, -1.0])
+    _run_and_check(bl, k, [0, 110, 300])
+    k = Case(dtype, 300, 3, 32, 1, 32, 2, 14)
+    k.dt = (k.dt.float() * 0.05).to(dtype)
+    k.dt_bias = torch.zeros(3)
+    _run_and_check(bl, k, [0, 110, 300], softplus=False)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_many_runs_joined(bl, dtype):
+    """More runs than the join takes at a time, behind a sequence of one run and before a padded one."""
+    k = Case(dtype, 1700, 1, 64, 1, 32, 3, 15)
+    k.a = -torch.tensor([0.05])
+    slots = k.slots.clone()
+    slots[2] = -1
+    for fresh in (True, False):
+        _run_and_check(bl, k, [0, 40, 1300, 1700], slots=slots, fresh=torch.tensor([fresh] * 3))
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
 @pytest.mark.parametrize("width, states", [(32, 16), (64, 128), (128, 256), (64, 64)])
 def test_steps_match_the_recurrence(bl, dtype, width, states):
     rows = 5

@@ -121,6 +121,7 @@ SCAN_BAD = [
     (dict(groups=3), "BILSTM_INVALID_ARGUMENT"),
     (dict(groups=0), "BILSTM_INVALID_ARGUMENT"),
     (dict(width=48), "BILSTM_UNSUPPORTED"),
+    (dict(heads=1 << 20), "BILSTM_DIMENSION_OVERFLOW"),  # 2^31 floats a state
     (dict(states=8), "BILSTM_UNSUPPORTED"),
     (dict(states=512), "BILSTM_UNSUPPORTED"),
     (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
@@ -162,6 +163,33 @@ def test_scan_step_refuses(bl):
     assert status(bl, "bilstm_scan_step", pack(form, scan_args(slots=(12 * P, 3)))) == "BILSTM_BUFFER_LENGTH"
     assert status(bl, "bilstm_scan_step", pack(form, scan_args(slots=(0, 0)))) == "BILSTM_INVALID_ARGUMENT"
     assert status(bl, "bilstm_scan_step", pack(form, scan_args(**step, width=16))) == "BILSTM_UNSUPPORTED"
+
+
+def test_scan_scratch(bl):
+    """None for whole or short sequences; else a state and a decay for every run of rows that can be."""
+    need = ctypes.c_uint64()
+    form = bl.sequence._SCAN
+
+    def scratch(**sizes):
+        f = dict(rows=4096, heads=64, width=64, groups=1, states=128, sequences=1)
+        f.update(sizes)
+        assert bl.library().bilstm_scan_scratch(pack(form, scan_args(**f)), ctypes.byref(need)) == 0
+        return need.value
+
+    state = 64 * 64 * 128 + 64
+    assert scratch() == (4096 // 256 + 1) * state * 4
+    assert scratch(rows=90) == 0 and scratch(rows=0) == 0 and scratch(sequences=0, rows=64) == 0
+    assert scratch(rows=4096, sequences=1024) == 0  # few rows a sequence
+    assert scratch(rows=16384, sequences=24) == (16384 // 512 + 24) * state * 4
+    assert scratch(rows=65536, sequences=256) == (65536 // 512 + 256) * state * 4
+    bad = pack(form, scan_args(width=7))
+    assert bl.STATUS[bl.library().bilstm_scan_scratch(bad, ctypes.byref(need))] == "BILSTM_UNSUPPORTED"
+
+
+@pytest.mark.parametrize("name", ["bilstm_causal_conv", "bilstm_causal_conv_step", "bilstm_scan", "bilstm_scan_step",
+                                  "bilstm_add_rms_norm", "bilstm_token_logprobs"])
+def test_no_arguments(bl, name):
+    assert bl.STATUS[getattr(bl.library(), name)(None, None)] == "BILSTM_INVALID_ARGUMENT"
 
 
 def norm_args(**over):
