@@ -57,7 +57,8 @@ __device__ __forceinline__ f4 mfma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_m
 __device__ __forceinline__ unsigned int round_pair(float &a, float &b) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     const b2 pair = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-    const unsigned int bits = __builtin_bit_cast(unsigned int, pair);
+    unsigned int bits = __builtin_bit_cast(unsigned int, pair);
+    asm("" : "+v"(bits));  // opaque, else the compiler rounds a a second time to widen it
     a -= __uint_as_float(bits << 16);
     b -= __uint_as_float(bits & 0xFFFF0000u);
     return bits;
