@@ -4,17 +4,22 @@
 //   y = v or v * sigmoid(v)
 //
 // 2W flops an element against 4 (16-bit) or 8 bytes: bound by memory. A thread takes 16 bytes of
-// channels (at any alignment; a row's last ones may be fewer) and a run of 8 or 16 rows of one sequence, with the
-// run's rows and the W - 1 rows before it in registers, so x is read once apart from the W - 1
-// rows at each run's start, which the neighbouring run has in the L2. All of a run's loads are
+// channels (at any alignment; a row's last ones may be fewer) and a run of 8 rows of one sequence,
+// with the run's rows and the W - 1 rows before it in registers, so x is read once apart from the
+// W - 1 rows at each run's start, which the neighbouring run has in the L2. All of a run's loads are
 // issued before the first product. The thread with a sequence's first run also writes the
 // sequence's new state: it is the only one that reads the old one, so nothing has to wait.
+//
+// Long runs read fewer rows twice, short ones put more loads in flight. In runs of 4, 8, 16 and 32 rows,
+// 4 taps: 16384 x 4352 bfloat16 67, 54, 54 and 57 us (5.3 TB/s in runs of 8), 4096 x 4352 21.1, 16.6, 19.5
+// and 23.4, 512 x 4352 5.2, 5.1, 6.9 and 10.9, 18848 x 384 float32 13.5, 12.6, 12.9 and 15.5 (4.6 TB/s).
 #include "sequence_device.h"
 
 namespace bl {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRun = 8;  // rows of a thread
 
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int count, float (&w)[V][W], float (&bias)[V]) {
@@ -35,7 +40,7 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int count, f
     }
 }
 
-template <typename T, int V, int W, int RUN, bool ALIGNED>
+template <typename T, int V, int W, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
     using X = Vec<T, V>;
     const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
@@ -44,14 +49,14 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
     const int c = static_cast<int>(id % vectors) * V;
     const int channels = a.channels - c;  // of this vector, at least V but for a row's last one
     auto load = [&](const T *p) { return load_vector<ALIGNED, T, V>(p, channels); };
-    const int j = sequence_of_run(a.seq, run, RUN);
+    const int j = sequence_of_run(a.seq, run, kRun);
     const Span span = span_of(a.seq, j);
-    const long long at = static_cast<long long>(run - run_base(a.seq, j, RUN)) * RUN;
+    const long long at = static_cast<long long>(run - run_base(a.seq, j, kRun)) * kRun;
     if (at < 0 || at >= span.length) return;
     const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
     if (place < 0) return;
     const int offset = static_cast<int>(at);
-    const int count = span.length - offset < RUN ? span.length - offset : RUN;
+    const int count = span.length - offset < kRun ? span.length - offset : kRun;
 
     const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(span.first) * a.x_stride + c;
     T *y = static_cast<T *>(a.y) + static_cast<size_t>(span.first) * a.y_stride + c;
@@ -59,9 +64,9 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
                    ? static_cast<T *>(a.state) + static_cast<size_t>(place) * (W - 1) * a.channels + c
                    : nullptr;
 
-    X rows[RUN + W - 1];  // rows offset - (W - 1) .. offset + RUN - 1
+    X rows[kRun + W - 1];  // rows offset - (W - 1) .. offset + kRun - 1
 #pragma unroll
-    for (int r = 0; r < RUN; ++r) {
+    for (int r = 0; r < kRun; ++r) {
         rows[W - 1 + r] = X{};
         if (r < count) rows[W - 1 + r] = load(x + static_cast<size_t>(offset + r) * a.x_stride);
     }
@@ -91,16 +96,16 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
     } else {
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
-            // a run starts at a multiple of RUN >= W - 1, so these rows are the sequence's own
+            // a run starts at a multiple of kRun >= W - 1, so these rows are the sequence's own
             rows[r] = load(x + static_cast<size_t>(offset - (W - 1) + r) * a.x_stride);
         }
     }
-    static_assert(RUN >= W - 1, "a run's predecessors lie in the run before it");
+    static_assert(kRun >= W - 1, "a run's predecessors lie in the run before it");
 
     float w[V][W], bias[V];
     load_taps<T, V, W>(a, c, channels, w, bias);
 #pragma unroll
-    for (int r = 0; r < RUN; ++r) {
+    for (int r = 0; r < kRun; ++r) {
         X out;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -146,13 +151,13 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigne
     store_vector<ALIGNED, T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + c, out, channels);
 }
 
-template <typename T, int W, int RUN, bool ALIGNED>
+template <typename T, int W, bool ALIGNED>
 hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     const unsigned vectors = static_cast<unsigned>((a.channels + V - 1) / V);
     const unsigned long long runs =
         step ? static_cast<unsigned long long>(a.seq.rows)
-             : static_cast<unsigned long long>(a.seq.rows) / RUN + static_cast<unsigned long long>(a.seq.sequences);
+             : static_cast<unsigned long long>(a.seq.rows) / kRun + static_cast<unsigned long long>(a.seq.sequences);
     const unsigned long long threads = runs * vectors;
     const unsigned long long blocks = (threads + kThreads - 1) / kThreads;
     if (blocks == 0) return hipSuccess;
@@ -161,28 +166,17 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     if (step) {
         hipLaunchKernelGGL((conv_step_kernel<T, V, W, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     } else {
-        hipLaunchKernelGGL((conv_kernel<T, V, W, RUN, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
+        hipLaunchKernelGGL((conv_kernel<T, V, W, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
     }
     return hipGetLastError();
-}
-
-// Long runs read fewer rows twice, short ones put more loads in flight where there is little work:
-// 18848 x 384 float32 takes 16.3, 15.1, 17.2 and 21.5 us in runs of 4, 8, 16 and 32 rows (1810 threads
-// a CU in runs of 4), 16384 x 4352 bfloat16 108, 77, 70 and 76 us (8700 a CU). So runs of 16 where they
-// leave every CU 1024 threads or more, else of 8.
-template <typename T, int W, bool ALIGNED>
-hipError_t by_run(const ConvArgs &a, bool step, hipStream_t stream) {
-    const double long_runs = static_cast<double>(a.seq.rows) / 16 * a.channels / (16 / sizeof(T));
-    return long_runs >= 256.0 * 1024.0 ? run_conv<T, W, 16, ALIGNED>(a, step, stream)
-                                       : run_conv<T, W, 8, ALIGNED>(a, step, stream);
 }
 
 template <typename T, bool ALIGNED>
 hipError_t by_taps(const ConvArgs &a, bool step, hipStream_t stream) {
     switch (a.taps) {
-        case 2: return by_run<T, 2, ALIGNED>(a, step, stream);
-        case 3: return by_run<T, 3, ALIGNED>(a, step, stream);
-        case 4: return by_run<T, 4, ALIGNED>(a, step, stream);
+        case 2: return run_conv<T, 2, ALIGNED>(a, step, stream);
+        case 3: return run_conv<T, 3, ALIGNED>(a, step, stream);
+        case 4: return run_conv<T, 4, ALIGNED>(a, step, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -192,6 +186,7 @@ hipError_t by_alignment(const ConvArgs &a, bool step, hipStream_t stream) {
     constexpr int kVec = 16 / static_cast<int>(sizeof(T));
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
                            reinterpret_cast<uintptr_t>(a.state);
+    // vectors at any element cost these 56, 18, 5.7 and 13.2 us in place of 54, 16.6, 5.1 and 12.6
     const bool wide = bits % 16 == 0 && a.channels % kVec == 0 && a.x_stride % kVec == 0 && a.y_stride % kVec == 0;
     return wide ? by_taps<T, true>(a, step, stream) : by_taps<T, false>(a, step, stream);
 }

@@ -13,8 +13,8 @@
 // left, every unmasked token is in the list, so the rest of it are the lowest tokens not in it.
 //
 // Two forms:
-//  * small vocabularies (up to kSmall): a group of 8 to 64 lanes a row, several rows a wave, the
-//    row in registers, `top` rounds of a maximum over the group;
+//  * small vocabularies (is_small): a group of 8 to 64 lanes a row, several rows a wave, the
+//    row in registers, `top` rounds of a maximum over the group and the first token that has it;
 //  * others: a workgroup takes a tile of 16384 16-bit or 8192 float32 logits into registers with
 //    16-byte loads (rows need no alignment: a row's first and last vector are read element by
 //    element). A wave finds its maximum first, so that every logit takes one exponential. A lower
@@ -34,7 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kList = 256;                    // candidates ranked by counting
 constexpr int kMostTiles = 129;               // 2^20 float32 logits and a vector's skew
-constexpr int kSmall = 1024;                  // vocabularies a group of lanes takes
+constexpr int kSmall = 1024;                  // vocabularies a group of lanes takes (is_small)
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -94,13 +94,14 @@ __device__ __forceinline__ Part moved(const Part &p, float m) {
 }
 
 // Maximum and sum over groups of lanes, 8 to 64; both lanes of a pair combine the same two numbers.
-template <int CONTROL>
-__device__ __forceinline__ float lane_pair(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CONTROL, 0xF, 0xF, true));
+template <int CONTROL, class V>
+__device__ __forceinline__ V lane_pair(V v) {
+    static_assert(sizeof(V) == 4, "a register");
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CONTROL, 0xF, 0xF, true));
 }
 
-template <int GROUP, class Op>
-__device__ __forceinline__ float over_lanes(float v, Op op) {
+template <int GROUP, class V, class Op>
+__device__ __forceinline__ V over_lanes(V v, Op op) {
     v = op(v, lane_pair<0xB1>(v));   // quad_perm 1,0,3,2
     v = op(v, lane_pair<0x4E>(v));   // quad_perm 2,3,0,1
     v = op(v, lane_pair<0x141>(v));  // row_half_mirror: the other quad of eight
@@ -251,17 +252,23 @@ __global__ __launch_bounds__(kThreads) void small_kernel(LogprobArgs a) {
     add_logits<EACH>(p, [&](int i) { return z[i]; });
     p.s = sum_over_lanes<GROUP>(p.s);
     p.w = sum_over_lanes<GROUP>(p.w);
-    Key last = ~static_cast<Key>(0);
-    for (int r = 0; r < a.top; ++r) {
-        Key best = 0;
+    if (a.top > 0) {
+        unsigned left[EACH];  // ordered bits, 0 for a masked token, one past the row or one listed
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int v = i * GROUP + lane;
-            const Key k = v < a.vocabulary ? key_of(z[i], v) : 0;
-            best = k < last && k > best ? k : best;
+        for (int i = 0; i < EACH; ++i) left[i] = masked(z[i]) ? 0 : ordered(z[i]);
+        for (int r = 0; r < a.top; ++r) {
+            unsigned best = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) best = left[i] > best ? left[i] : best;
+            best = over_lanes<GROUP>(best, [](unsigned u, unsigned v) { return u > v ? u : v; });
+            int token = 0x7FFFFFFF;
+#pragma unroll
+            for (int i = EACH - 1; i >= 0; --i) token = left[i] == best ? i * GROUP + lane : token;
+            token = over_lanes<GROUP>(token, [](int u, int v) { return u < v ? u : v; });
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) left[i] = i * GROUP + lane == token ? 0 : left[i];
+            if (lane == 0) tops[group][r] = best == 0 ? 0 : (static_cast<Key>(best) << 32) | static_cast<unsigned>(~token);
         }
-        last = most_of_lanes<GROUP>(best);
-        if (lane == 0) tops[group][r] = last;
     }
     __syncthreads();
     if (live) finish_row<T>(a, row, p, lane, GROUP, [&](int r) { return tops[group][r]; });
@@ -472,13 +479,23 @@ hipError_t run_small(const LogprobArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// A row in a wave needs no barrier and leaves few lanes idle, but its rounds go over all of a lane's
+// logits: kSmall logits, twice as many if few alternatives are asked for. A wave against a tile a row,
+// us, with 0, 5 and 32 alternatives: 4096 rows of 1000 bfloat16 5.8/26, 10.5/32.5 and 29.8/38.5; 2048 rows
+// of 2048 7.6/15.2, 12.2/19.0 and 31.6/24.5; float32 4.6/9.0, 9.8/12.5 and 29.1/18.3; 1024 rows of 4096
+// bfloat16 10.9/8.7, 18.7/11.9 and 49/16. A group as wide as the row needs: with 4 and 16 logits a lane
+// 16384 rows of 256 float32 take 15.9 and 26.5 us; 131072 rows of 32 take 20 us on 16 lanes, 46 on 32.
+bool is_small(int vocabulary, int top) { return vocabulary <= kSmall || (vocabulary <= 2 * kSmall && top <= 8); }
+
 template <typename T>
 hipError_t run(const LogprobArgs &a, hipStream_t stream) {
     if (a.vocabulary <= 8) return run_small<T, 8, 1>(a, stream);
     if (a.vocabulary <= 32) return run_small<T, 16, 2>(a, stream);
     if (a.vocabulary <= 128) return run_small<T, 32, 4>(a, stream);
     if (a.vocabulary <= 256) return run_small<T, 64, 4>(a, stream);
+    if (a.vocabulary <= 512) return run_small<T, 64, 8>(a, stream);
     if (a.vocabulary <= kSmall) return run_small<T, 64, kSmall / 64>(a, stream);
+    if (is_small(a.vocabulary, a.top)) return run_small<T, 64, kSmall / 32>(a, stream);
     const int tiles = tiles_of<T>(a.vocabulary);
     const long long blocks = static_cast<long long>(a.rows) * tiles;
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
@@ -497,7 +514,7 @@ hipError_t run(const LogprobArgs &a, hipStream_t stream) {
 
 size_t logprob_scratch_bytes(int rows, int vocabulary, int top, Elem type) {
     const int tiles = type == Elem::f32 ? tiles_of<float>(vocabulary) : tiles_of<__bf16>(vocabulary);
-    if (vocabulary <= kSmall || tiles == 1) return 0;
+    if (is_small(vocabulary, top) || tiles == 1) return 0;
     return static_cast<size_t>(rows) * tiles * part_words(top) * sizeof(Key);
 }
 

@@ -200,7 +200,6 @@ template <typename T, bool ALIGNED>
 hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     const int vectors = (a.width + V - 1) / V;
-    if (vectors <= 64) return run<T, ALIGNED, 64, 1>(a, eight, stream);
     if (vectors <= 4 * 64) return run<T, ALIGNED, 64, 4>(a, eight, stream);
     if (vectors <= 4 * 256) return run<T, ALIGNED, 256, 4>(a, eight, stream);
     if (vectors <= 4 * 1024) return run<T, ALIGNED, 1024, 4>(a, eight, stream);

@@ -98,13 +98,16 @@ hipError_t run_rows(const ScanArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// More passes keep more loads in flight and read b and c less often, fewer leave more workgroups: the
+// most that leave two workgroups a CU. Single tokens of 64 bfloat16 heads of 64 channels and 128 states
+// with 1, 2, 4 and 8 passes: 128 sequences 124, 93, 83 and 88 us, 8 sequences 11.9, 8.8, 8.0 and 8.9, one
+// 3.6, 3.7, 4.5 and 6.1; 64 of 4 float32 heads of 64 channels and 64 states 4.7, 4.3 and 4.8 with 1, 2, 4.
 template <typename T, int N>
 hipError_t by_passes(const ScanArgs &a, hipStream_t stream) {
-    constexpr int kStep = kThreads / (N / 4);
-    const int passes = (a.width + kStep - 1) / kStep;
-    if (passes >= 8) return run_rows<T, N, 8>(a, stream);
-    if (passes >= 4) return run_rows<T, N, 4>(a, stream);
-    if (passes >= 2) return run_rows<T, N, 2>(a, stream);
+    constexpr long long kStep = kThreads / (N / 4);
+    const long long most = static_cast<long long>(a.seq.sequences) * a.heads * ((a.width + kStep - 1) / kStep) / 512;
+    if (most >= 4 && a.width >= 4 * kStep) return run_rows<T, N, 4>(a, stream);
+    if (most >= 2 && a.width >= 2 * kStep) return run_rows<T, N, 2>(a, stream);
     return run_rows<T, N, 1>(a, stream);
 }
 
@@ -130,7 +133,10 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
 
 // Rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences. The lengths
 // of the sequences are on the device, so the rule goes by their sum and number.
-//  * Row by row up to kShort rows a sequence on average.
+//  * Row by row up to kShort rows a sequence on average. Row by row against in chunks, us, in sequences
+//    of 2, 4 and 8 rows: 32 of 64 bfloat16 heads of 64 channels and 128 states 37/34, 54/47 and 88/47;
+//    64 of 32 such heads of 256 states 65/81, 99/81 and 168/82; 512 of 4 float32 heads of 64 channels
+//    and 64 states 17/41, 25/47 and 40/47; 8 of 64 float16 heads of 16 states 4.3/6.8, 5.7/7.1 and 8.3/7.0.
 //  * Splitting costs the end states of most runs (the products with x and b a second time) and two
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
@@ -140,7 +146,7 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
 //    rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256, 384 and 512, 94 us whole.
 //  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {
-    constexpr long long kShort = 8, kPlaces = 512, kLeast = 96, kMost = 512;
+    constexpr long long kShort = 4, kPlaces = 512, kLeast = 96, kMost = 512;
     constexpr int kChannels = 128;  // of a workgroup
     const long long rows = a.seq.rows, sequences = a.seq.sequences;
     if (rows <= kShort * sequences) return 0;

@@ -7,8 +7,8 @@ from tests import sequence_plain as plain
 
 pytestmark = pytest.mark.gpu
 
-# groups of lanes (up to 1024), one tile, several tiles, odd sizes around their borders
-VOCABULARIES = [1, 2, 7, 8, 9, 31, 33, 129, 255, 257, 1024, 1025, 5000, 8185, 8186, 8189, 8190, 8193, 16377, 16378, 16390, 40001]
+# groups of lanes (up to 1024, up to 2048 for few alternatives), one tile, several tiles, odd sizes around their borders
+VOCABULARIES = [1, 2, 7, 8, 9, 31, 33, 129, 255, 257, 512, 513, 1024, 1025, 2048, 2049, 5000, 8185, 8186, 8189, 8190, 8193, 16377, 16378, 16390, 40001]
 
 
 @pytest.fixture(scope="module")
@@ -50,10 +50,9 @@ def test_matches_the_definition(bl, dtype, vocabulary, top):
 
 
 @pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
-@pytest.mark.parametrize("vocabulary", [7, 200, 1000, 6000, 20001])
-def test_masks(bl, dtype, vocabulary):
+@pytest.mark.parametrize("vocabulary,top", [(7, 7), (200, 20), (400, 20), (1000, 20), (1500, 8), (1500, 20), (6000, 20), (20001, 20)])
+def test_masks(bl, dtype, vocabulary, top):
     """Rows with few tokens left, with none, masks of the type's lowest value, one token, equal logits."""
-    top = min(20, vocabulary)
     logits, tokens = _logits(dtype, 8, vocabulary, 3)
     keep = torch.arange(vocabulary) % 997 == 5
     logits[0, ~keep] = float("-inf")

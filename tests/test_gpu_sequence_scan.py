@@ -179,6 +179,16 @@ def test_steps_match_the_recurrence(bl, dtype, width, states):
 
 
 @pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width,states", [(32, 64), (64, 64), (64, 128), (32, 256), (128, 32), (128, 16)])
+def test_many_sequences_of_few_rows(bl, dtype, width, states):
+    """Enough sequences that a workgroup takes several passes over the state's rows."""
+    sequences, heads = 150, 8
+    starts = _starts([(7 * j) % 6 for j in range(sequences)], before=2)
+    k = Case(dtype, starts[-1] + 3, heads, width, 2, states, sequences, 21)
+    _run_and_check(bl, k, starts)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
 def test_a_prompt_and_steps_match_one_longer_prompt(bl, dtype):
     rows, more = 90, 6
     k = Case(dtype, rows + more, 4, 64, 1, 128, 1, 8)
