@@ -131,7 +131,7 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
     }
 }
 
-// Rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences. The lengths
+// Most rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences. The lengths
 // of the sequences are on the device, so the rule goes by their sum and number.
 //  * Row by row up to kShort rows a sequence on average. Row by row against in chunks, us, in sequences
 //    of 2, 4 and 8 rows: 32 of 64 bfloat16 heads of 64 channels and 128 states 37/34, 54/47 and 88/47;
@@ -141,8 +141,8 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
 //    sequence of 4096 rows 124, 98, 84, 101, 92 and 120 us in runs of 96, 192, 256, 384, 512 and 768 rows,
-//    over 400 us whole; 24 unequal ones of 16384 rows together 350, 310, 299, 273 and 294 us in runs of
-//    192, 256, 384, 512 and 768. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589
+//    over 400 us whole; 24 unequal ones of 16384 rows together 296, 286, 266 and 273 us in runs of at
+//    most 320, 384, 512 and 640. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589
 //    rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256, 384 and 512, 94 us whole.
 //  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {

@@ -51,6 +51,15 @@ struct Parts3 {
     b8 hi, mid, lo;
 };
 
+// Rows of each run of a sequence, its last one may have fewer: as few runs as `most` rows allow, of equal
+// length, as a short rest would leave its place in the launch empty.
+__device__ __forceinline__ int rows_of_runs(int length, int most) {
+    const unsigned rows = static_cast<unsigned>(length), top = static_cast<unsigned>(most);
+    const unsigned runs = (rows + top - 1) / top;
+    const unsigned each = ((rows + runs - 1) / runs + 31) / 32 * 32;
+    return static_cast<int>(each < top ? each : top);
+}
+
 __device__ __forceinline__ f4 mfma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
 // Pairs of values in bf16 (one v_cvt_pk_bf16_f32), and what the rounding left of them.
@@ -337,11 +346,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const int j = sequence_of_run_wave(a.seq, run, run_rows);
     const Span span = span_of(a.seq, j);
     const int first_run = run_base(a.seq, j, run_rows);
-    const long long offset = static_cast<long long>(run - first_run) * run_rows;
+    if (span.length == 0) return;
+    const int each = rows_of_runs(span.length, run_rows);
+    const long long offset = static_cast<long long>(run - first_run) * each;
     if (offset < 0 || offset >= span.length) return;
     const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
     if (place < 0) return;
-    const int rows = static_cast<int>(span.length - offset < run_rows ? span.length - offset : run_rows);
+    const int rows = static_cast<int>(span.length - offset < each ? span.length - offset : each);
     const bool last = offset + rows == span.length;
     const bool first = offset == 0;
     if (!WHOLE && last) return;
@@ -724,7 +735,8 @@ inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, 
     const int j = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
     const int at = static_cast<int>(blockIdx.x % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
     const Span span = span_of(a.seq, j);
-    const int count = (span.length - 1) / run_rows;  // runs before the last one
+    if (span.length == 0) return;
+    const int count = (span.length - 1) / rows_of_runs(span.length, run_rows);  // runs before the last one
     const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
     if (at >= lanes || count < 1 || place < 0) return;
     const bool kept = a.state != nullptr && !starts_fresh(a.seq, j);
