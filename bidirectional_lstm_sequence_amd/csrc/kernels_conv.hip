@@ -13,6 +13,7 @@
 // Long runs read fewer rows twice, short ones put more loads in flight. In runs of 4, 8, 16 and 32 rows,
 // 4 taps: 16384 x 4352 bfloat16 67, 54, 54 and 57 us (5.3 TB/s in runs of 8), 4096 x 4352 21.1, 16.6, 19.5
 // and 23.4, 512 x 4352 5.2, 5.1, 6.9 and 10.9, 18848 x 384 float32 13.5, 12.6, 12.9 and 15.5 (4.6 TB/s).
+// A large copy reaches 4.8 TB/s on the same card. New rows of a few sequences are bound by the launch.
 #include "sequence_device.h"
 
 namespace bl {

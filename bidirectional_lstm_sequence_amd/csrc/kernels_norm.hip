@@ -7,6 +7,9 @@
 // squares and max|s w| come out of the same pass: max|y| = r max|s w| needs no second look at the
 // row. Rows that no register file holds (kBlocks) are read a second time for the outputs, from
 // the L2 where they fit. The sum s is not rounded to the tensor's type before it is normed.
+//
+// 8192 x 5120 bfloat16 rows with a residual to e4m3 (7 bytes an element) take 61 us, 4.8 TB/s, which is
+// what a large copy reaches; 18848 x 256 float32 rows with a residual 13.5 us, 5.7 TB/s, partly from caches.
 #include "sequence_device.h"
 
 namespace bl {
@@ -196,6 +199,10 @@ hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
 
 // A wave a row while a lane needs at most four vectors (no barrier, four rows a workgroup), then a
 // workgroup of 256, then one of 1024 lanes, then the form that reads the row twice.
+// A group of lanes as wide as its row, with four vectors a lane: a wider one idles and has to meet at
+// barriers. 20 million bfloat16 elements with a residual in groups of 64, 256 and 1024 lanes: rows of 256
+// 30, 77 and 293 us, of 1024 27, 31 and 78, of 2048 27, 26 and 42, of 8192 (256 and 1024) 26.4 and 26.4.
+// Rows of 32768 take 27.5 us out of registers and 36.5 read twice.
 template <typename T, bool ALIGNED>
 hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
@@ -213,6 +220,7 @@ hipError_t by_alignment(const NormArgs &a, Eight eight, hipStream_t stream) {
                            reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
                            reinterpret_cast<uintptr_t>(a.y);
     const size_t strides = a.x_stride | a.residual_stride | a.residual_out_stride | a.y_stride | a.q_stride;
+    // vectors at any element cost rows of 256 31 us in place of 30, of 2048 27.4 for 26.6, wider ones nothing
     const bool wide = bits % 16 == 0 && reinterpret_cast<uintptr_t>(a.q) % kVec == 0 && a.width % kVec == 0 &&
                       strides % kVec == 0;
     return wide ? by_width<T, true>(a, eight, stream) : by_width<T, false>(a, eight, stream);

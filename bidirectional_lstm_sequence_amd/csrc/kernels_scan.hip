@@ -13,7 +13,8 @@ constexpr int kThreads = 256;
 
 // A workgroup takes kThreads / (N / 4) * PASSES state rows of one head of one sequence and walks
 // over its rows, four states of a state row a lane. The single-token form is a sequence of one
-// row, bound by the state's bytes: all of a lane's state is loaded before it is used.
+// row, bound by the state's bytes: all of a lane's state is loaded before it is used. 256 sequences of
+// 64 heads of 64 channels and 128 states (1.08 GB of state moved) take 210 us, 5.1 TB/s; one takes 4 us.
 template <typename T, int N, int PASSES>
 __global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int parts) {
     constexpr int kLanes = N / 4;
