@@ -302,7 +302,7 @@ bilstm_status scan(const char *call, const bilstm_scan_args *args, bool step, vo
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: state does not fit the address space", call);
     }
     BL_CHECK(check_buffer(call, "state", a.state, state_len, 16, true));
-    const uint64_t need = step ? 0 : scan_scratch_bytes(k, elem_of(a.type));
+    const uint64_t need = step ? 0 : scan_scratch_bytes(k);
     if (need > 0) {
         BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
         if (a.scratch.len < need) {
@@ -527,7 +527,7 @@ bilstm_status bilstm_scan_scratch(const bilstm_scan_args *args, uint64_t *bytes)
     ScanArgs k;
     BL_CHECK(scan_sizes("scan_scratch", args, false, &k));
     if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "scan_scratch: bytes is NULL");
-    *bytes = scan_scratch_bytes(k, elem_of(args->type));
+    *bytes = scan_scratch_bytes(k);
     return BILSTM_OK;
 }
 

@@ -2,8 +2,12 @@
 //
 //   D_t = softplus(dt_t + bias);  S_t = exp(D_t a) S_{t-1} + D_t x_t (x) b_t;  y_t = S_t c_t + d x_t
 //
-// per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z). Two forms: row
-// by row (here: single tokens and short sequences) and in chunks of rows (scan_chunks.h).
+// per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z). Two forms:
+// single tokens (here) and packed sequences in chunks of rows (scan_chunks.h). A single row of a packed
+// sequence is a chunk of one row there: walking over a packed sequence's rows one by one takes 17 us
+// against 35 for 512 single rows of 4 float32 heads of 64 channels and 64 states, but 99 against 62 for 64
+// sequences of 4 rows of 32 bfloat16 heads of 64 channels and 256 states, and about a microsecond a row
+// for one long sequence among many short ones, which the host cannot see.
 #include "scan_device.h"
 
 namespace bl {
@@ -11,90 +15,76 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A workgroup takes kThreads / (N / 4) * PASSES state rows of one head of one sequence and walks
-// over its rows, four states of a state row a lane. The single-token form is a sequence of one
-// row, bound by the state's bytes: all of a lane's state is loaded before it is used. 256 sequences of
-// 64 heads of 64 channels and 128 states (1.08 GB of state moved) take 210 us, 5.1 TB/s; one takes 4 us.
+// One new row a sequence, bound by the state's bytes: a workgroup takes kThreads / (N / 4) * PASSES
+// state rows of one head of one sequence, four states of a state row a lane, and loads all of a lane's
+// state before it is used. 256 sequences of 64 heads of 64 channels and 128 states (1.08 GB of state
+// moved) take 210 us, 5.1 TB/s; one takes 4 us.
 template <typename T, int N, int PASSES>
-__global__ __launch_bounds__(kThreads) void scan_rows_kernel(ScanArgs a, int parts) {
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int parts) {
     constexpr int kLanes = N / 4;
     constexpr int kStep = kThreads / kLanes;  // state rows of one pass
     const int lane = threadIdx.x % kLanes;
     const int part = static_cast<int>(blockIdx.x) % parts;
     const int h = static_cast<int>(blockIdx.x) / parts % a.heads;
-    const int j = static_cast<int>(blockIdx.x) / parts / a.heads;
-    const Span span = span_of(a.seq, j);
-    if (span.length == 0) return;
-    const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
+    const int row = static_cast<int>(blockIdx.x) / parts / a.heads;
+    const int place = place_of(a.seq, row);
     if (place < 0) return;
     const int g = h / (a.heads / a.groups);
     const int p0 = part * kStep * PASSES + threadIdx.x / kLanes;
-    float *state = a.state != nullptr
-                       ? a.state + (static_cast<size_t>(place) * a.heads + h) * a.width * N + lane * 4
-                       : nullptr;
-    const bool kept = state != nullptr && !starts_fresh(a.seq, j);
+    float *state = a.state + (static_cast<size_t>(place) * a.heads + h) * a.width * N + lane * 4;
     float s[PASSES][4];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int p = p0 + i * kStep;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
-        if (kept && p < a.width) load_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
+        if (p < a.width) load_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
     }
-    const float decay = a.a[h];
     const float skip = a.d != nullptr ? a.d[h] : 0.0f;
     const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
-    for (int t = 0; t < span.length; ++t) {
-        const long long row = static_cast<long long>(span.first) + t;
-        float b[4], c[4];
-        const T *bp = static_cast<const T *>(a.b) + row * a.b_stride + g * N + lane * 4;
-        const T *cp = static_cast<const T *>(a.c) + row * a.c_stride + g * N + lane * 4;
+    float b[4], c[4];
+    const T *bp = static_cast<const T *>(a.b) + row * a.b_stride + g * N + lane * 4;
+    const T *cp = static_cast<const T *>(a.c) + row * a.c_stride + g * N + lane * 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            b[e] = static_cast<float>(bp[e]);
-            c[e] = static_cast<float>(cp[e]);
-        }
-        const float step = step_from(static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]), bias, a.softplus);
-        const float keep = expf(step * decay);
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int p = p0 + i * kStep;
-            const bool live = p < a.width;
-            const float x = live ? static_cast<float>(static_cast<const T *>(a.x)[row * a.x_stride + h * a.width + p]) : 0.0f;
-            const float in = step * x;
-            float y = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[i][e] = fmaf(s[i][e], keep, in * b[e]);
-                y = fmaf(s[i][e], c[e], y);
-            }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) y += __shfl_xor(y, o);
-            if (lane == 0 && live) {
-                y = fmaf(skip, x, y);
-                if (a.z != nullptr) {
-                    y *= silu<T>(static_cast<float>(static_cast<const T *>(a.z)[row * a.z_stride + h * a.width + p]));
-                }
-                static_cast<T *>(a.y)[row * a.y_stride + h * a.width + p] = static_cast<T>(y);
-            }
-        }
+    for (int e = 0; e < 4; ++e) {
+        b[e] = static_cast<float>(bp[e]);
+        c[e] = static_cast<float>(cp[e]);
     }
-    if (state == nullptr) return;
+    const float step = step_from(static_cast<float>(static_cast<const T *>(a.dt)[row * a.dt_stride + h]), bias, a.softplus);
+    const float keep = expf(step * a.a[h]);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int p = p0 + i * kStep;
-        if (p < a.width) store_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
+        const bool live = p < a.width;
+        const float x = live ? static_cast<float>(static_cast<const T *>(a.x)[row * a.x_stride + h * a.width + p]) : 0.0f;
+        const float in = step * x;
+        float y = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[i][e] = fmaf(s[i][e], keep, in * b[e]);
+            y = fmaf(s[i][e], c[e], y);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) y += __shfl_xor(y, o);
+        if (lane == 0 && live) {
+            y = fmaf(skip, x, y);
+            if (a.z != nullptr) {
+                y *= silu<T>(static_cast<float>(static_cast<const T *>(a.z)[row * a.z_stride + h * a.width + p]));
+            }
+            static_cast<T *>(a.y)[row * a.y_stride + h * a.width + p] = static_cast<T>(y);
+        }
+        if (live) store_floats<float, 4>(state + static_cast<size_t>(p) * N, s[i]);
     }
 }
 
 template <typename T, int N, int PASSES>
-hipError_t run_rows(const ScanArgs &a, hipStream_t stream) {
+hipError_t run_step(const ScanArgs &a, hipStream_t stream) {
     constexpr int kStep = kThreads / (N / 4) * PASSES;
     const int parts = (a.width + kStep - 1) / kStep;
     const unsigned long long blocks =
         static_cast<unsigned long long>(a.seq.sequences) * static_cast<unsigned>(a.heads) * static_cast<unsigned>(parts);
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((scan_rows_kernel<T, N, PASSES>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a,
+    hipLaunchKernelGGL((scan_step_kernel<T, N, PASSES>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a,
                        parts);
     return hipGetLastError();
 }
@@ -107,9 +97,9 @@ template <typename T, int N>
 hipError_t by_passes(const ScanArgs &a, hipStream_t stream) {
     constexpr long long kStep = kThreads / (N / 4);
     const long long most = static_cast<long long>(a.seq.sequences) * a.heads * ((a.width + kStep - 1) / kStep) / 512;
-    if (most >= 4 && a.width >= 4 * kStep) return run_rows<T, N, 4>(a, stream);
-    if (most >= 2 && a.width >= 2 * kStep) return run_rows<T, N, 2>(a, stream);
-    return run_rows<T, N, 1>(a, stream);
+    if (most >= 4 && a.width >= 4 * kStep) return run_step<T, N, 4>(a, stream);
+    if (most >= 2 && a.width >= 2 * kStep) return run_step<T, N, 2>(a, stream);
+    return run_step<T, N, 1>(a, stream);
 }
 
 template <typename T>
@@ -124,20 +114,8 @@ hipError_t by_states(const ScanArgs &a, hipStream_t stream) {
     }
 }
 
-hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
-    switch (type) {
-        case Elem::f32: return by_states<float>(a, stream);
-        case Elem::bf16: return by_states<__bf16>(a, stream);
-        default: return by_states<_Float16>(a, stream);
-    }
-}
-
-// Most rows of a run of the chunked form: 0 = row by row, more than `rows` = whole sequences. The lengths
-// of the sequences are on the device, so the rule goes by their sum and number.
-//  * Row by row up to kShort rows a sequence on average. Row by row against in chunks, us, in sequences
-//    of 2, 4 and 8 rows: 32 of 64 bfloat16 heads of 64 channels and 128 states 37/34, 54/47 and 88/47;
-//    64 of 32 such heads of 256 states 65/81, 99/81 and 168/82; 512 of 4 float32 heads of 64 channels
-//    and 64 states 17/41, 25/47 and 40/47; 8 of 64 float16 heads of 16 states 4.3/6.8, 5.7/7.1 and 8.3/7.0.
+// Most rows of a run of the chunked form; more than `rows` = whole sequences. The lengths of the sequences
+// are on the device, so the rule goes by their sum and number.
 //  * Splitting costs the end states of most runs (the products with x and b a second time) and two
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
@@ -147,10 +125,9 @@ hipError_t by_type(const ScanArgs &a, Elem type, hipStream_t stream) {
 //    rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256, 384 and 512, 94 us whole.
 //  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {
-    constexpr long long kShort = 4, kPlaces = 512, kLeast = 96, kMost = 512;
+    constexpr long long kPlaces = 512, kLeast = 96, kMost = 512;
     constexpr int kChannels = 128;  // of a workgroup
     const long long rows = a.seq.rows, sequences = a.seq.sequences;
-    if (rows <= kShort * sequences) return 0;
     const long long blocks = a.groups * ((a.heads / a.groups * static_cast<long long>(a.width) + kChannels - 1) / kChannels);
     long long run = rows * blocks / kPlaces;
     run = run < kLeast ? kLeast : (run > kMost ? kMost : run);
@@ -161,16 +138,18 @@ int run_rows_of(const ScanArgs &a) {
 
 }  // namespace
 
-size_t scan_scratch_bytes(const ScanArgs &a, Elem) {
+size_t scan_scratch_bytes(const ScanArgs &a) {
+    if (a.seq.rows == 0 || a.seq.sequences == 0) return 0;
     const int run = run_rows_of(a);
-    if (run == 0 || run > a.seq.rows) return 0;
-    const size_t parts = (static_cast<size_t>(a.seq.rows / run) + a.seq.sequences) * a.heads;
-    return parts * (static_cast<size_t>(a.width) * a.states + 1) * sizeof(float);
+    if (run > a.seq.rows) return 0;
+    // slots_of: of the later runs, of the first ones; the decays
+    const size_t blocks = static_cast<size_t>(a.seq.rows / run);
+    const size_t first = static_cast<size_t>(a.seq.sequences) <= blocks ? a.seq.sequences : blocks + 1;
+    return ((blocks + first) * a.width * a.states + blocks) * a.heads * sizeof(float);
 }
 
 hipError_t launch_scan(const ScanArgs &a, Elem type, hipStream_t stream) {
     const int run = run_rows_of(a);
-    if (run == 0) return by_type(a, type, stream);
     switch (type) {
         case Elem::f32: return launch_scan_chunks<float>(a, run, stream);
         case Elem::bf16: return launch_scan_chunks<__bf16>(a, run, stream);
@@ -178,6 +157,12 @@ hipError_t launch_scan(const ScanArgs &a, Elem type, hipStream_t stream) {
     }
 }
 
-hipError_t launch_scan_step(const ScanArgs &args, Elem type, hipStream_t stream) { return by_type(args, type, stream); }
+hipError_t launch_scan_step(const ScanArgs &a, Elem type, hipStream_t stream) {
+    switch (type) {
+        case Elem::f32: return by_states<float>(a, stream);
+        case Elem::bf16: return by_states<__bf16>(a, stream);
+        default: return by_states<_Float16>(a, stream);
+    }
+}
 
 }  // namespace bl

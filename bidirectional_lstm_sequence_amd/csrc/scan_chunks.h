@@ -22,10 +22,11 @@
 // What bounds it. With 128 bfloat16 states a chunk of a wave is 100 matrix instructions and 700 others
 // (half of them split float32 values into bf16 parts), with two waves a SIMD, as a wave's state and
 // fragments take 250 registers: vector units busy half of the time, matrix units a quarter; the rest
-// are waits for the products' results and the tail of unequal runs. 24 prompts of 16384 rows together, 64 heads of 64 channels and 128 states: 266 us (end
-// states of the runs 51, their join 26, the runs 190) where the bytes alone take 107. One prompt of 4096
-// rows 84 us (bytes 22), 32 windows of 589 float32 rows, 4 heads of 64 channels and 64 states, 53 us
-// (bytes 11): few workgroups, each a chain of dependent chunks.
+// are waits for the products' results and the tail of unequal runs. 24 prompts of 16384 rows
+// together, 64 heads of 64 channels and 128 states: 266 us (end states of the runs 51, their join 26,
+// the runs 190) where the bytes alone take 107. One prompt of 4096 rows 84 us (bytes 22), 32 windows
+// of 589 float32 rows, 4 heads of 64 channels and 64 states, 53 us (bytes 11): few workgroups, each a
+// chain of dependent chunks.
 //
 // Precision. Exponents are summed in float64 and kept as two floats, so a difference of two of
 // them carries no more than the rounding of the difference. 16-bit inputs enter products as they
@@ -66,6 +67,21 @@ __device__ __forceinline__ int rows_of_runs(int length, int most) {
     const unsigned runs = (rows + top - 1) / top;
     const unsigned each = ((rows + runs - 1) / runs + 31) / 32 * 32;
     return static_cast<int>(each < top ? each : top);
+}
+
+// Where a split sequence's runs keep their states in scratch, which is sized by the rows and not by the
+// sequences. Of a sequence that starts in block `at` of run_rows rows, run k >= 1 of n has slot
+// at + k - 1: as (n - 1) run_rows < its length, the block borders at + 1 .. at + n - 1 all lie inside the
+// sequence, so nobody else has them. Its own old state goes to slot `kept`: of split sequences, longer than
+// run_rows each, one at most starts in a block. The decay of run k stands at at + k.
+struct Slots {
+    int at, kept, count;
+};
+
+__device__ __forceinline__ Slots slots_of(const SequenceArgs &s, int j, int first, int run_rows) {
+    const int blocks = s.rows / run_rows, at = first / run_rows;
+    const bool few = s.sequences <= blocks;
+    return {at, blocks + (few ? j : at), blocks + (few ? s.sequences : blocks + 1)};
 }
 
 __device__ __forceinline__ f4 mfma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -315,8 +331,8 @@ __device__ __forceinline__ double running_sum(double v) {
     return (threadIdx.x & 16) != 0 ? v + other : v;
 }
 
-// A split sequence takes three launches. Scratch holds run r's first state, [runs][heads * width][N]
-// floats, then the log2 of its decay, [runs][heads].
+// A split sequence takes three launches. Scratch holds first states of runs, [slots][heads * width][N]
+// floats, then the log2 of their decays, [rows / run_rows][heads] (slots_of).
 //  * scan_chunk_kernel without WHOLE: the end state of every run but a sequence's last from a zero start,
 //    as the first state of the next run;
 //  * scan_join_kernel: first states from the sequence's own;
@@ -324,7 +340,7 @@ __device__ __forceinline__ double running_sum(double v) {
 //    copied: a sequence's first and last run work at the same time.
 // Sequences of one run need only the last launch.
 template <typename T, int N, int CT, bool WIDE, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int runs, int blocks) {
+__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int blocks) {
     using F = Operand<T>;
     using Rows = ChunkRows<T, WIDE>;
     constexpr int NP = N < 32 ? 32 : N;       // states, padded with zeros to a K step
@@ -351,12 +367,15 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const int quad = lane >> 4;
     const int block = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
     const int run = static_cast<int>(blockIdx.x / static_cast<unsigned>(blocks));
-    const int j = sequence_of_run_wave(a.seq, run, run_rows);
+    // end states: item `run` is the run whose first state slot `run` takes, of the sequence with the border of
+    // blocks behind it (slots_of)
+    const int j = WHOLE ? sequence_of_run_wave(a.seq, run, run_rows)
+                        : sequence_of_row_wave(a.seq, (run + 1) * run_rows - 1);
     const Span span = span_of(a.seq, j);
-    const int first_run = run_base(a.seq, j, run_rows);
     if (span.length == 0) return;
     const int each = rows_of_runs(span.length, run_rows);
-    const long long offset = static_cast<long long>(run - first_run) * each;
+    const int k = run - (WHOLE ? run_base(a.seq, j, run_rows) : span.first / run_rows);  // of the sequence
+    const long long offset = static_cast<long long>(k) * each;
     if (offset < 0 || offset >= span.length) return;
     const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
     if (place < 0) return;
@@ -381,8 +400,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const size_t state_channel = static_cast<size_t>(channel0) + wave_channel + col;
     float *cache = a.state != nullptr ? a.state + (place * all_channels + state_channel) * N + 4 * quad : nullptr;
     float *parts = static_cast<float *>(a.scratch);
-    auto part = [&](int r) { return parts + (r * all_channels + state_channel) * N + 4 * quad; };
-    float *totals = parts + runs * all_channels * N;
+    auto part = [&](int slot) { return parts + (slot * all_channels + state_channel) * N + 4 * quad; };
+    const Slots slots = slots_of(a.seq, j, span.first, run_rows);
+    float *totals = parts + slots.count * all_channels * N;
 
     f4 s[CT][kTiles];
 #pragma unroll
@@ -408,9 +428,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     };
     if (WHOLE && active) {
         if (!first) {
-            load_state(part(run));
+            load_state(part(slots.at + k - 1));
         } else if (cache != nullptr && !starts_fresh(a.seq, j)) {
-            load_state(last ? cache : part(run));
+            load_state(last ? cache : part(slots.kept));
         }
     }
 
@@ -726,10 +746,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     if constexpr (WHOLE) {
         if (last && cache != nullptr) store_state(cache);
     } else {
-        store_state(part(run + 1));
+        store_state(part(slots.at + k));
         run_total += __shfl_xor(run_total, 32);
         if (lane == 0 && (channel0 + wave_channel) % a.width == 0) {
-            totals[static_cast<size_t>(run) * a.heads + h] = static_cast<float>(run_total);
+            totals[static_cast<size_t>(slots.at + k) * a.heads + h] = static_cast<float>(run_total);
         }
     }
 }
@@ -737,31 +757,39 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
 // One lane a channel and four states of a sequence: its state, then for each run but the last
 // s = decay * s + the run's own end state, each the next run's first state. The parts of kAhead runs are on
 // their way at once. From a zero start nothing changes up to the second run.
-inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int runs, int lanes) {
+inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int lanes) {
     constexpr int kAhead = 8;
     const int each = static_cast<int>((static_cast<long long>(lanes) + kThreads - 1) / kThreads);
-    const int j = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
+    const int item = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
     const int at = static_cast<int>(blockIdx.x % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
+    // few sequences: each; else, in each block of rows, the last one that starts there: no other can be split
+    int j = item;
+    const bool few = a.seq.sequences <= a.seq.rows / run_rows;
+    if (!few) {
+        const long long end = (static_cast<long long>(item) + 1) * run_rows;
+        j = sequence_of_row_wave(a.seq, static_cast<int>(end < a.seq.rows ? end : a.seq.rows) - 1);
+    }
     const Span span = span_of(a.seq, j);
-    if (span.length == 0) return;
+    if (span.length == 0 || (!few && span.first / run_rows != item)) return;
     const int count = (span.length - 1) / rows_of_runs(span.length, run_rows);  // runs before the last one
     const int place = a.state != nullptr ? place_of(a.seq, j) : 0;
     if (at >= lanes || count < 1 || place < 0) return;
     const bool kept = a.state != nullptr && !starts_fresh(a.seq, j);
-    const int first = run_base(a.seq, j, run_rows);
+    const Slots slots = slots_of(a.seq, j, span.first, run_rows);
     const size_t run_floats = static_cast<size_t>(lanes) * 4;
-    f4 *parts = reinterpret_cast<f4 *>(static_cast<float *>(a.scratch) + first * run_floats) + at;
-    const float *totals = static_cast<const float *>(a.scratch) + runs * run_floats +
-                          static_cast<size_t>(first) * a.heads + at / (a.width * a.states / 4);
+    f4 *all = reinterpret_cast<f4 *>(a.scratch) + at;
+    f4 *parts = all + static_cast<size_t>(slots.at) * lanes;  // of the runs from the second on
+    const float *totals = static_cast<const float *>(a.scratch) + slots.count * run_floats +
+                          static_cast<size_t>(slots.at) * a.heads + at / (a.width * a.states / 4);
     f4 s = {0.f, 0.f, 0.f, 0.f};
-    if (kept) parts[0] = s = reinterpret_cast<const f4 *>(a.state + place * run_floats)[at];
+    if (kept) all[static_cast<size_t>(slots.kept) * lanes] = s = reinterpret_cast<const f4 *>(a.state + place * run_floats)[at];
     for (int r0 = 0; r0 < count; r0 += kAhead) {
         f4 own[kAhead];
         float decay[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = r0 + i < count ? r0 + i : count - 1;
-            own[i] = parts[static_cast<size_t>(r + 1) * lanes];
+            own[i] = parts[static_cast<size_t>(r) * lanes];
             decay[i] = totals[static_cast<size_t>(r) * a.heads];
         }
 #pragma unroll
@@ -771,7 +799,7 @@ inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, 
                 s = own[i];
             } else {
                 s = s * __builtin_amdgcn_exp2f(decay[i]) + own[i];
-                parts[static_cast<size_t>(r0 + i + 1) * lanes] = s;
+                parts[static_cast<size_t>(r0 + i) * lanes] = s;
             }
         }
     }
@@ -781,21 +809,22 @@ template <typename T, int N, int CT, bool WIDE>
 hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
     const int group_channels = a.heads / a.groups * a.width;
     const int blocks = a.groups * ((group_channels + 64 * CT - 1) / (64 * CT));
-    const long long runs = static_cast<long long>(a.seq.rows / run_rows) + a.seq.sequences;
+    const long long splits = a.seq.rows / run_rows, runs = splits + a.seq.sequences;
     const int lanes = a.heads * a.width * (N / 4);
-    const long long joins = static_cast<long long>(a.seq.sequences) * ((lanes + kThreads - 1) / kThreads);
+    const long long joins = (a.seq.sequences <= splits ? a.seq.sequences : splits + 1) * ((lanes + kThreads - 1) / kThreads);
     if (runs * blocks > 0x7FFFFFFFll || joins > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(runs * blocks)), threads(kThreads);
-    const int count = static_cast<int>(runs);
-    if (run_rows <= a.seq.rows) {
-        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, false>), grid, threads, 0, stream, a, run_rows, count, blocks);
+    const dim3 threads(kThreads);
+    if (splits > 0) {
+        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, false>), dim3(static_cast<unsigned>(splits * blocks)), threads, 0,
+                           stream, a, run_rows, blocks);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, count, lanes);
+        hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, lanes);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, true>), grid, threads, 0, stream, a, run_rows, count, blocks);
+    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, true>), dim3(static_cast<unsigned>(runs * blocks)), threads, 0, stream,
+                       a, run_rows, blocks);
     return hipGetLastError();
 }
 

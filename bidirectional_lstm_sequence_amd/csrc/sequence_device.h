@@ -117,20 +117,32 @@ __device__ __forceinline__ int sequence_of_run(const SequenceArgs &s, int run, i
     return low;
 }
 
-// The same for a whole wave with one run: 64 places of the table at a time, so that 64 sequences take
-// one load's time and 4096 take two.
-__device__ __forceinline__ int sequence_of_run_wave(const SequenceArgs &s, int run, int size) {
+// The last sequence that passes, for a whole wave, where no sequence passes behind one that does not: 64
+// places of the table at a time, so that 64 sequences take one load's time and 4096 take two. The
+// first one is taken to pass.
+template <class Passes>
+__device__ __forceinline__ int last_sequence_wave(const SequenceArgs &s, const Passes &passes) {
     const int lane = threadIdx.x & 63;
     int low = 0, count = s.sequences;  // the answer is in low .. low + count - 1
     while (count > 1) {
         const int step = (count + 63) / 64;
         const int at = lane * step;  // lane 0 always passes: the answer is at low or behind it
-        const bool passes = at < count && (lane == 0 || run_base(s, low + at, size) <= run);
-        const int ahead = (__popcll(__ballot(passes)) - 1) * step;
+        const bool ok = at < count && (lane == 0 || passes(low + at));
+        const int ahead = (__popcll(__ballot(ok)) - 1) * step;
         low += ahead;
         count = count - ahead < step ? count - ahead : step;
     }
     return __builtin_amdgcn_readfirstlane(low);
+}
+
+// The same as sequence_of_run for a whole wave with one run.
+__device__ __forceinline__ int sequence_of_run_wave(const SequenceArgs &s, int run, int size) {
+    return last_sequence_wave(s, [&](int j) { return run_base(s, j, size) <= run; });
+}
+
+// The sequence with this row, for a whole wave.
+__device__ __forceinline__ int sequence_of_row_wave(const SequenceArgs &s, int row) {
+    return last_sequence_wave(s, [&](int j) { return clamp_row(s.starts[j], s.rows) <= row; });
 }
 
 // The cache place of sequence j: -1 for one that is padding.

@@ -50,7 +50,7 @@ struct ScanArgs {
     void *scratch = nullptr;
 };
 
-size_t scan_scratch_bytes(const ScanArgs &args, Elem type);
+size_t scan_scratch_bytes(const ScanArgs &args);
 hipError_t launch_scan(const ScanArgs &args, Elem type, hipStream_t stream);
 hipError_t launch_scan_step(const ScanArgs &args, Elem type, hipStream_t stream);
 

@@ -181,11 +181,36 @@ def test_steps_match_the_recurrence(bl, dtype, width, states):
 @pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
 @pytest.mark.parametrize("width,states", [(32, 64), (64, 64), (64, 128), (32, 256), (128, 32), (128, 16)])
 def test_many_sequences_of_few_rows(bl, dtype, width, states):
-    """Enough sequences that a workgroup takes several passes over the state's rows."""
+    """Sequences of up to five rows, some of them empty."""
     sequences, heads = 150, 8
     starts = _starts([(7 * j) % 6 for j in range(sequences)], before=2)
     k = Case(dtype, starts[-1] + 3, heads, width, 2, states, sequences, 21)
     _run_and_check(bl, k, starts)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width,states", [(64, 64), (32, 16)])
+def test_long_sequences_among_many_short_ones(bl, dtype, width, states):
+    """More sequences than scratch has blocks of rows; two of them are split into runs."""
+    starts = _starts([1] * 150 + [700] + [0] * 100 + [1, 2] * 20 + [500, 97])
+    k = Case(dtype, starts[-1], 4, width, 2, states, len(starts) - 1, 22)
+    _run_and_check(bl, k, starts)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_a_step_of_many_sequences(bl, dtype):
+    """Enough rows that a workgroup takes several passes over a state's rows."""
+    rows, heads, width, states = 70, 8, 64, 128
+    k = Case(dtype, rows, heads, width, 2, states, rows, 23)
+    x, b, c = k.views(k.wide)
+    gx, gb, gc = k.views(k.wide.cuda())
+    state = k.state.cuda()
+    y = bl.selective_scan_step(gx, k.dt.cuda(), k.a.cuda(), gb, gc, state, d=k.d.cuda(), z=k.z.cuda(),
+                               dt_bias=k.dt_bias.cuda(), slots=k.slots.cuda())
+    ref, ref_state, bound, state_bound = plain.scan(x, k.dt, k.a, b, c, list(range(rows + 1)), k.d, k.z, k.dt_bias, True,
+                                                    k.state, k.slots.tolist(), None, torch.zeros_like(x))
+    _compare(y, ref, bound, "y")
+    _compare(state, ref_state, state_bound, "state")
 
 
 @pytest.mark.parametrize("dtype", plain.TYPES, ids=str)

@@ -166,7 +166,8 @@ def test_scan_step_refuses(bl):
 
 
 def test_scan_scratch(bl):
-    """None for whole or short sequences; else a state and a decay for every run of rows that can be."""
+    """None for whole sequences; else a state and a decay for every block of as many rows as a run has, and
+    a state for every sequence that can be split."""
     need = ctypes.c_uint64()
     form = bl.sequence._SCAN
 
@@ -176,12 +177,14 @@ def test_scan_scratch(bl):
         assert bl.library().bilstm_scan_scratch(pack(form, scan_args(**f)), ctypes.byref(need)) == 0
         return need.value
 
-    state = 64 * 64 * 128 + 64
-    assert scratch() == (4096 // 256 + 1) * state * 4
+    def bytes_of(blocks, first):
+        return ((blocks + first) * 64 * 64 * 128 + blocks * 64) * 4
+
+    assert scratch() == bytes_of(4096 // 256, 1)
     assert scratch(rows=90) == 0 and scratch(rows=0) == 0 and scratch(sequences=0, rows=64) == 0
-    assert scratch(rows=4096, sequences=1024) == 0  # few rows a sequence
-    assert scratch(rows=16384, sequences=24) == (16384 // 512 + 24) * state * 4
-    assert scratch(rows=65536, sequences=256) == (65536 // 512 + 256) * state * 4
+    assert scratch(rows=4096, sequences=1024) == bytes_of(16, 17)  # one of them may have all the rows
+    assert scratch(rows=16384, sequences=24) == bytes_of(32, 24)
+    assert scratch(rows=65536, sequences=256) == bytes_of(128, 129)
     bad = pack(form, scan_args(width=7))
     assert bl.STATUS[bl.library().bilstm_scan_scratch(bad, ctypes.byref(need))] == "BILSTM_UNSUPPORTED"
 
