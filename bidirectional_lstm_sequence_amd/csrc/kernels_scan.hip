@@ -120,12 +120,13 @@ hipError_t by_states(const ScanArgs &a, hipStream_t stream) {
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
 //    sequence of 4096 rows 124, 98, 84, 101, 92 and 120 us in runs of 96, 192, 256, 384, 512 and 768 rows,
-//    over 400 us whole; 24 unequal ones of 16384 rows together 296, 286, 266 and 273 us in runs of at
-//    most 320, 384, 512 and 640. 4 float32 heads of 64 channels and 64 states, 32 sequences of 589
-//    rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256, 384 and 512, 94 us whole.
+//    over 400 us whole; 24 unequal ones of 16384 rows together (the mean of 12 such batches) 324, 293,
+//    279, 274, 271 and 279 us in runs of at most 256, 384, 512, 640, 768 and 1024. 4 float32 heads of 64
+//    channels and 64 states, 32 sequences of 589 rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256,
+//    384 and 512, 94 us whole.
 //  * With four times as many sequences as places only a sequence of over twice the mean is split.
 int run_rows_of(const ScanArgs &a) {
-    constexpr long long kPlaces = 512, kLeast = 96, kMost = 512;
+    constexpr long long kPlaces = 512, kLeast = 96, kMost = 768;
     constexpr int kChannels = 128;  // of a workgroup
     const long long rows = a.seq.rows, sequences = a.seq.sequences;
     const long long blocks = a.groups * ((a.heads / a.groups * static_cast<long long>(a.width) + kChannels - 1) / kChannels);

@@ -183,8 +183,8 @@ def test_scan_scratch(bl):
     assert scratch() == bytes_of(4096 // 256, 1)
     assert scratch(rows=90) == 0 and scratch(rows=0) == 0 and scratch(sequences=0, rows=64) == 0
     assert scratch(rows=4096, sequences=1024) == bytes_of(16, 17)  # one of them may have all the rows
-    assert scratch(rows=16384, sequences=24) == bytes_of(32, 24)
-    assert scratch(rows=65536, sequences=256) == bytes_of(128, 129)
+    assert scratch(rows=16384, sequences=24) == bytes_of(21, 22)
+    assert scratch(rows=65536, sequences=256) == bytes_of(85, 86)
     bad = pack(form, scan_args(width=7))
     assert bl.STATUS[bl.library().bilstm_scan_scratch(bad, ctypes.byref(need))] == "BILSTM_UNSUPPORTED"
 
