@@ -2,14 +2,15 @@
 //
 //   s = x + residual;  r = 1 / sqrt(mean(s^2) + eps);  y = s r w;  scale = max|y| / top;  q = y / scale
 //
-// About 10 flops an element against 3 to 16 bytes: bound by memory. A group of lanes takes a row
-// and keeps it in registers, so every input is read once and every output written once. The sum of
-// squares and max|s w| come out of the same pass: max|y| = r max|s w| needs no second look at the
-// row. Rows that no register file holds (kBlocks) are read a second time for the outputs, from
-// the L2 where they fit. The sum s is not rounded to the tensor's type before it is normed.
+// About 20 flops an element, a division among them, against 3 to 16 bytes: bound by memory. A group of
+// lanes takes a row and keeps it in registers, so every input is read once and every output written once:
+// the sum of squares comes out of a first pass over them, y and max|y| out of a second, the codes out of
+// a third. Scales and codes are those of the float32 y itself, so max|y| has a reduction of its own. Rows
+// that no register file holds (BLOCKS = 0) are read a second time for y and in 8 bits a third, from the
+// L2 where they fit. The sum s is not rounded to the tensor's type before it is normed.
 //
-// 8192 x 5120 bfloat16 rows with a residual to e4m3 (7 bytes an element) take 61 us, 4.8 TB/s, which is
-// what a large copy reaches; 18848 x 256 float32 rows with a residual 13.5 us, 5.7 TB/s, partly from caches.
+// 8192 x 5120 bfloat16 rows with a residual to e4m3 (7 bytes an element) take 59 us, 5.0 TB/s, where a
+// large copy reaches 4.8; 18848 x 256 float32 rows with a residual 14 us, 5.5 TB/s, partly from caches.
 #include "sequence_device.h"
 
 namespace bl {
@@ -17,42 +18,34 @@ namespace {
 
 constexpr float kLeastScale = 0x1p-100f;
 
-// Sum and maximum over the lanes of a group: 64 (a wave) or a whole workgroup.
-template <int GROUP>
-__device__ __forceinline__ void reduce(float &sum, float &most) {
+// A sum or maximum over the lanes of a group: 64 (a wave) or a whole workgroup. Each CALL of a kernel has
+// its own place for the waves' parts, so none has to wait until the last one's have been read.
+template <int GROUP, int CALL, class Op>
+__device__ __forceinline__ float over_group(float v, Op op) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        sum += __shfl_xor(sum, o);
-        most = fmaxf(most, __shfl_xor(most, o));
-    }
+    for (int o = 32; o > 0; o >>= 1) v = op(v, __shfl_xor(v, o));
     if constexpr (GROUP > 64) {
-        __shared__ float sums[GROUP / 64], mosts[GROUP / 64];
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-            sums[wave] = sum;
-            mosts[wave] = most;
-        }
+        __shared__ float parts[GROUP / 64];
+        if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = v;
         __syncthreads();
-        sum = sums[0];
-        most = mosts[0];
+        v = parts[0];
 #pragma unroll
-        for (int w = 1; w < GROUP / 64; ++w) {
-            sum += sums[w];
-            most = fmaxf(most, mosts[w]);
-        }
+        for (int w = 1; w < GROUP / 64; ++w) v = op(v, parts[w]);
     }
+    return v;
 }
 
-// V values of y as 8-bit codes. e4m3: v_cvt_pk_fp8_f32 rounds to nearest even (OCP e4m3 on gfx950);
-// the clamp keeps a quotient that rounding left just above the top inside the range.
+// V values of y as 8-bit codes of the quotients y / scale, rounded to float32 as a division does.
+// e4m3: v_cvt_pk_fp8_f32 rounds to nearest even (OCP e4m3 on gfx950); the clamp keeps a quotient that
+// rounding left just above the top inside the range.
 template <bool ALIGNED, int V, Eight E>
-__device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V], float inverse, int count) {
+__device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V], float scale, int count) {
     unsigned char code[V];
     if constexpr (E == Eight::e4m3) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-            const float u = fminf(fmaxf(y[i] * inverse, -448.0f), 448.0f);
-            const float v = fminf(fmaxf(y[i + 1] * inverse, -448.0f), 448.0f);
+            const float u = fminf(fmaxf(y[i] / scale, -448.0f), 448.0f);
+            const float v = fminf(fmaxf(y[i + 1] / scale, -448.0f), 448.0f);
             const int two = __builtin_amdgcn_cvt_pk_fp8_f32(u, v, 0, false);
             code[i] = static_cast<unsigned char>(two);
             code[i + 1] = static_cast<unsigned char>(two >> 8);
@@ -61,7 +54,7 @@ __device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             code[i] = static_cast<unsigned char>(
-                static_cast<int>(rintf(fminf(fmaxf(y[i] * inverse, -127.0f), 127.0f))));
+                static_cast<int>(rintf(fminf(fmaxf(y[i] / scale, -127.0f), 127.0f))));
         }
     }
     Vec<unsigned char, V> v;
@@ -71,7 +64,7 @@ __device__ __forceinline__ void store_eight(unsigned char *p, const float (&y)[V
 }
 
 // GROUP lanes a row, BLOCKS vectors of 16 bytes a lane in registers; BLOCKS = 0: any width, the row is
-// read again for the outputs. ALIGNED: rows and width are multiples of a vector; else vectors lie at
+// read again for y and for the codes. ALIGNED: rows and width are multiples of a vector; else vectors lie at
 // any element and a row's last one may be short.
 template <typename T, bool ALIGNED, int GROUP, int BLOCKS, Eight E>
 __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArgs a) {
@@ -108,39 +101,39 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
             for (int i = 0; i < V; ++i) s[i] += r[i];
         }
     };
-    float sum = 0.0f, most = 0.0f;
-    auto measure = [&](int c, const float (&s)[V]) {
-        float w[V];
-        if constexpr (E != Eight::none) floats(weight, c, w);
+    float sum = 0.0f, r = 0.0f, most = 0.0f, scale = 1.0f;
+    auto measure = [&](const float (&s)[V]) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sum = fmaf(s[i], s[i], sum);
-            if constexpr (E != Eight::none) most = fmaxf(most, fabsf(s[i] * w[i]));
-        }
+        for (int i = 0; i < V; ++i) sum = fmaf(s[i], s[i], sum);
     };
-    float r = 0.0f, inverse = 0.0f;
     auto settle = [&] {
-        reduce<GROUP>(sum, most);
+        sum = over_group<GROUP, 0>(sum, [](float u, float v) { return u + v; });
         // correctly rounded square root and division: once a row
         r = 1.0f / sqrtf(sum / static_cast<float>(a.width) + a.eps);
+    };
+    auto norm = [&](int c, float (&s)[V]) {
+        float w[V];
+        floats(weight, c, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = s[i] * r * w[i];
+            if constexpr (E != Eight::none) most = __builtin_elementwise_maximum(most, fabsf(s[i]));  // a NaN stays
+        }
+    };
+    auto settle_scale = [&] {
         if constexpr (E != Eight::none) {
             constexpr float kTop = E == Eight::e4m3 ? 448.0f : 127.0f;
-            // a NaN or an infinity is in `sum`, where the maximum may have dropped it
-            const float top = sum < __builtin_huge_valf() ? most * r : __builtin_nanf("");
-            float scale = top == 0.0f ? 1.0f : top / kTop;
-            if (scale < kLeastScale) scale = kLeastScale;  // its reciprocal stays finite
-            inverse = 1.0f / scale;
+            most = over_group<GROUP, 1>(most, [](float u, float v) { return __builtin_elementwise_maximum(u, v); });
+            const bool number = sum < __builtin_huge_valf() && most < __builtin_huge_valf();
+            scale = most == 0.0f ? 1.0f : most / kTop;
+            if (scale < kLeastScale) scale = kLeastScale;  // quotients of it stay finite
+            if (!number) scale = __builtin_nanf("");
             if (lane == 0) a.scales[row] = scale;
         }
     };
-    auto emit = [&](int c, const float (&s)[V]) {
-        float w[V], out[V];
-        floats(weight, c, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = s[i] * r * w[i];
-        if (residual_out != nullptr) store(residual_out, c, s);
-        if (y != nullptr) store(y, c, out);
-        if constexpr (E != Eight::none) store_eight<ALIGNED, V, E>(q + c, out, inverse, a.width - c);
+    auto emit = [&](int c, const float (&y_row)[V]) {
+        if (y != nullptr) store(y, c, y_row);
+        if constexpr (E != Eight::none) store_eight<ALIGNED, V, E>(q + c, y_row, scale, a.width - c);
     };
 
     if constexpr (BLOCKS > 0) {
@@ -153,27 +146,44 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
             if (c < a.width) load(c, s[b]);
         }
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-            const int c = (b * GROUP + lane) * V;
-            if (c < a.width) measure(c, s[b]);
-        }
+        for (int b = 0; b < BLOCKS; ++b) measure(s[b]);
         settle();
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
             const int c = (b * GROUP + lane) * V;
-            if (c < a.width) emit(c, s[b]);
+            if (c >= a.width) continue;
+            if (residual_out != nullptr) store(residual_out, c, s[b]);
+            norm(c, s[b]);
+            if constexpr (E == Eight::none) emit(c, s[b]);
+        }
+        if constexpr (E != Eight::none) {
+            settle_scale();
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int c = (b * GROUP + lane) * V;
+                if (c < a.width) emit(c, s[b]);
+            }
         }
     } else {
-        // outputs may be the inputs' own memory: nothing is written before a lane's second look,
+        // outputs may be the inputs' own memory: nothing is written before a lane's last look,
         // and a lane reads only what it writes itself
         float s[V];
         for (int c = lane * V; c < a.width; c += GROUP * V) {
             load(c, s);
-            measure(c, s);
+            measure(s);
         }
         settle();
+        if constexpr (E != Eight::none) {
+            for (int c = lane * V; c < a.width; c += GROUP * V) {
+                load(c, s);
+                norm(c, s);
+            }
+            settle_scale();
+        }
         for (int c = lane * V; c < a.width; c += GROUP * V) {
             load(c, s);
+            if (residual_out != nullptr) store(residual_out, c, s);
+            norm(c, s);
             emit(c, s);
         }
     }
@@ -198,11 +208,11 @@ hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
 }
 
 // A wave a row while a lane needs at most four vectors (no barrier, four rows a workgroup), then a
-// workgroup of 256, then one of 1024 lanes, then the form that reads the row twice.
+// workgroup of 256, then one of 1024 lanes, then the form that reads the row again.
 // A group of lanes as wide as its row, with four vectors a lane: a wider one idles and has to meet at
 // barriers. 20 million bfloat16 elements with a residual in groups of 64, 256 and 1024 lanes: rows of 256
 // 30, 77 and 293 us, of 1024 27, 31 and 78, of 2048 27, 26 and 42, of 8192 (256 and 1024) 26.4 and 26.4.
-// Rows of 32768 take 27.5 us out of registers and 36.5 read twice.
+// Rows of 32768 take 27.5 us out of registers and 36.5 read twice; 512 rows of 40000 to e4m3, read three times, 46.
 template <typename T, bool ALIGNED>
 hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));

@@ -493,9 +493,10 @@ bilstm_status bilstm_scan_step(const bilstm_scan_args *args, void *stream);
  *   s = x + residual (x alone without a residual), kept in float32 for what follows
  *   residual_out = s;  y = s / sqrt(mean(s^2) + eps) * weight
  *   scale = max|y| / 448 (e4m3) or / 127 (int8), at least 2^-100, and 1 where y is all zeros;
- *   q = y / scale, rounded to nearest, ties to even
- * A row with a NaN or an infinity, or whose sum of squares leaves float32's range, gets what the
- * formulas give for y in float32, and a NaN scale.
+ *   q = y / scale, rounded to nearest, ties to even; both from y in float32, before the rounding to
+ *   its type, and the quotients in float32
+ * A row with a NaN or an infinity in x, residual or y (a weight may bring one), or whose sum of squares
+ * passes float32's largest number, gets what the formulas give for y in float32, and a NaN scale.
  */
 typedef enum {
     BILSTM_EIGHT_NONE = 0,

@@ -151,3 +151,36 @@ def test_the_binding_refuses_what_the_operators_do_not_take(bl):
             call()
     with torch.no_grad():
         assert bl.add_rms_norm(x, w.clone().requires_grad_()).y.shape == x.shape
+
+
+CODES = {"e4m3": (448.0, lambda v: v.clamp(-448.0, 448.0).to(torch.float8_e4m3fn)),
+         "int8": (127.0, lambda v: torch.round(v).clamp(-127.0, 127.0).to(torch.int8))}
+
+
+@pytest.mark.parametrize("width", [64, 1000, 2048, 4097, 20000])
+@pytest.mark.parametrize("eight", ["e4m3", "int8"])
+def test_codes_are_those_of_the_quotients(bl, width, eight):
+    """The scale is max|y| / top and a code the nearest to y / scale, in float32 as y is: bit for bit, in every
+    form of the kernel. A row has about 2^-18 values a code's rounding tells apart in the quotient's last bit."""
+    rows = (1 << 21) // width
+    x, r, w = _inputs(torch.float32, rows, width, 31)
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), eight_bit=eight, keep_y=True)
+    top, code = CODES[eight]
+    y, scales = got.y.cpu(), got.scales.cpu()
+    assert torch.equal(scales, y.abs().amax(1) / top)
+    expect = code(y / scales[:, None])
+    assert torch.equal(got.q.cpu().view(torch.uint8), expect.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width", [96, 3000, 40000])
+@pytest.mark.parametrize("eight", ["e4m3", "int8"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_weights_that_are_not_numbers(bl, dtype, width, eight, bad):
+    """What is not a number in y makes the row's scale none, wherever it came from."""
+    x, _, w = _inputs(dtype, 3, width, 32)
+    x[1, 7] = 0.0
+    w[7] = bad
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), eight_bit=eight, keep_y=True)
+    assert torch.isnan(got.scales).all()
+    assert not torch.isfinite(got.y[:, 7]).any() and torch.isfinite(got.y[:, 8:]).all()
