@@ -426,6 +426,7 @@ bilstm_status norm(const char *call, const bilstm_norm_args *args, void *stream)
     k.q_stride = eight ? a.q.stride : 0;
     k.rows = static_cast<int>(a.rows);
     k.width = static_cast<int>(a.width);
+    k.inverse_width = 1.0 / a.width;
     k.eps = a.eps;
     DeviceScope scope(a.device);
     BL_CHECK(scope.enter(call));

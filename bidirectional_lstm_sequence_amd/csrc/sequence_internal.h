@@ -64,6 +64,7 @@ struct NormArgs {
     size_t x_stride = 0, residual_stride = 0, residual_out_stride = 0, y_stride = 0, q_stride = 0;
     int rows = 0;
     int width = 0;
+    double inverse_width = 0.0;
     float eps = 0.0f;
 };
 

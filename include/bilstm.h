@@ -491,7 +491,7 @@ bilstm_status bilstm_scan_step(const bilstm_scan_args *args, void *stream);
 /*
  * Root-mean-square norm of each row with the residual's addition, and an output in 8 bits:
  *   s = x + residual (x alone without a residual), kept in float32 for what follows
- *   residual_out = s;  y = s / sqrt(mean(s^2) + eps) * weight
+ *   residual_out = s;  y = s / sqrt(mean(s^2) + eps) * weight, zeros for a row of zeros without an eps
  *   scale = max|y| / 448 (e4m3) or / 127 (int8), at least 2^-100, and 1 where y is all zeros;
  *   q = y / scale, rounded to nearest, ties to even; both from y in float32, before the rounding to
  *   its type, and the quotients in float32

@@ -184,3 +184,37 @@ def test_weights_that_are_not_numbers(bl, dtype, width, eight, bad):
     got = bl.add_rms_norm(x.cuda(), w.cuda(), eight_bit=eight, keep_y=True)
     assert torch.isnan(got.scales).all()
     assert not torch.isfinite(got.y[:, 7]).any() and torch.isfinite(got.y[:, 8:]).all()
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("width", [1, 96, 3000, 9000, 40000])
+@pytest.mark.parametrize("eight", [None, "e4m3", "int8"])
+@pytest.mark.parametrize("eps", [0.0, 1e-42])
+def test_tiny_rows_without_eps(bl, dtype, width, eight, eps):
+    """Squares below float32's range, down to its smallest number, and rows of zeros. plain.norm's bound holds
+    for them as for any row: sums of squares of values times a power of two round as others do."""
+    x, _, w = _inputs(dtype, 6, width, 33)
+    x[0] = 0.0
+    small = [1e-18, 1e-25, 1e-38, 1e-44] if dtype != torch.float16 else [1e-2, 1e-3, 1e-5, 6e-8]
+    for i, size in enumerate(small):
+        x[1 + i] = (torch.sign(x[1 + i].float()) * (0.5 + torch.rand(width, generator=torch.Generator().manual_seed(i))) * size).to(dtype)
+        if not x[1 + i].any():
+            x[1 + i] = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    eps = float(torch.tensor(eps, dtype=torch.float32))  # what the call gets
+    got = bl.add_rms_norm(x.cuda(), w.cuda(), eps, eight_bit=eight, keep_y=True)
+    rest = bl.NormResult(got.y[1:], None if eight is None else got.q[1:], None if eight is None else got.scales[1:], None)
+    _check(rest, x[1:], None, w, eps, eight)
+    assert not got.y[0].any()
+    if eight:
+        assert got.scales[0].item() == 1.0 and not got.q[0].float().any()
+
+
+def test_tiny_rows_in_place(bl):
+    """The sum with a residual comes back unchanged from rows that are looked at a second time."""
+    for width in (96, 3000, 9000, 40000):
+        x, r, w = _inputs(torch.float32, 4, width, 34)
+        x, r = x * 1e-30, r * 1e-30
+        xg, rg = x.cuda(), r.cuda()
+        apart = bl.add_rms_norm(x.cuda(), w.cuda(), 0.0, residual=r.cuda())
+        bl.add_rms_norm(xg, w.cuda(), 0.0, residual=rg, out=rg, residual_out=xg)
+        assert torch.equal(xg.cpu(), x + r) and torch.equal(rg, apart.y) and torch.equal(apart.residual, xg)
