@@ -65,18 +65,21 @@ __device__ __forceinline__ void store_floats(T *p, const float (&in)[N]) {
     }
 }
 
-// v * sigmoid(v) on v_exp_f32 and v_rcp_f32 (1 ulp each). For 32-bit tensors the exponent's rounding
-// is carried along: t + rest = -v log2 e, e^-v = 2^t (1 + rest ln 2). For 16-bit ones it is dropped:
-// |v| 2^-24 of the value, far inside the output's rounding.
-template <typename T>
-__device__ __forceinline__ float silu(float v) {
+// e^-v on v_exp_f32 (1 ulp; 0 below float32's normal range) with its exponent's rounding carried along:
+// t + rest = -v log2 e, e^-v = 2^t (1 + rest ln 2). Where 2^t is 0 or infinite, rest may be neither.
+__device__ __forceinline__ float exp_of_minus(float v) {
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911266175e-8f, kLn2 = 0.6931471805599453f;
     const float t = -kLog2e * v;
-    float e = __builtin_amdgcn_exp2f(t);
-    if constexpr (sizeof(T) == 4) {
-        const float rest = fmaf(-kLog2e, v, -t) - kLog2eLow * v;
-        e = e < __builtin_huge_valf() ? fmaf(e, rest * kLn2, e) : e;
-    }
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float rest = fmaf(-kLog2e, v, -t) - kLog2eLow * v;
+    return e > 0.0f && e < __builtin_huge_valf() ? fmaf(e, rest * kLn2, e) : e;
+}
+
+// v * sigmoid(v), with v_rcp_f32 (1 ulp). For 16-bit tensors the exponent's rounding is dropped: |v| 2^-24
+// of the value, far inside the output's rounding. A sigmoid below 2^-126, v < -87, counts as 0.
+template <typename T>
+__device__ __forceinline__ float silu(float v) {
+    const float e = sizeof(T) == 4 ? exp_of_minus(v) : __builtin_amdgcn_exp2f(-1.4426950408889634f * v);
     return v * __builtin_amdgcn_rcpf(1.0f + e);
 }
 

@@ -370,7 +370,8 @@ void bilstm_heads_destroy(bilstm_heads *heads);
  *    the same after the call as before it.
  *  - `type` is the element type of the tensors that are not said to be float or integers. Sums,
  *    states of the scan and statistics are held in float32 (logarithms of decays in more);
- *    outputs are rounded once.
+ *    outputs are rounded once. A sigmoid or an exponential below float32's normal range, 2^-126, may
+ *    count as 0.
  *  - Matrices of rows come with a row stride in elements (>= the row's width): element (i, j) is
  *    data[i * stride + j]. `len` is the number of elements from `data` on that belong to the
  *    buffer; it must hold (rows - 1) * stride + width elements (BILSTM_BUFFER_LENGTH). Buffers

@@ -162,3 +162,39 @@ def test_own_stream_and_captured_graph(bl):
         assert torch.equal(y, expect[k])
         x.mul_(1.0)
     assert torch.equal(s, expect_state)
+
+
+# values where a sigmoid's exponential leaves float32's range on either side, and what is not a number
+GATE_VALUES = [0.0, -0.0, 1e-30, -1e-30, 1.0, -1.0, 20.0, -20.0, 60.0, -60.0, 86.0, -86.0, 88.0, -88.0, 90.0, -90.0, -100.0,
+               -104.0, 127.0, -127.0, 1e4, -1e4, 6e4, -6e4, 1e30, -1e30, 2.3e38, 2.4e38, -2.4e38, 3e38, -3e38, float("inf"),
+               float("-inf"), float("nan")]
+
+
+def _check_gate(got, v):
+    """``got`` is v * sigmoid(v), with a bound of plain.conv's: the exponential's rounded argument, itself and the
+    reciprocal, the sum and the product. A sigmoid below float32's normal range may count as zero."""
+    got, dtype = got.cpu(), v.dtype
+    x = v.double()
+    expect = torch.where(x == float("-inf"), float("nan"), x * plain.sigmoid(x))
+    fine = torch.isfinite(expect)
+    assert torch.equal(torch.isnan(got), torch.isnan(expect)), (got, expect)
+    assert torch.equal(got[~fine & ~torch.isnan(expect)].double(), expect[~fine & ~torch.isnan(expect)])
+    error = torch.where(fine, (6 + x.abs().clamp(max=1e3)) * plain.U32 * expect.abs() + x.abs().clamp(max=1e3) * 2.0 ** -126, 0.0)
+    off = (got.double() - expect).abs()
+    assert (off[fine] <= plain.rounded(expect, error, dtype)[fine]).all(), (v[fine], got[fine], expect[fine])
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("step", [False, True])
+def test_gate_of_any_value(bl, dtype, step):
+    """One tap of 1, so that the gate gets x itself: infinities, values near the type's largest, far negative ones."""
+    v = torch.tensor(GATE_VALUES).to(dtype)
+    x = v[:, None].repeat(1, 24).contiguous()
+    weight = torch.zeros(24, 2, dtype=dtype)
+    weight[:, 1] = 1.0
+    rows = x.shape[0]
+    if step:
+        y = bl.causal_conv_step(x.cuda(), weight.cuda(), torch.zeros(rows, 1, 24, dtype=dtype, device="cuda"))
+    else:
+        y = bl.causal_conv(x.cuda(), weight.cuda(), torch.arange(rows + 1, dtype=torch.int32, device="cuda"))
+    _check_gate(y, x)

@@ -300,3 +300,22 @@ def test_captured_graph_stream_and_repeated_calls(bl):
         assert torch.equal(y, expect[i])
         torch.zeros(1000, device="cuda").sum().item()
     assert torch.equal(state, eager)
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("step", [False, True])
+def test_gates_of_any_value(bl, dtype, step):
+    """y = d x = 1 before the gate: z * sigmoid(z) itself."""
+    from tests.test_gpu_sequence_conv import GATE_VALUES, _check_gate
+    v = torch.tensor(GATE_VALUES).to(dtype)
+    rows = v.shape[0]
+    one = lambda *s: torch.ones(*s, dtype=dtype, device="cuda")  # noqa: E731
+    z = v[:, None, None].repeat(1, 2, 32).contiguous()
+    b, a, d = torch.zeros(rows, 1, 16, dtype=dtype, device="cuda"), -torch.ones(2, device="cuda"), torch.ones(2, device="cuda")
+    if step:
+        y = bl.selective_scan_step(one(rows, 2, 32), one(rows, 2), a, b, b, torch.zeros(rows, 2, 32, 16, device="cuda"), d=d,
+                                   z=z.cuda())
+    else:
+        y = bl.selective_scan(one(rows, 2, 32), one(rows, 2), a, b, b, torch.tensor([0, rows], dtype=torch.int32).cuda(), d=d,
+                              z=z.cuda())
+    _check_gate(y, z)
