@@ -22,8 +22,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRun = 8;  // rows of a thread
 
+// channels: left of the row from c on, of which this vector takes at most V.
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int count, float (&w)[V][W], float (&bias)[V]) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int channels, float (&w)[V][W], float (&bias)[V]) {
+    const int count = channels < V ? channels : V;
     const T *wp = static_cast<const T *>(a.weight) + static_cast<size_t>(c) * W;
     Vec<T, V> raw[W];  // the channels' taps as they lie, W after W
 #pragma unroll
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigne
 template <typename T, int W, bool ALIGNED>
 hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    const unsigned vectors = static_cast<unsigned>((a.channels + V - 1) / V);
+    const unsigned vectors = (static_cast<unsigned>(a.channels) + V - 1) / V;
     const unsigned long long runs =
         step ? static_cast<unsigned long long>(a.seq.rows)
              : static_cast<unsigned long long>(a.seq.rows) / kRun + static_cast<unsigned long long>(a.seq.sequences);

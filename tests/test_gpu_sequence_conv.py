@@ -198,3 +198,22 @@ def test_gate_of_any_value(bl, dtype, step):
     else:
         y = bl.causal_conv(x.cuda(), weight.cuda(), torch.arange(rows + 1, dtype=torch.int32, device="cuda"))
     _check_gate(y, x)
+
+
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("channels, taps", [((1 << 29) + 13, 4), ((1 << 31) - 1, 2)])
+def test_channels_whose_taps_pass_32_bits(bl, step, channels, taps):
+    """A row's number of taps, and of vectors of channels, beyond 31 bits, up to the most channels there are.
+    Looked at where they would wrap and at both ends."""
+    g = torch.Generator(device="cuda").manual_seed(41)
+    make = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    x, weight, state = make(2, channels), make(channels, taps), make(2, taps - 1, channels)
+    at = torch.cat([torch.arange(0, 40), torch.arange((1 << 28) - 20, (1 << 28) + 20), torch.arange(channels - 40, channels)])
+    on = at.cuda()
+    few = (x[:, on].cpu(), weight[on].cpu(), state[:, :, on].cpu())
+    if step:
+        y = bl.causal_conv_step(x, weight, state)
+    else:
+        y = bl.causal_conv(x, weight, torch.tensor([0, 1, 2], dtype=torch.int32).cuda(), state=state)
+    ref, ref_state, bound = plain.conv(few[0], few[1], [0, 1, 2], None, few[2], None, None, True, torch.zeros_like(few[0]))
+    _compare(y[:, on], state[:, :, on], ref, ref_state, bound)
