@@ -331,6 +331,12 @@ __device__ __forceinline__ double running_sum(double v) {
     return (threadIdx.x & 16) != 0 ? v + other : v;
 }
 
+// A lane's value for the whole wave.
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const int2 w = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(w.x, lane), __builtin_amdgcn_readlane(w.y, lane)));
+}
+
 // A split sequence takes three launches. Scratch holds first states of runs, [slots][heads * width][N]
 // floats, then the log2 of their decays, [rows / run_rows][heads] (slots_of).
 //  * scan_chunk_kernel without WHOLE: the end state of every run but a sequence's last from a zero start,
@@ -486,18 +492,26 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const double exponent = static_cast<double>(a.a[h]) * 1.4426950408889634074;
     double run_total = 0.0;
     // log2 of the decay over a chunk: lanes 0..31 of the even one, 32..63 of the odd one
-    float totals_now = 0.0f, totals_next = 0.0f;
+    double totals_now = 0.0, totals_next = 0.0;
     // The state is held without the decay of the last chunks, 2^scale, until that leaves 2^-20..2^20:
-    // its registers are then multiplied once for several chunks.
-    float scale = 0.0f;
+    // its registers are then multiplied once for several chunks. The chunks' exponents are summed in 64
+    // bits: a float32 sum of up to 20 would round each of them to 2^-20, always the same way where dt is constant.
+    double scale = 0.0;
+    float scale_hi = 0.0f, scale_rest = 0.0f;  // 2^scale = 2^scale_hi (1 + scale_rest)
+    auto part_scale = [&] {
+        scale_hi = static_cast<float>(scale);
+        scale_rest = static_cast<float>(scale - static_cast<double>(scale_hi)) * 0.6931471805599453f;
+    };
     auto settle_scale = [&] {
-        const float by = __builtin_amdgcn_exp2f(scale);
+        float by = __builtin_amdgcn_exp2f(scale_hi);
+        if (fabsf(scale_hi) < 150.0f) by = fmaf(by, scale_rest, by);  // else 0 or infinite, with no rest to speak of
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) s[ct][i] *= by;
         }
-        scale = 0.0f;
+        scale = 0.0;
+        scale_hi = scale_rest = 0.0f;
     };
     // steps and decays of the two chunks whose dt came last; a row behind the end has step 0 and decay 1
     auto decays = [&](int chunk) {
@@ -512,7 +526,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         table[6 * L + lane] = __builtin_amdgcn_exp2f(hi);
         table[8 * L + lane] = step * __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
         run_total += total;  // lane 0: of even chunks, lane 32: of odd ones
-        return static_cast<float>(total);
+        return total;
     };
 
     fetch(0);
@@ -541,11 +555,18 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
         if (!active) continue;
         const float *cum_hi = &decay_tables[wave][chunk >> 1 & 1][0][0] + (chunk & 1) * L, *cum_lo = cum_hi + 2 * L,
                     *steps = cum_hi + 4 * L, *since = cum_hi + 6 * L, *to_end = cum_hi + 8 * L;
-        const float total = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(totals_now), (chunk & 1) * 32));
+        const double total = lane_of(totals_now, (chunk & 1) * 32);
         const size_t t0 = static_cast<size_t>(chunk) * L;
         Vec<T, 4> z[2][CT];
         f4 y[2][CT], gram[3];  // blocks (s, t) = (0, 0), (0, 1), (1, 1)
-        const float state_decay = __builtin_amdgcn_exp2f(scale);
+        float state_decay = __builtin_amdgcn_exp2f(scale_hi);
+        state_decay = fmaf(state_decay, scale_rest, state_decay);
+        // behind the chunk; long before its use, as it is a chain of dependent instructions
+        scale += total;
+        part_scale();
+        const bool settles = !(fabsf(scale_hi) < 20.0f);
+        float unscaled = __builtin_amdgcn_exp2f(-scale_hi);
+        unscaled = fmaf(unscaled, -scale_rest, unscaled);
         if (gated) {
             const Rows z_rows(zg + t0 * a.z_stride, a.z_stride, n, live_channels);
 #pragma unroll
@@ -628,8 +649,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                 for (int ct = 0; ct < CT; ++ct) y[tb][ct] *= decay;
             }
         }
-        scale += total;
-        if (!(fabsf(scale) < 20.0f)) settle_scale();
+        if (settles) {
+            settle_scale();
+            unscaled = 1.0f;
+        }
         __builtin_amdgcn_sched_barrier(0);  // the registers do not hold more at once
         // 2. the state behind the chunk
         typename F::In x[CT];
@@ -640,7 +663,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
             float weight[2][4];
             load_floats<float, 4>(to_end + 4 * quad, weight[0]);
             load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
-            const float unscaled = __builtin_amdgcn_exp2f(-scale);
 #pragma unroll
             for (int e = 0; e < 8; ++e) weight[e >> 2][e & 3] *= unscaled;
 #pragma unroll

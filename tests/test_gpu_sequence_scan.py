@@ -338,3 +338,26 @@ def test_steps_are_as_exact_as_float32_holds(bl, packed):
     expect = torch.nn.functional.softplus(v.double(), threshold=1000)
     off = (got - expect).abs() / expect
     assert (off <= 6 * plain.U32).all(), (off.max(), v[off.argmax()])
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+def test_decays_of_many_chunks(bl, dtype):
+    """A state that nothing is added to, over 256 chunks of one run: S exp(8192 D a). Each chunk's exponent comes
+    from 64 bits; the state is multiplied by a power of two at most three times, of an exponent of at most 20 a
+    time: an exponential of 1 ulp, what its argument's rounding left and the product, 5 half steps of float32."""
+    heads, states, sequences, length = 64, 16, 32, 8192
+    rest = length // 2 * sequences + 32 - length
+    starts = _starts([length] + [rest // (sequences - 1)] * (sequences - 1))
+    rows = starts[-1]
+    g = torch.Generator().manual_seed(63)
+    a = -(torch.rand(heads, generator=g) * 0.06 + 0.012)
+    zeros = lambda *s: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    bc = zeros(rows, heads, states).fill_(1.0)
+    state = torch.randn(sequences, heads, 32, states, generator=g)
+    got = state.cuda()
+    bl.selective_scan(zeros(rows, heads, 32), zeros(rows, heads).fill_(2.0 ** -5), a.cuda(), bc, bc,
+                      torch.tensor(starts, dtype=torch.int32).cuda(), softplus=False, state=got)
+    for j in range(sequences):
+        expect = state[j].double() * torch.exp((starts[j + 1] - starts[j]) * 2.0 ** -5 * a.double())[:, None, None]
+        off = (got[j].cpu().double() - expect).abs() / expect.abs()
+        assert (off <= 15 * plain.U32).all(), (j, off.max())
