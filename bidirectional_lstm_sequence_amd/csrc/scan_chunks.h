@@ -134,7 +134,7 @@ __device__ __forceinline__ constexpr int place_of_row(int t) {
 
 // Operands of the products for one input type: fragments of 8 values of K for row (or column)
 // lane % 16, K = 16 e + 4 (lane / 16) + r in place 4 e + r. In: values of an input tensor; Made: float32
-// values on their way to an output; Kept: to the state. A product is a sum of terms, a matrix
+// values. A product is a sum of terms, a matrix
 // instruction each; callers take one term of several products before the next, as instructions on one
 // accumulator wait for each other.
 template <typename T>
@@ -157,8 +157,7 @@ __device__ __forceinline__ Vec<T, 8> column_values(const T *p, int stride, int l
 template <>
 struct Operand<__bf16> {
     typedef b8 In;
-    typedef Parts Made;
-    typedef Parts3 Kept;
+    typedef Parts3 Made;
     static __device__ __forceinline__ In rows(const __bf16 *p) { return row_values(p); }
     static __device__ __forceinline__ In columns(const __bf16 *p, int stride, int lane) {
         return column_values(p, stride, lane);
@@ -168,26 +167,18 @@ struct Operand<__bf16> {
         a[j] = static_cast<__bf16>(0.0f);
         return a;
     }
-    static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
-    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
-    static constexpr int kInTerms = 1, kMadeTerms = 2, kKeptTerms = 3;
+    static __device__ __forceinline__ Made make(float (&v)[8]) { return split3(v); }
+    static constexpr int kInTerms = 1, kMadeTerms = 3;
     static __device__ __forceinline__ f4 in_term(int, const In &a, const In &b, f4 c) { return mfma(a, b, c); }
-    static __device__ __forceinline__ f4 made_term(int k, const Made &a, const In &b, f4 c) {
-        return mfma(k == 0 ? a.lo : a.hi, b, c);
-    }
-    static __device__ __forceinline__ f4 made_term(int k, const In &a, const Made &b, f4 c) {
-        return mfma(a, k == 0 ? b.lo : b.hi, c);
-    }
-    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const Kept &b, f4 c) {
-        return mfma(a, k == 0 ? b.lo : (k == 1 ? b.mid : b.hi), c);
-    }
+    static __device__ __forceinline__ const b8 &part(int k, const Made &a) { return k == 0 ? a.lo : (k == 1 ? a.mid : a.hi); }
+    static __device__ __forceinline__ f4 made_term(int k, const Made &a, const In &b, f4 c) { return mfma(part(k, a), b, c); }
+    static __device__ __forceinline__ f4 made_term(int k, const In &a, const Made &b, f4 c) { return mfma(a, part(k, b), c); }
 };
 
 template <>
 struct Operand<_Float16> {
     typedef Parts In;  // exact: 8 + 8 bits hold the 11 of an fp16
-    typedef Parts Made;
-    typedef Parts3 Kept;
+    typedef Parts3 Made;
     static __device__ __forceinline__ In widen(const Vec<_Float16, 8> &h) {
         float v[8];
 #pragma unroll
@@ -205,17 +196,17 @@ struct Operand<_Float16> {
         a.hi[j] = a.lo[j] = static_cast<__bf16>(0.0f);
         return a;
     }
-    static __device__ __forceinline__ Made make(float (&v)[8]) { return split(v); }
-    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return split3(v); }
-    static constexpr int kInTerms = 3, kMadeTerms = 3, kKeptTerms = 5;
-    // the product of the two small parts, at most 2^-16 of the whole, is left out
-    static __device__ __forceinline__ f4 in_term(int k, const Parts &a, const Parts &b, f4 c) {
-        return mfma(k == 0 ? a.lo : a.hi, k == 1 ? b.lo : b.hi, c);
+    static __device__ __forceinline__ Made make(float (&v)[8]) { return split3(v); }
+    static constexpr int kInTerms = 4, kMadeTerms = 5;
+    static __device__ __forceinline__ f4 in_term(int k, const In &a, const In &b, f4 c) {
+        return mfma(k == 0 || k == 1 ? a.lo : a.hi, k == 0 || k == 2 ? b.lo : b.hi, c);
     }
-    static __device__ __forceinline__ f4 made_term(int k, const Parts &a, const Parts &b, f4 c) { return in_term(k, a, b, c); }
     // products of parts that make at most 2^-24 of the whole are left out
-    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const Kept &b, f4 c) {
+    static __device__ __forceinline__ f4 made_term(int k, const In &a, const Made &b, f4 c) {
         return mfma(k == 1 || k == 3 ? a.lo : a.hi, k == 0 ? b.lo : (k == 1 || k == 2 ? b.mid : b.hi), c);
+    }
+    static __device__ __forceinline__ f4 made_term(int k, const Made &a, const In &b, f4 c) {
+        return mfma(k == 0 ? a.lo : (k == 1 || k == 2 ? a.mid : a.hi), k == 1 || k == 3 ? b.lo : b.hi, c);
     }
 };
 
@@ -225,7 +216,6 @@ struct Operand<float> {
         float v[8];
     };
     typedef In Made;
-    typedef In Kept;
     static __device__ __forceinline__ In rows(const float *p) {
         In r;
         const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(p + 16);
@@ -254,13 +244,11 @@ struct Operand<float> {
         for (int j = 0; j < 8; ++j) r.v[j] = v[j];
         return r;
     }
-    static __device__ __forceinline__ Kept keep(float (&v)[8]) { return make(v); }
-    static constexpr int kInTerms = 8, kMadeTerms = 8, kKeptTerms = 8;
+    static constexpr int kInTerms = 8, kMadeTerms = 8;
     static __device__ __forceinline__ f4 in_term(int k, const In &a, const In &b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[k], b.v[k], c, 0, 0, 0);
     }
     static __device__ __forceinline__ f4 made_term(int k, const In &a, const In &b, f4 c) { return in_term(k, a, b, c); }
-    static __device__ __forceinline__ f4 kept_term(int k, const In &a, const In &b, f4 c) { return in_term(k, a, b, c); }
 };
 
 // The rows of a chunk in memory: n rows from `base` on. WIDE: 16-byte aligned rows through a buffer
@@ -659,7 +647,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) x[ct] = F::columns(xs + wave_channel + 16 * ct, XS, lane);
         {
-            typename F::Kept right[CT];
+            typename F::Made right[CT];
             float weight[2][4];
             load_floats<float, 4>(to_end + 4 * quad, weight[0]);
             load_floats<float, 4>(to_end + 16 + 4 * quad, weight[1]);
@@ -670,7 +658,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                 float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = F::value(x[ct], e) * weight[e >> 2][e & 3];
-                right[ct] = F::keep(w);
+                right[ct] = F::make(w);
             }
             constexpr int kPair = kTiles < 2 ? 1 : 2;
             typename F::In left[2][kPair];
@@ -683,12 +671,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
                     for (int k = 0; k < kPair; ++k) left[(i + 1) & 1][k] = F::columns(bs + 16 * (kPair * (i + 1) + k), CS, lane);
                 }
 #pragma unroll
-                for (int term = 0; term < F::kKeptTerms; ++term) {
+                for (int term = 0; term < F::kMadeTerms; ++term) {
 #pragma unroll
                     for (int k = 0; k < kPair; ++k) {
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) {
-                            s[ct][kPair * i + k] = F::kept_term(term, left[i & 1][k], right[ct], s[ct][kPair * i + k]);
+                            s[ct][kPair * i + k] = F::made_term(term, left[i & 1][k], right[ct], s[ct][kPair * i + k]);
                         }
                     }
                 }

@@ -361,3 +361,50 @@ def test_decays_of_many_chunks(bl, dtype):
         expect = state[j].double() * torch.exp((starts[j + 1] - starts[j]) * 2.0 ** -5 * a.double())[:, None, None]
         off = (got[j].cpu().double() - expect).abs() / expect.abs()
         assert (off <= 15 * plain.U32).all(), (j, off.max())
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("states", [16, 32, 64, 128, 256])
+def test_states_and_weights_are_read_whole(bl, dtype, states):
+    """Outputs that are small beside their two terms, so that what a product leaves out of the state or of a
+    chunk's weights shows: two states of a channel that c weighs against each other, and two rows of x of opposite
+    sign under nearly equal weights. All other terms are exactly zero. Each term rounds a decay (its exponential of
+    1 ulp and a product), a step, a weight and what three parts leave, at most 8 half steps of float32, and the sum
+    rounds once for each of a term's up to 5 products: 18 of both terms. What both terms share, sums over all states
+    among it, rounds y itself."""
+    rows, heads, width = 40, 2, 64
+    g = torch.Generator().manual_seed(65)
+    a = -torch.tensor([1e-5, 1e-4])
+    dt, b = torch.ones(rows, heads).to(dtype), (0.5 + torch.rand(1, 1, states, generator=g)).to(dtype).repeat(rows, 1, 1)
+    c = (0.5 + torch.rand(1, 1, states, generator=g)).to(dtype).repeat(rows, 1, 1)
+    starts = torch.tensor([0, rows], dtype=torch.int32).cuda()
+    decay = torch.exp((torch.arange(rows) + 1.0).double()[:, None] * a.double())  # of the first state, up to each row
+    cd, none, nothing = c[0, 0].double(), torch.zeros(1, heads, width, states), torch.zeros(rows, heads, width)
+
+    def check(x, state, expect, weight):
+        y = bl.selective_scan(x.to(dtype).cuda(), dt.cuda(), a.cuda(), b.cuda(), c.cuda(), starts, softplus=False, state=state.cuda())
+        error = 18 * plain.U32 * weight + (3 * states + 40) * plain.U32 * expect.abs()
+        _compare(y, expect, plain.rounded(expect, error, dtype), "y")
+
+    # two states of each channel
+    first, second = torch.randint(0, states // 2, (2, heads, width), generator=g)
+    second = second + states // 2
+    value = torch.randn(heads, width, generator=g)
+    other = (-value.double() * cd[first] / cd[second]).float()
+    state = none.clone()
+    state[0].scatter_(2, first[..., None], value[..., None])
+    state[0].scatter_(2, second[..., None], other[..., None])
+    pair = value.double() * cd[first], other.double() * cd[second]
+    check(nothing, state, decay[:, :, None] * (pair[0] + pair[1]), decay[:, :, None] * (pair[0].abs() + pair[1].abs()))
+    # two rows of x, in one chunk or in two
+    dot = (b[0, 0].double() * cd).sum()
+    for at in ((0, 1), (3, 29), (14, 17), (1, 39)):
+        x = nothing.clone()
+        x[at[0]] = (0.5 + torch.rand(heads, width, generator=g)).to(dtype).float()
+        x[at[1]] = -x[at[0]]
+        terms = torch.zeros(2, rows, heads, width, dtype=torch.float64)
+        for k in range(2):
+            since = torch.arange(rows).double() - at[k]
+            reach = torch.where(since[:, None] >= 0, torch.exp(since.clamp(min=0)[:, None] * a.double()), 0.0)
+            terms[k] = reach[:, :, None] * x[at[k]].double() * dot
+        check(x, none, terms.sum(0), terms.abs().sum(0))
