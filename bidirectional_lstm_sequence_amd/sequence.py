@@ -6,7 +6,7 @@ Tensors are CUDA (HIP) tensors of one device; float32, bfloat16 and float16 are 
 tensor is said to be of another type. Rows may have a stride; what lies within a row must be
 contiguous. Work is enqueued on ``stream`` (the device's current stream if None), and outputs and
 scratch memory that a call allocates belong to that stream. Serving only: a tensor that requires a
-gradient is refused while gradients are enabled.
+gradient is refused while gradients are enabled, one with a forward-mode tangent always.
 """
 
 from __future__ import annotations
@@ -51,6 +51,7 @@ class _Torch:
         self.uint8, self.bool = torch.uint8, torch.bool
         self.eight = {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
         self.grad = torch.is_grad_enabled
+        self.forward = torch.autograd.forward_ad
         self.on_stream = torch.cuda.stream
         # the handle alone, without a Stream object around it
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -71,7 +72,7 @@ def _get_torch() -> _Torch:
 class _Call:
     """What the tensors of one call have in common: the device, and the element type of most."""
 
-    __slots__ = ("torch", "like", "device", "dtype", "kind", "grad", "stream")
+    __slots__ = ("torch", "like", "device", "dtype", "kind", "grad", "dual", "stream")
 
     def __init__(self, first, name: str, stream):
         self.torch = t = _torch or _get_torch()
@@ -84,6 +85,8 @@ class _Call:
             raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor, got {self.dtype}")
         self.device = first.get_device()
         self.grad = t.grad()
+        # outside of every level no tensor has a tangent
+        self.dual = getattr(t.forward, "_current_level", 0) >= 0
         if stream is not None and stream.device_index != self.device:
             raise ValueError(f"stream belongs to device {stream.device_index}, {name} to device {self.device}")
         self.stream = stream
@@ -91,7 +94,7 @@ class _Call:
     def _check(self, t, name: str, dtype, shape) -> None:
         try:
             if (t.get_device() == self.device and t.dtype == dtype and t.shape == shape
-                    and not (self.grad and t.requires_grad)):
+                    and not (self.grad and t.requires_grad) and not self.dual):
                 return
         except AttributeError:
             pass
@@ -101,7 +104,9 @@ class _Call:
             raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.requires_grad:
+        if self.dual and self.torch.forward.unpack_dual(t).tangent is not None:
+            raise TypeError(f"{name} has a forward-mode tangent; these operators have no derivatives")
+        if self.grad and t.requires_grad:
             raise TypeError(f"{name} requires a gradient; these operators have none (use torch.no_grad())")
 
     def rows(self, t, name: str, shape: tuple, dtype=None) -> tuple:

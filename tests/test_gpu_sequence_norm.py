@@ -218,3 +218,25 @@ def test_tiny_rows_in_place(bl):
         apart = bl.add_rms_norm(x.cuda(), w.cuda(), 0.0, residual=r.cuda())
         bl.add_rms_norm(xg, w.cuda(), 0.0, residual=rg, out=rg, residual_out=xg)
         assert torch.equal(xg.cpu(), x + r) and torch.equal(rg, apart.y) and torch.equal(apart.residual, xg)
+
+
+def test_the_binding_refuses_forward_mode_tangents(bl):
+    """These operators have no derivatives of either mode."""
+    import torch.autograd.forward_ad as fw
+    x, r, w = (t.cuda() for t in _inputs(torch.float32, 4, 64, 36))
+    tokens = torch.zeros(4, dtype=torch.int64, device="cuda")
+    starts = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    with fw.dual_level():
+        dual = fw.make_dual(x, torch.ones_like(x))
+        for call in (lambda: bl.add_rms_norm(dual, w), lambda: bl.add_rms_norm(x, w, residual=dual),
+                     lambda: bl.token_logprobs(dual, tokens), lambda: bl.causal_conv(dual, x.new_ones(64, 2), starts),
+                     lambda: bl.causal_conv_step(x, x.new_ones(64, 2), fw.make_dual(x.new_zeros(4, 1, 64), x.new_ones(4, 1, 64))),
+                     lambda: bl.selective_scan(dual.view(4, 2, 32), x.new_ones(4, 2), -x.new_ones(2), x.new_ones(4, 1, 16),
+                                               x.new_ones(4, 1, 16), starts)):
+            with pytest.raises(TypeError, match="tangent"):
+                call()
+            with torch.no_grad(), pytest.raises(TypeError, match="tangent"):
+                call()
+        assert bl.add_rms_norm(x, w).y.shape == x.shape
+        assert bl.add_rms_norm(fw.unpack_dual(dual).primal, w).y.shape == x.shape
+    assert bl.add_rms_norm(x, w).y.shape == x.shape
