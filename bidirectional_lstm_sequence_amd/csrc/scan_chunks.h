@@ -30,11 +30,12 @@
 //
 // Precision. Exponents are summed in float64, within a chunk and over the chunks of a run (whose total the
 // join takes in float32), and kept as two floats, so a difference of two of them carries no more than the
-// rounding of the difference. 16-bit inputs enter products as they are (fp16 as two bf16 parts, exactly). Float32 operands, w x, M and S, enter as
-// three bf16 parts, each rounding leaving at most 2^-8 of what it rounds, so 2^-24 is left as in float32
-// itself; of fp16's products of parts those of 2^-24 and less are left out. float32 inputs take the FP32
-// matrix instructions. Sums and the state are float32. Two parts for M and S would leave 2^-16 of terms that
-// may cancel; the third costs the packed prompts 12 % (304 us, 270), of float16 22 %.
+// rounding of the difference. 16-bit inputs enter products as they are (fp16 as two bf16 parts, exactly).
+// Float32 operands, w x, M and S, enter as three bf16 parts, each rounding leaving at most 2^-8 of what it
+// rounds, so 2^-24 is left as in float32 itself; of fp16's products of parts those of 2^-24 and less are
+// left out. float32 inputs take the FP32 matrix instructions. Sums and the state are float32. Two parts for
+// M and S would leave 2^-16 of terms that may cancel; the third costs the packed prompts 12 % (304 us,
+// 270), of float16 22 %.
 // A non-finite x must not reach the rows before it through a zero of M: where a wave's outputs hold
 // one, it takes step 3 again without such x and sets what follows them in their channel to NaN.
 #pragma once
