@@ -24,6 +24,9 @@ _SCAN = struct.Struct("<iiQIIIIIIii" + _VIEW * 5 + _BUFFER * 7 + _VIEW + _BUFFER
 _NORM = struct.Struct("<iiQIifi" + _VIEW * 2 + _BUFFER + _VIEW * 3 + _BUFFER)
 _LOGPROBS = struct.Struct("<iiQIIIi" + _VIEW + _BUFFER * 6)
 
+_nothing = (ctypes.c_float * 8)()
+_NO_PLACES = (ctypes.addressof(_nothing) + 15) // 16 * 16
+
 NO_BUFFER = (0, 0)
 NO_ROWS = (0, 0, 0)
 
@@ -134,6 +137,12 @@ class _Call:
             raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
         return t.data_ptr(), t.numel()
 
+    def cache(self, t, shape: tuple, dtype=None) -> tuple:
+        """``buffer`` of a state. One of no places or elements, which has no memory, is still not the lack of one:
+        the library, which tells them apart by the pointer, gets the address of a float that it never reads."""
+        pointer, count = self.buffer(t, "state", shape, dtype)
+        return (pointer, count) if pointer or t is None else (_NO_PLACES, count)
+
     def empty(self, shape, dtype=None):
         """A new tensor that belongs to the call's stream."""
         if self.stream is None:
@@ -207,7 +216,7 @@ def causal_conv(x, weight, seq_starts, bias=None, state=None, slots=None, fresh=
     call.run("bilstm_causal_conv", _CONV.pack(
         call.device, call.kind, rows, channels, taps, count, cache, 1 if silu else 0, 0, *xv,
         *call.buffer(weight, "weight", (channels, taps)), *call.buffer(bias, "bias", (channels,)), *starts,
-        *call.buffer(state, "state", (cache, taps - 1, channels)), *places, *begin, *yv))
+        *call.cache(state, (cache, taps - 1, channels)), *places, *begin, *yv))
     return out
 
 
@@ -224,7 +233,7 @@ def causal_conv_step(x, weight, state, bias=None, slots=None, silu: bool = True,
     call.run("bilstm_causal_conv_step", _CONV.pack(
         call.device, call.kind, rows, channels, taps, 0, cache, 1 if silu else 0, 0, *xv,
         *call.buffer(weight, "weight", (channels, taps)), *call.buffer(bias, "bias", (channels,)), *NO_BUFFER,
-        *call.buffer(state, "state", (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), call.torch.int32),
+        *call.cache(state, (cache, taps - 1, channels)), *call.buffer(slots, "slots", (rows,), call.torch.int32),
         *NO_BUFFER, *yv))
     return out
 
@@ -247,7 +256,7 @@ def _scan(name: str, x, dt, a, b, c, seq_starts, d, z, dt_bias, softplus, state,
             *call.rows(b, "b", (rows, groups, states)), *call.rows(c, "c", (rows, groups, states)), *(NO_ROWS if z is None else call.rows(z, "z", shape)),
             *call.buffer(a, "a", (heads,), torch.float32), *call.buffer(d, "d", (heads,), torch.float32),
             *call.buffer(dt_bias, "dt_bias", (heads,), torch.float32), *starts,
-            *call.buffer(state, "state", (cache, heads, width, states), torch.float32), *places, *begin,
+            *call.cache(state, (cache, heads, width, states), torch.float32), *places, *begin,
             *call.rows(out, "out", shape))
     hold, scratch = None, NO_BUFFER
     if seq_starts is not None:

@@ -217,3 +217,29 @@ def test_channels_whose_taps_pass_32_bits(bl, step, channels, taps):
         y = bl.causal_conv(x, weight, torch.tensor([0, 1, 2], dtype=torch.int32).cuda(), state=state)
     ref, ref_state, bound = plain.conv(few[0], few[1], [0, 1, 2], None, few[2], None, None, True, torch.zeros_like(few[0]))
     _compare(y[:, on], state[:, :, on], ref, ref_state, bound)
+
+
+def test_a_state_without_places(bl):
+    """A cache of no places is not the lack of one: no sequence may take a place in it."""
+    x = torch.randn(3, 8).cuda()
+    w, none = torch.randn(8, 2).cuda(), torch.zeros(0, 1, 8).cuda()
+    starts = torch.tensor([0, 3], dtype=torch.int32).cuda()
+    out = torch.full((3, 8), 5.0).cuda()
+    with pytest.raises(bl.BilstmError):
+        bl.causal_conv(x, w, starts, state=none, out=out)
+    with pytest.raises(bl.BilstmError):
+        bl.causal_conv_step(x, w, none, out=out)
+    heads, dt, a, b = x.new_ones(3, 1, 32), x.new_ones(3, 1), -x.new_ones(1), x.new_ones(3, 1, 16)
+    with pytest.raises(bl.BilstmError):
+        bl.selective_scan(heads, dt, a, b, b, starts, state=x.new_zeros(0, 1, 32, 16))
+    with pytest.raises(bl.BilstmError):
+        bl.selective_scan_step(heads, dt, a, b, b, x.new_zeros(0, 1, 32, 16))
+    # with slots every sequence is padding: its rows stay as they were
+    slots = torch.tensor([0], dtype=torch.int32).cuda()
+    bl.causal_conv(x, w, starts, state=none, slots=slots, out=out)
+    bl.causal_conv_step(x, w, none, slots=slots.repeat(3), out=out)
+    assert (out == 5.0).all()
+    kept = x.new_full((3, 1, 32), 5.0)
+    bl.selective_scan(heads, dt, a, b, b, starts, state=x.new_zeros(0, 1, 32, 16), slots=slots, out=kept)
+    bl.selective_scan_step(heads, dt, a, b, b, x.new_zeros(0, 1, 32, 16), slots=slots.repeat(3), out=kept)
+    assert (kept == 5.0).all()
