@@ -228,8 +228,9 @@ bilstm_status conv(const char *call, const bilstm_conv_args *args, bool step, vo
     BL_CHECK(check_apart(call, "y", y, "x", x));
     BL_CHECK(check_apart(call, "y", y, "state", state));
     BL_CHECK(check_apart(call, "state", state, "x", x));
-    const Bytes inputs[] = {bytes_of(a.weight, size), bytes_of(a.bias, size), bytes_of(a.starts, 4), bytes_of(a.slots, 4),
-                            bytes_of(a.fresh, 1)};
+    const bilstm_buffer none = {nullptr, 0};
+    const Bytes inputs[] = {bytes_of(a.weight, size), bytes_of(a.bias, size), bytes_of(step ? none : a.starts, 4),
+                            bytes_of(a.slots, 4), bytes_of(step ? none : a.fresh, 1)};
     for (const Bytes &in : inputs) {
         BL_CHECK(check_apart(call, "y", y, "an input", in));
         BL_CHECK(check_apart(call, "state", state, "an input", in));
@@ -267,7 +268,7 @@ bilstm_status scan_sizes(const char *call, const bilstm_scan_args *args, bool st
         return fail(BILSTM_UNSUPPORTED, "%s: %u states (16, 32, 64, 128 and 256 are built)", call, a.states);
     }
     if (static_cast<uint64_t>(a.heads) * a.width * a.states > (1u << 30) || a.rows > kMostRows ||
-        a.sequences > kMostSequences) {
+        (!step && a.sequences > kMostSequences)) {
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows of %u heads exceed the kernels' indexing", call,
                     static_cast<unsigned long long>(a.rows), a.heads);
     }

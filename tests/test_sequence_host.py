@@ -327,3 +327,20 @@ def test_binding_refuses_before_the_library(bl):
         bl.add_rms_norm(x, torch.ones(8))
     with pytest.raises(TypeError):
         bl.token_logprobs(x, torch.zeros(4, dtype=torch.int64))
+
+
+def test_steps_ignore_what_the_header_says(bl):
+    """starts, fresh and the number of sequences are not read in the single-token forms, whatever they hold."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are numbers: nothing may be launched")
+    conv = dict(slots=(6 * P, 64), places=64, state=(5 * P, 64 * 96))
+    scan = dict(slots=(12 * P, 64))
+    for over in (dict(), dict(starts=(8 * P, 1), fresh=(8 * P, 7)), dict(starts=(5 * P + 1, 1 << 40), fresh=(5 * P, 1)),
+                 dict(sequences=(1 << 32) - 1)):
+        args = pack(bl.sequence._CONV, conv_args(**conv, **over))
+        assert status(bl, "bilstm_causal_conv_step", args) == "BILSTM_UNSUPPORTED", bl.last_error()
+        assert "no HIP device" in bl.last_error()
+        args = pack(bl.sequence._SCAN, scan_args(**scan, **over))
+        assert status(bl, "bilstm_scan_step", args) == "BILSTM_UNSUPPORTED", bl.last_error()
+        assert "no HIP device" in bl.last_error()
