@@ -165,13 +165,8 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     const unsigned long long blocks = (threads + kThreads - 1) / kThreads;
     if (blocks == 0) return hipSuccess;
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (step) {
-        hipLaunchKernelGGL((conv_step_kernel<T, V, W, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
-    } else {
-        hipLaunchKernelGGL((conv_kernel<T, V, W, ALIGNED>), grid, dim3(kThreads), 0, stream, a, vectors, threads);
-    }
-    return hipGetLastError();
+    return launch(step ? conv_step_kernel<T, V, W, ALIGNED> : conv_kernel<T, V, W, ALIGNED>, static_cast<unsigned>(blocks),
+                  kThreads, stream, a, vectors, threads);
 }
 
 template <typename T, bool ALIGNED>

@@ -477,8 +477,7 @@ template <typename T, int GROUP, int EACH>
 hipError_t run_small(const LogprobArgs &a, hipStream_t stream) {
     constexpr int kRows = kThreads / GROUP;
     const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.rows) + kRows - 1) / kRows);
-    hipLaunchKernelGGL((small_kernel<T, GROUP, EACH>), dim3(blocks), dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+    return launch(small_kernel<T, GROUP, EACH>, blocks, kThreads, stream, a);
 }
 
 // A row in a wave needs no barrier and leaves few lanes idle, but its rounds go over all of a lane's
@@ -501,15 +500,10 @@ hipError_t run(const LogprobArgs &a, hipStream_t stream) {
     const int tiles = tiles_of<T>(a.vocabulary);
     const long long blocks = static_cast<long long>(a.rows) * tiles;
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    if (tiles == 1) {
-        hipLaunchKernelGGL((tile_kernel<T, true>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, tiles);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((tile_kernel<T, false>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, tiles);
-    hipError_t e = hipGetLastError();
+    if (tiles == 1) return launch(tile_kernel<T, true>, static_cast<unsigned>(blocks), kThreads, stream, a, tiles);
+    const hipError_t e = launch(tile_kernel<T, false>, static_cast<unsigned>(blocks), kThreads, stream, a, tiles);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<T>), dim3(static_cast<unsigned>(a.rows)), dim3(kThreads), 0, stream, a, tiles);
-    return hipGetLastError();
+    return launch(join_kernel<T>, static_cast<unsigned>(a.rows), kThreads, stream, a, tiles);
 }
 
 }  // namespace

@@ -216,18 +216,12 @@ template <typename T, bool ALIGNED, int GROUP, int BLOCKS>
 hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
     constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
     constexpr int kRows = kThreads / GROUP;
-    const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.rows) + kRows - 1) / kRows));
+    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.rows) + kRows - 1) / kRows);
     switch (eight) {
-        case Eight::none:
-            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::none>), grid, dim3(kThreads), 0, stream, a);
-            break;
-        case Eight::e4m3:
-            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::e4m3>), grid, dim3(kThreads), 0, stream, a);
-            break;
-        default:
-            hipLaunchKernelGGL((norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::int8>), grid, dim3(kThreads), 0, stream, a);
+        case Eight::none: return launch(norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::none>, blocks, kThreads, stream, a);
+        case Eight::e4m3: return launch(norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::e4m3>, blocks, kThreads, stream, a);
+        default: return launch(norm_kernel<T, ALIGNED, GROUP, BLOCKS, Eight::int8>, blocks, kThreads, stream, a);
     }
-    return hipGetLastError();
 }
 
 // A wave a row while a lane needs at most four vectors (no barrier, four rows a workgroup), then a

@@ -84,9 +84,7 @@ hipError_t run_step(const ScanArgs &a, hipStream_t stream) {
     const unsigned long long blocks =
         static_cast<unsigned long long>(a.seq.sequences) * static_cast<unsigned>(a.heads) * static_cast<unsigned>(parts);
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((scan_step_kernel<T, N, PASSES>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a,
-                       parts);
-    return hipGetLastError();
+    return launch(scan_step_kernel<T, N, PASSES>, static_cast<unsigned>(blocks), kThreads, stream, a, parts);
 }
 
 // More passes keep more loads in flight and read b and c less often, fewer leave more workgroups: the

@@ -825,19 +825,14 @@ hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
     const int lanes = a.heads * a.width * (N / 4);
     const long long joins = (a.seq.sequences <= splits ? a.seq.sequences : splits + 1) * ((lanes + kThreads - 1) / kThreads);
     if (runs * blocks > 0x7FFFFFFFll || joins > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    const dim3 threads(kThreads);
     if (splits > 0) {
-        hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, false>), dim3(static_cast<unsigned>(splits * blocks)), threads, 0,
-                           stream, a, run_rows, blocks);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(scan_join_kernel, dim3(static_cast<unsigned>(joins)), threads, 0, stream, a, run_rows, lanes);
-        e = hipGetLastError();
+        hipError_t e = launch(scan_chunk_kernel<T, N, CT, WIDE, false>, static_cast<unsigned>(splits * blocks), kThreads, stream,
+                              a, run_rows, blocks);
+        if (e == hipSuccess) e = launch(scan_join_kernel, static_cast<unsigned>(joins), kThreads, stream, a, run_rows, lanes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((scan_chunk_kernel<T, N, CT, WIDE, true>), dim3(static_cast<unsigned>(runs * blocks)), threads, 0, stream,
-                       a, run_rows, blocks);
-    return hipGetLastError();
+    return launch(scan_chunk_kernel<T, N, CT, WIDE, true>, static_cast<unsigned>(runs * blocks), kThreads, stream, a, run_rows,
+                  blocks);
 }
 
 template <typename T, int N>

@@ -7,6 +7,22 @@
 
 namespace bl {
 
+// Starts a kernel and returns what became of this launch: the thread's last error, which a launch by its
+// own syntax leaves, may be an earlier call's.
+template <class T>
+struct AsIs {
+    typedef T type;
+};
+
+template <class... Params>
+hipError_t launch(void (*kernel)(Params...), unsigned blocks, unsigned threads, hipStream_t stream,
+                  typename AsIs<Params>::type... params) {
+    void *values[] = {static_cast<void *>(&params)...};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(blocks), dim3(threads), values, 0, stream);
+    if (e != hipSuccess) (void)hipGetLastError();  // it is returned
+    return e;
+}
+
 template <typename T, int N>
 using Vec = T __attribute__((ext_vector_type(N)));
 

@@ -240,3 +240,35 @@ def test_the_binding_refuses_forward_mode_tangents(bl):
         assert bl.add_rms_norm(x, w).y.shape == x.shape
         assert bl.add_rms_norm(fw.unpack_dual(dual).primal, w).y.shape == x.shape
     assert bl.add_rms_norm(x, w).y.shape == x.shape
+
+
+def test_an_error_from_before_is_not_the_calls(bl):
+    """An error that an earlier, refused HIP call left behind is neither reported by a sound call nor taken away."""
+    import ctypes
+    paths = {line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line}
+    assert len(paths) == 1
+    hip = ctypes.CDLL(paths.pop())
+    x, r, w = (t.cuda() for t in _inputs(torch.float32, 4, 64, 35))
+    starts = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    tokens, large = torch.zeros(4, dtype=torch.int64, device="cuda"), x.new_zeros(4, 20000)
+    taps, rows, states = x.new_ones(64, 2), x.new_zeros(4, 1, 64), x.new_zeros(4, 2, 32, 16)
+    heads, dt, a, b = x.view(4, 2, 32), x.new_ones(4, 2), -x.new_ones(2), x.new_ones(4, 1, 16)
+    many, many_dt, many_b = x.new_ones(400, 2, 32), x.new_ones(400, 2), x.new_ones(400, 1, 16)
+    whole = torch.tensor([0, 400], dtype=torch.int32).cuda()
+    cases = [lambda: bl.add_rms_norm(x, w, residual=r, eight_bit="int8"), lambda: bl.causal_conv(x, taps, starts),
+             lambda: bl.causal_conv_step(x, taps, rows), lambda: bl.token_logprobs(x, tokens, top=2),
+             lambda: bl.token_logprobs(large, tokens, top=2), lambda: bl.selective_scan(heads, dt, a, b, b, starts),
+             lambda: bl.selective_scan(many, many_dt, a, many_b, many_b, whole),
+             lambda: bl.selective_scan_step(heads, dt, a, b, b, states)]
+    for case in cases:
+        case()
+    torch.cuda.synchronize()
+    for case in cases:
+        refused = hip.hipSetDevice(1 << 20)
+        assert refused != 0
+        try:
+            case()
+        finally:
+            left = hip.hipGetLastError()
+        assert left == refused
+    torch.cuda.synchronize()
