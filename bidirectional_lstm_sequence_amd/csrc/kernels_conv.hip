@@ -46,7 +46,7 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, int channels
 template <typename T, int V, int W, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
     using X = Vec<T, V>;
-    const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
+    const unsigned long long id = static_cast<unsigned long long>(workgroup_number()) * kThreads + threadIdx.x;
     if (id >= threads) return;
     const int run = static_cast<int>(id / vectors);
     const int c = static_cast<int>(id % vectors) * V;
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, unsigned vec
 template <typename T, int V, int W, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, unsigned vectors, unsigned long long threads) {
     using X = Vec<T, V>;
-    const unsigned long long id = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
+    const unsigned long long id = static_cast<unsigned long long>(workgroup_number()) * kThreads + threadIdx.x;
     if (id >= threads) return;
     const int row = static_cast<int>(id / vectors);
     const int c = static_cast<int>(id % vectors) * V;
@@ -164,9 +164,8 @@ hipError_t run_conv(const ConvArgs &a, bool step, hipStream_t stream) {
     const unsigned long long threads = runs * vectors;
     const unsigned long long blocks = (threads + kThreads - 1) / kThreads;
     if (blocks == 0) return hipSuccess;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    return launch(step ? conv_step_kernel<T, V, W, ALIGNED> : conv_kernel<T, V, W, ALIGNED>, static_cast<unsigned>(blocks),
-                  kThreads, stream, a, vectors, threads);
+    return launch(step ? conv_step_kernel<T, V, W, ALIGNED> : conv_kernel<T, V, W, ALIGNED>, blocks, kThreads, stream, a,
+                  vectors, threads);
 }
 
 template <typename T, bool ALIGNED>

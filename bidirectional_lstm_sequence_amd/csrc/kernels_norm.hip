@@ -73,7 +73,7 @@ __global__ __launch_bounds__(GROUP < 256 ? 256 : GROUP) void norm_kernel(NormArg
     constexpr int kThreads = GROUP < 256 ? 256 : GROUP;
     constexpr int kRows = kThreads / GROUP;
     const int lane = threadIdx.x % GROUP;
-    const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / GROUP;
+    const long long row = static_cast<long long>(workgroup_number()) * kRows + threadIdx.x / GROUP;
     if (row >= a.rows) return;  // whole waves (GROUP = 64) or no workgroup at all: no barrier is left behind
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
     const T *residual = a.residual != nullptr ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;

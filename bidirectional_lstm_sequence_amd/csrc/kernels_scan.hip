@@ -24,9 +24,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int par
     constexpr int kLanes = N / 4;
     constexpr int kStep = kThreads / kLanes;  // state rows of one pass
     const int lane = threadIdx.x % kLanes;
-    const int part = static_cast<int>(blockIdx.x) % parts;
-    const int h = static_cast<int>(blockIdx.x) / parts % a.heads;
-    const int row = static_cast<int>(blockIdx.x) / parts / a.heads;
+    const unsigned number = workgroup_number();
+    const int part = static_cast<int>(number % static_cast<unsigned>(parts));
+    const int h = static_cast<int>(number / static_cast<unsigned>(parts) % static_cast<unsigned>(a.heads));
+    const int row = static_cast<int>(number / static_cast<unsigned>(parts) / static_cast<unsigned>(a.heads));
+    if (row >= a.seq.rows) return;
     const int place = place_of(a.seq, row);
     if (place < 0) return;
     const int g = h / (a.heads / a.groups);
@@ -83,8 +85,7 @@ hipError_t run_step(const ScanArgs &a, hipStream_t stream) {
     const int parts = (a.width + kStep - 1) / kStep;
     const unsigned long long blocks =
         static_cast<unsigned long long>(a.seq.sequences) * static_cast<unsigned>(a.heads) * static_cast<unsigned>(parts);
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    return launch(scan_step_kernel<T, N, PASSES>, static_cast<unsigned>(blocks), kThreads, stream, a, parts);
+    return launch(scan_step_kernel<T, N, PASSES>, blocks, kThreads, stream, a, parts);
 }
 
 // More passes keep more loads in flight and read b and c less often, fewer leave more workgroups: the

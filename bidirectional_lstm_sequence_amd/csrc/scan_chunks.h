@@ -336,7 +336,7 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
 //    copied: a sequence's first and last run work at the same time.
 // Sequences of one run need only the last launch.
 template <typename T, int N, int CT, bool WIDE, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int blocks) {
+__global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int run_rows, int blocks, int items) {
     using F = Operand<T>;
     using Rows = ChunkRows<T, WIDE>;
     constexpr int NP = N < 32 ? 32 : N;       // states, padded with zeros to a K step
@@ -361,8 +361,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15;
     const int quad = lane >> 4;
-    const int block = static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks));
-    const int run = static_cast<int>(blockIdx.x / static_cast<unsigned>(blocks));
+    const int block = static_cast<int>(workgroup_number() % static_cast<unsigned>(blocks));
+    const int run = static_cast<int>(workgroup_number() / static_cast<unsigned>(blocks));
+    if (run >= items) return;
     // end states: item `run` is the run whose first state slot `run` takes, of the sequence with the border of
     // blocks behind it (slots_of)
     const int j = WHOLE ? sequence_of_run_wave(a.seq, run, run_rows)
@@ -769,11 +770,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_chunk_kernel(ScanArgs a, int
 // One lane a channel and four states of a sequence: its state, then for each run but the last
 // s = decay * s + the run's own end state, each the next run's first state. The parts of kAhead runs are on
 // their way at once. From a zero start nothing changes up to the second run.
-inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int lanes) {
+inline __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int run_rows, int lanes, int items) {
     constexpr int kAhead = 8;
     const int each = static_cast<int>((static_cast<long long>(lanes) + kThreads - 1) / kThreads);
-    const int item = static_cast<int>(blockIdx.x / static_cast<unsigned>(each));
-    const int at = static_cast<int>(blockIdx.x % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
+    const int item = static_cast<int>(workgroup_number() / static_cast<unsigned>(each));
+    const int at = static_cast<int>(workgroup_number() % static_cast<unsigned>(each)) * kThreads + threadIdx.x;
+    if (item >= items) return;
     // few sequences: each; else, in each block of rows, the last one that starts there: no other can be split
     int j = item;
     const bool few = a.seq.sequences <= a.seq.rows / run_rows;
@@ -821,18 +823,18 @@ template <typename T, int N, int CT, bool WIDE>
 hipError_t run_chunks(const ScanArgs &a, int run_rows, hipStream_t stream) {
     const int group_channels = a.heads / a.groups * a.width;
     const int blocks = a.groups * ((group_channels + 64 * CT - 1) / (64 * CT));
-    const long long splits = a.seq.rows / run_rows, runs = splits + a.seq.sequences;
-    const int lanes = a.heads * a.width * (N / 4);
-    const long long joins = (a.seq.sequences <= splits ? a.seq.sequences : splits + 1) * ((lanes + kThreads - 1) / kThreads);
-    if (runs * blocks > 0x7FFFFFFFll || joins > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    const int splits = a.seq.rows / run_rows, runs = splits + a.seq.sequences;
+    const int lanes = a.heads * a.width * (N / 4), lane_blocks = (lanes + kThreads - 1) / kThreads;
+    const int joined = a.seq.sequences <= splits ? a.seq.sequences : splits + 1;
+    auto times = [](int m, int n) { return static_cast<unsigned long long>(m) * static_cast<unsigned>(n); };
+    if (times(runs, blocks) > kMostWorkgroups) return hipErrorInvalidConfiguration;  // before anything has run
     if (splits > 0) {
-        hipError_t e = launch(scan_chunk_kernel<T, N, CT, WIDE, false>, static_cast<unsigned>(splits * blocks), kThreads, stream,
-                              a, run_rows, blocks);
-        if (e == hipSuccess) e = launch(scan_join_kernel, static_cast<unsigned>(joins), kThreads, stream, a, run_rows, lanes);
+        hipError_t e = launch(scan_chunk_kernel<T, N, CT, WIDE, false>, times(splits, blocks), kThreads, stream, a, run_rows, blocks,
+                              splits);
+        if (e == hipSuccess) e = launch(scan_join_kernel, times(joined, lane_blocks), kThreads, stream, a, run_rows, lanes, joined);
         if (e != hipSuccess) return e;
     }
-    return launch(scan_chunk_kernel<T, N, CT, WIDE, true>, static_cast<unsigned>(runs * blocks), kThreads, stream, a, run_rows,
-                  blocks);
+    return launch(scan_chunk_kernel<T, N, CT, WIDE, true>, times(runs, blocks), kThreads, stream, a, run_rows, blocks, runs);
 }
 
 template <typename T, int N>

@@ -7,18 +7,30 @@
 
 namespace bl {
 
-// Starts a kernel and returns what became of this launch: the thread's last error, which a launch by its
-// own syntax leaves, may be an earlier call's.
+// A grid's first dimension counts work-items in 32 bits and is cut short without an error beyond. Workgroups
+// of a larger launch are numbered over two dimensions, kColumns in a row; the numbers of the last row may
+// pass the count, which every kernel checks.
+constexpr unsigned kColumns = 1u << 20;
+constexpr unsigned long long kMostWorkgroups = (1ull << 31) - kColumns;  // so that every number fits an int
+
+__device__ __forceinline__ unsigned workgroup_number() { return blockIdx.y * kColumns + blockIdx.x; }
+
 template <class T>
 struct AsIs {
     typedef T type;
 };
 
+// Starts a kernel of `blocks` workgroups, at most kMostWorkgroups, and returns what became of this launch: the
+// thread's last error, which a launch by its own syntax leaves, may be an earlier call's.
 template <class... Params>
-hipError_t launch(void (*kernel)(Params...), unsigned blocks, unsigned threads, hipStream_t stream,
+hipError_t launch(void (*kernel)(Params...), unsigned long long blocks, unsigned threads, hipStream_t stream,
                   typename AsIs<Params>::type... params) {
+    if (blocks > kMostWorkgroups) return hipErrorInvalidConfiguration;
+    const bool narrow = blocks * threads <= 0xFFFFFFFFull;
+    const dim3 grid(narrow ? static_cast<unsigned>(blocks) : kColumns,
+                    narrow ? 1u : static_cast<unsigned>((blocks + kColumns - 1) / kColumns));
     void *values[] = {static_cast<void *>(&params)...};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(blocks), dim3(threads), values, 0, stream);
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, dim3(threads), values, 0, stream);
     if (e != hipSuccess) (void)hipGetLastError();  // it is returned
     return e;
 }
