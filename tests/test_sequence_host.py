@@ -344,3 +344,41 @@ def test_steps_ignore_what_the_header_says(bl):
         args = pack(bl.sequence._SCAN, scan_args(**scan, **over))
         assert status(bl, "bilstm_scan_step", args) == "BILSTM_UNSUPPORTED", bl.last_error()
         assert "no HIP device" in bl.last_error()
+
+
+def _long_scan(**over):
+    """4096 rows of 64 heads, two sequences: long enough that sequences are split and scratch is needed."""
+    f = dict(rows=4096, heads=64, width=64, groups=1, states=32, sequences=2, places=5, x=(P, 4096 * 4096, 4096),
+             dt=(64 * P, 4096 * 64, 64), b=(65 * P, 4096 * 32, 32), c=(66 * P, 4096 * 32, 32), z=(0, 0, 0), a=(67 * P, 64),
+             d=(0, 0), dt_bias=(0, 0), starts=(68 * P, 3), state=(70 * P, 5 * 4096 * 32), slots=(80 * P, 2),
+             fresh=(81 * P, 2), y=(128 * P, 4096 * 4096, 4096), scratch=(256 * P, 1 << 40))
+    f.update(over)
+    return scan_args(**f)
+
+
+def test_scan_scratch_is_checked(bl):
+    """What a split sequence writes to scratch stays inside it and apart from everything else."""
+    import torch
+    form, need = bl.sequence._SCAN, ctypes.c_uint64()
+    assert bl.library().bilstm_scan_scratch(pack(form, _long_scan()), ctypes.byref(need)) == 0
+    assert need.value > 0
+    for scratch, expected in (((256 * P, need.value - 1), "BILSTM_BUFFER_LENGTH"),
+                              ((256 * P, 0), "BILSTM_BUFFER_LENGTH"),
+                              ((0, 0), "BILSTM_INVALID_ARGUMENT"),
+                              ((0, need.value), "BILSTM_INVALID_ARGUMENT"),
+                              ((256 * P + 8, need.value), "BILSTM_INVALID_ARGUMENT"),
+                              ((P, need.value), "BILSTM_INVALID_ARGUMENT"),  # x
+                              ((65 * P, need.value), "BILSTM_INVALID_ARGUMENT"),  # b and what follows
+                              ((70 * P + 5 * 4096 * 32 * 4 - 16, need.value), "BILSTM_INVALID_ARGUMENT"),  # the state's last floats
+                              ((128 * P - need.value // 16 * 16 + 16, need.value), "BILSTM_INVALID_ARGUMENT"),  # into y
+                              ((128 * P, need.value), "BILSTM_INVALID_ARGUMENT")):
+        assert status(bl, "bilstm_scan", pack(form, _long_scan(scratch=scratch))) == expected, scratch
+        assert bl.last_error().startswith("scan:")
+    if not torch.cuda.is_available():  # else something would be launched
+        for scratch in ((256 * P, need.value), (256 * P, need.value + 5)):
+            assert status(bl, "bilstm_scan", pack(form, _long_scan(scratch=scratch))) == "BILSTM_UNSUPPORTED"
+            assert "no HIP device" in bl.last_error()
+        # sequences that are not split need none, whatever is passed for it
+        for scratch in ((0, 0), (256 * P + 1, 3)):
+            short = scan_args(scratch=scratch)
+            assert status(bl, "bilstm_scan", pack(form, short)) == "BILSTM_UNSUPPORTED"
