@@ -120,7 +120,7 @@ def logprobs(logits, tokens, top):
     return (given, entropy, order, top_lp), (given_bound, entropy_bound, top_bound)
 
 
-def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y):
+def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y, whole_parts=False):
     """The recurrence step by step. Returns y, state, and the bounds of both (y's after its rounding).
 
     ``state`` may be None; all tensors on the CPU, y holds what rows of no sequence keep.
@@ -140,6 +140,8 @@ def scan(x, dt, a, b, c, starts, d, z, dt_bias, softplus, state, slots, fresh, y
     # out too: 2^-15. Three parts in products that meet the state leave 2^-24, and as much for fp16 inputs.
     parts = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -15}[dtype]
     kept = 0.0 if dtype == torch.float32 else 2.0 ** -23
+    if whole_parts:  # three parts in the products that only meet an output too
+        parts = kept
     y, bound = y.double().clone(), torch.zeros(y.shape, dtype=torch.float64)
     state = None if state is None else state.double().clone()
     state_bound = None if state is None else torch.zeros_like(state)

@@ -408,3 +408,54 @@ def test_states_and_weights_are_read_whole(bl, dtype, states):
             reach = torch.where(since[:, None] >= 0, torch.exp(since.clamp(min=0)[:, None] * a.double()), 0.0)
             terms[k] = reach[:, :, None] * x[at[k]].double() * dot
         check(x, none, terms.sum(0), terms.abs().sum(0))
+
+
+class Long(Case):
+    """Many groups of one head each, so that few channels make many workgroups: long runs of rows."""
+
+    def __init__(self, dtype, rows, heads, states, sequences, seed):
+        super().__init__(dtype, rows, heads, 32, heads, states, sequences, seed)
+
+    def run(self, bl, starts):
+        gx, gb, gc = self.views(self.wide.cuda())
+        state = self.state.cuda()
+        y = bl.selective_scan(gx, self.dt.cuda(), self.a.cuda(), gb, gc, torch.tensor(starts, dtype=torch.int32).cuda(),
+                              d=self.d.cuda(), z=self.z.cuda(), dt_bias=self.dt_bias.cuda(), state=state,
+                              slots=self.slots.cuda(), fresh=self.fresh.cuda())
+        return y.cpu(), state.cpu()
+
+    def check(self, got, starts, heads, sequences):
+        """Some heads of some sequences: they know nothing of each other."""
+        y, state = got
+        x, b, c = self.views(self.wide)
+        for j in sequences:
+            at, place = slice(starts[j], starts[j + 1]), int(self.slots[j])
+            part = lambda t: t[at][:, heads]  # noqa: E731
+            ref, ref_state, bound, state_bound = plain.scan(
+                part(x), part(self.dt), self.a[heads], part(b), part(c), [0, starts[j + 1] - starts[j]], self.d[heads],
+                part(self.z), self.dt_bias[heads], True, self.state[place: place + 1, heads], None, [bool(self.fresh[j])],
+                torch.zeros_like(part(x)), whole_parts=True)
+            _compare(part(y), ref, bound, f"y of sequence {j}")
+            _compare(state[place: place + 1, heads], ref_state, state_bound, f"state of sequence {j}")
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("states", [16, 128])
+def test_long_runs(bl, dtype, states):
+    """One sequence in 17 runs of 23 chunks: slow, ordinary and fast decays, settled never, now and then and always."""
+    k = Long(dtype, 12300, 32, states, 1, 61)
+    k.a[:3] = -torch.tensor([0.02, 0.6, 12.0])
+    k.check(k.run(bl, [0, 12300]), [0, 12300], [0, 1, 2, 31], [0])
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("states", [16, 64])
+def test_many_long_sequences_stay_whole(bl, dtype, states):
+    """Four times as many workgroups as there is room for: sequences of up to twice the mean are not split (29
+    chunks in one run), one of more is."""
+    lengths = [900, 40, 0, 1, 2100, 33] + [437 + 3 * j for j in range(58)]
+    starts = _starts(lengths)
+    k = Long(dtype, starts[-1], 32, states, len(lengths), 62)
+    assert 900 < 2 * starts[-1] // len(lengths) < 2100 and len(lengths) * 32 >= 2048
+    k.a[:3] = -torch.tensor([0.02, 0.6, 12.0])
+    k.check(k.run(bl, starts), starts, [0, 1, 2, 31], [0, 1, 3, 4, 5, len(lengths) - 1])
