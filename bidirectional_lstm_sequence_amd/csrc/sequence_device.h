@@ -72,25 +72,17 @@ __device__ __forceinline__ void store_vector(T *p, const Vec<T, N> &v, int count
 
 template <typename T, int N>
 __device__ __forceinline__ void load_floats(const T *p, float (&out)[N]) {
-    if constexpr (N == 1) {
-        out[0] = static_cast<float>(p[0]);
-    } else {
-        const Vec<T, N> v = *reinterpret_cast<const Vec<T, N> *>(p);
+    const Vec<T, N> v = *reinterpret_cast<const Vec<T, N> *>(p);
 #pragma unroll
-        for (int i = 0; i < N; ++i) out[i] = static_cast<float>(v[i]);
-    }
+    for (int i = 0; i < N; ++i) out[i] = static_cast<float>(v[i]);
 }
 
 template <typename T, int N>
 __device__ __forceinline__ void store_floats(T *p, const float (&in)[N]) {
-    if constexpr (N == 1) {
-        p[0] = static_cast<T>(in[0]);
-    } else {
-        Vec<T, N> v;
+    Vec<T, N> v;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = static_cast<T>(in[i]);
-        *reinterpret_cast<Vec<T, N> *>(p) = v;
-    }
+    for (int i = 0; i < N; ++i) v[i] = static_cast<T>(in[i]);
+    *reinterpret_cast<Vec<T, N> *>(p) = v;
 }
 
 // e^-v on v_exp_f32 (1 ulp; 0 below float32's normal range) with its exponent's rounding carried along:
@@ -120,7 +112,6 @@ struct Span {
 __device__ __forceinline__ int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
 
 __device__ __forceinline__ Span span_of(const SequenceArgs &s, int j) {
-    if (s.starts == nullptr) return {j, 1};
     const int first = clamp_row(s.starts[j], s.rows);
     const int end = clamp_row(s.starts[j + 1], s.rows);
     return {first, end > first ? end - first : 0};

@@ -11,8 +11,8 @@ namespace bl {
 
 enum class Elem { f32, bf16, f16 };
 
-// Packed sequences and the cache places that go with them; see include/bilstm.h. starts == nullptr:
-// the single-token form, row i is sequence i.
+// Packed sequences and the cache places that go with them; see include/bilstm.h. In the
+// single-token form, without starts, row i is sequence i.
 struct SequenceArgs {
     const int *starts = nullptr;
     const int *slots = nullptr;
