@@ -9,8 +9,9 @@
 // that no register file holds (BLOCKS = 0) are read a second time for y and in 8 bits a third, from the
 // L2 where they fit. The sum s is not rounded to the tensor's type before it is normed.
 //
-// 8192 x 5120 bfloat16 rows with a residual to e4m3 (7 bytes an element) take 59 us, 5.0 TB/s, where a
-// large copy reaches 4.8; 18848 x 256 float32 rows with a residual 14 us, 5.5 TB/s, partly from caches.
+// 8192 x 5120 rows with a residual to e4m3 or int8 take 56 us in bfloat16 (7 bytes an element), 5.2 TB/s, 58 in
+// float16 and 107 in float32 (13 bytes), where a large copy reaches 4.8; 18848 x 256 float32 rows with a
+// residual 14 us, 5.5 TB/s, partly from caches.
 #include "sequence_device.h"
 
 namespace bl {
@@ -238,7 +239,7 @@ hipError_t run(const NormArgs &a, Eight eight, hipStream_t stream) {
 // workgroup of 256, then one of 1024 lanes, then the form that reads the row again.
 // A group of lanes as wide as its row, with four vectors a lane: a wider one idles and has to meet at
 // barriers. 20 million bfloat16 elements with a residual in groups of 64, 256 and 1024 lanes: rows of 256
-// 30, 77 and 293 us, of 1024 27, 31 and 78, of 2048 27, 26 and 42, of 8192 (256 and 1024) 26.4 and 26.4.
+// 32, 82 and 293 us, of 1024 27, 31 and 78, of 2048 27, 26 and 43, of 8192 (256 and 1024) 26.6 and 26.5.
 // Rows of 32768 take 27.2 us out of registers and 36.1 read again; to e4m3, read three times, 29.9 and 45.6.
 template <typename T, bool ALIGNED>
 hipError_t by_width(const NormArgs &a, Eight eight, hipStream_t stream) {
@@ -257,7 +258,7 @@ hipError_t by_alignment(const NormArgs &a, Eight eight, hipStream_t stream) {
                            reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
                            reinterpret_cast<uintptr_t>(a.y);
     const size_t strides = a.x_stride | a.residual_stride | a.residual_out_stride | a.y_stride | a.q_stride;
-    // vectors at any element cost rows of 256 31 us in place of 30, of 2048 27.4 for 26.6, wider ones nothing
+    // vectors at any element cost rows of 256 33 us in place of 31.5, of 2048 27.7 for 26.9, of 32768 31.2 for 27.2
     const bool wide = bits % 16 == 0 && reinterpret_cast<uintptr_t>(a.q) % kVec == 0 && a.width % kVec == 0 &&
                       strides % kVec == 0;
     return wide ? by_width<T, true>(a, eight, stream) : by_width<T, false>(a, eight, stream);

@@ -4,8 +4,8 @@
 //
 // per head, with a state S of [width][states] in float32, optionally y * z sigmoid(z). Two forms:
 // single tokens (here) and packed sequences in chunks of rows (scan_chunks.h). A single row of a packed
-// sequence is a chunk of one row there: walking over a packed sequence's rows one by one takes 17 us
-// against 35 for 512 single rows of 4 float32 heads of 64 channels and 64 states, but 99 against 62 for 64
+// sequence is a chunk of one row there: walking over a packed sequence's rows one by one took 17 us
+// against 34 for 512 single rows of 4 float32 heads of 64 channels and 64 states, but 99 against 52 for 64
 // sequences of 4 rows of 32 bfloat16 heads of 64 channels and 256 states, and about a microsecond a row
 // for one long sequence among many short ones, which the host cannot see.
 #include "scan_device.h"
@@ -118,12 +118,16 @@ hipError_t by_states(const ScanArgs &a, hipStream_t stream) {
 //  * Splitting costs the end states of most runs (the products with x and b a second time) and two
 //    launches; it pays while whole sequences leave the chip's 512 places (two workgroups a CU) empty, or
 //    one long sequence outlives the others. Measured with 64 heads of 64 channels and 128 states: one
-//    sequence of 4096 rows 124, 98, 84, 101, 92 and 120 us in runs of 96, 192, 256, 384, 512 and 768 rows,
-//    over 400 us whole; 24 unequal ones of 16384 rows together (the mean of 12 such batches) 324, 293,
-//    279, 274, 271 and 279 us in runs of at most 256, 384, 512, 640, 768 and 1024. 4 float32 heads of 64
-//    channels and 64 states, 32 sequences of 589 rows: 53, 60, 64, 87 and 111 us in runs of 96, 128, 256,
-//    384 and 512, 94 us whole.
-//  * With four times as many sequences as places only a sequence of over twice the mean is split.
+//    sequence of 4096 rows 126, 99, 89, 110, 97 and 121 us in runs of 96, 192, 256, 384, 512 and 768 rows,
+//    446 us whole; 24 unequal ones of 16384 rows together (the mean of 12 such batches) 324, 298, 287, 291,
+//    295 and 313 us in runs of at most 256, 384, 512, 640, 768 and 1024. 4 float32 heads of 64 channels and
+//    64 states, 32 sequences of 589 rows: 71, 63, 55, 62, 59, 76 and 77 us in runs of 32, 64, 96, 128, 256, 384
+//    and 512, 92 us whole. The least run is where one sequence of 600 rows of the 64 heads is fastest: 50, 40,
+//    38, 39 and 42 us in runs of 32, 64, 96, 128 and 160; fewer workgroups would take shorter ones, as 1500 rows
+//    of the 4 heads 26, 28, 34 and 40 in runs of 32, 64, 96 and 128.
+//  * With four times as many workgroups as places only a sequence of over twice the mean is split. Unequal
+//    sequences of the 64 heads with and without this: 128 of 131072 rows together 1725 and 1924 us, 64 of 65536
+//    936 and 977, 256 of 65536 978 and 979, but 64 of 32768 509 and 503, 512 of 131072 1950 and 1906.
 int run_rows_of(const ScanArgs &a) {
     constexpr long long kPlaces = 512, kLeast = 96, kMost = 768;
     constexpr int kChannels = 128;  // of a workgroup

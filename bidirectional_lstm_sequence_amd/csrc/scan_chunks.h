@@ -19,14 +19,14 @@
 // it, and G that of 3 without a pass through LDS. b and x are read by columns with
 // ds_read_b64_tr_b16 (16-bit types).
 //
-// What bounds it. With 128 bfloat16 states a chunk of a wave is 100 matrix instructions and 700 others
-// (half of them split float32 values into bf16 parts), with two waves a SIMD, as a wave's state and
-// fragments take 250 registers: vector units busy 45 % of the time, matrix units 21 %; the rest are
+// What bounds it. With 128 bfloat16 states a chunk of a wave is 120 matrix instructions and 920 others
+// (more than half of them split float32 values into bf16 parts), with two waves a SIMD, as a wave's state and
+// fragments take 250 registers: vector units busy 49 % of the time, matrix units 22 %; the rest are
 // waits for the products' results and the tail of unequal runs. 24 prompts of 16384 rows
-// together, 64 heads of 64 channels and 128 states: 271 us (end states of the runs 46, their join 23,
-// the runs 200) where the bytes alone take 107. One prompt of 4096 rows 84 us (bytes 22), 32 windows
-// of 589 float32 rows, 4 heads of 64 channels and 64 states, 53 us (bytes 11): few workgroups, each a
-// chain of dependent chunks.
+// together, 64 heads of 64 channels and 128 states: a call takes 304 us where the bytes alone take 107; in a
+// trace, where no launch begins before the last one's end, end states of the runs 49 us, their join 24, the
+// runs 262. One prompt of 4096 rows 90 us (bytes 22), 32 windows of 589 float32 rows, 4 heads of 64 channels
+// and 64 states, 54 us (bytes 11): few workgroups, each a chain of dependent chunks.
 //
 // Precision. Exponents are summed in float64, within a chunk and over the chunks of a run (whose total the
 // join takes in float32), and kept as two floats, so a difference of two of them carries no more than the
@@ -35,7 +35,7 @@
 // rounds, so 2^-24 is left as in float32 itself; of fp16's products of parts those of 2^-24 and less are
 // left out. float32 inputs take the FP32 matrix instructions. Sums and the state are float32. Two parts for
 // M and S would leave 2^-16 of terms that may cancel; the third costs the packed prompts 12 % (304 us,
-// 270), of float16 22 %.
+// 270), of float16 18 % (524, 443).
 // A non-finite x must not reach the rows before it through a zero of M: where a wave's outputs hold
 // one, it takes step 3 again without such x and sets what follows them in their channel to NaN.
 #pragma once
@@ -841,8 +841,8 @@ template <typename T, int N>
 hipError_t by_alignment(ScanArgs a, int run_rows, hipStream_t stream) {
     // Two tiles of channels a wave read the fragments of b and c half as often, but 256 states of them
     // leave 16-bit types no registers for the rest. 24 sequences of 683 rows, 64 heads of 64 channels,
-    // with one and two: 128 bfloat16 states 335 and 294 us; 256 states 506 and 712 in bfloat16, 991 and
-    // 1152 in float16, 1694 and 1375 in float32.
+    // with one and two: 128 states 266 and 223 us in bfloat16, 462 and 380 in float16, 631 and 548 in float32;
+    // 256 states 391 and 696, 852 and 993, 1323 and 998; 64 states 197 and 195, 311 and 231, 366 and 325.
     constexpr int CT = N > 128 && sizeof(T) == 2 ? 1 : 2;
     if (a.seq.rows == 1) {  // a single row's strides say nothing
         a.x_stride = a.y_stride = a.z_stride = static_cast<size_t>(a.heads) * a.width;
@@ -851,7 +851,7 @@ hipError_t by_alignment(ScanArgs a, int run_rows, hipStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.b) |
                            reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.y);
     const size_t strides = a.x_stride | a.b_stride | a.c_stride | a.z_stride | a.y_stride;
-    // loads element by element: 506 -> 522 us at those 256 bfloat16 states, 294 -> 313 at 128
+    // loads element by element: 391 -> 404 us at those 256 bfloat16 states, 225 -> 247 at 128
     const bool wide = bits % 16 == 0 && strides % (16 / sizeof(T)) == 0 && strides < (1u << 22);
     return wide ? run_chunks<T, N, CT, true>(a, run_rows, stream) : run_chunks<T, N, CT, false>(a, run_rows, stream);
 }
