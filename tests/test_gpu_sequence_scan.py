@@ -459,3 +459,45 @@ def test_many_long_sequences_stay_whole(bl, dtype, states):
     assert 900 < 2 * starts[-1] // len(lengths) < 2100 and len(lengths) * 32 >= 2048
     k.a[:3] = -torch.tensor([0.02, 0.6, 12.0])
     k.check(k.run(bl, starts), starts, [0, 1, 2, 31], [0, 1, 3, 4, 5, len(lengths) - 1])
+
+
+@pytest.mark.parametrize("dtype", plain.TYPES, ids=str)
+@pytest.mark.parametrize("name", ["dt", "b", "c", "z"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_what_other_inputs_that_are_not_numbers_reach(bl, dtype, name, bad):
+    """dt: its head from its row on; b: its group from its row on; c: its group's row; z: its element. Everything
+    before, beside and behind, in other sequences too, is as without it; split and whole sequences, and states."""
+    starts = [0, 30, 230, 260]
+    k = Case(dtype, 260, 4, 64, 2, 64, 3, 66)
+    k.fresh[:] = False
+    row = 75
+    x, b, c = k.views(k.wide)
+    ref, ref_state, bound, state_bound = plain.scan(x, k.dt, k.a, b, c, starts, k.d, k.z, k.dt_bias, True, k.state,
+                                                    k.slots.tolist(), None, torch.zeros_like(x))
+    wide, dt, z, state = k.wide.clone(), k.dt.clone(), k.z.clone(), k.state.cuda()
+    hit, hit_state = torch.zeros(260, 4, 64, dtype=torch.bool), torch.zeros(4, 64, 64, dtype=torch.bool)
+    if name == "dt":
+        dt[row, 1] = abs(bad)  # minus infinity would be a step of zero
+        hit[row:230, 1], hit_state[1] = True, True
+    elif name == "b":
+        k.views(wide)[1][row, 1, 5] = bad
+        hit[row:230, 2:], hit_state[2:, :, 5] = True, True
+    elif name == "c":
+        k.views(wide)[2][row, 0, 7] = bad
+        hit[row, :2] = True
+    else:
+        z[row, 3, 11] = bad
+        hit[row, 3, 11] = True
+    gx, gb, gc = k.views(wide.cuda())
+    y = bl.selective_scan(gx, dt.cuda(), k.a.cuda(), gb, gc, torch.tensor(starts, dtype=torch.int32).cuda(), d=k.d.cuda(),
+                          z=z.cuda(), dt_bias=k.dt_bias.cuda(), state=state, slots=k.slots.cuda())
+    y, state = y.cpu().double(), state.cpu().double()
+    assert not torch.isfinite(y[hit]).any()
+    off = (y - ref).abs()[~hit]
+    assert (off <= bound[~hit]).all(), (off - bound[~hit]).max()
+    place = int(k.slots[1])
+    assert not torch.isfinite(state[place][hit_state]).any()
+    rest = torch.ones(state.shape, dtype=torch.bool)
+    rest[place] = ~hit_state
+    off = (state - ref_state).abs()[rest]
+    assert (off <= state_bound[rest]).all()
