@@ -136,9 +136,8 @@ __device__ __forceinline__ constexpr int place_of_row(int t) {
 
 // Operands of the products for one input type: fragments of 8 values of K for row (or column)
 // lane % 16, K = 16 e + 4 (lane / 16) + r in place 4 e + r. In: values of an input tensor; Made: float32
-// values. A product is a sum of terms, a matrix
-// instruction each; callers take one term of several products before the next, as instructions on one
-// accumulator wait for each other.
+// values. A product is a sum of terms, a matrix instruction each; callers take one term of several products
+// before the next, as instructions on one accumulator wait for each other.
 template <typename T>
 struct Operand;
 
