@@ -16,7 +16,8 @@ import numpy as np
 
 from . import sequence
 from .sequence import (NormResult, TokenLogprobs, add_rms_norm, causal_conv, causal_conv_step,  # noqa: F401
-                       selective_scan, selective_scan_step, token_logprobs)
+                       cross_attention, cross_attention_step, linear, selective_scan, selective_scan_step,
+                       token_logprobs)
 
 HIDDEN = 128
 GATES = 512
@@ -39,7 +40,9 @@ EXPORTS = ["bilstm_plan_create", "bilstm_plan_create_ex", "bilstm_forward", "bil
            "bilstm_heads_destroy", "bilstm_forward_noalloc", "bilstm_probe_fma_rate",
            "bilstm_probe_mfma_rate", "bilstm_causal_conv", "bilstm_causal_conv_step",
            "bilstm_scan", "bilstm_scan_step", "bilstm_scan_scratch",
-           "bilstm_add_rms_norm", "bilstm_token_logprobs", "bilstm_token_logprobs_scratch"]
+           "bilstm_add_rms_norm", "bilstm_token_logprobs", "bilstm_token_logprobs_scratch",
+           "bilstm_cross_attention", "bilstm_cross_attention_step", "bilstm_cross_attention_scratch",
+           "bilstm_cross_attention_step_scratch", "bilstm_linear", "bilstm_linear_scratch"]
 HEAD_IN, HEAD_MID, HEAD_CLASSES = 256, 128, 7
 
 

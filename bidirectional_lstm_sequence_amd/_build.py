@@ -17,7 +17,7 @@ SOURCES = ["host_plan.cpp", "host_pack_schedule.cpp", "host_heads.cpp", "host_li
            "kernels_projection.hip", "kernels_recurrence.hip", "kernels_heads.hip",
            "forward_noalloc.hip", "host_sequence.cpp", "kernels_conv.hip", "kernels_scan.hip",
            "kernels_scan_f32.hip", "kernels_scan_bf16.hip", "kernels_scan_f16.hip",
-           "kernels_norm.hip", "kernels_logprobs.hip"]
+           "kernels_norm.hip", "kernels_logprobs.hip", "kernels_attention.hip", "kernels_linear.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

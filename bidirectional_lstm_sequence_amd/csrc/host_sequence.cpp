@@ -513,6 +513,207 @@ bilstm_status logprobs(const char *call, const bilstm_logprobs_args *args, void 
     return launched(call, launch_token_logprobs(k, elem_of(a.type), static_cast<hipStream_t>(stream)));
 }
 
+// ---- cross attention -------------------------------------------------------------------------
+
+// The sizes of an attention, without its pointers.
+bilstm_status attention_sizes(const char *call, const bilstm_attention_args *args, bool step, AttentionArgs *k) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    const bilstm_attention_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.heads == 0 || a.heads > 65536 || a.groups == 0 || a.heads % a.groups != 0) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %u heads that read %u", call, a.heads, a.groups);
+    }
+    if (a.width == 0 || a.width > 256) {
+        return fail(BILSTM_UNSUPPORTED, "%s: heads of %u elements (1 to 256 are built)", call, a.width);
+    }
+    if (a.rows > kMostRows || a.memory_rows > kMostRows || a.places > kMostRows || (!step && a.sequences > kMostSequences)) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows or %llu memory rows exceed the kernels' indexing", call,
+                    static_cast<unsigned long long>(a.rows), static_cast<unsigned long long>(a.memory_rows));
+    }
+    k->heads = static_cast<int>(a.heads);
+    k->groups = static_cast<int>(a.groups);
+    k->per = static_cast<int>(a.heads / a.groups);
+    k->width = static_cast<int>(a.width);
+    k->memory_rows = static_cast<int>(a.memory_rows);
+    k->step = step;
+    k->seq.rows = static_cast<int>(a.rows);
+    k->seq.sequences = static_cast<int>(step ? a.rows : a.sequences);
+    k->seq.places = static_cast<int>(a.places);
+    return BILSTM_OK;
+}
+
+bilstm_status attention(const char *call, const bilstm_attention_args *args, bool step, void *stream) {
+    AttentionArgs k;
+    BL_CHECK(attention_sizes(call, args, step, &k));
+    const bilstm_attention_args &a = *args;
+    if (a.reserved[0] != 0 || a.reserved[1] != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
+    if (!(a.scale > 0.0f) || a.scale > 3.0e38f) return fail(BILSTM_INVALID_ARGUMENT, "%s: scale is not a number > 0", call);
+    const uint64_t count = step ? a.rows : a.sequences;
+    if (a.rows == 0 || count == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type);
+    const uint64_t inner = static_cast<uint64_t>(a.heads) * a.width, shared = static_cast<uint64_t>(a.groups) * a.width;
+    const bilstm_buffer none = {nullptr, 0};
+    const bilstm_rows no_rows = {nullptr, 0, 0};
+    BL_CHECK(check_rows(call, "q", a.q, a.rows, inner, size));
+    if (a.memory_rows > 0) {
+        BL_CHECK(check_rows(call, "k", a.k, a.memory_rows, shared, size));
+        BL_CHECK(check_rows(call, "v", a.v, a.memory_rows, shared, size));
+        BL_CHECK(check_buffer(call, "mask", a.mask, a.memory_rows, 1, true));
+    }
+    if (!step) BL_CHECK(check_buffer(call, "starts", a.starts, count + 1, 4, false));
+    BL_CHECK(check_buffer(call, "slots", a.slots, count, 4, true));
+    if (a.slots.data == nullptr && count > a.places) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: %llu sequences without slots, but only %u memories", call,
+                    static_cast<unsigned long long>(count), a.places);
+    }
+    BL_CHECK(check_buffer(call, "memory_starts", a.memory_starts, static_cast<uint64_t>(a.places) + 1, 4, false));
+    if (a.places > 0) BL_CHECK(check_buffer(call, "memory_lengths", a.memory_lengths, a.places, 4, true));
+    BL_CHECK(check_rows(call, "y", a.y, a.rows, inner, size));
+    const uint64_t need = attention_scratch_bytes(k);
+    if (need > 0) {
+        BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
+        if (a.scratch.len < need) {
+            return fail(BILSTM_BUFFER_LENGTH, "%s: scratch: expected at least %llu bytes, got %llu", call,
+                        static_cast<unsigned long long>(need), static_cast<unsigned long long>(a.scratch.len));
+        }
+    }
+    struct Region {
+        const char *name;
+        Bytes bytes;
+    };
+    const bool held = a.memory_rows > 0;
+    const Region ins[] = {{"q", bytes_of(a.q, a.rows, inner, size)},
+                          {"k", bytes_of(held ? a.k : no_rows, a.memory_rows, shared, size)},
+                          {"v", bytes_of(held ? a.v : no_rows, a.memory_rows, shared, size)},
+                          {"mask", bytes_of(held ? a.mask : none, 1)},
+                          {"starts", bytes_of(step ? none : a.starts, 4)},
+                          {"slots", bytes_of(a.slots, 4)},
+                          {"memory_starts", bytes_of(a.memory_starts, 4)},
+                          {"memory_lengths", bytes_of(a.places > 0 ? a.memory_lengths : none, 4)}};
+    const Region outs[] = {{"y", bytes_of(a.y, a.rows, inner, size)}, {"scratch", bytes_of(need > 0 ? a.scratch : none, 1)}};
+    for (const Region &o : outs) {
+        for (const Region &in : ins) BL_CHECK(check_apart(call, o.name, o.bytes, in.name, in.bytes));
+    }
+    BL_CHECK(check_apart(call, "scratch", outs[1].bytes, "y", outs[0].bytes));
+    k.q = a.q.data;
+    k.k = held ? a.k.data : nullptr;
+    k.v = held ? a.v.data : nullptr;
+    k.mask = held ? static_cast<const unsigned char *>(a.mask.data) : nullptr;
+    k.memory_starts = static_cast<const int *>(a.memory_starts.data);
+    k.memory_lengths = a.places > 0 ? static_cast<const int *>(a.memory_lengths.data) : nullptr;
+    k.y = const_cast<void *>(a.y.data);
+    k.scratch = static_cast<float *>(const_cast<void *>(a.scratch.data));
+    k.q_stride = a.q.stride;
+    k.k_stride = held ? a.k.stride : 0;
+    k.v_stride = held ? a.v.stride : 0;
+    k.y_stride = a.y.stride;
+    k.scale = a.scale;
+    k.seq.starts = step ? nullptr : static_cast<const int *>(a.starts.data);
+    k.seq.slots = static_cast<const int *>(a.slots.data);
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    return launched(call, launch_attention(k, elem_of(a.type), static_cast<hipStream_t>(stream)));
+}
+
+bilstm_status attention_scratch(const char *call, const bilstm_attention_args *args, bool step, uint64_t *bytes) {
+    AttentionArgs k;
+    BL_CHECK(attention_sizes(call, args, step, &k));
+    if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: bytes is NULL", call);
+    *bytes = attention_scratch_bytes(k);
+    return BILSTM_OK;
+}
+
+// ---- matrix product ----------------------------------------------------------------------------
+
+bilstm_status linear_sizes(const char *call, const bilstm_linear_args *args, LinearArgs *k) {
+    if (args == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "%s: args is NULL", call);
+    const bilstm_linear_args &a = *args;
+    BL_CHECK(check_type(call, a.type));
+    if (a.eight < BILSTM_EIGHT_NONE || a.eight > BILSTM_EIGHT_INT8) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: unknown 8-bit type %d", call, a.eight);
+    }
+    if (a.in == 0 || a.out == 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: %u inputs, %u outputs", call, a.in, a.out);
+    // 2^16 products of two int8 codes stay below 2^31
+    if (a.rows > kMostRows || a.in > (1u << 28) || a.out > (1u << 28) || (a.eight == BILSTM_EIGHT_INT8 && a.in > (1u << 16))) {
+        return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows, %u inputs, %u outputs exceed the kernel's indexing", call,
+                    static_cast<unsigned long long>(a.rows), a.in, a.out);
+    }
+    k->rows = static_cast<int>(a.rows);
+    k->in = static_cast<int>(a.in);
+    k->out = static_cast<int>(a.out);
+    return BILSTM_OK;
+}
+
+bilstm_status linear(const char *call, const bilstm_linear_args *args, void *stream) {
+    LinearArgs k;
+    BL_CHECK(linear_sizes(call, args, &k));
+    const bilstm_linear_args &a = *args;
+    if (a.reserved != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
+    if (a.activation < BILSTM_ACT_NONE || a.activation > BILSTM_ACT_SILU) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: unknown activation %d", call, a.activation);
+    }
+    if (!(a.slope >= -3.0e38f && a.slope <= 3.0e38f)) return fail(BILSTM_INVALID_ARGUMENT, "%s: slope is not finite", call);
+    const bool eight = a.eight != BILSTM_EIGHT_NONE;
+    if (!eight && (a.x_scales.data != nullptr || a.weight_scales.data != nullptr)) {
+        return fail(BILSTM_INVALID_ARGUMENT, "%s: scales need an 8-bit type", call);
+    }
+    if (a.rows == 0) return BILSTM_OK;
+    const uint64_t size = size_of(a.type), part = eight ? 1 : size;
+    BL_CHECK(check_rows(call, "x", a.x, a.rows, a.in, part));
+    BL_CHECK(check_rows(call, "weight", a.weight, a.out, a.in, part));
+    BL_CHECK(check_buffer(call, "bias", a.bias, a.out, size, true));
+    if (a.residual.data != nullptr) BL_CHECK(check_rows(call, "residual", a.residual, a.rows, a.out, size));
+    if (eight) {
+        BL_CHECK(check_buffer(call, "x_scales", a.x_scales, a.rows, 4, false));
+        BL_CHECK(check_buffer(call, "weight_scales", a.weight_scales, a.out, 4, false));
+    }
+    BL_CHECK(check_rows(call, "y", a.y, a.rows, a.out, size));
+    const uint64_t need = linear_scratch_bytes(k, elem_of(a.type), static_cast<Eight>(a.eight));
+    if (need > 0) {
+        BL_CHECK(check_pointer(call, "scratch", a.scratch.data, 16));
+        if (a.scratch.len < need) {
+            return fail(BILSTM_BUFFER_LENGTH, "%s: scratch: expected at least %llu bytes, got %llu", call,
+                        static_cast<unsigned long long>(need), static_cast<unsigned long long>(a.scratch.len));
+        }
+    }
+    struct Region {
+        const char *name;
+        Bytes bytes;
+    };
+    const bilstm_buffer none = {nullptr, 0};
+    const Region ins[] = {{"x", bytes_of(a.x, a.rows, a.in, part)},
+                          {"weight", bytes_of(a.weight, a.out, a.in, part)},
+                          {"bias", bytes_of(a.bias, size)},
+                          {"x_scales", bytes_of(eight ? a.x_scales : none, 4)},
+                          {"weight_scales", bytes_of(eight ? a.weight_scales : none, 4)}};
+    const Bytes y = bytes_of(a.y, a.rows, a.out, size), scratch = bytes_of(need > 0 ? a.scratch : none, 1);
+    const Bytes residual = bytes_of(a.residual, a.rows, a.out, size);
+    for (const Region &in : ins) {
+        BL_CHECK(check_apart(call, "y", y, in.name, in.bytes));
+        BL_CHECK(check_apart(call, "scratch", scratch, in.name, in.bytes));
+    }
+    if (!same_view(a.y, a.residual, a.rows)) BL_CHECK(check_apart(call, "y", y, "residual", residual));
+    BL_CHECK(check_apart(call, "scratch", scratch, "residual", residual));
+    BL_CHECK(check_apart(call, "scratch", scratch, "y", y));
+    k.x = a.x.data;
+    k.weight = a.weight.data;
+    k.bias = a.bias.data;
+    k.residual = a.residual.data;
+    k.x_scales = static_cast<const float *>(a.x_scales.data);
+    k.weight_scales = static_cast<const float *>(a.weight_scales.data);
+    k.y = const_cast<void *>(a.y.data);
+    k.scratch = static_cast<float *>(const_cast<void *>(a.scratch.data));
+    k.x_stride = a.x.stride;
+    k.weight_stride = a.weight.stride;
+    k.residual_stride = a.residual.data != nullptr ? a.residual.stride : 0;
+    k.y_stride = a.y.stride;
+    k.activation = a.activation;
+    k.slope = a.slope;
+    DeviceScope scope(a.device);
+    BL_CHECK(scope.enter(call));
+    return launched(call, launch_linear(k, elem_of(a.type), static_cast<Eight>(a.eight), static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -552,5 +753,31 @@ bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, ui
 bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stream) {
     return logprobs("token_logprobs", args, stream);
 }
+
+bilstm_status bilstm_cross_attention_scratch(const bilstm_attention_args *args, uint64_t *bytes) {
+    return attention_scratch("cross_attention_scratch", args, false, bytes);
+}
+
+bilstm_status bilstm_cross_attention_step_scratch(const bilstm_attention_args *args, uint64_t *bytes) {
+    return attention_scratch("cross_attention_step_scratch", args, true, bytes);
+}
+
+bilstm_status bilstm_cross_attention(const bilstm_attention_args *args, void *stream) {
+    return attention("cross_attention", args, false, stream);
+}
+
+bilstm_status bilstm_cross_attention_step(const bilstm_attention_args *args, void *stream) {
+    return attention("cross_attention_step", args, true, stream);
+}
+
+bilstm_status bilstm_linear_scratch(const bilstm_linear_args *args, uint64_t *bytes) {
+    LinearArgs k;
+    BL_CHECK(linear_sizes("linear_scratch", args, &k));
+    if (bytes == nullptr) return fail(BILSTM_INVALID_ARGUMENT, "linear_scratch: bytes is NULL");
+    *bytes = linear_scratch_bytes(k, elem_of(args->type), static_cast<Eight>(args->eight));
+    return BILSTM_OK;
+}
+
+bilstm_status bilstm_linear(const bilstm_linear_args *args, void *stream) { return linear("linear", args, stream); }
 
 }  // extern "C"

@@ -1,0 +1,399 @@
+// Cross attention: rows of packed sequences, or one row a sequence, read memories of frames.
+//
+//   s[f] = scale q . k[f];  y = sum_f e^(s[f] - m) v[f] / sum_f e^(s[f] - m),  m = max_f s[f]
+//
+// in one pass over the frames with the running maximum and sum.
+#include "attention_device.h"
+
+namespace bl {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;  // packed rows of a workgroup
+
+// Rows of RB bytes in LDS: chunk c of 16 bytes of row r lies at place(r, c). Keys are read a chunk of 32 rows at a
+// time, values four rows by 16 columns at a time (float32: a row of 32 columns).
+template <int RB>
+__device__ __forceinline__ int key_place(int r, int c) {
+    return RB >= 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3);
+}
+
+template <int RB>
+__device__ __forceinline__ int value_place(int r, int c) {
+    return RB >= 128 ? c ^ (r & 3) << 1 : c ^ (r & 2);
+}
+
+// Products of 32 x 32. A fragment of keys or queries: row lane % 32, chunk 2 s + lane / 32 of 16 bytes.
+// The first product gives frames by rows: a lane holds of its row, lane % 32, the frames
+// 8 (i / 4) + 4 (lane / 32) + i % 4 in i = 0 .. 15. That is how the second product takes them, with the values'
+// frames in the same order, so that weights never leave their lane.
+template <typename T>
+struct Of {
+    typedef Vec<T, 8> Frag;
+    static constexpr int kFrames = 64;  // of a tile
+    // Weights are e^(s - m) times 2^lift: those of fp16 keep their 11 bits down to 2^-24 of the largest.
+    static constexpr float kLift = __is_same(T, _Float16) ? 10.0f : 0.0f;
+    static __device__ __forceinline__ F16x mul(const Frag &a, const Frag &b, const F16x &c) {
+        if constexpr (__is_same(T, __bf16)) {
+            return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+        } else {
+            return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+        }
+    }
+    // Four rows from r on by columns: 16 lanes name four elements each of rows r .. r + 3 and receive a column.
+    template <int RB>
+    static __device__ __forceinline__ Vec<T, 4> columns(const char *values, int r, int d, int lane) {
+        typedef short S4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) S4 *Lds;
+        const int row = r + ((lane & 15) >> 2), c = d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+        const char *p = values + row * RB + value_place<RB>(row, c >> 3) * 16 + (c & 7) * 2;
+        return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
+    }
+    // out += values' columns d .. d + 31 of 32 frames from r on, times their weights
+    template <int RB>
+    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const float (&p)[16], F16x out, int lane) {
+        const int h = lane >> 5;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            Frag w;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = static_cast<T>(p[8 * c + j]);
+            const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, d, lane),
+                                                   columns<RB>(values, r + 16 * c + 8 + 4 * h, d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
+            out = mul(v, w, out);
+        }
+        return out;
+    }
+};
+
+template <>
+struct Of<float> {
+    typedef Vec<float, 4> Frag;
+    static constexpr int kFrames = 32;
+    static constexpr float kLift = 0.0f;
+    static __device__ __forceinline__ F16x mul(const Frag &a, const Frag &b, F16x c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+    template <int RB>
+    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const float (&p)[16], F16x out, int lane) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = d + (lane & 31);
+            const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<RB>(row, c >> 2) * 16 + (c & 3) * 4);
+            out = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out, 0, 0, 0);
+        }
+        return out;
+    }
+};
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// D: columns of a tile, the width rounded up; columns behind the width are zeros.
+template <typename T, int D, bool ALIGNED>
+__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a) {
+    typedef Of<T> O;
+    constexpr int kSize = static_cast<int>(sizeof(T)), kPer = 16 / kSize;
+    constexpr int kFrames = D == 256 ? 32 : O::kFrames;
+    constexpr int RB = D * kSize;
+    constexpr int kTile = kFrames * RB;  // bytes of a tile's keys, and of its values
+    constexpr int kLoads = kTile / 1024 / kWaves;
+    constexpr int kSlabs = RB / 32;
+    constexpr int kBlocks = kFrames / 32, kColumns = D / 32;
+    static_assert(kTile % (1024 * kWaves) == 0, "whole instructions a wave");
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kTile];
+
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Work w = work_of(a, kRows, kFrames);
+    if (w.count == 0) return;  // uniform
+
+    // this lane's row, and its queries
+    const int at = wave * 32 + (lane & 31);
+    const bool real = at < w.count;
+    const long long packed = w.first + (real ? at : 0);
+    const long long row = w.row + packed / a.per;
+    const int head = w.group * a.per + static_cast<int>(packed % a.per);
+    const T *const q = static_cast<const T *>(a.q) + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(head) * a.width;
+    typename O::Frag qf[kSlabs];
+#pragma unroll
+    for (int s = 0; s < kSlabs; ++s) {
+        const int c = (2 * s + half) * kPer;
+        qf[s] = __builtin_bit_cast(typename O::Frag, load_vector<false, T, kPer>(q + c, a.width - c));
+    }
+
+    const T *const k = static_cast<const T *>(a.k) + static_cast<size_t>(w.memory) * a.k_stride + static_cast<size_t>(w.group) * a.width;
+    const T *const v = static_cast<const T *>(a.v) + static_cast<size_t>(w.memory) * a.v_stride + static_cast<size_t>(w.group) * a.width;
+    const unsigned char *const mask = a.mask != nullptr ? a.mask + w.memory : nullptr;
+
+    // Which of 64 frames from f on count: bit i is frame f + i. `byte` is the mask's for frame f + lane.
+    auto mask_byte = [&](int f) -> int { return mask != nullptr && f + lane < w.end ? mask[f + lane] : 1; };
+    auto counted = [&](int f, int byte) -> unsigned long long {
+        return __ballot(f + lane < w.end && lane < kFrames && byte != 0);
+    };
+
+    int load_row[kLoads], key_chunk[kLoads], value_chunk[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int byte = (i * kWaves + wave) * 1024 + lane * 16;
+        load_row[i] = byte / RB;
+        key_chunk[i] = key_place<RB>(load_row[i], byte % RB / 16);
+        value_chunk[i] = value_place<RB>(load_row[i], byte % RB / 16);
+    }
+    auto issue = [&](int slot, int f, unsigned long long bits) {
+        if constexpr (ALIGNED) {
+            const T *const kt = k + static_cast<size_t>(f) * a.k_stride, *const vt = v + static_cast<size_t>(f) * a.v_stride;
+            char *const base = lds + slot * 2 * kTile;
+            const int bytes = a.width * kSize;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const bool in = bits >> load_row[i] & 1;
+                const unsigned ko = static_cast<unsigned>(load_row[i] * a.k_stride * kSize) + 16u * key_chunk[i];
+                load_to_lds(kt, base + (i * kWaves + wave) * 1024, in && 16 * key_chunk[i] < bytes ? ko : kOutOfRange, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const bool in = bits >> load_row[i] & 1;
+                const unsigned vo = static_cast<unsigned>(load_row[i] * a.v_stride * kSize) + 16u * value_chunk[i];
+                load_to_lds(vt, base + kTile + (i * kWaves + wave) * 1024, in && 16 * value_chunk[i] < bytes ? vo : kOutOfRange, 0);
+            }
+        }
+    };
+    U4 held_keys[ALIGNED ? 1 : kLoads], held_values[ALIGNED ? 1 : kLoads];
+    auto fetch = [&](int f, unsigned long long bits) {
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const bool in = bits >> load_row[i] & 1;
+                const int kc = key_chunk[i] * kPer, vc = value_chunk[i] * kPer;
+                const size_t r = static_cast<size_t>(f) + load_row[i];
+                held_keys[i] = __builtin_bit_cast(U4, load_vector<false, T, kPer>(k + r * a.k_stride + kc, in ? a.width - kc : 0));
+                held_values[i] = __builtin_bit_cast(U4, load_vector<false, T, kPer>(v + r * a.v_stride + vc, in ? a.width - vc : 0));
+            }
+        }
+    };
+    auto put = [&](int slot) {
+        if constexpr (!ALIGNED) {
+            char *const base = lds + slot * 2 * kTile + wave * 1024 + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                *reinterpret_cast<U4 *>(base + i * kWaves * 1024) = held_keys[i];
+                *reinterpret_cast<U4 *>(base + kTile + i * kWaves * 1024) = held_values[i];
+            }
+        }
+    };
+
+    const float c = a.scale * 1.4426950408889634f;
+    float most = -__builtin_huge_valf(), sum = 0.0f;  // sum: this half's frames
+    F16x out[kColumns];
+#pragma unroll
+    for (int d = 0; d < kColumns; ++d) out[d] = F16x{};
+
+    auto tile = [&](int slot, unsigned long long bits) {
+        const char *const keys = lds + slot * 2 * kTile, *const values = keys + kTile;
+        float p[kBlocks][16];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            F16x s = {};
+            const int r = b * 32 + (lane & 31);
+#pragma unroll
+            for (int i = 0; i < kSlabs; ++i) {
+                s = O::mul(*reinterpret_cast<const typename O::Frag *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16), qf[i], s);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[b][i] = s[i];
+        }
+        constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
+        if (bits != kAll) {  // uniform
+            const unsigned long long mine = bits >> 4 * half;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!(mine >> (32 * b + 8 * (i / 4) + i % 4) & 1)) p[b][i] = -__builtin_huge_valf();
+        }
+        float top = most;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, p[b][i]);
+        top = fmaxf(top, other_half(top));
+        const float from = top == -__builtin_huge_valf() ? 0.0f : top;  // no frame yet: weights of 0
+        const float down = __builtin_amdgcn_exp2f((most - from) * c);
+        const float shift = fmaf(from, c, -O::kLift);
+        most = top;
+        float add = 0.0f;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
+                add += p[b][i];
+            }
+        sum = fmaf(sum, down, add);
+#pragma unroll
+        for (int d = 0; d < kColumns; ++d) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[d][i] *= down;
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int d = 0; d < kColumns; ++d) out[d] = O::template weigh<RB>(values, 32 * b, 32 * d, p[b], out[d], lane);
+    };
+
+    if (w.begin < w.end) {
+        unsigned long long bits = counted(w.begin, mask_byte(w.begin));
+        int next_byte = mask_byte(w.begin + kFrames);
+        if constexpr (ALIGNED) {
+            issue(0, w.begin, bits);
+        } else {
+            fetch(w.begin, bits);
+        }
+        for (int f = w.begin, slot = 0; f < w.end; f += kFrames, slot ^= 1) {
+            const bool more = f + kFrames < w.end;
+            const unsigned long long next = counted(f + kFrames, next_byte);
+            if constexpr (ALIGNED) {
+                meet();  // the tile has landed, and every wave is done with the other one
+                if (more) {
+                    issue(slot ^ 1, f + kFrames, next);
+                    next_byte = mask_byte(f + 2 * kFrames);
+                }
+            } else {
+                put(slot);
+                __syncthreads();
+                if (more) {
+                    fetch(f + kFrames, next);
+                    next_byte = mask_byte(f + 2 * kFrames);
+                }
+            }
+            tile(slot, bits);
+            bits = next;
+        }
+    }
+
+    sum += other_half(sum);
+    if (!real) return;
+    if (a.splits > 1) {
+        float *const part = part_values(a, w.split, row, head);
+#pragma unroll
+        for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int col = 32 * d + 2 * i + 4 * half;
+                if (col < a.padded) *reinterpret_cast<Vec<float, 4> *>(part + col) = {out[d][i], out[d][i + 1], out[d][i + 2], out[d][i + 3]};
+            }
+        if (half == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row, head)) = {fmaf(most, c, -O::kLift), sum};
+        return;
+    }
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;  // no frame: zeros
+    T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
+#pragma unroll
+    for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int col = 32 * d + 2 * i + 4 * half;
+            Vec<T, 4> four;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(out[d][i + e] * inverse);
+            if (col < a.width) store_vector<false, T, 4>(y + col, four, a.width - col);
+        }
+}
+
+// The parts of a row and head, moved to the largest exponent of all, and their quotient.
+template <typename T>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+    const long long number = static_cast<long long>(workgroup_number()) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (number >= static_cast<long long>(a.seq.rows) * a.heads) return;
+    const long long row = number / a.heads;
+    const int head = static_cast<int>(number % a.heads);
+    int j = static_cast<int>(row);
+    if (a.seq.starts != nullptr) {
+        j = sequence_of_row_wave(a.seq, static_cast<int>(row));
+        const Span span = span_of(a.seq, j);
+        if (row < span.first || row >= span.first + span.length) return;  // of no sequence
+    }
+    if (place_of(a.seq, j) < 0) return;
+    float top = -__builtin_huge_valf();
+    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, part_sums(a, s, row, head)[0]);
+    const float from = top == -__builtin_huge_valf() ? 0.0f : top;
+    float sum = 0.0f;
+    Vec<float, 4> v = {};
+    const int col = lane * 4;
+    for (int s = 0; s < a.splits; ++s) {
+        const float *const part = part_sums(a, s, row, head);
+        const float down = __builtin_amdgcn_exp2f(part[0] - from);
+        sum = fmaf(part[1], down, sum);
+        if (col < a.padded) {
+            const Vec<float, 4> add = *reinterpret_cast<const Vec<float, 4> *>(part_values(a, s, row, head) + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(add[e], down, v[e]);
+        }
+    }
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
+    Vec<T, 4> four;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(v[e] * inverse);
+    if (col < a.width) store_vector<false, T, 4>(y + col, four, a.width - col);
+}
+
+unsigned long long tiles_of(const AttentionArgs &a) {
+    if (a.step) return static_cast<unsigned long long>(a.seq.sequences) * ((a.per + kRows - 1) / kRows);
+    return static_cast<unsigned long long>(a.seq.rows) * a.per / kRows + a.seq.sequences;
+}
+
+int splits_of(const AttentionArgs &a) {
+    const unsigned long long work = tiles_of(a) * a.groups;
+    const long long frames = a.seq.places > 0 ? a.memory_rows / a.seq.places : 0;
+    int splits = 1;
+    while (splits < 16 && work * splits * 2 <= 1024 && frames / (splits * 2) >= 128) splits *= 2;
+    return splits;
+}
+
+template <typename T, int D, bool ALIGNED>
+hipError_t run(AttentionArgs a, hipStream_t stream) {
+    a.splits = splits_of(a);
+    a.padded = (a.width + 3) / 4 * 4;
+    const hipError_t e = launch(attention_kernel<T, D, ALIGNED>, tiles_of(a) * a.groups * a.splits, 64 * kWaves, stream, a);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const unsigned long long parts = static_cast<unsigned long long>(a.seq.rows) * a.heads;
+    return launch(attention_join_kernel<T>, (parts + 3) / 4, 256, stream, a);
+}
+
+template <typename T, bool ALIGNED>
+hipError_t by_width(const AttentionArgs &a, hipStream_t stream) {
+    if (a.width <= 32) return run<T, 32, ALIGNED>(a, stream);
+    if (a.width <= 64) return run<T, 64, ALIGNED>(a, stream);
+    if (a.width <= 128) return run<T, 128, ALIGNED>(a, stream);
+    return run<T, 256, ALIGNED>(a, stream);
+}
+
+template <typename T>
+hipError_t by_alignment(const AttentionArgs &a, hipStream_t stream) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          (a.k_stride | a.v_stride | static_cast<uint64_t>(a.width)) * sizeof(T);
+    const uint64_t longest = (a.k_stride > a.v_stride ? a.k_stride : a.v_stride) * sizeof(T);
+    return bits % 16 == 0 && longest <= kBufferBytes / 128 ? by_width<T, true>(a, stream) : by_width<T, false>(a, stream);
+}
+
+}  // namespace
+
+size_t attention_scratch_bytes(const AttentionArgs &a) {
+    if (a.seq.rows <= 0 || a.seq.sequences <= 0) return 0;
+    const int splits = splits_of(a);
+    return splits > 1 ? static_cast<size_t>(splits) * a.seq.rows * a.heads * ((a.width + 3) / 4 * 4 + 2) * 4 : 0;
+}
+
+hipError_t launch_attention(const AttentionArgs &a, Elem type, hipStream_t stream) {
+    if (a.seq.rows <= 0 || a.seq.sequences <= 0) return hipSuccess;
+    switch (type) {
+        case Elem::f32: return by_alignment<float>(a, stream);
+        case Elem::bf16: return by_alignment<__bf16>(a, stream);
+        default: return by_alignment<_Float16>(a, stream);
+    }
+}
+
+}  // namespace bl

@@ -89,4 +89,40 @@ constexpr int kMostTop = 32;
 size_t logprob_scratch_bytes(int rows, int vocabulary, int top, Elem type);
 hipError_t launch_token_logprobs(const LogprobArgs &args, Elem type, hipStream_t stream);
 
+// Sequences of rows (or, with `step`, single rows) that read memories: places are the memories.
+struct AttentionArgs {
+    const void *q = nullptr, *k = nullptr, *v = nullptr;
+    const int *memory_starts = nullptr;
+    const int *memory_lengths = nullptr;
+    const unsigned char *mask = nullptr;
+    void *y = nullptr;
+    float *scratch = nullptr;
+    size_t q_stride = 0, k_stride = 0, v_stride = 0, y_stride = 0;
+    int heads = 0, groups = 0, width = 0;
+    int per = 0;  // heads that share keys and values
+    int memory_rows = 0;
+    float scale = 0.0f;
+    bool step = false;
+    SequenceArgs seq;
+    int splits = 0, padded = 0;  // the launch's own
+};
+
+size_t attention_scratch_bytes(const AttentionArgs &args);
+hipError_t launch_attention(const AttentionArgs &args, Elem type, hipStream_t stream);
+
+struct LinearArgs {
+    const void *x = nullptr, *weight = nullptr, *bias = nullptr, *residual = nullptr;
+    const float *x_scales = nullptr, *weight_scales = nullptr;
+    void *y = nullptr;
+    float *scratch = nullptr;
+    size_t x_stride = 0, weight_stride = 0, residual_stride = 0, y_stride = 0;
+    int rows = 0, in = 0, out = 0;
+    int activation = 0;
+    float slope = 0.0f;
+    int steps = 0, splits = 0, tiles_m = 0, tiles_n = 0;  // the launch's own
+};
+
+size_t linear_scratch_bytes(const LinearArgs &args, Elem type, Eight eight);
+hipError_t launch_linear(const LinearArgs &args, Elem type, Eight eight, hipStream_t stream);
+
 }  // namespace bl

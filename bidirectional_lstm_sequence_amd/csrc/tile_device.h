@@ -1,0 +1,33 @@
+// Device helpers of the kernels that bring tiles to LDS without a pass through registers.
+#pragma once
+
+#include "sequence_device.h"
+
+namespace bl {
+
+constexpr int kBufferWord3 = 0x00020000;  // a raw buffer of bytes
+constexpr int kBufferBytes = 0x7FFFFFFF;
+constexpr unsigned kOutOfRange = 0x80000000u;  // an offset behind every buffer: zeros come
+
+// 16 bytes a lane from base + offset + step to 1024 bytes in a row at `lds` (both uniform, lane i's at lds + 16 i).
+// The host's pass over a kernel does not know the descriptor's type and would drop the kernel.
+__device__ __forceinline__ void load_to_lds(const void *base, char *lds, unsigned offset, int step) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, kBufferBytes, kBufferWord3),
+        (__attribute__((address_space(3))) void *)(lds), 16, offset, step, 0, 0);
+#else
+    (void)base, (void)lds, (void)offset, (void)step;
+#endif
+}
+
+// What this wave loads has landed and what it reads has arrived, then every wave's. A bare barrier: the fence of
+// __syncthreads has the compiler order more than that.
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+}  // namespace bl

@@ -1,6 +1,6 @@
 """Operators of causal sequence layers: argument marshalling for the ``bilstm_causal_conv``,
-``bilstm_scan``, ``bilstm_add_rms_norm`` and ``bilstm_token_logprobs`` entry points of bilstm.h,
-which gives the formulas and the conventions of packed sequences and state caches.
+``bilstm_scan``, ``bilstm_add_rms_norm``, ``bilstm_token_logprobs``, ``bilstm_cross_attention`` and
+``bilstm_linear`` entry points of bilstm.h, which gives the formulas and the conventions of packed sequences and state caches.
 
 Tensors are CUDA (HIP) tensors of one device; float32, bfloat16 and float16 are taken unless a
 tensor is said to be of another type. Rows may have a stride; what lies within a row must be
@@ -23,6 +23,8 @@ _CONV = struct.Struct("<iiQIIIIii" + _VIEW + _BUFFER * 6 + _VIEW)
 _SCAN = struct.Struct("<iiQIIIIIIii" + _VIEW * 5 + _BUFFER * 7 + _VIEW + _BUFFER)
 _NORM = struct.Struct("<iiQIifi" + _VIEW * 2 + _BUFFER + _VIEW * 3 + _BUFFER)
 _LOGPROBS = struct.Struct("<iiQIIIi" + _VIEW + _BUFFER * 6)
+_ATTENTION = struct.Struct("<iiQQIIIIIfii" + _VIEW * 3 + _BUFFER * 5 + _VIEW + _BUFFER)
+_LINEAR = struct.Struct("<iiQIIiifi" + _VIEW * 2 + _BUFFER + _VIEW + _BUFFER * 2 + _VIEW + _BUFFER)
 
 _nothing = (ctypes.c_float * 8)()
 _NO_PLACES = (ctypes.addressof(_nothing) + 15) // 16 * 16
@@ -36,8 +38,10 @@ def signatures() -> dict:
     args = [ctypes.c_char_p, P]
     sizes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint64)]
     sig = {name: (args, ctypes.c_int) for name in ("bilstm_causal_conv", "bilstm_causal_conv_step", "bilstm_scan",
-                                                   "bilstm_scan_step", "bilstm_add_rms_norm", "bilstm_token_logprobs")}
-    for name in ("bilstm_scan_scratch", "bilstm_token_logprobs_scratch"):
+                                                   "bilstm_scan_step", "bilstm_add_rms_norm", "bilstm_token_logprobs",
+                                                   "bilstm_cross_attention", "bilstm_cross_attention_step", "bilstm_linear")}
+    for name in ("bilstm_scan_scratch", "bilstm_token_logprobs_scratch", "bilstm_cross_attention_scratch",
+                 "bilstm_cross_attention_step_scratch", "bilstm_linear_scratch"):
         sig[name] = (sizes, ctypes.c_int)
     return sig
 
@@ -51,7 +55,8 @@ class _Torch:
         self.Tensor, self.empty = torch.Tensor, torch.empty
         self.kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         self.float32, self.int32, self.int64 = torch.float32, torch.int32, torch.int64
-        self.uint8, self.bool = torch.uint8, torch.bool
+        self.uint8, self.bool, self.bfloat16 = torch.uint8, torch.bool, torch.bfloat16
+        self.eight_kinds = {torch.float8_e4m3fn: 1, torch.int8: 2}
         self.eight = {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
         self.grad = torch.is_grad_enabled
         self.forward = torch.autograd.forward_ad
@@ -77,15 +82,16 @@ class _Call:
 
     __slots__ = ("torch", "like", "device", "dtype", "kind", "grad", "dual", "stream")
 
-    def __init__(self, first, name: str, stream):
+    def __init__(self, first, name: str, stream, dtype=None):
         self.torch = t = _torch or _get_torch()
         if not isinstance(first, t.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
         self.like = first
-        self.dtype = first.dtype
+        self.dtype = first.dtype if dtype is None else dtype
         self.kind = t.kinds.get(self.dtype)
         if self.kind is None:
-            raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor, got {self.dtype}")
+            what = name if dtype is None else "what comes of " + name
+            raise TypeError(f"{what} must be a float32, bfloat16 or float16 tensor, got {self.dtype}")
         self.device = first.get_device()
         self.grad = t.grad()
         # outside of every level no tensor has a tangent
@@ -370,3 +376,107 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
         *sizes, 0, *view, *ids, *place(logprobs), *place(entropy), *place(top_tokens), *place(top_logprobs), *scratch))
     del hold  # its memory goes back to the call's stream, behind the call's work
     return TokenLogprobs(logprobs, entropy, top_tokens, top_logprobs)
+
+
+def _attention(name: str, q, k, v, seq_starts, memory_starts, memory_lengths, slots, mask, scale, out, stream):
+    call = _Call(q, "q", stream)
+    torch = call.torch
+    rows, heads, width = shape = _dims(q, "q", 3)
+    held = _dims(k, "k", 3)
+    memory_rows, groups = held[0], held[1]
+    if held[2] != width:
+        raise ValueError(f"k has heads of {held[2]} elements, q of {width}")
+    places = _dims(memory_starts, "memory_starts", 1)[0] - 1
+    if places < 0:
+        raise ValueError("memory_starts must hold one row number more than there are memories")
+    if seq_starts is None:
+        count, starts, named = 0, NO_BUFFER, rows
+    else:
+        named = count = _dims(seq_starts, "seq_starts", 1)[0] - 1
+        if count < 0:
+            raise ValueError("seq_starts must hold one row number more than there are sequences")
+        starts = call.buffer(seq_starts, "seq_starts", (count + 1,), torch.int32)
+    flag = torch.bool if getattr(mask, "dtype", None) == torch.bool else torch.uint8
+    if scale is None:
+        scale = 1.0 / width ** 0.5 if width else 1.0
+    if out is None:
+        out = call.empty(shape)
+    sizes = (call.device, call.kind, rows, memory_rows, heads, groups, width, count, places)
+    head = (*sizes, scale, 0, 0, *call.rows(q, "q", shape), *call.rows(k, "k", held), *call.rows(v, "v", held), *starts,
+            *call.buffer(slots, "slots", (named,), torch.int32),
+            *call.buffer(memory_starts, "memory_starts", (places + 1,), torch.int32),
+            *call.buffer(memory_lengths, "memory_lengths", (places,), torch.int32),
+            *call.buffer(mask, "mask", (memory_rows,), flag), *call.rows(out, "out", shape))
+    hold, scratch = call.scratch(_scratch_bytes(name + "_scratch", _ATTENTION.pack(*sizes, 1.0, *(0,) * 26)))
+    call.run(name, _ATTENTION.pack(*head, *scratch))
+    del hold  # its memory goes back to the call's stream, behind the call's work
+    return out
+
+
+def cross_attention(q, k, v, seq_starts, memory_starts, memory_lengths=None, slots=None, mask=None, scale=None, out=None,
+                    stream=None):
+    """Cross attention of packed sequences of rows to memories of frames; returns y like ``q``.
+
+    ``q`` [rows, heads, width]; ``k`` and ``v`` [memory rows, key heads, width] (head h reads key head
+    h * key heads // heads; at most 256 elements a head); ``seq_starts`` as in ``causal_conv``. Memory p is
+    rows memory_starts[p] .. memory_starts[p + 1] - 1 of ``k`` and ``v`` (``memory_starts`` int32 [memories
+    + 1]), of which the first ``memory_lengths[p]`` count (int32 [memories]; all if None), without those
+    where ``mask`` (bool [memory rows]) is false. ``slots`` int32 [sequences] names the memory each
+    sequence reads (j if None; several may read one, one outside skips the sequence). ``scale`` is
+    1 / sqrt(width) if None. A row with nothing to read gets zeros. Rows of no sequence are not written:
+    pass ``out`` to keep what they hold. Hypotheses of one stream are rows of one sequence.
+    """
+    if seq_starts is None:
+        raise ValueError("seq_starts must hold the sequences' first rows (cross_attention_step takes single rows)")
+    return _attention("bilstm_cross_attention", q, k, v, seq_starts, memory_starts, memory_lengths, slots, mask, scale, out,
+                      stream)
+
+
+def cross_attention_step(q, k, v, memory_starts, memory_lengths=None, slots=None, mask=None, scale=None, out=None,
+                         stream=None):
+    """``cross_attention`` of one row per sequence: row i of ``q`` reads memory ``slots[i]`` (i if None)."""
+    return _attention("bilstm_cross_attention_step", q, k, v, None, memory_starts, memory_lengths, slots, mask, scale, out,
+                      stream)
+
+
+_ACTIVATIONS = {None: 0, "relu": 1, "leaky_relu": 2, "gelu": 3, "silu": 4}
+
+
+def linear(x, weight, bias=None, activation=None, residual=None, x_scales=None, weight_scales=None, slope: float = 0.01,
+           out_type=None, out=None, stream=None):
+    """Matrix product y = act(x weight^T + bias) + residual of ``x`` [rows, in] and ``weight`` [out, in].
+
+    ``activation`` is None, "relu", "leaky_relu" (with ``slope``), "gelu" (with erf) or "silu"; ``bias``
+    [out] and ``residual`` [rows, out] are of y's type, which is ``x``'s. Rows in 8 bits (float8_e4m3fn or
+    int8, as ``add_rms_norm`` gives them) take a weight of the same type and ``x_scales`` [rows] and
+    ``weight_scales`` [out], float32; y's type is then ``out_type``, of ``out`` or bfloat16. ``out`` may be
+    ``residual`` itself.
+    """
+    t = _torch or _get_torch()
+    eight = t.eight_kinds.get(getattr(x, "dtype", None), 0)
+    if eight:
+        kind = out_type or getattr(out, "dtype", None) or t.bfloat16
+        call = _Call(x, "x", stream, kind)
+    else:
+        call = _Call(x, "x", stream)
+        if out_type is not None and out_type != call.dtype:
+            raise TypeError(f"x of {call.dtype} gives y of the same type, not {out_type}")
+        if x_scales is not None or weight_scales is not None:
+            raise ValueError("scales need rows in 8 bits")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None, 'relu', 'leaky_relu', 'gelu' or 'silu', got {activation!r}")
+    rows, inputs = _dims(x, "x", 2)
+    outputs = _dims(weight, "weight", 2)[0]
+    shape = (rows, outputs)
+    if out is None:
+        out = call.empty(shape, call.dtype)
+    sizes = (call.device, call.kind, rows, inputs, outputs, eight)
+    head = (*sizes, _ACTIVATIONS[activation], slope, 0, *call.rows(x, "x", (rows, inputs), x.dtype),
+            *call.rows(weight, "weight", (outputs, inputs), x.dtype), *call.buffer(bias, "bias", (outputs,)),
+            *(NO_ROWS if residual is None else call.rows(residual, "residual", shape)),
+            *call.buffer(x_scales, "x_scales", (rows,), t.float32),
+            *call.buffer(weight_scales, "weight_scales", (outputs,), t.float32), *call.rows(out, "out", shape))
+    hold, scratch = call.scratch(_scratch_bytes("bilstm_linear_scratch", _LINEAR.pack(*sizes, 0, 0.0, *(0,) * 21)))
+    call.run("bilstm_linear", _LINEAR.pack(*head, *scratch))
+    del hold  # its memory goes back to the call's stream, behind the call's work
+    return out

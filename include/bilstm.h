@@ -560,6 +560,95 @@ bilstm_status bilstm_token_logprobs_scratch(const bilstm_logprobs_args *args, ui
 
 bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stream);
 
+/*
+ * Cross attention: rows read memories of frames (the stack's output through two projections, as keys and values).
+ * Per row i of a sequence and head h of group g = h * groups / heads, over the frames f of the sequence's memory
+ * that count:
+ *   s[f] = scale * sum_c q[i][h][c] * k[f][g][c];  y[i][h] = sum_f softmax(s)[f] * v[f][g]
+ * Memory p is the rows memory_starts[p] .. memory_starts[p + 1] - 1 of k and v, of which the first
+ * memory_lengths[p] count, without those whose mask is 0. What the others hold is never used, not-a-numbers included.
+ * Scores, maxima and sums are held in float32; weights enter their product with the values in the tensors' type.
+ * A row without a frame that counts, or with scores of minus infinity alone, gets zeros.
+ * Here `places` are the memories and `slots` names the memory that each sequence reads: several may read one, and
+ * a slot outside 0 .. places - 1 marks padding. memory_starts hold `places` + 1 non-decreasing row numbers; values
+ * outside 0 .. memory_rows, and lengths outside the memory, are clamped.
+ */
+typedef struct {
+    int32_t device;
+    int32_t type;         /* bilstm_type of q, k, v and y */
+    uint64_t rows;        /* rows of q and y, at most 2^31 - 1 */
+    uint64_t memory_rows; /* rows of k, v and mask, at most 2^31 - 1 */
+    uint32_t heads;       /* of q and y: 1 .. 65536, a multiple of groups */
+    uint32_t groups;      /* heads of k and v, each read by heads / groups heads of q */
+    uint32_t width;       /* 1 .. 256 elements a head */
+    uint32_t sequences;   /* bilstm_cross_attention: number of sequences; the step form ignores it */
+    uint32_t places;      /* memories */
+    float scale;          /* > 0 */
+    int32_t reserved[2];  /* 0 */
+    bilstm_rows q;        /* [rows][heads * width] */
+    bilstm_rows k;        /* [memory_rows][groups * width] */
+    bilstm_rows v;        /* [memory_rows][groups * width] */
+    bilstm_buffer starts; /* int32 [sequences + 1]; the step form ignores it */
+    bilstm_buffer slots;  /* int32 [sequences] or [rows], optional */
+    bilstm_buffer memory_starts;  /* int32 [places + 1] */
+    bilstm_buffer memory_lengths; /* int32 [places], optional: all rows count */
+    bilstm_buffer mask;           /* uint8 [memory_rows], optional: all rows count */
+    bilstm_rows y;                /* [rows][heads * width]; must not overlap any input */
+    bilstm_buffer scratch;        /* at least bilstm_cross_attention_scratch() bytes (len in bytes), 16-byte aligned */
+} bilstm_attention_args;
+
+/* Bytes of scratch memory for these sizes (reads device, type, rows, memory_rows, heads, groups, width, sequences and
+ * places of `args`; no pointer), for rows of packed sequences and for single rows. */
+bilstm_status bilstm_cross_attention_scratch(const bilstm_attention_args *args, uint64_t *bytes);
+bilstm_status bilstm_cross_attention_step_scratch(const bilstm_attention_args *args, uint64_t *bytes);
+
+/* Rows of packed sequences. Asynchronous on `stream`. */
+bilstm_status bilstm_cross_attention(const bilstm_attention_args *args, void *stream);
+
+/* One row per sequence: row i reads memory slots[i]. */
+bilstm_status bilstm_cross_attention_step(const bilstm_attention_args *args, void *stream);
+
+/*
+ * Matrix product of rows with bias, activation and residual:
+ *   v[i][o] = sum_c x[i][c] * weight[o][c], times x_scales[i] * weight_scales[o] for 8-bit rows, plus bias[o]
+ *   y[i][o] = act(v) + residual[i][o]
+ * x and weight are of `type`, or with `eight` of 8 bits, as bilstm_add_rms_norm gives its rows and their scales.
+ * Sums are held in float32 (int8: exactly, in int32), y is rounded once. Of e4m3 with y in 16 bits the matrix
+ * cores drop what lies below 2^-13 of the largest of eight neighbouring products; with y in float32 nothing is dropped.
+ */
+typedef enum {
+    BILSTM_ACT_NONE = 0,
+    BILSTM_ACT_RELU = 1,       /* max(v, 0) */
+    BILSTM_ACT_LEAKY_RELU = 2, /* v if v > 0, else v * slope */
+    BILSTM_ACT_GELU = 3,       /* v (1 + erf(v / sqrt 2)) / 2 */
+    BILSTM_ACT_SILU = 4        /* v / (1 + e^-v) */
+} bilstm_activation;
+
+typedef struct {
+    int32_t device;
+    int32_t type;          /* bilstm_type of bias, residual and y, and without `eight` of x and weight */
+    uint64_t rows;         /* at most 2^31 - 1 */
+    uint32_t in;           /* 1 .. 2^28; int8: at most 2^16 */
+    uint32_t out;          /* 1 .. 2^28 */
+    int32_t eight;         /* bilstm_eight of x and weight */
+    int32_t activation;    /* bilstm_activation */
+    float slope;           /* of BILSTM_ACT_LEAKY_RELU, finite */
+    int32_t reserved;      /* 0 */
+    bilstm_rows x;         /* [rows][in] */
+    bilstm_rows weight;    /* [out][in] */
+    bilstm_buffer bias;    /* [out], optional */
+    bilstm_rows residual;  /* [rows][out], optional */
+    bilstm_buffer x_scales;      /* float [rows], with eight */
+    bilstm_buffer weight_scales; /* float [out], with eight */
+    bilstm_rows y;         /* [rows][out]; may be residual itself */
+    bilstm_buffer scratch; /* at least bilstm_linear_scratch() bytes (len in bytes), 16-byte aligned */
+} bilstm_linear_args;
+
+/* Bytes of scratch memory for these sizes (reads device, type, rows, in, out and eight of `args`; no pointer). */
+bilstm_status bilstm_linear_scratch(const bilstm_linear_args *args, uint64_t *bytes);
+
+bilstm_status bilstm_linear(const bilstm_linear_args *args, void *stream);
+
 /* ---- host-only helpers: no GPU call, usable without a device ---------------------- */
 
 /*
