@@ -6,25 +6,24 @@
 namespace bl {
 namespace {
 
-// Workgroup tiles: BM rows by BN outputs, WM x WN waves.
+// One tile of BM rows by BN outputs, WM x WN waves, K steps of 128 bytes through STAGES stages of LDS.
 //
 // ALIGNED: rows of x and weight are whole 16-byte chunks at multiples of 16 bytes and a tile's rows lie within
 // 2 GB: chunks go straight to LDS, and those behind a row's end, which the buffer's range cuts off, are zeros.
 // Else chunks of any alignment pass through registers.
-template <class P, typename Y, int BM, int BN, int WM, int WN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WM * WN) void linear_kernel(LinearArgs a) {
+template <class P, typename Y, int BM, int BN, int WM, int WN, int STAGES, bool ALIGNED>
+__device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile &t, char *lds) {
     typedef typename P::Elem E;
     constexpr int kWaves = WM * WN;
     constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements of a chunk
-    constexpr int kStage = (BM + BN) * kTileBytes;
-    constexpr int kLoads = (BM + BN) / 8 / kWaves;  // a wave's instructions of 8 rows each
+    constexpr int kStage = (BM + BN) * kRowBytes;
+    constexpr int kXLoads = BM / 8 / kWaves, kLoads = (BM + BN) / 8 / kWaves;  // a wave's instructions of 8 rows
     constexpr int NI = BN / WN / 16, NJ = BM / WM / 16;
-    static_assert((BM / 8) % kWaves == 0 && (BN / 8) % kWaves == 0, "whole instructions a wave");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    constexpr int kStep = kRowBytes / static_cast<int>(sizeof(E));
+    static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "whole instructions a wave");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Tile t = tile_of(a, BM, BN);
     if (t.m >= a.rows || t.first >= t.end) return;  // uniform
 
     const E *const x = static_cast<const E *>(a.x) + static_cast<size_t>(t.m) * a.x_stride;
@@ -38,71 +37,61 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_kernel(LinearArgs a) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = {};
 
-    // Row r of a stage holds its chunk c at place c ^ (r & 7), so that the 16 rows of a fragment fall on all banks.
-    const int chunk = (lane & 7) ^ (lane >> 3);  // what this lane brings: rows 8 apart share r & 7
-    unsigned offset[kLoads];
+    // What this lane brings: of each instruction's rows one, the chunk that belongs at its place. Rows behind the
+    // last one repeat it.
+    const int load_row = lane >> 3, chunk = (lane & 7) ^ load_row;
+    auto row_of = [&](int i) { return ((i < kXLoads ? i : i - kXLoads) * kWaves + wave) * 8 + load_row; };
+    auto place_of = [&](int i) { return ((i < kXLoads ? i : i - kXLoads) * kWaves + wave) * 1024 + (i < kXLoads ? 0 : BM * kRowBytes); };
+    unsigned offset[ALIGNED ? kLoads : 1];
     if constexpr (ALIGNED) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const bool of_x = i < BM / 8 / kWaves;
-            const int r = (of_x ? i * kWaves + wave : (i - BM / 8 / kWaves) * kWaves + wave) * 8 + (lane >> 3);
-            const int last = (of_x ? rows : outs) - 1;
-            const size_t stride = of_x ? a.x_stride : a.weight_stride;
+            const int r = row_of(i), last = (i < kXLoads ? rows : outs) - 1;
+            const size_t stride = i < kXLoads ? a.x_stride : a.weight_stride;
             offset[i] = static_cast<unsigned>((r < last ? r : last) * stride * sizeof(E)) + 16u * chunk;
         }
     }
-    auto issue = [&](int slot, int k0) {  // k0 in elements
-        char *const base = lds + slot * kStage;
+    auto issue = [&](int slot, int kt) {
         if constexpr (ALIGNED) {
+            const int k0 = kt * kStep;
             const bool inside = k0 + chunk * kPer < a.in;
-            const int kb = k0 * static_cast<int>(sizeof(E));
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const bool of_x = i < BM / 8 / kWaves;
-                const int place = of_x ? i * kWaves + wave : BM / 8 + (i - BM / 8 / kWaves) * kWaves + wave;
-                load_to_lds(of_x ? x : w, base + place * 1024, inside ? offset[i] : kOutOfRange, kb);
+                load_to_lds(i < kXLoads ? x : w, lds + slot * kStage + place_of(i), inside ? offset[i] : kOutOfRange, kt * kRowBytes);
             }
         }
     };
-    typedef unsigned int u4 __attribute__((ext_vector_type(4)));
-    u4 held[ALIGNED ? 1 : kLoads];
-    auto fetch = [&](int k0) {
+    I4 held[ALIGNED ? 1 : kLoads];
+    auto fetch = [&](int kt) {
         if constexpr (!ALIGNED) {
+            const int k = kt * kStep + chunk * kPer;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const bool of_x = i < BM / 8 / kWaves;
-                const int r = (of_x ? i * kWaves + wave : (i - BM / 8 / kWaves) * kWaves + wave) * 8 + (lane >> 3);
-                const int last = (of_x ? rows : outs) - 1;
-                const int k = k0 + chunk * kPer;
-                const E *p = (of_x ? x : w) + static_cast<size_t>(r < last ? r : last) * (of_x ? a.x_stride : a.weight_stride) + k;
-                held[i] = __builtin_bit_cast(u4, load_vector<false, typename P::Raw, kPer>(
-                                                     reinterpret_cast<const typename P::Raw *>(p), a.in - k));
+                const int r = row_of(i), last = (i < kXLoads ? rows : outs) - 1;
+                const E *p = (i < kXLoads ? x : w) + static_cast<size_t>(r < last ? r : last) * (i < kXLoads ? a.x_stride : a.weight_stride) + k;
+                held[i] = __builtin_bit_cast(I4, load_vector<false, E, kPer>(p, a.in - k));
             }
         }
     };
     auto put = [&](int slot) {
         if constexpr (!ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const bool of_x = i < BM / 8 / kWaves;
-                const int place = of_x ? i * kWaves + wave : BM / 8 + (i - BM / 8 / kWaves) * kWaves + wave;
-                *reinterpret_cast<u4 *>(lds + slot * kStage + place * 1024 + lane * 16) = held[i];
-            }
+            for (int i = 0; i < kLoads; ++i) *reinterpret_cast<I4 *>(lds + slot * kStage + place_of(i) + lane * 16) = held[i];
         }
     };
 
     const int wm = wave % WM, wn = wave / WM;
-    const int fr = lane & 15, quad = lane >> 4;
+    const int fr = lane & 15, quad = lane >> 4, turned = fr & 7;
     auto products = [&](int slot) {
-        const char *const xs = lds + slot * kStage + (wm * (BM / WM) + fr) * kTileBytes;
-        const char *const ws = lds + slot * kStage + (BM + wn * (BN / WN) + fr) * kTileBytes;
+        const char *const xs = lds + slot * kStage + (wm * (BM / WM) + fr) * kRowBytes;
+        const char *const ws = lds + slot * kStage + (BM + wn * (BN / WN) + fr) * kRowBytes;
 #pragma unroll
-        for (int s = 0; s < P::kSlabs; ++s) {
+        for (int s = 0; s < kRowBytes / P::kSlab; ++s) {
             typename P::Frag wf[NI], xf[NJ];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) wf[i] = P::load(ws + i * 16 * kTileBytes, s, quad, fr & 7);
+            for (int i = 0; i < NI; ++i) wf[i] = P::load(ws + i * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) xf[j] = P::load(xs + j * 16 * kTileBytes, s, quad, fr & 7);
+            for (int j = 0; j < NJ; ++j) xf[j] = P::load(xs + j * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -110,43 +99,118 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_kernel(LinearArgs a) {
         }
     };
 
-    constexpr int kStep = kTileBytes / static_cast<int>(sizeof(E));
     if constexpr (ALIGNED) {
-        issue(0, t.first * kStep);
-        for (int kt = t.first, slot = 0; kt < t.end; ++kt, slot ^= 1) {
-            meet();  // the stage has landed, and every wave is done with the other one
-            if (kt + 1 < t.end) issue(slot ^ 1, (kt + 1) * kStep);
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (t.first + s < t.end) issue(s, t.first + s);
+        int slot = 0;
+        for (int kt = t.first; kt < t.end; ++kt) {
+            // step kt has landed, and every wave is done with the stage before it, which takes the step after the
+            // STAGES - 2 that are under way
+            if (kt + STAGES - 2 < t.end) {
+                meet<(STAGES - 2) * kLoads>();
+            } else {
+                meet<0>();
+            }
+            const int ahead = slot == 0 ? STAGES - 1 : slot - 1;
+            if (kt + STAGES - 1 < t.end) issue(ahead, kt + STAGES - 1);
             products(slot);
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
         }
     } else {
-        fetch(t.first * kStep);
+        fetch(t.first);
         for (int kt = t.first, slot = 0; kt < t.end; ++kt, slot ^= 1) {
             put(slot);
             __syncthreads();  // a stage is written again two rounds on, behind the next barrier
-            if (kt + 1 < t.end) fetch((kt + 1) * kStep);
+            if (kt + 1 < t.end) fetch(kt + 1);
             products(slot);
         }
     }
 
-    // Outputs 4 quad .. 4 quad + 3 of a fragment's 16, row fr of its 16.
+    if (a.splits > 1) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int row = t.m + wm * (BM / WM) + j * 16 + fr;
-        if (row >= a.rows) continue;
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int out = t.n + wn * (BN / WN) + i * 16 + 4 * quad;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][j][e]);
-            if (out >= a.out) continue;
-            if (a.splits > 1) {
-                store_part(a, t.split, row, out, v);
-            } else {
-                finish<Y, P::kScaled>(a, row, out, v);
+            for (int i = 0; i < NI; ++i) {
+                const int row = t.m + wm * (BM / WM) + 16 * j + fr, out = t.n + wn * (BN / WN) + 16 * i + 4 * quad;
+                const typename P::Acc &c = acc[i][j];
+                if (row < a.rows && out < a.out) {
+                    *reinterpret_cast<F4 *>(part_of(a, t.split, row, out)) =
+                        F4{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
+                }
             }
+        return;
+    }
+    // Through LDS, 32 rows of the wave at a time, to whole lines of 16 bytes a lane: stores of four outputs from where
+    // the products leave them would fill a quarter of a line each. The loop over the lines is not unrolled: as straight
+    // code the epilogue of 256 x 256 outputs was 130 KB and took 25 us to fetch.
+    constexpr int W = 16 * NI, V = 16 / static_cast<int>(sizeof(Y)), kLanes = W / V, kItems = 32 * kLanes;
+    constexpr int kRow = W + 4;  // floats: the padding spreads rows over the banks
+    static_assert(2 * BN * 4 + kWaves * 32 * kRow * 4 <= STAGES * kStage, "the epilogue fits the stages");
+    static_assert(kItems % 64 == 0 && 64 % kLanes == 0, "a lane keeps its outputs");
+    meet<0>();  // every wave is done with the stages
+    float *const scales = reinterpret_cast<float *>(lds), *const biases = scales + BN;
+    float *const mine = biases + BN + wave * 32 * kRow;
+    for (int i = tid; i < BN; i += 64 * kWaves) {
+        const int out = t.n + i;
+        scales[i] = P::kScaled && out < a.out ? a.weight_scales[out] : 1.0f;
+        biases[i] = a.bias != nullptr && out < a.out ? static_cast<float>(static_cast<const Y *>(a.bias)[out]) : 0.0f;
+    }
+    __syncthreads();
+    const int at = lane % kLanes * V, out = t.n + wn * (BN / WN) + at;
+    float scale[V], bias[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        scale[e] = scales[wn * (BN / WN) + at + e];
+        bias[e] = biases[wn * (BN / WN) + at + e];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) {
+        // what the next line takes from memory is under way while the current one is computed
+        const int last = t.m + wm * (BM / WM) + 16 * j + 32;
+        int row = last - 32 + lane / kLanes;
+        auto row_scale_at = [&](int r) { return P::kScaled && r < last && r < a.rows ? a.x_scales[r] : 1.0f; };
+        Vec<Y, V> residual = residual_of<Y, V>(a, row, out);
+        float row_scale = row_scale_at(row);
+        const float *line = mine + lane / kLanes * kRow + at;
+        own_lds();
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const typename P::Acc &c = acc[i][j + h];
+                *reinterpret_cast<F4 *>(mine + (16 * h + fr) * kRow + 16 * i + 4 * quad) =
+                    F4{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
+            }
+        own_lds();
+#pragma unroll 1
+        for (; row < last; row += 64 / kLanes, line += 64 / kLanes * kRow) {
+            const int next_row = row + 64 / kLanes;
+            const Vec<Y, V> next = residual_of<Y, V>(a, next_row < last ? next_row : a.rows, out);
+            const float next_scale = row_scale_at(next_row);
+            if (row < a.rows && out < a.out) {
+                float sum[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] = line[e];
+                finish<Y, P::kScaled, V>(a, row, out, sum, row_scale, scale, bias, residual);
+            }
+            residual = next;
+            row_scale = next_scale;
         }
     }
+}
+
+template <class P, typename Y, int BM, int BN, int WM, int WN, int STAGES, bool ALIGNED>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_kernel(LinearArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[STAGES * (BM + BN) * kRowBytes];
+    const Tile t = tile_of(a, BM, BN);
+    if constexpr (BM == 256) {
+        if (t.halved) {
+            product_of_tile<P, Y, BM / 2, BN, WM, WN, STAGES, ALIGNED>(a, t, lds);
+            return;
+        }
+    }
+    product_of_tile<P, Y, BM, BN, WM, WN, STAGES, ALIGNED>(a, t, lds);
 }
 
 // The parts of split sums, added in order, and the epilogue.
@@ -154,41 +218,41 @@ template <typename Y, bool SCALED>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
     const unsigned quads = (static_cast<unsigned>(a.out) + 3) / 4;
     const unsigned long long at = static_cast<unsigned long long>(workgroup_number()) * 256 + threadIdx.x;
-    const unsigned long long row = at / quads;
-    if (row >= static_cast<unsigned>(a.rows)) return;
-    const int out = static_cast<int>(at - row * quads) * 4;
-    float v[4] = {};
+    const unsigned long long long_row = at / quads;
+    if (long_row >= static_cast<unsigned>(a.rows)) return;
+    const int row = static_cast<int>(long_row), out = static_cast<int>(at - long_row * quads) * 4;
+    const Vec<Y, 4> residual = residual_of<Y, 4>(a, row, out);
+    float v[4] = {}, scale[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {}, row_scale = 1.0f;
+    if constexpr (SCALED) row_scale = a.x_scales[row];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (out + e >= a.out) continue;
+        if constexpr (SCALED) scale[e] = a.weight_scales[out + e];
+        if (a.bias != nullptr) bias[e] = static_cast<float>(static_cast<const Y *>(a.bias)[out + e]);
+    }
     for (int s = 0; s < a.splits; ++s) {
-        const float *p = part_of(a, s, static_cast<int>(row), out);
-        const Vec<float, 4> part = *reinterpret_cast<const Vec<float, 4> *>(p);
+        const Vec<float, 4> part = *reinterpret_cast<const Vec<float, 4> *>(part_of(a, s, row, out));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += part[e];
     }
-    finish<Y, SCALED>(a, static_cast<int>(row), out, v);
+    finish<Y, SCALED, 4>(a, row, out, v, row_scale, scale, bias, residual);
 }
 
 struct Form {
     int bm, bn, splits;
 };
 
-// K steps of 128 bytes.
-int steps_of(const LinearArgs &a, int size) { return (static_cast<int>((static_cast<long long>(a.in) * size + kTileBytes - 1) / kTileBytes)); }
+constexpr long long kCus = 256;
 
 Form form_of(const LinearArgs &a, int size, bool aligned) {
-    Form f = {};
     const auto tiles = [&](int bm, int bn) {
         return ((static_cast<long long>(a.rows) + bm - 1) / bm) * ((static_cast<long long>(a.out) + bn - 1) / bn);
     };
-    if (aligned && tiles(256, 256) >= 256) {
-        f = {256, 256, 1};
-    } else if (tiles(128, 128) >= 256) {
-        f = {128, 128, 1};
-    } else {
-        f = {64, 64, 1};
-        const int steps = steps_of(a, size);
-        const long long t = tiles(64, 64);
-        while (f.splits < 16 && t * f.splits * 2 <= 1024 && steps / (f.splits * 2) >= 4) f.splits *= 2;
-    }
+    if (aligned && tiles(256, 256) >= kCus) return {256, 256, 1};
+    if (tiles(128, 128) >= kCus) return {128, 128, 1};
+    Form f = {64, 64, 1};
+    const long long steps = (static_cast<long long>(a.in) * size + kRowBytes - 1) / kRowBytes, t = tiles(64, 64);
+    while (f.splits < 16 && t * f.splits * 2 <= 1024 && steps / (f.splits * 2) >= 4) f.splits *= 2;
     return f;
 }
 
@@ -197,17 +261,25 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
     const Form f = form_of(a, sizeof(typename P::Elem), ALIGNED);
     const long long m = (static_cast<long long>(a.rows) + f.bm - 1) / f.bm, n = (static_cast<long long>(a.out) + f.bn - 1) / f.bn;
     a.splits = f.splits;
-    a.steps = steps_of(a, sizeof(typename P::Elem));
+    a.steps = static_cast<int>((static_cast<long long>(a.in) * sizeof(typename P::Elem) + kRowBytes - 1) / kRowBytes);
     a.tiles_m = static_cast<int>(m);
     a.tiles_n = static_cast<int>(n);
-    const unsigned long long blocks = static_cast<unsigned long long>(m) * n * f.splits;
+    unsigned long long blocks = static_cast<unsigned long long>(m) * n * f.splits;
+    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    a.whole = static_cast<int>(blocks);
     hipError_t e = hipSuccess;
     if (f.bm == 256) {
-        if constexpr (ALIGNED) e = launch(linear_kernel<P, Y, 256, 256, 2, 4, ALIGNED>, blocks, 512, stream, a);
+        // One tile a CU at a time: where the last round has work for half of the CUs or less, its tiles are halved.
+        const unsigned long long rest = blocks % kCus;
+        if (rest <= kCus / 2) {
+            a.whole = static_cast<int>(blocks - rest);
+            blocks += rest;
+        }
+        if constexpr (ALIGNED) e = launch(linear_kernel<P, Y, 256, 256, 2, 4, 2, ALIGNED>, blocks, 512, stream, a);
     } else if (f.bm == 128) {
-        e = launch(linear_kernel<P, Y, 128, 128, 2, 2, ALIGNED>, blocks, 256, stream, a);
+        e = launch(linear_kernel<P, Y, 128, 128, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
     } else {
-        e = launch(linear_kernel<P, Y, 64, 64, 2, 2, ALIGNED>, blocks, 256, stream, a);
+        e = launch(linear_kernel<P, Y, 64, 64, 2, 2, ALIGNED ? 3 : 2, ALIGNED>, blocks, 256, stream, a);
     }
     if (e != hipSuccess || f.splits == 1) return e;
     const unsigned long long quads = (static_cast<unsigned long long>(a.out) + 3) / 4 * static_cast<unsigned long long>(a.rows);

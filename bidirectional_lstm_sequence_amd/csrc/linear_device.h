@@ -5,24 +5,27 @@
 
 namespace bl {
 
-constexpr int kTileBytes = 128;  // of one row's K step
-
 typedef float F4 __attribute__((ext_vector_type(4)));
 typedef int I4 __attribute__((ext_vector_type(4)));
 typedef int I8 __attribute__((ext_vector_type(8)));
 
-// Operands by element type. A fragment holds, for row lane % 16 of 16, what lane / 16 contributes to K; as both
-// operands number K alike, any share of a row's chunks will do. `place` is the row's number modulo 8.
+// A row of a stage holds 128 bytes of its K, chunk c of 16 bytes at place c ^ (row & 7): the rows of a fragment fall
+// on all banks.
+constexpr int kRowBytes = 128;
+
+// Operands by element type, for products of 16 x 16 (those of 32 x 32 took 2.1 us a step of 256 x 256 x 64 bfloat16,
+// these 1.6). A fragment holds, for row lane % 16, what lane / 16 contributes to slab s of K; as both operands number
+// K alike, any share of a slab's chunks will do. An accumulator's element e is row 4 (lane / 16) + e of the first
+// operand and row lane % 16 of the second. `turned` is row & 7.
 template <typename T>
 struct Of16 {
     typedef T Elem;
-    typedef T Raw;
     typedef Vec<T, 8> Frag;
     typedef F4 Acc;
-    static constexpr int kSlabs = 2;
+    static constexpr int kSlab = 64;  // bytes of K
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ Frag load(const char *row, int slab, int quad, int place) {
-        return *reinterpret_cast<const Frag *>(row + (((slab * 4 + quad) ^ place) * 16));
+    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
+        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
     }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
         if constexpr (__is_same(T, __bf16)) {
@@ -35,13 +38,12 @@ struct Of16 {
 
 struct OfF32 {
     typedef float Elem;
-    typedef float Raw;
     typedef F4 Frag;
     typedef F4 Acc;
-    static constexpr int kSlabs = 2;
+    static constexpr int kSlab = 64;
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ Frag load(const char *row, int slab, int quad, int place) {
-        return *reinterpret_cast<const Frag *>(row + (((slab * 4 + quad) ^ place) * 16));
+    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
+        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
     }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, Acc c) {
 #pragma unroll
@@ -56,14 +58,13 @@ struct OfF32 {
 // the codes themselves are within 2^-4 of what they stand for. So this one is for outputs of 16 bits.
 struct OfE4m3 {
     typedef unsigned char Elem;
-    typedef unsigned char Raw;
     typedef I8 Frag;
     typedef F4 Acc;
-    static constexpr int kSlabs = 1;
+    static constexpr int kSlab = 128;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int, int quad, int place) {
-        const I4 low = *reinterpret_cast<const I4 *>(row + ((quad ^ place) * 16));
-        const I4 high = *reinterpret_cast<const I4 *>(row + (((quad + 4) ^ place) * 16));
+    static __device__ __forceinline__ Frag load(const char *row, int, int quad, int turned) {
+        const I4 low = *reinterpret_cast<const I4 *>(row + (quad ^ turned) * 16);
+        const I4 high = *reinterpret_cast<const I4 *>(row + ((4 + quad) ^ turned) * 16);
         return __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
@@ -74,15 +75,14 @@ struct OfE4m3 {
 // For outputs of 32 bits e4m3 is widened to bf16, exactly.
 struct OfE4m3Exact {
     typedef unsigned char Elem;
-    typedef unsigned char Raw;
     struct Frag {
         Vec<__bf16, 8> part[2];
     };
     typedef F4 Acc;
-    static constexpr int kSlabs = 2;
+    static constexpr int kSlab = 64;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int slab, int quad, int place) {
-        const I4 codes = *reinterpret_cast<const I4 *>(row + (((slab * 4 + quad) ^ place) * 16));
+    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
+        const I4 codes = *reinterpret_cast<const I4 *>(row + ((4 * s + quad) ^ turned) * 16);
         Frag f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -103,22 +103,23 @@ struct OfE4m3Exact {
 
 struct OfInt8 {
     typedef unsigned char Elem;
-    typedef unsigned char Raw;
     typedef I4 Frag;
     typedef I4 Acc;
-    static constexpr int kSlabs = 2;
+    static constexpr int kSlab = 64;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int slab, int quad, int place) {
-        return *reinterpret_cast<const Frag *>(row + (((slab * 4 + quad) ^ place) * 16));
+    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
+        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
     }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
     }
 };
 
-// A workgroup's tile: first row and output, and its share first .. end - 1 of the K steps.
+// A workgroup's tile: first row and output, and its share first .. end - 1 of the K steps. Number `whole` and those
+// behind it are tiles' halves: the lower or upper half of the rows.
 struct Tile {
     int m, n, first, end, split;
+    bool halved;
 };
 
 // Workgroups go to the 8 XCDs in turn. Each XCD takes a range of tiles in a row, eight row tiles by all outputs
@@ -126,24 +127,31 @@ struct Tile {
 __device__ __forceinline__ Tile tile_of(const LinearArgs &a, int bm, int bn) {
     const unsigned total = static_cast<unsigned>(a.tiles_m) * a.tiles_n;
     unsigned number = workgroup_number();
-    const unsigned split = number / total;
+    Tile tile;
+    const unsigned whole = static_cast<unsigned>(a.whole);
+    const unsigned split = a.splits > 1 ? number / total : 0;
+    tile.split = static_cast<int>(split);
+    tile.halved = number >= whole;
+    tile.first = static_cast<int>(static_cast<long long>(a.steps) * split / a.splits);
+    tile.end = static_cast<int>(static_cast<long long>(a.steps) * (split + 1) / a.splits);
+    unsigned lower = 0;
     number -= split * total;
+    if (tile.halved) {
+        lower = (number - whole) & 1;
+        number = whole + (number - whole) / 2;
+    }
+    if (split >= static_cast<unsigned>(a.splits) || number >= total) {
+        tile.m = a.rows;  // a number behind the last one
+        tile.n = tile.first = tile.end = 0;
+        return tile;
+    }
     const unsigned per = total / 8, rest = total % 8, xcd = number % 8, at = number / 8;
     const unsigned t = xcd * per + (xcd < rest ? xcd : rest) + at;
     constexpr unsigned kGroup = 8;
     const unsigned wide = kGroup * a.tiles_n, group = t / wide, inside = t - group * wide;
     const unsigned left = a.tiles_m - group * kGroup, high = left < kGroup ? left : kGroup;
-    Tile tile;
-    tile.split = static_cast<int>(split);
-    if (split >= static_cast<unsigned>(a.splits)) {
-        tile.m = a.rows;  // a number behind the last one
-        tile.n = tile.first = tile.end = 0;
-        return tile;
-    }
-    tile.m = static_cast<int>(group * kGroup + inside % high) * bm;
+    tile.m = static_cast<int>(group * kGroup + inside % high) * bm + static_cast<int>(lower) * bm / 2;
     tile.n = static_cast<int>(inside / high) * bn;
-    tile.first = static_cast<int>(static_cast<long long>(a.steps) * split / a.splits);
-    tile.end = static_cast<int>(static_cast<long long>(a.steps) * (split + 1) / a.splits);
     return tile;
 }
 
@@ -152,47 +160,79 @@ __device__ __forceinline__ float *part_of(const LinearArgs &a, int split, int ro
     return a.scratch + (static_cast<size_t>(split) * a.rows + row) * width + out;
 }
 
-__device__ __forceinline__ void store_part(const LinearArgs &a, int split, int row, int out, const float (&v)[4]) {
-    *reinterpret_cast<F4 *>(part_of(a, split, row, out)) = F4{v[0], v[1], v[2], v[3]};
+// v times the normal distribution's integral, by e^(z^2) erfc(z) = t P(t), t = 1 / (1 + c z), z = |v| / sqrt 2. P is
+// a fit of the least relative error for z of 0 .. 14, where e^(-z^2) vanishes: 2.5e-8 (degree 8) for float32,
+// 1.0e-6 (degree 6), 2^-19, for 16 bits. Nothing cancels: the tail of negative v keeps its digits.
+template <typename Y>
+__device__ __forceinline__ float gelu(float v) {
+    const float u = fabsf(v);
+    float t, p;
+    if constexpr (sizeof(Y) == 4) {
+        t = __builtin_amdgcn_rcpf(fmaf(u, 0.38f * 0.70710678f, 1.0f));
+        p = fmaf(0.0584217790f, t, -0.2598602861f);
+        p = fmaf(p, t, 0.3593385990f);
+        p = fmaf(p, t, -0.1568387683f);
+        p = fmaf(p, t, 0.2272185822f);
+        p = fmaf(p, t, 0.1396805625f);
+        p = fmaf(p, t, 0.2036852319f);
+        p = fmaf(p, t, 0.2139444557f);
+        p = fmaf(p, t, 0.2144098326f);
+    } else {
+        t = __builtin_amdgcn_rcpf(fmaf(u, 0.38f * 0.70710678f, 1.0f));
+        p = fmaf(-0.1254189850f, t, 0.3360414801f);
+        p = fmaf(p, t, -0.0699207990f);
+        p = fmaf(p, t, 0.2478400746f);
+        p = fmaf(p, t, 0.1805920497f);
+        p = fmaf(p, t, 0.2165778670f);
+        p = fmaf(p, t, 0.2142872767f);
+    }
+    const float tail = 0.5f * (p * t) * __builtin_amdgcn_exp2f(-0.72134752f * (v * v));
+    const float part = v < 0.0f ? tail : 1.0f - tail;
+    return v == -__builtin_huge_valf() ? 0.0f : v * part;
 }
 
+template <typename Y>
 __device__ __forceinline__ float activate(float v, int kind, float slope) {
     switch (kind) {
         case 1: return __builtin_elementwise_maximum(v, 0.0f);
         case 2: return v > 0.0f ? v : v * slope;
-        case 3: return 0.5f * v * erfcf(v * -0.7071067811865476f);  // 1 + erf, without its cancellation
-        case 4: return silu<float>(v);
+        case 3: return gelu<Y>(v);
+        case 4: return v == -__builtin_huge_valf() ? 0.0f : silu<Y>(v);
         default: return v;
     }
 }
 
-// The epilogue of four outputs in a row from `out` on.
-template <typename Y, bool SCALED>
-__device__ __forceinline__ void finish(const LinearArgs &a, int row, int out, float (&v)[4]) {
-    const int count = a.out - out;
+// The epilogue of V outputs in a row from `out` on; `scale` and `bias` are theirs.
+template <typename Y, bool SCALED, int V>
+__device__ __forceinline__ void finish(const LinearArgs &a, int row, int out, float (&v)[V], float row_scale, const float (&scale)[V],
+                                       const float (&bias)[V], const Vec<Y, V> &residual) {
     if constexpr (SCALED) {
-        const float xs = a.x_scales[row];
-        const Vec<float, 4> ws = load_vector<false, float, 4>(a.weight_scales + out, count);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = v[e] * xs * ws[e];
+        for (int e = 0; e < V; ++e) v[e] = v[e] * row_scale * scale[e];
     }
     if (a.bias != nullptr) {
-        const Vec<Y, 4> b = load_vector<false, Y, 4>(static_cast<const Y *>(a.bias) + out, count);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += static_cast<float>(b[e]);
+        for (int e = 0; e < V; ++e) v[e] += bias[e];
     }
+    if (a.activation != 0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], a.activation, a.slope);
+        for (int e = 0; e < V; ++e) v[e] = activate<Y>(v[e], a.activation, a.slope);
+    }
     if (a.residual != nullptr) {
-        const Y *p = static_cast<const Y *>(a.residual) + static_cast<size_t>(row) * a.residual_stride + out;
-        const Vec<Y, 4> r = load_vector<false, Y, 4>(p, count);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += static_cast<float>(r[e]);
+        for (int e = 0; e < V; ++e) v[e] += static_cast<float>(residual[e]);
     }
-    Vec<Y, 4> y;
+    Vec<Y, V> y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = static_cast<Y>(v[e]);
-    store_vector<false, Y, 4>(static_cast<Y *>(a.y) + static_cast<size_t>(row) * a.y_stride + out, y, count);
+    for (int e = 0; e < V; ++e) y[e] = static_cast<Y>(v[e]);
+    store_vector<false, Y, V>(static_cast<Y *>(a.y) + static_cast<size_t>(row) * a.y_stride + out, y, a.out - out);
+}
+
+template <typename Y, int V>
+__device__ __forceinline__ Vec<Y, V> residual_of(const LinearArgs &a, int row, int out) {
+    if (a.residual == nullptr || row >= a.rows) return Vec<Y, V>{};
+    const Y *p = static_cast<const Y *>(a.residual) + static_cast<size_t>(row) * a.residual_stride + out;
+    return load_vector<false, Y, V>(p, a.out - out);
 }
 
 }  // namespace bl

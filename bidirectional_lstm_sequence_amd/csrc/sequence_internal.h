@@ -119,7 +119,7 @@ struct LinearArgs {
     int rows = 0, in = 0, out = 0;
     int activation = 0;
     float slope = 0.0f;
-    int steps = 0, splits = 0, tiles_m = 0, tiles_n = 0;  // the launch's own
+    int steps = 0, splits = 0, tiles_m = 0, tiles_n = 0, whole = 0;  // the launch's own
 };
 
 size_t linear_scratch_bytes(const LinearArgs &args, Elem type, Eight eight);

@@ -21,12 +21,21 @@ __device__ __forceinline__ void load_to_lds(const void *base, char *lds, unsigne
 #endif
 }
 
-// What this wave loads has landed and what it reads has arrived, then every wave's. A bare barrier: the fence of
-// __syncthreads has the compiler order more than that.
+// All but the last LEFT of this wave's loads have landed and what it reads has arrived, then every wave's. A bare
+// barrier: the fence of __syncthreads would wait for all loads.
+template <int LEFT = 0>
 __device__ __forceinline__ void meet() {
+    static_assert(LEFT < 64, "vmcnt holds six bits");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);  // vmcnt LEFT, lgkmcnt 0
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A wave's own LDS: what its lanes have written is there for all of them, and what they have read is read.
+__device__ __forceinline__ void own_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
     asm volatile("" ::: "memory");
 }
 
