@@ -11,16 +11,18 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;  // packed rows of a workgroup
 
-// Rows of RB bytes in LDS: chunk c of 16 bytes of row r lies at place(r, c). Keys are read a chunk of 32 rows at a
-// time, values four rows by 16 columns at a time (float32: a row of 32 columns).
+// Rows of RB bytes in LDS: chunk c of 16 bytes of row r lies at place(r, c), so that what one instruction reads falls
+// on all 64 banks. Keys are read a chunk of 32 rows at a time; values four rows by 64 bytes, or in float32 two rows,
+// four apart, by 128.
 template <int RB>
 __device__ __forceinline__ int key_place(int r, int c) {
     return RB >= 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3);
 }
 
-template <int RB>
+template <typename T, int RB>
 __device__ __forceinline__ int value_place(int r, int c) {
-    return RB >= 128 ? c ^ (r & 3) << 1 : c ^ (r & 2);
+    if constexpr (sizeof(T) == 4) return RB >= 256 ? c ^ (r & 4) << 1 : c;
+    return RB >= 256 ? c ^ (r & 3) << 2 : (RB == 128 ? c ^ (r & 2) << 1 : c);
 }
 
 // Products of 32 x 32. A fragment of keys or queries: row lane % 32, chunk 2 s + lane / 32 of 16 bytes.
@@ -31,8 +33,10 @@ template <typename T>
 struct Of {
     typedef Vec<T, 8> Frag;
     static constexpr int kFrames = 64;  // of a tile
-    // Weights are e^(s - m) times 2^lift: those of fp16 keep their 11 bits down to 2^-24 of the largest.
+    // Weights are e^(s - m) times 2^kLift, for an m within 2^kLag of the largest: those of fp16 keep their 11 bits
+    // down to 2^-24 of the largest and stay below 2^15.
     static constexpr float kLift = __is_same(T, _Float16) ? 10.0f : 0.0f;
+    static constexpr float kLag = __is_same(T, _Float16) ? 5.0f : 8.0f;
     static __device__ __forceinline__ F16x mul(const Frag &a, const Frag &b, const F16x &c) {
         if constexpr (__is_same(T, __bf16)) {
             return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -46,12 +50,12 @@ struct Of {
         typedef short S4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) S4 *Lds;
         const int row = r + ((lane & 15) >> 2), c = d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
-        const char *p = values + row * RB + value_place<RB>(row, c >> 3) * 16 + (c & 7) * 2;
+        const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
     // out += values' columns d .. d + 31 of 32 frames from r on, times their weights
     template <int RB>
-    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const float (&p)[16], F16x out, int lane) {
+    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const F16x &p, F16x out, int lane) {
         const int h = lane >> 5;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -70,18 +74,18 @@ template <>
 struct Of<float> {
     typedef Vec<float, 4> Frag;
     static constexpr int kFrames = 32;
-    static constexpr float kLift = 0.0f;
+    static constexpr float kLift = 0.0f, kLag = 8.0f;
     static __device__ __forceinline__ F16x mul(const Frag &a, const Frag &b, F16x c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
     template <int RB>
-    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const float (&p)[16], F16x out, int lane) {
+    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const F16x &p, F16x out, int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = d + (lane & 31);
-            const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<RB>(row, c >> 2) * 16 + (c & 3) * 4);
+            const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4);
             out = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out, 0, 0, 0);
         }
         return out;
@@ -92,7 +96,7 @@ __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32);
 
 // D: columns of a tile, the width rounded up; columns behind the width are zeros.
 template <typename T, int D, bool ALIGNED>
-__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void attention_kernel(AttentionArgs a) {
     typedef Of<T> O;
     constexpr int kSize = static_cast<int>(sizeof(T)), kPer = 16 / kSize;
     constexpr int kFrames = D == 256 ? 32 : O::kFrames;
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a)
         const int byte = (i * kWaves + wave) * 1024 + lane * 16;
         load_row[i] = byte / RB;
         key_chunk[i] = key_place<RB>(load_row[i], byte % RB / 16);
-        value_chunk[i] = value_place<RB>(load_row[i], byte % RB / 16);
+        value_chunk[i] = value_place<T, RB>(load_row[i], byte % RB / 16);
     }
     auto issue = [&](int slot, int f, unsigned long long bits) {
         if constexpr (ALIGNED) {
@@ -185,6 +189,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a)
     };
 
     const float c = a.scale * 1.4426950408889634f;
+    constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
     float most = -__builtin_huge_valf(), sum = 0.0f;  // sum: this half's frames
     F16x out[kColumns];
 #pragma unroll
@@ -192,37 +197,43 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a)
 
     auto tile = [&](int slot, unsigned long long bits) {
         const char *const keys = lds + slot * 2 * kTile, *const values = keys + kTile;
-        float p[kBlocks][16];
+        F16x p[kBlocks];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            F16x s = {};
-            const int r = b * 32 + (lane & 31);
-#pragma unroll
-            for (int i = 0; i < kSlabs; ++i) {
-                s = O::mul(*reinterpret_cast<const typename O::Frag *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16), qf[i], s);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[b][i] = s[i];
-        }
-        constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
-        if (bits != kAll) {  // uniform
+        for (int b = 0; b < kBlocks; ++b) p[b] = F16x{};
+        if (bits != kAll) {  // uniform; keys that do not count are zeros and leave their scores at minus infinity
             const unsigned long long mine = bits >> 4 * half;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (!(mine >> (32 * b + 8 * (i / 4) + i % 4) & 1)) p[b][i] = -__builtin_huge_valf();
+                for (int i = 0; i < 16; ++i) p[b][i] = mine >> (32 * b + 8 * (i / 4) + i % 4) & 1 ? 0.0f : -__builtin_huge_valf();
         }
-        float top = most;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int r = b * 32 + (lane & 31);
+#pragma unroll
+            for (int i = 0; i < kSlabs; ++i) {
+                p[b] = O::mul(*reinterpret_cast<const typename O::Frag *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16), qf[i], p[b]);
+            }
+        }
+        float top = -__builtin_huge_valf();
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, p[b][i]);
         top = fmaxf(top, other_half(top));
-        const float from = top == -__builtin_huge_valf() ? 0.0f : top;  // no frame yet: weights of 0
-        const float down = __builtin_amdgcn_exp2f((most - from) * c);
-        const float shift = fmaf(from, c, -O::kLift);
-        most = top;
+        // Weights are measured from `most`, which follows the maximum only where that is kLag further up: sums and
+        // values then move with it. They rarely have to, and a wave whose rows stay skips it.
+        if (__any((top - most) * c > O::kLag)) {  // also from minus infinity; never where both are
+            const float next = fmaxf(top, most);
+            const float down = most == -__builtin_huge_valf() ? 0.0f : __builtin_amdgcn_exp2f((most - next) * c);
+            most = next;
+            sum *= down;
+#pragma unroll
+            for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[d][i] *= down;
+        }
+        const float shift = most == -__builtin_huge_valf() ? 0.0f : fmaf(most, c, -O::kLift);  // no frame yet: weights of 0
         float add = 0.0f;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
@@ -231,12 +242,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionArgs a)
                 p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
                 add += p[b][i];
             }
-        sum = fmaf(sum, down, add);
-#pragma unroll
-        for (int d = 0; d < kColumns; ++d) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[d][i] *= down;
-        }
+        sum += add;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
