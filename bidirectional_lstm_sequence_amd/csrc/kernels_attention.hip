@@ -53,20 +53,22 @@ struct Of {
         const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
-    // out += values' columns d .. d + 31 of 32 frames from r on, times their weights
-    template <int RB>
-    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const F16x &p, F16x out, int lane) {
+    // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
+    template <int RB, int N>
+    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
         const int h = lane >> 5;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             Frag w;
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = static_cast<T>(p[8 * c + j]);
-            const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, d, lane),
-                                                   columns<RB>(values, r + 16 * c + 8 + 4 * h, d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
-            out = mul(v, w, out);
+#pragma unroll
+            for (int d = 0; d < N; ++d) {
+                const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
+                                                       columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
+                out[d] = mul(v, w, out[d]);
+            }
         }
-        return out;
     }
 };
 
@@ -80,15 +82,16 @@ struct Of<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
-    template <int RB>
-    static __device__ __forceinline__ F16x weigh(const char *values, int r, int d, const F16x &p, F16x out, int lane) {
+    template <int RB, int N>
+    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = d + (lane & 31);
-            const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4);
-            out = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out, 0, 0, 0);
-        }
-        return out;
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int d = 0; d < N; ++d) {
+                const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = 32 * d + (lane & 31);
+                const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4);
+                out[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out[d], 0, 0, 0);
+            }
     }
 };
 
@@ -137,6 +140,7 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         return __ballot(f + lane < w.end && lane < kFrames && byte != 0);
     };
 
+    constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
     int load_row[kLoads], key_chunk[kLoads], value_chunk[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -145,22 +149,32 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         key_chunk[i] = key_place<RB>(load_row[i], byte % RB / 16);
         value_chunk[i] = value_place<T, RB>(load_row[i], byte % RB / 16);
     }
+    unsigned key_offset[ALIGNED ? kLoads : 1], value_offset[ALIGNED ? kLoads : 1];
+    if constexpr (ALIGNED) {
+        const int bytes = a.width * kSize;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int kc = 16 * key_chunk[i], vc = 16 * value_chunk[i];
+            key_offset[i] = kc < bytes ? static_cast<unsigned>(load_row[i] * a.k_stride * kSize) + kc : kOutOfRange;
+            value_offset[i] = vc < bytes ? static_cast<unsigned>(load_row[i] * a.v_stride * kSize) + vc : kOutOfRange;
+        }
+    }
     auto issue = [&](int slot, int f, unsigned long long bits) {
         if constexpr (ALIGNED) {
             const T *const kt = k + static_cast<size_t>(f) * a.k_stride, *const vt = v + static_cast<size_t>(f) * a.v_stride;
-            char *const base = lds + slot * 2 * kTile;
-            const int bytes = a.width * kSize;
+            char *const base = lds + slot * 2 * kTile + wave * 1024;
+            if (bits == kAll) {  // uniform
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const bool in = bits >> load_row[i] & 1;
-                const unsigned ko = static_cast<unsigned>(load_row[i] * a.k_stride * kSize) + 16u * key_chunk[i];
-                load_to_lds(kt, base + (i * kWaves + wave) * 1024, in && 16 * key_chunk[i] < bytes ? ko : kOutOfRange, 0);
-            }
+                for (int i = 0; i < kLoads; ++i) load_to_lds(kt, base + i * kWaves * 1024, key_offset[i], 0);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const bool in = bits >> load_row[i] & 1;
-                const unsigned vo = static_cast<unsigned>(load_row[i] * a.v_stride * kSize) + 16u * value_chunk[i];
-                load_to_lds(vt, base + kTile + (i * kWaves + wave) * 1024, in && 16 * value_chunk[i] < bytes ? vo : kOutOfRange, 0);
+                for (int i = 0; i < kLoads; ++i) load_to_lds(vt, base + kTile + i * kWaves * 1024, value_offset[i], 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const bool in = bits >> load_row[i] & 1;
+                    load_to_lds(kt, base + i * kWaves * 1024, in ? key_offset[i] : kOutOfRange, 0);
+                    load_to_lds(vt, base + kTile + i * kWaves * 1024, in ? value_offset[i] : kOutOfRange, 0);
+                }
             }
         }
     };
@@ -189,7 +203,6 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
     };
 
     const float c = a.scale * 1.4426950408889634f;
-    constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
     float most = -__builtin_huge_valf(), sum = 0.0f;  // sum: this half's frames
     F16x out[kColumns];
 #pragma unroll
@@ -197,6 +210,7 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
 
     auto tile = [&](int slot, unsigned long long bits) {
         const char *const keys = lds + slot * 2 * kTile, *const values = keys + kTile;
+        __builtin_amdgcn_s_setprio(1);
         F16x p[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) p[b] = F16x{};
@@ -208,13 +222,13 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
                 for (int i = 0; i < 16; ++i) p[b][i] = mine >> (32 * b + 8 * (i / 4) + i % 4) & 1 ? 0.0f : -__builtin_huge_valf();
         }
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const int r = b * 32 + (lane & 31);
+        for (int i = 0; i < kSlabs; ++i)
 #pragma unroll
-            for (int i = 0; i < kSlabs; ++i) {
+            for (int b = 0; b < kBlocks; ++b) {
+                const int r = b * 32 + (lane & 31);
                 p[b] = O::mul(*reinterpret_cast<const typename O::Frag *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16), qf[i], p[b]);
             }
-        }
+        __builtin_amdgcn_s_setprio(0);
         float top = -__builtin_huge_valf();
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
@@ -244,9 +258,7 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
             }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int d = 0; d < kColumns; ++d) out[d] = O::template weigh<RB>(values, 32 * b, 32 * d, p[b], out[d], lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, p[b], out, lane);
     };
 
     if (w.begin < w.end) {
