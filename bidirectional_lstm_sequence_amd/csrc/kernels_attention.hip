@@ -8,8 +8,13 @@
 namespace bl {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kRows = 32 * kWaves;  // packed rows of a workgroup
+// A workgroup has either 128 packed rows, 32 a wave, and its waves read tiles of frames together (many); or up to 32
+// packed rows, and its waves read every fourth tile each, whose sums they join (few). kRows and kWaves say of which.
+template <bool FEW>
+constexpr int kRows = FEW ? 32 : 128;
+
+template <bool FEW, int RB>  // few: as many as have two tiles of 32 frames in 128 KB
+constexpr int kWaves = !FEW || RB <= 256 ? 4 : (RB == 512 ? 2 : 1);
 
 // Rows of RB bytes in LDS: chunk c of 16 bytes of row r lies at place(r, c), so that what one instruction reads falls
 // on all 64 banks. Keys are read a chunk of 32 rows at a time; values four rows by 64 bytes, or in float32 two rows,
@@ -98,26 +103,29 @@ struct Of<float> {
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
 // D: columns of a tile, the width rounded up; columns behind the width are zeros.
-template <typename T, int D, bool ALIGNED>
-__global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void attention_kernel(AttentionArgs a) {
+template <typename T, int D, bool FEW, bool ALIGNED>
+__global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (D * sizeof(T) <= 256 ? 2 : 1)) void attention_kernel(AttentionArgs a) {
     typedef Of<T> O;
     constexpr int kSize = static_cast<int>(sizeof(T)), kPer = 16 / kSize;
-    constexpr int kFrames = D == 256 ? 32 : O::kFrames;
     constexpr int RB = D * kSize;
+    constexpr int kFrames = FEW || D == 256 ? 32 : O::kFrames;
     constexpr int kTile = kFrames * RB;  // bytes of a tile's keys, and of its values
-    constexpr int kLoads = kTile / 1024 / kWaves;
+    constexpr int kAll = kWaves<FEW, RB>, kSharers = FEW ? 1 : kAll;  // waves; those that bring a tile
+    constexpr int kLoads = kTile / 1024 / kSharers;
     constexpr int kSlabs = RB / 32;
     constexpr int kBlocks = kFrames / 32, kColumns = D / 32;
-    static_assert(kTile % (1024 * kWaves) == 0, "whole instructions a wave");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kTile];
+    static_assert(kTile % (1024 * kSharers) == 0, "whole instructions a wave");
+    __shared__ __attribute__((aligned(1024))) char lds_of_all[2 * 2 * kTile * (FEW ? kAll : 1)];
 
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Work w = work_of(a, kRows, kFrames);
+    const int sharer = FEW ? 0 : wave;
+    char *const lds = lds_of_all + (FEW ? wave * 4 * kTile : 0);
+    const Work w = work_of(a, kRows<FEW>, kFrames);
     if (w.count == 0) return;  // uniform
 
     // this lane's row, and its queries
-    const int at = wave * 32 + (lane & 31);
+    const int at = sharer * 32 + (lane & 31);
     const bool real = at < w.count;
     const long long packed = w.first + (real ? at : 0);
     const long long row = w.row + packed / a.per;
@@ -140,11 +148,11 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         return __ballot(f + lane < w.end && lane < kFrames && byte != 0);
     };
 
-    constexpr unsigned long long kAll = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
+    constexpr unsigned long long kWhole = kFrames == 64 ? ~0ull : (1ull << kFrames) - 1;
     int load_row[kLoads], key_chunk[kLoads], value_chunk[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int byte = (i * kWaves + wave) * 1024 + lane * 16;
+        const int byte = (i * kSharers + sharer) * 1024 + lane * 16;
         load_row[i] = byte / RB;
         key_chunk[i] = key_place<RB>(load_row[i], byte % RB / 16);
         value_chunk[i] = value_place<T, RB>(load_row[i], byte % RB / 16);
@@ -162,18 +170,18 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
     auto issue = [&](int slot, int f, unsigned long long bits) {
         if constexpr (ALIGNED) {
             const T *const kt = k + static_cast<size_t>(f) * a.k_stride, *const vt = v + static_cast<size_t>(f) * a.v_stride;
-            char *const base = lds + slot * 2 * kTile + wave * 1024;
-            if (bits == kAll) {  // uniform
+            char *const base = lds + slot * 2 * kTile + sharer * 1024;
+            if (bits == kWhole) {  // uniform
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) load_to_lds(kt, base + i * kWaves * 1024, key_offset[i], 0);
+                for (int i = 0; i < kLoads; ++i) load_to_lds(kt, base + i * kSharers * 1024, key_offset[i], 0);
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) load_to_lds(vt, base + kTile + i * kWaves * 1024, value_offset[i], 0);
+                for (int i = 0; i < kLoads; ++i) load_to_lds(vt, base + kTile + i * kSharers * 1024, value_offset[i], 0);
             } else {
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
                     const bool in = bits >> load_row[i] & 1;
-                    load_to_lds(kt, base + i * kWaves * 1024, in ? key_offset[i] : kOutOfRange, 0);
-                    load_to_lds(vt, base + kTile + i * kWaves * 1024, in ? value_offset[i] : kOutOfRange, 0);
+                    load_to_lds(kt, base + i * kSharers * 1024, in ? key_offset[i] : kOutOfRange, 0);
+                    load_to_lds(vt, base + kTile + i * kSharers * 1024, in ? value_offset[i] : kOutOfRange, 0);
                 }
             }
         }
@@ -193,11 +201,11 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
     };
     auto put = [&](int slot) {
         if constexpr (!ALIGNED) {
-            char *const base = lds + slot * 2 * kTile + wave * 1024 + lane * 16;
+            char *const base = lds + slot * 2 * kTile + sharer * 1024 + lane * 16;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                *reinterpret_cast<U4 *>(base + i * kWaves * 1024) = held_keys[i];
-                *reinterpret_cast<U4 *>(base + kTile + i * kWaves * 1024) = held_values[i];
+                *reinterpret_cast<U4 *>(base + i * kSharers * 1024) = held_keys[i];
+                *reinterpret_cast<U4 *>(base + kTile + i * kSharers * 1024) = held_values[i];
             }
         }
     };
@@ -214,7 +222,7 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         F16x p[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) p[b] = F16x{};
-        if (bits != kAll) {  // uniform; keys that do not count are zeros and leave their scores at minus infinity
+        if (bits != kWhole) {  // uniform; keys that do not count are zeros and leave their scores at minus infinity
             const unsigned long long mine = bits >> 4 * half;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
@@ -261,37 +269,86 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, p[b], out, lane);
     };
 
-    if (w.begin < w.end) {
-        unsigned long long bits = counted(w.begin, mask_byte(w.begin));
-        int next_byte = mask_byte(w.begin + kFrames);
+    constexpr int kStride = FEW ? kAll * kFrames : kFrames;
+    const int begin = w.begin + (FEW ? wave * kFrames : 0);
+    if (begin < w.end) {  // uniform where waves meet
+        unsigned long long bits = counted(begin, mask_byte(begin));
+        int next_byte = mask_byte(begin + kStride);
         if constexpr (ALIGNED) {
-            issue(0, w.begin, bits);
+            issue(0, begin, bits);
         } else {
-            fetch(w.begin, bits);
+            fetch(begin, bits);
         }
-        for (int f = w.begin, slot = 0; f < w.end; f += kFrames, slot ^= 1) {
-            const bool more = f + kFrames < w.end;
-            const unsigned long long next = counted(f + kFrames, next_byte);
+        for (int f = begin, slot = 0; f < w.end; f += kStride, slot ^= 1) {
+            const bool more = w.end - f > kStride;
+            const unsigned long long next = more ? counted(f + kStride, next_byte) : 0;
             if constexpr (ALIGNED) {
-                meet();  // the tile has landed, and every wave is done with the other one
-                if (more) {
-                    issue(slot ^ 1, f + kFrames, next);
-                    next_byte = mask_byte(f + 2 * kFrames);
-                }
+                meet<0, !FEW>();  // the tile has landed, and every wave is done with the other one
+                if (more) issue(slot ^ 1, f + kStride, next);
             } else {
                 put(slot);
-                __syncthreads();
-                if (more) {
-                    fetch(f + kFrames, next);
-                    next_byte = mask_byte(f + 2 * kFrames);
+                if constexpr (FEW) {
+                    own_lds();
+                } else {
+                    __syncthreads();
                 }
+                if (more) fetch(f + kStride, next);
             }
+            if (w.end - f > 2 * kStride) next_byte = mask_byte(f + 2 * kStride);
             tile(slot, bits);
             bits = next;
         }
     }
 
     sum += other_half(sum);
+    if constexpr (FEW) {
+        // every wave's share of the rows to its own LDS, and from there to whole lines
+        constexpr int kRow = D + 4;  // floats: the padding spreads rows over the banks
+        constexpr int kShare = kTile;  // floats from one wave's share to the next
+        static_assert((32 * kRow + 64) * 4 <= 4 * kTile, "a share fits the wave's tiles");
+        float *const mine = reinterpret_cast<float *>(lds), *const shares = reinterpret_cast<float *>(lds_of_all);
+        own_lds();
+#pragma unroll
+        for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                *reinterpret_cast<Vec<float, 4> *>(mine + at * kRow + 32 * d + 2 * i + 4 * half) = {out[d][i], out[d][i + 1], out[d][i + 2],
+                                                                                                    out[d][i + 3]};
+            }
+        if (half == 0) *reinterpret_cast<Vec<float, 2> *>(mine + 32 * kRow + 2 * at) = {most, sum};
+        __syncthreads();
+        for (int item = threadIdx.x; item < w.count * (D / 4); item += 64 * kAll) {
+            const int r = item / (D / 4), col = item % (D / 4) * 4;
+            if (col >= a.width) continue;
+            float top = -__builtin_huge_valf(), total = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kAll; ++u) top = fmaxf(top, shares[u * kShare + 32 * kRow + 2 * r]);
+            const float from = top == -__builtin_huge_valf() ? 0.0f : top;
+            Vec<float, 4> value = {};
+#pragma unroll
+            for (int u = 0; u < kAll; ++u) {
+                const float *const share = shares + u * kShare;
+                const float down = __builtin_amdgcn_exp2f((share[32 * kRow + 2 * r] - from) * c);
+                total = fmaf(share[32 * kRow + 2 * r + 1], down, total);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) value[e] = fmaf(share[r * kRow + col + e], down, value[e]);
+            }
+            const long long packed_r = w.first + r, row_r = w.row + packed_r / a.per;
+            const int head_r = w.group * a.per + static_cast<int>(packed_r % a.per);
+            if (a.splits > 1) {
+                *reinterpret_cast<Vec<float, 4> *>(part_values(a, w.split, row_r, head_r) + col) = value;
+                if (col == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row_r, head_r)) = {fmaf(top, c, -O::kLift), total};
+            } else {
+                const float inverse = total == 0.0f ? 0.0f : 1.0f / total;  // no frame: zeros
+                Vec<T, 4> four;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(value[e] * inverse);
+                T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row_r) * a.y_stride + static_cast<size_t>(head_r) * a.width;
+                store_vector<false, T, 4>(y + col, four, a.width - col);
+            }
+        }
+        return;
+    }
     if (!real) return;
     if (a.splits > 1) {
         float *const part = part_values(a, w.split, row, head);
@@ -319,74 +376,89 @@ __global__ __launch_bounds__(64 * kWaves, D * sizeof(T) <= 256 ? 2 : 1) void att
         }
 }
 
-// The parts of a row and head, moved to the largest exponent of all, and their quotient.
+// The parts of up to kJoinRows packed rows of one group, moved to the largest exponent of all, and their quotients. Four
+// columns a lane.
+constexpr int kJoinRows = 16;
+
 template <typename T>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
-    const long long number = static_cast<long long>(workgroup_number()) * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (number >= static_cast<long long>(a.seq.rows) * a.heads) return;
-    const long long row = number / a.heads;
-    const int head = static_cast<int>(number % a.heads);
-    int j = static_cast<int>(row);
-    if (a.seq.starts != nullptr) {
-        j = sequence_of_row_wave(a.seq, static_cast<int>(row));
-        const Span span = span_of(a.seq, j);
-        if (row < span.first || row >= span.first + span.length) return;  // of no sequence
-    }
-    if (place_of(a.seq, j) < 0) return;
-    float top = -__builtin_huge_valf();
-    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, part_sums(a, s, row, head)[0]);
-    const float from = top == -__builtin_huge_valf() ? 0.0f : top;
-    float sum = 0.0f;
-    Vec<float, 4> v = {};
-    const int col = lane * 4;
-    for (int s = 0; s < a.splits; ++s) {
-        const float *const part = part_sums(a, s, row, head);
-        const float down = __builtin_amdgcn_exp2f(part[0] - from);
-        sum = fmaf(part[1], down, sum);
-        if (col < a.padded) {
+    const int splits = a.splits;
+    AttentionArgs whole = a;
+    whole.splits = 1;
+    const Work w = work_of(whole, kJoinRows, 1);
+    const int lanes = a.padded / 4;
+    for (int item = threadIdx.x; item < w.count * lanes; item += 256) {
+        const long long packed = w.first + item / lanes;
+        const int col = item % lanes * 4;
+        const long long row = w.row + packed / a.per;
+        const int head = w.group * a.per + static_cast<int>(packed % a.per);
+        float top = -__builtin_huge_valf();
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) top = fmaxf(top, part_sums(a, s, row, head)[0]);
+        const float from = top == -__builtin_huge_valf() ? 0.0f : top;
+        float sum = 0.0f;
+        Vec<float, 4> v = {};
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+            const Vec<float, 2> part = *reinterpret_cast<const Vec<float, 2> *>(part_sums(a, s, row, head));
             const Vec<float, 4> add = *reinterpret_cast<const Vec<float, 4> *>(part_values(a, s, row, head) + col);
+            const float down = __builtin_amdgcn_exp2f(part[0] - from);
+            sum = fmaf(part[1], down, sum);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = fmaf(add[e], down, v[e]);
         }
-    }
-    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
-    Vec<T, 4> four;
+        const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
+        Vec<T, 4> four;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(v[e] * inverse);
-    if (col < a.width) store_vector<false, T, 4>(y + col, four, a.width - col);
+        for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(v[e] * inverse);
+        store_vector<false, T, 4>(y + col, four, a.width - col);
+    }
 }
 
-unsigned long long tiles_of(const AttentionArgs &a) {
-    if (a.step) return static_cast<unsigned long long>(a.seq.sequences) * ((a.per + kRows - 1) / kRows);
-    return static_cast<unsigned long long>(a.seq.rows) * a.per / kRows + a.seq.sequences;
+unsigned long long tiles_of(const AttentionArgs &a, int size) {
+    if (a.step) return static_cast<unsigned long long>(a.seq.sequences) * ((a.per + size - 1) / size);
+    return static_cast<unsigned long long>(a.seq.rows) * a.per / size + a.seq.sequences;
 }
 
+// Whether a sequence has 32 packed rows or less on average. The lengths are on the device: a long sequence among many
+// short ones is then read by several workgroups of 32.
+bool few_rows(const AttentionArgs &a) {
+    return static_cast<unsigned long long>(a.seq.rows) * a.per <= 32ull * a.seq.sequences;
+}
+
+// Frames are split over workgroups where those are few, by what the average sequence and memory have.
 int splits_of(const AttentionArgs &a) {
-    const unsigned long long work = tiles_of(a) * a.groups;
-    const long long frames = a.seq.places > 0 ? a.memory_rows / a.seq.places : 0;
+    const bool few = few_rows(a);
+    const unsigned long long each = (static_cast<unsigned long long>(a.seq.rows) * a.per + a.seq.sequences - 1) / a.seq.sequences;
+    const unsigned long long size = few ? 32 : 128, work = (each + size - 1) / size * a.seq.sequences * a.groups;
+    const long long frames = a.seq.places > 0 ? a.memory_rows / a.seq.places : 0, least = few ? 512 : 128;
     int splits = 1;
-    while (splits < 16 && work * splits * 2 <= 1024 && frames / (splits * 2) >= 128) splits *= 2;
+    while (splits < 16 && work * splits * 2 <= 512 && frames / (splits * 2) >= least) splits *= 2;
     return splits;
 }
 
-template <typename T, int D, bool ALIGNED>
+template <typename T, int D, bool FEW, bool ALIGNED>
 hipError_t run(AttentionArgs a, hipStream_t stream) {
     a.splits = splits_of(a);
     a.padded = (a.width + 3) / 4 * 4;
-    const hipError_t e = launch(attention_kernel<T, D, ALIGNED>, tiles_of(a) * a.groups * a.splits, 64 * kWaves, stream, a);
+    const hipError_t e = launch(attention_kernel<T, D, FEW, ALIGNED>, tiles_of(a, kRows<FEW>) * a.groups * a.splits,
+                                64 * kWaves<FEW, D * sizeof(T)>, stream, a);
     if (e != hipSuccess || a.splits == 1) return e;
-    const unsigned long long parts = static_cast<unsigned long long>(a.seq.rows) * a.heads;
-    return launch(attention_join_kernel<T>, (parts + 3) / 4, 256, stream, a);
+    return launch(attention_join_kernel<T>, tiles_of(a, kJoinRows) * a.groups, 256, stream, a);
+}
+
+template <typename T, bool FEW, bool ALIGNED>
+hipError_t by_width(const AttentionArgs &a, hipStream_t stream) {
+    if (a.width <= 32) return run<T, 32, FEW, ALIGNED>(a, stream);
+    if (a.width <= 64) return run<T, 64, FEW, ALIGNED>(a, stream);
+    if (a.width <= 128) return run<T, 128, FEW, ALIGNED>(a, stream);
+    return run<T, 256, FEW, ALIGNED>(a, stream);
 }
 
 template <typename T, bool ALIGNED>
-hipError_t by_width(const AttentionArgs &a, hipStream_t stream) {
-    if (a.width <= 32) return run<T, 32, ALIGNED>(a, stream);
-    if (a.width <= 64) return run<T, 64, ALIGNED>(a, stream);
-    if (a.width <= 128) return run<T, 128, ALIGNED>(a, stream);
-    return run<T, 256, ALIGNED>(a, stream);
+hipError_t by_rows(const AttentionArgs &a, hipStream_t stream) {
+    return few_rows(a) ? by_width<T, true, ALIGNED>(a, stream) : by_width<T, false, ALIGNED>(a, stream);
 }
 
 template <typename T>
@@ -394,7 +466,7 @@ hipError_t by_alignment(const AttentionArgs &a, hipStream_t stream) {
     const uint64_t bits = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           (a.k_stride | a.v_stride | static_cast<uint64_t>(a.width)) * sizeof(T);
     const uint64_t longest = (a.k_stride > a.v_stride ? a.k_stride : a.v_stride) * sizeof(T);
-    return bits % 16 == 0 && longest <= kBufferBytes / 128 ? by_width<T, true>(a, stream) : by_width<T, false>(a, stream);
+    return bits % 16 == 0 && longest <= kBufferBytes / 128 ? by_rows<T, true>(a, stream) : by_rows<T, false>(a, stream);
 }
 
 }  // namespace

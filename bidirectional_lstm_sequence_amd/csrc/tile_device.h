@@ -23,12 +23,12 @@ __device__ __forceinline__ void load_to_lds(const void *base, char *lds, unsigne
 
 // All but the last LEFT of this wave's loads have landed and what it reads has arrived, then every wave's. A bare
 // barrier: the fence of __syncthreads would wait for all loads.
-template <int LEFT = 0>
+template <int LEFT = 0, bool ALL = true>  // ALL = false: this wave's alone
 __device__ __forceinline__ void meet() {
     static_assert(LEFT < 64, "vmcnt holds six bits");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);  // vmcnt LEFT, lgkmcnt 0
-    __builtin_amdgcn_s_barrier();
+    if constexpr (ALL) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
