@@ -89,9 +89,9 @@ __device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile 
         for (int s = 0; s < kRowBytes / P::kSlab; ++s) {
             typename P::Frag wf[NI], xf[NJ];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) wf[i] = P::load(ws + i * 16 * kRowBytes, s, quad, turned);
+            for (int i = 0; i < NI; ++i) wf[i] = staged<P>(ws + i * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) xf[j] = P::load(xs + j * 16 * kRowBytes, s, quad, turned);
+            for (int j = 0; j < NJ; ++j) xf[j] = staged<P>(xs + j * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -213,6 +213,137 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_kernel(LinearArgs a) {
     product_of_tile<P, Y, BM, BN, WM, WN, STAGES, ALIGNED>(a, t, lds);
 }
 
+// Few rows: the weights' bytes are what counts. A workgroup has 16 NI outputs of all rows, up to 16 NJ; each of its
+// waves takes its share of the K steps, alone, through STAGES stages of its own, and their sums meet in LDS.
+// Eight rows of 128 bytes an instruction, on their way to LDS, come faster than the 16 of 64 bytes that the matrix
+// instruction takes: 52 MB in 11.0 us where those took 14.7.
+constexpr int kFewWaves = 4;
+
+template <class P, typename Y, int NI, int NJ, int STAGES, bool ALIGNED>
+__global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a) {
+    typedef typename P::Elem E;
+    constexpr int kPer = 16 / static_cast<int>(sizeof(E)), kStep = kRowBytes / static_cast<int>(sizeof(E));
+    constexpr int kRow = 16 * NI + 4, kStage = 16 * (NI + NJ) * kRowBytes, kLoads = 2 * (NI + NJ);
+    __shared__ __attribute__((aligned(1024))) char lds_of_all[kFewWaves * STAGES * kStage];
+    static_assert(16 * NJ * kRow * 4 <= STAGES * kStage, "a share of the sums fits the wave's stages");
+    const unsigned number = workgroup_number();
+    const int split = static_cast<int>(number / a.tiles_n), first_out = static_cast<int>(number % a.tiles_n) * 16 * NI;
+    if (split >= a.splits) return;
+    const int lane = threadIdx.x & 63, fr = lane & 15, quad = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char *const lds = lds_of_all + wave * STAGES * kStage;
+    const int part = split * kFewWaves + wave, parts = a.splits * kFewWaves;
+    const int begin = static_cast<int>(static_cast<long long>(a.steps) * part / parts);
+    const int end = static_cast<int>(static_cast<long long>(a.steps) * (part + 1) / parts);
+
+    // what this lane brings: of each instruction's eight rows one; rows and outputs behind the last ones repeat it
+    const E *const weight = static_cast<const E *>(a.weight) + static_cast<size_t>(first_out) * a.weight_stride;
+    const E *const x = static_cast<const E *>(a.x);
+    const int load_row = lane >> 3, chunk = (lane & 7) ^ load_row;
+    size_t at[kLoads];  // elements
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const bool of_w = i < 2 * NI;
+        const int r = (of_w ? i : i - 2 * NI) * 8 + load_row, last = of_w ? a.out - 1 - first_out : a.rows - 1;
+        at[i] = (r < last ? r : last) * (of_w ? a.weight_stride : a.x_stride) + chunk * kPer;
+    }
+    auto issue = [&](int slot, int kt) {
+        if constexpr (ALIGNED) {
+            const bool inside = kt * kStep + chunk * kPer < a.in;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                load_to_lds(i < 2 * NI ? weight : x, lds + slot * kStage + i * 1024,
+                            inside ? static_cast<unsigned>(at[i] * sizeof(E)) : kOutOfRange, kt * kRowBytes);
+            }
+        }
+    };
+    I4 held[ALIGNED ? 1 : kLoads];
+    auto fetch = [&](int kt) {
+        if constexpr (!ALIGNED) {
+            const int k = kt * kStep;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                held[i] = __builtin_bit_cast(I4, load_vector<false, E, kPer>((i < 2 * NI ? weight : x) + at[i] + k, a.in - k - chunk * kPer));
+            }
+        }
+    };
+    typename P::Acc acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = {};
+    auto products = [&](int slot) {
+        const char *const ws = lds + slot * kStage + fr * kRowBytes, *const xs = ws + 16 * NI * kRowBytes;
+#pragma unroll
+        for (int s = 0; s < kRowBytes / P::kSlab; ++s) {
+            typename P::Frag wf[NI], xf[NJ];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) wf[i] = staged<P>(ws + i * 16 * kRowBytes, s, quad, fr & 7);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) xf[j] = staged<P>(xs + j * 16 * kRowBytes, s, quad, fr & 7);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = P::mul(wf[i], xf[j], acc[i][j]);
+        }
+    };
+    if constexpr (ALIGNED) {
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (begin + s < end) issue(s, begin + s);
+        int slot = 0;
+        for (int kt = begin; kt < end; ++kt) {
+            if (kt + STAGES - 2 < end) {  // step kt has landed; what follows it is under way
+                meet<(STAGES - 2) * kLoads, false>();
+            } else {
+                meet<0, false>();
+            }
+            if (kt + STAGES - 1 < end) issue(slot == 0 ? STAGES - 1 : slot - 1, kt + STAGES - 1);
+            products(slot);
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
+    } else {
+        if (begin < end) fetch(begin);
+        for (int kt = begin, slot = 0; kt < end; ++kt, slot ^= 1) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) *reinterpret_cast<I4 *>(lds + slot * kStage + i * 1024 + lane * 16) = held[i];
+            own_lds();
+            if (kt + 1 < end) fetch(kt + 1);
+            products(slot);
+        }
+    }
+    own_lds();
+    float *const shares = reinterpret_cast<float *>(lds_of_all), *const mine = reinterpret_cast<float *>(lds);
+    constexpr int kShare = STAGES * kStage / 4;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const typename P::Acc &c = acc[i][j];
+            *reinterpret_cast<F4 *>(mine + (16 * j + fr) * kRow + 16 * i + 4 * quad) =
+                F4{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
+        }
+    __syncthreads();
+    // four outputs a thread
+    constexpr int kQuads = 4 * NI;
+    for (int item = threadIdx.x; item < 16 * NJ * kQuads; item += 64 * kFewWaves) {
+        const int row = item / kQuads, col = item % kQuads * 4, out = first_out + col;
+        if (row >= a.rows || out >= a.out) continue;
+        float v[4] = {};
+#pragma unroll
+        for (int u = 0; u < kFewWaves; ++u) {
+            const F4 share = *reinterpret_cast<const F4 *>(shares + u * kShare + row * kRow + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += share[e];
+        }
+        if (a.splits > 1) {
+            *reinterpret_cast<F4 *>(part_of(a, split, row, out)) = F4{v[0], v[1], v[2], v[3]};
+            continue;
+        }
+        finish_quad<Y, P::kScaled>(a, row, out, v);
+    }
+}
+
 // The parts of split sums, added in order, and the epilogue.
 template <typename Y, bool SCALED>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
@@ -221,21 +352,14 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
     const unsigned long long long_row = at / quads;
     if (long_row >= static_cast<unsigned>(a.rows)) return;
     const int row = static_cast<int>(long_row), out = static_cast<int>(at - long_row * quads) * 4;
-    const Vec<Y, 4> residual = residual_of<Y, 4>(a, row, out);
-    float v[4] = {}, scale[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {}, row_scale = 1.0f;
-    if constexpr (SCALED) row_scale = a.x_scales[row];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (out + e >= a.out) continue;
-        if constexpr (SCALED) scale[e] = a.weight_scales[out + e];
-        if (a.bias != nullptr) bias[e] = static_cast<float>(static_cast<const Y *>(a.bias)[out + e]);
-    }
+    float v[4] = {};
+#pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
         const Vec<float, 4> part = *reinterpret_cast<const Vec<float, 4> *>(part_of(a, s, row, out));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += part[e];
     }
-    finish<Y, SCALED, 4>(a, row, out, v, row_scale, scale, bias, residual);
+    finish_quad<Y, SCALED>(a, row, out, v);
 }
 
 struct Form {
@@ -243,15 +367,22 @@ struct Form {
 };
 
 constexpr long long kCus = 256;
+constexpr int kFewRows = 32;
 
 Form form_of(const LinearArgs &a, int size, bool aligned) {
     const auto tiles = [&](int bm, int bn) {
         return ((static_cast<long long>(a.rows) + bm - 1) / bm) * ((static_cast<long long>(a.out) + bn - 1) / bn);
     };
+    const long long steps = (static_cast<long long>(a.in) * size + kRowBytes - 1) / kRowBytes;
+    if (a.rows <= kFewRows) {
+        Form f = {a.rows <= 16 ? 16 : 32, a.rows <= 16 ? 16 : 32, 1};
+        while (f.splits < 16 && tiles(f.bm, f.bn) * f.splits * 2 <= kCus && steps / (f.splits * 2) >= 4 * kFewWaves) f.splits *= 2;
+        return f;
+    }
     if (aligned && tiles(256, 256) >= kCus) return {256, 256, 1};
     if (tiles(128, 128) >= kCus) return {128, 128, 1};
     Form f = {64, 64, 1};
-    const long long steps = (static_cast<long long>(a.in) * size + kRowBytes - 1) / kRowBytes, t = tiles(64, 64);
+    const long long t = tiles(64, 64);
     while (f.splits < 16 && t * f.splits * 2 <= 1024 && steps / (f.splits * 2) >= 4) f.splits *= 2;
     return f;
 }
@@ -268,7 +399,14 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     a.whole = static_cast<int>(blocks);
     hipError_t e = hipSuccess;
-    if (f.bm == 256) {
+    if (a.rows <= kFewRows) {
+        constexpr unsigned kThreads = 64 * kFewWaves;
+        if (f.bm == 16) {
+            e = launch(linear_few_kernel<P, Y, 1, 1, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
+        } else {
+            e = launch(linear_few_kernel<P, Y, 2, 2, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
+        }
+    } else if (f.bm == 256) {
         // One tile a CU at a time: where the last round has work for half of the CUs or less, its tiles are halved.
         const unsigned long long rest = blocks % kCus;
         if (rest <= kCus / 2) {

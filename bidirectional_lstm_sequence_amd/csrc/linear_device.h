@@ -24,9 +24,8 @@ struct Of16 {
     typedef F4 Acc;
     static constexpr int kSlab = 64;  // bytes of K
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
-        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
-    }
+    static constexpr int kChunks = 1;  // of 16 bytes in a fragment
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[1]) { return __builtin_bit_cast(Frag, chunk[0]); }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
         if constexpr (__is_same(T, __bf16)) {
             return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -42,9 +41,8 @@ struct OfF32 {
     typedef F4 Acc;
     static constexpr int kSlab = 64;
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
-        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
-    }
+    static constexpr int kChunks = 1;  // of 16 bytes in a fragment
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[1]) { return __builtin_bit_cast(Frag, chunk[0]); }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, Acc c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
@@ -62,10 +60,9 @@ struct OfE4m3 {
     typedef F4 Acc;
     static constexpr int kSlab = 128;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int, int quad, int turned) {
-        const I4 low = *reinterpret_cast<const I4 *>(row + (quad ^ turned) * 16);
-        const I4 high = *reinterpret_cast<const I4 *>(row + ((4 + quad) ^ turned) * 16);
-        return __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
+    static constexpr int kChunks = 2;
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[2]) {
+        return __builtin_shufflevector(chunk[0], chunk[1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
@@ -81,8 +78,9 @@ struct OfE4m3Exact {
     typedef F4 Acc;
     static constexpr int kSlab = 64;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
-        const I4 codes = *reinterpret_cast<const I4 *>(row + ((4 * s + quad) ^ turned) * 16);
+    static constexpr int kChunks = 1;
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[1]) {
+        const I4 &codes = chunk[0];
         Frag f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -107,13 +105,21 @@ struct OfInt8 {
     typedef I4 Acc;
     static constexpr int kSlab = 64;
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ Frag load(const char *row, int s, int quad, int turned) {
-        return *reinterpret_cast<const Frag *>(row + ((4 * s + quad) ^ turned) * 16);
-    }
+    static constexpr int kChunks = 1;  // of 16 bytes in a fragment
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[1]) { return __builtin_bit_cast(Frag, chunk[0]); }
     static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, const Acc &c) {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
     }
 };
+
+// What lane / 16 contributes to slab s from a stage's row.
+template <class P>
+__device__ __forceinline__ typename P::Frag staged(const char *row, int s, int quad, int turned) {
+    I4 chunk[P::kChunks];
+#pragma unroll
+    for (int c = 0; c < P::kChunks; ++c) chunk[c] = *reinterpret_cast<const I4 *>(row + ((4 * (s * P::kChunks + c) + quad) ^ turned) * 16);
+    return P::of(chunk);
+}
 
 // A workgroup's tile: first row and output, and its share first .. end - 1 of the K steps. Number `whole` and those
 // behind it are tiles' halves: the lower or upper half of the rows.
@@ -233,6 +239,26 @@ __device__ __forceinline__ Vec<Y, V> residual_of(const LinearArgs &a, int row, i
     if (a.residual == nullptr || row >= a.rows) return Vec<Y, V>{};
     const Y *p = static_cast<const Y *>(a.residual) + static_cast<size_t>(row) * a.residual_stride + out;
     return load_vector<false, Y, V>(p, a.out - out);
+}
+
+// Four outputs in a row with all that they take.
+template <typename Y, bool SCALED>
+__device__ __forceinline__ void finish_quad(const LinearArgs &a, int row, int out, float (&v)[4]) {
+    const int count = a.out - out;
+    const Vec<Y, 4> residual = residual_of<Y, 4>(a, row, out);
+    float scale[4] = {}, bias[4] = {}, row_scale = 1.0f;
+    if constexpr (SCALED) {
+        row_scale = a.x_scales[row];
+        const Vec<float, 4> s = load_vector<false, float, 4>(a.weight_scales + out, count);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scale[e] = s[e];
+    }
+    if (a.bias != nullptr) {
+        const Vec<Y, 4> b = load_vector<false, Y, 4>(static_cast<const Y *>(a.bias) + out, count);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = static_cast<float>(b[e]);
+    }
+    finish<Y, SCALED, 4>(a, row, out, v, row_scale, scale, bias, residual);
 }
 
 }  // namespace bl
