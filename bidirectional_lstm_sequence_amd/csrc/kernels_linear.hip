@@ -32,10 +32,6 @@ __device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile 
     const int outs = a.out - t.n < BN ? a.out - t.n : BN;
 
     typename P::Acc acc[NI][NJ];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = {};
 
     // What this lane brings: of each instruction's rows one, the chunk that belongs at its place. Rows behind the
     // last one repeat it.
@@ -82,48 +78,81 @@ __device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile 
 
     const int wm = wave % WM, wn = wave / WM;
     const int fr = lane & 15, quad = lane >> 4, turned = fr & 7;
-    auto products = [&](int slot) {
+    // sums[i][j] += what a stage gives for the wave's 16 outputs from 16 (first + i) and 16 rows from 16 j
+    auto products = [&](int slot, auto by, int first, auto &sums) {
+        typedef decltype(by) Q;
+        constexpr int kOuts = sizeof(sums) / sizeof(sums[0]);
         const char *const xs = lds + slot * kStage + (wm * (BM / WM) + fr) * kRowBytes;
-        const char *const ws = lds + slot * kStage + (BM + wn * (BN / WN) + fr) * kRowBytes;
+        const char *const ws = lds + slot * kStage + (BM + wn * (BN / WN) + 16 * first + fr) * kRowBytes;
 #pragma unroll
-        for (int s = 0; s < kRowBytes / P::kSlab; ++s) {
-            typename P::Frag wf[NI], xf[NJ];
+        for (int s = 0; s < kRowBytes / Q::kSlab; ++s) {
+            typename Q::Frag wf[kOuts], xf[NJ];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) wf[i] = staged<P>(ws + i * 16 * kRowBytes, s, quad, turned);
+            for (int i = 0; i < kOuts; ++i) wf[i] = staged<Q>(ws + i * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) xf[j] = staged<P>(xs + j * 16 * kRowBytes, s, quad, turned);
+            for (int j = 0; j < NJ; ++j) xf[j] = staged<Q>(xs + j * 16 * kRowBytes, s, quad, turned);
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
+            for (int i = 0; i < kOuts; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) acc[i][j] = P::mul(wf[i], xf[j], acc[i][j]);
+                for (int j = 0; j < NJ; ++j) sums[i][j] = Q::mul(wf[i], xf[j], sums[i][j]);
         }
     };
-
-    if constexpr (ALIGNED) {
+    auto sum_up = [&](auto by, int first, auto &sums) {
+        if constexpr (ALIGNED) {
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (t.first + s < t.end) issue(s, t.first + s);
-        int slot = 0;
-        for (int kt = t.first; kt < t.end; ++kt) {
-            // step kt has landed, and every wave is done with the stage before it, which takes the step after the
-            // STAGES - 2 that are under way
-            if (kt + STAGES - 2 < t.end) {
-                meet<(STAGES - 2) * kLoads>();
-            } else {
-                meet<0>();
+            for (int s = 0; s < STAGES - 1; ++s)
+                if (t.first + s < t.end) issue(s, t.first + s);
+            int slot = 0;
+            for (int kt = t.first; kt < t.end; ++kt) {
+                // step kt has landed, and every wave is done with the stage before it, which takes the step after the
+                // STAGES - 2 that are under way
+                if (kt + STAGES - 2 < t.end) {
+                    meet<(STAGES - 2) * kLoads>();
+                } else {
+                    meet<0>();
+                }
+                const int ahead = slot == 0 ? STAGES - 1 : slot - 1;
+                if (kt + STAGES - 1 < t.end) issue(ahead, kt + STAGES - 1);
+                products(slot, by, first, sums);
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
             }
-            const int ahead = slot == 0 ? STAGES - 1 : slot - 1;
-            if (kt + STAGES - 1 < t.end) issue(ahead, kt + STAGES - 1);
-            products(slot);
-            slot = slot + 1 == STAGES ? 0 : slot + 1;
+        } else {
+            fetch(t.first);
+            for (int kt = t.first, slot = 0; kt < t.end; ++kt, slot ^= 1) {
+                put(slot);
+                __syncthreads();  // a stage is written again two rounds on, behind the next barrier
+                if (kt + 1 < t.end) fetch(kt + 1);
+                products(slot, by, first, sums);
+            }
         }
-    } else {
-        fetch(t.first);
-        for (int kt = t.first, slot = 0; kt < t.end; ++kt, slot ^= 1) {
-            put(slot);
-            __syncthreads();  // a stage is written again two rounds on, behind the next barrier
-            if (kt + 1 < t.end) fetch(kt + 1);
-            products(slot);
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = {};
+    sum_up(P{}, 0, acc);
+    if constexpr (__is_same(P, OfF32Split)) {
+        auto odd = [](float v) { return !(fabsf(v) < __builtin_huge_valf()); };
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) any |= odd(acc[i][j][e]);
+        if (__syncthreads_or(any)) {
+            // sixteen outputs at a time, for the registers; sums that are finite stay as they are
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                F4 again[1][NJ] = {};
+                sum_up(OfF32{}, i, again);
+                meet<0>();
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (odd(acc[i][j][e])) acc[i][j][e] = again[0][j][e];
+            }
         }
     }
 
@@ -379,13 +408,22 @@ Form form_of(const LinearArgs &a, int size, bool aligned) {
         while (f.splits < 16 && tiles(f.bm, f.bn) * f.splits * 2 <= kCus && steps / (f.splits * 2) >= 4 * kFewWaves) f.splits *= 2;
         return f;
     }
-    if (aligned && tiles(256, 256) >= kCus) return {256, 256, 1};
-    if (tiles(128, 128) >= kCus) return {128, 128, 1};
+    if (aligned && size < 4 && tiles(256, 256) >= kCus) return {256, 256, 1};
+    if (tiles(128, 128) >= 4 * kCus) return {128, 128, 1};
     Form f = {64, 64, 1};
     const long long t = tiles(64, 64);
-    while (f.splits < 16 && t * f.splits * 2 <= 1024 && steps / (f.splits * 2) >= 4) f.splits *= 2;
+    while (f.splits < 16 && t * f.splits * 2 <= 3 * kCus && steps / (f.splits * 2) >= 8) f.splits *= 2;
     return f;
 }
+
+template <class P>
+struct FewOf {
+    typedef P type;
+};
+template <>
+struct FewOf<OfF32Split> {
+    typedef OfF32 type;  // bound by memory, it needs no parts
+};
 
 template <class P, typename Y, bool ALIGNED>
 hipError_t by_form(LinearArgs a, hipStream_t stream) {
@@ -399,12 +437,13 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     a.whole = static_cast<int>(blocks);
     hipError_t e = hipSuccess;
+    typedef typename FewOf<P>::type Few;
     if (a.rows <= kFewRows) {
         constexpr unsigned kThreads = 64 * kFewWaves;
         if (f.bm == 16) {
-            e = launch(linear_few_kernel<P, Y, 1, 1, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
+            e = launch(linear_few_kernel<Few, Y, 1, 1, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
         } else {
-            e = launch(linear_few_kernel<P, Y, 2, 2, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
+            e = launch(linear_few_kernel<Few, Y, 2, 2, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
         }
     } else if (f.bm == 256) {
         // One tile a CU at a time: where the last round has work for half of the CUs or less, its tiles are halved.
@@ -413,11 +452,11 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
             a.whole = static_cast<int>(blocks - rest);
             blocks += rest;
         }
-        if constexpr (ALIGNED) e = launch(linear_kernel<P, Y, 256, 256, 2, 4, 2, ALIGNED>, blocks, 512, stream, a);
+        if constexpr (ALIGNED && sizeof(typename P::Elem) < 4) e = launch(linear_kernel<P, Y, 256, 256, 2, 4, 2, ALIGNED>, blocks, 512, stream, a);
     } else if (f.bm == 128) {
         e = launch(linear_kernel<P, Y, 128, 128, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
     } else {
-        e = launch(linear_kernel<P, Y, 64, 64, 2, 2, ALIGNED ? 3 : 2, ALIGNED>, blocks, 256, stream, a);
+        e = launch(linear_kernel<P, Y, 64, 64, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
     }
     if (e != hipSuccess || f.splits == 1) return e;
     const unsigned long long quads = (static_cast<unsigned long long>(a.out) + 3) / 4 * static_cast<unsigned long long>(a.rows);
@@ -470,7 +509,7 @@ hipError_t launch_linear(const LinearArgs &a, Elem type, Eight eight, hipStream_
         default: break;
     }
     switch (type) {
-        case Elem::f32: return by_alignment<OfF32, float>(a, stream);
+        case Elem::f32: return by_alignment<OfF32Split, float>(a, stream);
         case Elem::bf16: return by_alignment<Of16<__bf16>, __bf16>(a, stream);
         default: return by_alignment<Of16<_Float16>, _Float16>(a, stream);
     }

@@ -50,6 +50,50 @@ struct OfF32 {
     }
 };
 
+// float32 by three bf16 parts of each operand, which hold its 24 bits: six products of parts (those left out are below
+// 2^-25 of the whole) at sixteen times the rate of float32's. A part of an infinity, or of what bf16 rounds to one, is
+// not a number; a tile with sums that are not finite is computed again by OfF32.
+struct OfF32Split {
+    typedef float Elem;
+    struct Frag {
+        Vec<__bf16, 8> part[3];
+    };
+    typedef F4 Acc;
+    static constexpr int kSlab = 128;
+    static constexpr bool kScaled = false;
+    static constexpr int kChunks = 2;
+    static __device__ __forceinline__ Frag of(const I4 (&chunk)[2]) {
+        typedef __bf16 B2 __attribute__((ext_vector_type(2)));
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __int_as_float(chunk[e / 4][e % 4]);
+        Frag f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            I4 bits;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const B2 pair = {static_cast<__bf16>(v[e]), static_cast<__bf16>(v[e + 1])};
+                unsigned both = __builtin_bit_cast(unsigned, pair);
+                asm("" : "+v"(both));  // opaque, else the compiler rounds a second time to widen
+                bits[e / 2] = static_cast<int>(both);
+                v[e] -= __uint_as_float(both << 16);
+                v[e + 1] -= __uint_as_float(both & 0xFFFF0000u);
+            }
+            f.part[p] = __builtin_bit_cast(Vec<__bf16, 8>, bits);
+        }
+        return f;
+    }
+    static __device__ __forceinline__ Acc mul(const Frag &a, const Frag &b, Acc c) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[2], b.part[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[0], b.part[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[1], b.part[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[1], b.part[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[0], b.part[1], c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[0], b.part[0], c, 0, 0, 0);
+    }
+};
+
 // e4m3 by the instruction with block scales, here 2^0, at twice the rate of 16 bits. The matrix cores bring eight
 // neighbouring products of 8-bit floats to the place of the largest and drop what lies below 2^-13 of it (also
 // without scales, measured; further sums are those of float32): at most 2^-10 of that product for the eight, where
