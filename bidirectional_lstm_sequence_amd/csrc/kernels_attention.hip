@@ -8,13 +8,14 @@
 namespace bl {
 namespace {
 
-// A workgroup has either 128 packed rows, 32 a wave, and its waves read tiles of frames together (many); or up to 32
-// packed rows, and its waves read every fourth tile each, whose sums they join (few). kRows and kWaves say of which.
-template <bool FEW>
-constexpr int kRows = FEW ? 32 : 128;
-
+// A workgroup has either 128 or 256 packed rows, 32 a wave, and its waves read tiles of frames together (many); or up
+// to 32 packed rows, and its waves read every fourth tile each, whose sums they join (few). Many with keys of RB = 512
+// bytes take eight waves, so that two share a SIMD: 389 us where four take 611 (8192 rows, 16 heads of 256).
 template <bool FEW, int RB>  // few: as many as have two tiles of 32 frames in 128 KB
-constexpr int kWaves = !FEW || RB <= 256 ? 4 : (RB == 512 ? 2 : 1);
+constexpr int kWaves = FEW ? (RB <= 256 ? 4 : (RB == 512 ? 2 : 1)) : (RB == 512 ? 8 : 4);
+
+template <bool FEW, int RB>
+constexpr int kRows = FEW ? 32 : 32 * kWaves<FEW, RB>;
 
 // Rows of RB bytes in LDS: chunk c of 16 bytes of row r lies at place(r, c), so that what one instruction reads falls
 // on all 64 banks. Keys are read a chunk of 32 rows at a time; values four rows by 64 bytes, or in float32 two rows,
@@ -94,7 +95,8 @@ struct Of<float> {
 #pragma unroll
             for (int d = 0; d < N; ++d) {
                 const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = 32 * d + (lane & 31);
-                const float v = *reinterpret_cast<const float *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4);
+                const float v = __uint_as_float(
+                    *reinterpret_cast<const unsigned *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4));
                 out[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out[d], 0, 0, 0);
             }
     }
@@ -104,7 +106,7 @@ __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32);
 
 // D: columns of a tile, the width rounded up; columns behind the width are zeros.
 template <typename T, int D, bool FEW, bool ALIGNED>
-__global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (D * sizeof(T) <= 256 ? 2 : 1)) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * sizeof(T) <= 512 ? 2 : 1)) void attention_kernel(AttentionArgs a) {
     typedef Of<T> O;
     constexpr int kSize = static_cast<int>(sizeof(T)), kPer = 16 / kSize;
     constexpr int RB = D * kSize;
@@ -121,7 +123,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (D * sizeof(T) <
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sharer = FEW ? 0 : wave;
     char *const lds = lds_of_all + (FEW ? wave * 4 * kTile : 0);
-    const Work w = work_of(a, kRows<FEW>, kFrames);
+    const Work w = work_of(a, kRows<FEW, RB>, kFrames);
     if (w.count == 0) return;  // uniform
 
     // this lane's row, and its queries
@@ -234,7 +236,9 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (D * sizeof(T) <
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int r = b * 32 + (lane & 31);
-                p[b] = O::mul(*reinterpret_cast<const typename O::Frag *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16), qf[i], p[b]);
+                // read as integers: before floats from LDS the compiler waits for all loads to LDS under way
+                const U4 chunk = *reinterpret_cast<const U4 *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16);
+                p[b] = O::mul(__builtin_bit_cast(typename O::Frag, chunk), qf[i], p[b]);
             }
         __builtin_amdgcn_s_setprio(0);
         float top = -__builtin_huge_valf();
@@ -442,7 +446,7 @@ template <typename T, int D, bool FEW, bool ALIGNED>
 hipError_t run(AttentionArgs a, hipStream_t stream) {
     a.splits = splits_of(a);
     a.padded = (a.width + 3) / 4 * 4;
-    const hipError_t e = launch(attention_kernel<T, D, FEW, ALIGNED>, tiles_of(a, kRows<FEW>) * a.groups * a.splits,
+    const hipError_t e = launch(attention_kernel<T, D, FEW, ALIGNED>, tiles_of(a, kRows<FEW, D * sizeof(T)>) * a.groups * a.splits,
                                 64 * kWaves<FEW, D * sizeof(T)>, stream, a);
     if (e != hipSuccess || a.splits == 1) return e;
     return launch(attention_join_kernel<T>, tiles_of(a, kJoinRows) * a.groups, 256, stream, a);
