@@ -22,7 +22,7 @@ constexpr int kRows = FEW ? 32 : 32 * kWaves<FEW, RB>;
 // four apart, by 128.
 template <int RB>
 __device__ __forceinline__ int key_place(int r, int c) {
-    return RB >= 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3);
+    return RB >= 256 ? c ^ (r & 15) : (RB == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3));
 }
 
 template <typename T, int RB>
