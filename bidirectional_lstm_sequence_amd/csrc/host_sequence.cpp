@@ -15,6 +15,8 @@ namespace {
 
 constexpr uint64_t kMostRows = 0x7FFFFFFFull;
 constexpr uint32_t kMostSequences = 1u << 30;
+constexpr uint64_t kMostMemory = 1ull << 30;                // tiles of frames end within 32 bits
+constexpr uint64_t kMostProductRows = (1ull << 31) - 1024;  // and tiles of rows
 
 // Byte range of a view, for overlap checks; strided views repeat `width` bytes every `stride`.
 struct Bytes {
@@ -526,7 +528,7 @@ bilstm_status attention_sizes(const char *call, const bilstm_attention_args *arg
     if (a.width == 0 || a.width > 256) {
         return fail(BILSTM_UNSUPPORTED, "%s: heads of %u elements (1 to 256 are built)", call, a.width);
     }
-    if (a.rows > kMostRows || a.memory_rows > kMostRows || a.places > kMostRows || (!step && a.sequences > kMostSequences)) {
+    if (a.rows > kMostRows || a.memory_rows > kMostMemory || a.places > kMostRows || (!step && a.sequences > kMostSequences)) {
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows or %llu memory rows exceed the kernels' indexing", call,
                     static_cast<unsigned long long>(a.rows), static_cast<unsigned long long>(a.memory_rows));
     }
@@ -634,7 +636,7 @@ bilstm_status linear_sizes(const char *call, const bilstm_linear_args *args, Lin
     }
     if (a.in == 0 || a.out == 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: %u inputs, %u outputs", call, a.in, a.out);
     // 2^16 products of two int8 codes stay below 2^31
-    if (a.rows > kMostRows || a.in > (1u << 28) || a.out > (1u << 28) || (a.eight == BILSTM_EIGHT_INT8 && a.in > (1u << 16))) {
+    if (a.rows > kMostProductRows || a.in > (1u << 28) || a.out > (1u << 28) || (a.eight == BILSTM_EIGHT_INT8 && a.in > (1u << 16))) {
         return fail(BILSTM_DIMENSION_OVERFLOW, "%s: %llu rows, %u inputs, %u outputs exceed the kernel's indexing", call,
                     static_cast<unsigned long long>(a.rows), a.in, a.out);
     }

@@ -247,11 +247,12 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, p[b][i]);
         top = fmaxf(top, other_half(top));
-        // Weights are measured from `most`, which follows the maximum only where that is kLag further up: sums and
+        // Weights are measured from `most`, which follows a row's maximum only where that is kLag further up: its sums and
         // values then move with it. They rarely have to, and a wave whose rows stay skips it.
-        if (__any((top - most) * c > O::kLag)) {  // also from minus infinity; never where both are
-            const float next = fmaxf(top, most);
-            const float down = most == -__builtin_huge_valf() ? 0.0f : __builtin_amdgcn_exp2f((most - next) * c);
+        const bool moves = (top - most) * c > O::kLag;  // also from minus infinity; never where both are
+        if (__any(moves)) {
+            const float next = moves ? top : most;
+            const float down = !moves ? 1.0f : (most == -__builtin_huge_valf() ? 0.0f : __builtin_amdgcn_exp2f((most - next) * c));
             most = next;
             sum *= down;
 #pragma unroll

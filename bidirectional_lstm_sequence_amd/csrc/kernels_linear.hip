@@ -163,10 +163,7 @@ __device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile 
             for (int i = 0; i < NI; ++i) {
                 const int row = t.m + wm * (BM / WM) + 16 * j + fr, out = t.n + wn * (BN / WN) + 16 * i + 4 * quad;
                 const typename P::Acc &c = acc[i][j];
-                if (row < a.rows && out < a.out) {
-                    *reinterpret_cast<F4 *>(part_of(a, t.split, row, out)) =
-                        F4{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
-                }
+                if (row < a.rows && out < a.out) *reinterpret_cast<typename P::Acc *>(part_of(a, t.split, row, out)) = c;
             }
         return;
     }
@@ -348,9 +345,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
     for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const typename P::Acc &c = acc[i][j];
-            *reinterpret_cast<F4 *>(mine + (16 * j + fr) * kRow + 16 * i + 4 * quad) =
-                F4{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
+            *reinterpret_cast<typename P::Acc *>(mine + (16 * j + fr) * kRow + 16 * i + 4 * quad) = acc[i][j];
         }
     __syncthreads();
     // four outputs a thread
@@ -358,37 +353,29 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinearArgs a
     for (int item = threadIdx.x; item < 16 * NJ * kQuads; item += 64 * kFewWaves) {
         const int row = item / kQuads, col = item % kQuads * 4, out = first_out + col;
         if (row >= a.rows || out >= a.out) continue;
-        float v[4] = {};
+        typename P::Acc v = {};
 #pragma unroll
-        for (int u = 0; u < kFewWaves; ++u) {
-            const F4 share = *reinterpret_cast<const F4 *>(shares + u * kShare + row * kRow + col);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += share[e];
-        }
+        for (int u = 0; u < kFewWaves; ++u) v += *reinterpret_cast<const typename P::Acc *>(shares + u * kShare + row * kRow + col);
         if (a.splits > 1) {
-            *reinterpret_cast<F4 *>(part_of(a, split, row, out)) = F4{v[0], v[1], v[2], v[3]};
-            continue;
+            *reinterpret_cast<typename P::Acc *>(part_of(a, split, row, out)) = v;
+        } else {
+            finish_quad<Y, P>(a, row, out, v);
         }
-        finish_quad<Y, P::kScaled>(a, row, out, v);
     }
 }
 
 // The parts of split sums, added in order, and the epilogue.
-template <typename Y, bool SCALED>
+template <class P, typename Y>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
     const unsigned quads = (static_cast<unsigned>(a.out) + 3) / 4;
     const unsigned long long at = static_cast<unsigned long long>(workgroup_number()) * 256 + threadIdx.x;
     const unsigned long long long_row = at / quads;
     if (long_row >= static_cast<unsigned>(a.rows)) return;
     const int row = static_cast<int>(long_row), out = static_cast<int>(at - long_row * quads) * 4;
-    float v[4] = {};
+    typename P::Acc v = {};
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const Vec<float, 4> part = *reinterpret_cast<const Vec<float, 4> *>(part_of(a, s, row, out));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += part[e];
-    }
-    finish_quad<Y, SCALED>(a, row, out, v);
+    for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const typename P::Acc *>(part_of(a, s, row, out));
+    finish_quad<Y, P>(a, row, out, v);
 }
 
 struct Form {
@@ -460,7 +447,7 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
     }
     if (e != hipSuccess || f.splits == 1) return e;
     const unsigned long long quads = (static_cast<unsigned long long>(a.out) + 3) / 4 * static_cast<unsigned long long>(a.rows);
-    return launch(linear_join_kernel<Y, P::kScaled>, (quads + 255) / 256, 256, stream, a);
+    return launch(linear_join_kernel<Few, Y>, (quads + 255) / 256, 256, stream, a);
 }
 
 bool aligned_rows(const LinearArgs &a, uint64_t size) {

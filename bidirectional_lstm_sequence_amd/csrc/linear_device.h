@@ -286,8 +286,10 @@ __device__ __forceinline__ Vec<Y, V> residual_of(const LinearArgs &a, int row, i
 }
 
 // Four outputs in a row with all that they take.
-template <typename Y, bool SCALED>
-__device__ __forceinline__ void finish_quad(const LinearArgs &a, int row, int out, float (&v)[4]) {
+template <typename Y, class P>
+__device__ __forceinline__ void finish_quad(const LinearArgs &a, int row, int out, const typename P::Acc &sum) {
+    constexpr bool SCALED = P::kScaled;
+    float v[4] = {static_cast<float>(sum[0]), static_cast<float>(sum[1]), static_cast<float>(sum[2]), static_cast<float>(sum[3])};
     const int count = a.out - out;
     const Vec<Y, 4> residual = residual_of<Y, 4>(a, row, out);
     float scale[4] = {}, bias[4] = {}, row_scale = 1.0f;

@@ -577,7 +577,7 @@ typedef struct {
     int32_t device;
     int32_t type;         /* bilstm_type of q, k, v and y */
     uint64_t rows;        /* rows of q and y, at most 2^31 - 1 */
-    uint64_t memory_rows; /* rows of k, v and mask, at most 2^31 - 1 */
+    uint64_t memory_rows; /* rows of k, v and mask, at most 2^30 */
     uint32_t heads;       /* of q and y: 1 .. 65536, a multiple of groups */
     uint32_t groups;      /* heads of k and v, each read by heads / groups heads of q */
     uint32_t width;       /* 1 .. 256 elements a head */
@@ -627,7 +627,7 @@ typedef enum {
 typedef struct {
     int32_t device;
     int32_t type;          /* bilstm_type of bias, residual and y, and without `eight` of x and weight */
-    uint64_t rows;         /* at most 2^31 - 1 */
+    uint64_t rows;         /* at most 2^31 - 1024 */
     uint32_t in;           /* 1 .. 2^28; int8: at most 2^16 */
     uint32_t out;          /* 1 .. 2^28 */
     int32_t eight;         /* bilstm_eight of x and weight */

@@ -154,6 +154,18 @@ def test_not_numbers_stay_in_their_rows(bl, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", [5, 150])
+def test_a_row_does_not_depend_on_its_neighbours(bl, dtype, rows):
+    """Neighbours whose maxima rise from tile to tile leave a row's bits as they are."""
+    q, k, v = _make(dtype, rows, 400, 2, 1, 64, 18)
+    k[:, 0, 0] = (torch.arange(400.0) / 50).to(dtype)
+    clean = _run(bl, q, k, v, [0, rows], [0, 400])
+    q[1::2, :, 0] = 60.0
+    got = _run(bl, q, k, v, [0, rows], [0, 400])
+    assert torch.equal(got[::2], clean[::2]) and not torch.equal(got[1::2], clean[1::2])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_scores_of_minus_infinity_and_of_any_size(bl, dtype):
     """Frames at minus infinity do not count, rows of them alone get zeros; scores may be far from 0."""
     q, k, v = _make(dtype, 34, 70, 1, 1, 8, 12)

@@ -160,6 +160,36 @@ def test_takes_the_norms_rows(bl, eight, rows):
     _same(got, *plain.linear(normed.q.cpu(), w, bias, "silu", None, normed.scales.cpu(), ws, 0.01, torch.bfloat16))
 
 
+@pytest.mark.parametrize("rows", [3, 20, 40, 300])
+def test_sums_of_int8_are_exact(bl, rows):
+    """Sums beyond 2^24, split or not, are rounded once: equal to the exact sum in float32."""
+    inputs, outputs = 32768, 40
+    g = torch.Generator().manual_seed(10)
+    x = torch.randint(-128, 128, (rows, inputs), generator=g).to(torch.int8)
+    w = torch.randint(-128, 128, (outputs, inputs), generator=g).to(torch.int8)
+    x[0], w[0] = 127, 127
+    w[1, : inputs // 2], w[1, inputs // 2:] = 127, -127  # what cancels over the splits
+    w[1, 5] = 126
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    got = bl.linear(x.cuda(), w.cuda(), x_scales=one(rows), weight_scales=one(outputs), out_type=torch.float32)
+    assert torch.equal(got.cpu(), (x.long() @ w.long().t()).float())
+
+
+@pytest.mark.parametrize("rows", [40, 300])
+def test_a_row_does_not_depend_on_its_neighbours(bl, rows):
+    """float32 sums that are not finite are computed again, and the others stay as they were."""
+    x, w, _, _, _, _ = _make(torch.float32, rows, 300, 200, 11)
+    clean = bl.linear(x.cuda(), w.cuda())
+    x[rows - 2] = torch.finfo(torch.float32).max  # rounds to infinity in bf16
+    got = bl.linear(x.cuda(), w.cuda())
+    rest = torch.arange(rows) != rows - 2
+    assert torch.equal(got[rest.cuda()], clean[rest.cuda()])
+    w = torch.zeros(200, 300)
+    w[:, 7] = 0.5
+    got = bl.linear(x.cuda(), w.cuda())
+    assert torch.equal(got[rows - 2].cpu(), torch.full((200,), torch.finfo(torch.float32).max / 2))
+
+
 def test_nothing_to_do(bl):
     for dtype in TYPES:
         w = torch.ones(5, 3, dtype=dtype, device="cuda")

@@ -51,6 +51,7 @@ ATTENTION_BAD = [
     (dict(width=257), "BILSTM_UNSUPPORTED"),
     (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(memory_rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(memory_rows=(1 << 30) + 1), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(sequences=(1 << 30) + 1), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(places=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(scale=0.0), "BILSTM_INVALID_ARGUMENT"),
@@ -144,6 +145,7 @@ LINEAR_BAD = [
     (dict(slope=float("inf")), "BILSTM_INVALID_ARGUMENT"),
     (dict(reserved=1), "BILSTM_INVALID_ARGUMENT"),
     (dict(rows=1 << 31), "BILSTM_DIMENSION_OVERFLOW"),
+    (dict(rows=(1 << 31) - 1023), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(inputs=(1 << 28) + 1), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(outputs=(1 << 28) + 1), "BILSTM_DIMENSION_OVERFLOW"),
     (dict(SCALED, eight=2, inputs=(1 << 16) + 1), "BILSTM_DIMENSION_OVERFLOW"),
