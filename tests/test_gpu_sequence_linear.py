@@ -60,7 +60,8 @@ def test_sizes(bl, dtype, rows, inputs, outputs):
 
 
 @pytest.mark.parametrize("dtype", TYPES + EIGHT, ids=str)
-@pytest.mark.parametrize("rows, inputs, outputs", [(2100, 320, 2050), (1111, 777, 999), (4096, 64, 4096), (700, 1000, 1300)])
+@pytest.mark.parametrize("rows, inputs, outputs", [(2100, 320, 2050), (1111, 777, 999), (4096, 64, 4096), (700, 1000, 1300), (4200, 72, 4200),
+                                                   (6000, 40, 2600)])
 def test_many_rows(bl, dtype, rows, inputs, outputs):
     x, w, bias, residual, xs, ws = _make(dtype, rows, inputs, outputs, 3, torch.bfloat16 if dtype in EIGHT else None)
     _check(bl, x, w, bias, residual, xs, ws)
