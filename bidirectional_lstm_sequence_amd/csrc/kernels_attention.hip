@@ -59,22 +59,43 @@ struct Of {
         const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
+    // 32 frames' weights as the second product takes them. Their sum is that of the rounded ones: what rounding adds to
+    // a weight then counts in both, and a row that one frame decides is as exact as that frame (one bfloat16 row over 589
+    // frames is off by 0.0023 of its size where unrounded sums gave 0.0036; the output's own rounding makes 0.0017).
+    // Weights in two parts would bring it to 0.0017 for half as many matrix instructions again.
+    struct Weights {
+        Frag part[2];
+    };
+    static __device__ __forceinline__ Weights pack(const F16x &p, float &sum) {
+        Weights w;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const Vec<T, 2> pair = {static_cast<T>(p[8 * c + j]), static_cast<T>(p[8 * c + j + 1])};
+                const Vec<T, 2> ones = {static_cast<T>(1.0f), static_cast<T>(1.0f)};
+                if constexpr (__is_same(T, __bf16)) {
+                    sum = __builtin_amdgcn_fdot2_f32_bf16(pair, ones, sum, false);
+                } else {
+                    sum = __builtin_amdgcn_fdot2(pair, ones, sum, false);
+                }
+                w.part[c][j] = pair[0];
+                w.part[c][j + 1] = pair[1];
+            }
+        return w;
+    }
     // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
     template <int RB, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
+    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &w, F16x (&out)[N], int lane) {
         const int h = lane >> 5;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            Frag w;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = static_cast<T>(p[8 * c + j]);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int d = 0; d < N; ++d) {
                 const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
                                                        columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
-                out[d] = mul(v, w, out[d]);
+                out[d] = mul(v, w.part[c], out[d]);
             }
-        }
     }
 };
 
@@ -83,13 +104,19 @@ struct Of<float> {
     typedef Vec<float, 4> Frag;
     static constexpr int kFrames = 32;
     static constexpr float kLift = 0.0f, kLag = 8.0f;
+    typedef F16x Weights;
+    static __device__ __forceinline__ Weights pack(const F16x &p, float &sum) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += p[i];
+        return p;
+    }
     static __device__ __forceinline__ F16x mul(const Frag &a, const Frag &b, F16x c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
     template <int RB, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
+    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &p, F16x (&out)[N], int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -262,16 +289,16 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
         const float shift = most == -__builtin_huge_valf() ? 0.0f : fmaf(most, c, -O::kLift);  // no frame yet: weights of 0
         float add = 0.0f;
+        typename O::Weights weights[kBlocks];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+        for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
-                add += p[b][i];
-            }
+            for (int i = 0; i < 16; ++i) p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
+            weights[b] = O::pack(p[b], add);
+        }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, p[b], out, lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, weights[b], out, lane);
     };
 
     constexpr int kStride = FEW ? kAll * kFrames : kFrames;

@@ -48,11 +48,15 @@ def attention(q, k, v, starts, memory_starts, lengths, slots, mask, scale, y):
         off = 2 * U32 * (width + 2) * size + U32 * (6 * most + 8 + 6 * tiles)
         value = torch.matmul(w, vs)
         weight = torch.matmul(w, vs.abs())
-        off = torch.where(w > 0, off, 0.0)
-        # each weight's error, its part in the sum of weights, and additions: 32 in a row within a tile for the sum,
-        # one a frame for the values
-        error = torch.matmul(w * (off + weights_off), vs.abs())
-        error = error + ((w * off).sum(2, keepdim=True) + U32 * (40 + tiles)) * weight + U32 * (held + 8) * weight
+        off = torch.where(w > 0, off, 0.0) + weights_off
+        # Weights w (1 + e) in the values' sum and in their own: y' - y = sum w e (v - y) / (1 + sum w e), where the last
+        # factor is below 1.01. Then additions: 40 in a row within a tile for the sum, one a frame for the values.
+        error = torch.zeros_like(value)
+        for column in range(0, width, 8):  # a few columns at a time, for the memory
+            at = slice(column, column + 8)
+            away = (vs[:, None, :, at] - value[:, :, None, at]).abs()
+            error[:, :, at] = 1.01 * ((w * off)[..., None] * away).sum(2)
+        error = error + U32 * (40 + tiles) * weight + U32 * (held + 8) * weight
         if dtype == torch.float16:  # weights below 2^-24 of the largest lose bits: half of 2^-24 * 2^-10 each
             error = error + 2.0 ** -35 / w.amax(2, keepdim=True).reciprocal() * vs.abs().sum(1)[:, None]
         out[here] = value.transpose(0, 1)
