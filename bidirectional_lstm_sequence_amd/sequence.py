@@ -1,6 +1,7 @@
 """Operators of causal sequence layers: argument marshalling for the ``bilstm_causal_conv``,
 ``bilstm_scan``, ``bilstm_add_rms_norm``, ``bilstm_token_logprobs``, ``bilstm_cross_attention`` and
-``bilstm_linear`` entry points of bilstm.h, which gives the formulas and the conventions of packed sequences and state caches.
+``bilstm_linear`` entry points of bilstm.h, which gives the formulas and the conventions of packed
+sequences and state caches.
 
 Tensors are CUDA (HIP) tensors of one device; float32, bfloat16 and float16 are taken unless a
 tensor is said to be of another type. Rows may have a stride; what lies within a row must be
