@@ -467,7 +467,7 @@ unsigned long long tiles_of(const AttentionArgs &a, int size) {
 // Whether a sequence has 32 packed rows or less on average: 256 rows of 4 heads over 589 frames take 31 us so and 36
 // with tiles of 128, a row alone has no join. With 64 packed rows the tiles of 128 are ahead where keys are long (512
 // rows over 2048 frames, heads of 128, 62 us and 81). The lengths are on the device: a long sequence among many short
-// ones is read by several workgroups of 32, about three times slower than by tiles of 128.
+// ones is read by workgroups of 32: a prompt of 4000 rows adds 94 us to 255 single rows' 378, alone it takes 58.
 bool few_rows(const AttentionArgs &a) {
     return static_cast<unsigned long long>(a.seq.rows) * a.per <= 32ull * a.seq.sequences;
 }

@@ -243,3 +243,23 @@ def test_nothing_to_do(bl):
         assert (out == 2).all()
         bl.cross_attention_step(q, k[:0], v[:0], whole([0, 0]), slots=whole([0, 0, -1, 1]), mask=torch.ones(0, dtype=torch.bool).cuda(), out=out)
         assert (out[:2] == 0).all() and (out[2:] == 2).all()
+
+
+def test_thousands_of_sequences(bl):
+    """More sequences than one round of the search looks at, most of one row, some of none, one long."""
+    count = 5000
+    rows = [j % 3 for j in range(count)]
+    rows[777] = 600
+    starts = [0]
+    for r in rows:
+        starts.append(starts[-1] + r)
+    q, k, v = _make(torch.bfloat16, starts[-1], 90, 2, 1, 32, 19)
+    _check(bl, q, k, v, starts, [0, 40, 41, 90], slots=[j % 4 - (j % 11 == 0) * 4 for j in range(count)])
+
+
+def test_a_mask_of_bytes(bl):
+    q, k, v = _make(torch.float16, 9, 80, 2, 2, 64, 20)
+    mask = torch.arange(80) % 3 != 1
+    want = _run(bl, q, k, v, [0, 9], [0, 80], mask=mask)
+    assert torch.equal(_run(bl, q, k, v, [0, 9], [0, 80], mask=mask.to(torch.uint8) * 255), want)
+    _check(bl, q, k, v, [0, 9], [0, 80], mask=mask)
