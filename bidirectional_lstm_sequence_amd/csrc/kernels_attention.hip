@@ -8,8 +8,8 @@
 // columns. Tiles of keys and values go straight from memory to two stages of LDS; frames that do not count come as zeros
 // (an offset behind the buffer) and their scores start from minus infinity, so what they hold never enters.
 //
-// Few rows are bound by the bytes of keys and values: 256 rows over 589 frames each, 4 key heads of 64, bfloat16, 31-33
-// us (floor 31 at the copy rate of 5.0 TB/s); 64 rows over 4096 frames, 8 key heads of 128, 185 us, 5.8 TB/s. Many rows:
+// Few rows are bound by the bytes of keys and values: 256 rows over 589 frames each, 4 key heads of 64, bfloat16, 32-34
+// us (floor 31 at the copy rate of 5.0 TB/s); 64 rows over 4096 frames, 8 key heads of 128, 188 us, 5.7 TB/s. Many rows:
 // 16384 over 2048 frames, 32 heads of 128, bfloat16, 707 us, 778 TFLOP/s, where matrix instructions alone, with neither
 // loads nor softmax, take 448-460: the card lowers its clock to 1.9 GHz under this load (2.2 in a plain product), and
 // what is left out in a trial shortens the call by its own share: loads to LDS 125 us, reads from LDS 80, softmax 65.
@@ -70,34 +70,44 @@ struct Of {
         const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
-    // 32 frames' weights as the second product takes them. Their sum is that of the rounded ones: what rounding adds to
-    // a weight then counts in both, and a row that one frame decides is as exact as that frame (one bfloat16 row over 589
-    // frames is off by 0.0023 of its size where unrounded sums gave 0.0036; the output's own rounding makes 0.0017).
-    // Weights in two parts would bring it to 0.0017 for half as many matrix instructions again.
+    // 32 frames' weights as the second product takes them: rounded, and with PARTS = 2 what the rounding left (2^-16 of
+    // a weight is lost then, no more than float32's 24 bits need for an output of 16). Their sum is that of the rounded
+    // ones: what rounding adds to a weight counts in both, and a row that one frame decides is as exact as that frame.
+    // A bfloat16 row over 589 frames is off by 0.0017 of its size with two parts, which is the output's own rounding, by
+    // 0.0023 with one and by 0.0036 with one and unrounded sums. Few rows wait for memory and take two; many rows take
+    // one, half as many matrix instructions again being a quarter of their time.
+    template <int PARTS>
     struct Weights {
-        Frag part[2];
+        Frag part[PARTS][2];
     };
-    static __device__ __forceinline__ Weights pack(const F16x &p, float &sum) {
-        Weights w;
+    template <int PARTS>
+    static __device__ __forceinline__ Weights<PARTS> pack(const F16x &p, float &sum) {
+        Weights<PARTS> w;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                const Vec<T, 2> pair = {static_cast<T>(p[8 * c + j]), static_cast<T>(p[8 * c + j + 1])};
-                const Vec<T, 2> ones = {static_cast<T>(1.0f), static_cast<T>(1.0f)};
-                if constexpr (__is_same(T, __bf16)) {
-                    sum = __builtin_amdgcn_fdot2_f32_bf16(pair, ones, sum, false);
-                } else {
-                    sum = __builtin_amdgcn_fdot2(pair, ones, sum, false);
+                float a = p[8 * c + j], b = p[8 * c + j + 1];
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) {
+                    const Vec<T, 2> pair = {static_cast<T>(a), static_cast<T>(b)};
+                    const Vec<T, 2> ones = {static_cast<T>(1.0f), static_cast<T>(1.0f)};
+                    if constexpr (__is_same(T, __bf16)) {
+                        sum = __builtin_amdgcn_fdot2_f32_bf16(pair, ones, sum, false);
+                    } else {
+                        sum = __builtin_amdgcn_fdot2(pair, ones, sum, false);
+                    }
+                    w.part[k][c][j] = pair[0];
+                    w.part[k][c][j + 1] = pair[1];
+                    a -= static_cast<float>(pair[0]);
+                    b -= static_cast<float>(pair[1]);
                 }
-                w.part[c][j] = pair[0];
-                w.part[c][j + 1] = pair[1];
             }
         return w;
     }
     // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
-    template <int RB, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &w, F16x (&out)[N], int lane) {
+    template <int RB, int PARTS, int N>
+    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights<PARTS> &w, F16x (&out)[N], int lane) {
         const int h = lane >> 5;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -105,7 +115,8 @@ struct Of {
             for (int d = 0; d < N; ++d) {
                 const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
                                                        columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
-                out[d] = mul(v, w.part[c], out[d]);
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) out[d] = mul(v, w.part[k][c], out[d]);
             }
     }
 };
@@ -115,8 +126,10 @@ struct Of<float> {
     typedef Vec<float, 4> Frag;
     static constexpr int kFrames = 32;
     static constexpr float kLift = 0.0f, kLag = 8.0f;
-    typedef F16x Weights;
-    static __device__ __forceinline__ Weights pack(const F16x &p, float &sum) {
+    template <int>
+    using Weights = F16x;
+    template <int>
+    static __device__ __forceinline__ F16x pack(const F16x &p, float &sum) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += p[i];
         return p;
@@ -126,8 +139,8 @@ struct Of<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
-    template <int RB, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &p, F16x (&out)[N], int lane) {
+    template <int RB, int PARTS, int N>
+    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -300,16 +313,17 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
         const float shift = most == -__builtin_huge_valf() ? 0.0f : fmaf(most, c, -O::kLift);  // no frame yet: weights of 0
         float add = 0.0f;
-        typename O::Weights weights[kBlocks];
+        constexpr int kParts = FEW ? 2 : 1;
+        typename O::template Weights<kParts> weights[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
-            weights[b] = O::pack(p[b], add);
+            weights[b] = O::template pack<kParts>(p[b], add);
         }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, weights[b], out, lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB, kParts>(values, 32 * b, weights[b], out, lane);
     };
 
     constexpr int kStride = FEW ? kAll * kFrames : kFrames;
