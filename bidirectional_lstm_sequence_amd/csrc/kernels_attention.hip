@@ -70,26 +70,22 @@ struct Of {
         const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
-    // 32 frames' weights as the second product takes them: rounded, and with PARTS = 2 what the rounding left (2^-16 of
-    // a weight is lost then, no more than float32's 24 bits need for an output of 16). Their sum is that of the rounded
-    // ones: what rounding adds to a weight counts in both, and a row that one frame decides is as exact as that frame.
-    // A bfloat16 row over 589 frames is off by 0.0017 of its size with two parts, which is the output's own rounding, by
-    // 0.0023 with one and by 0.0036 with one and unrounded sums. Few rows wait for memory and take two; many rows take
-    // one, half as many matrix instructions again being a quarter of their time.
-    template <int PARTS>
+    // 32 frames' weights as the second product takes them, in two parts: rounded, and what the rounding left (2^-16 of a
+    // weight is lost then, no more than float32's 24 bits need for an output of 16). Their sum is that of both parts. A
+    // bfloat16 row over 589 frames is off by 0.0017 of its size so, which is the output's own rounding, by 0.0023 with one
+    // part; values that nearly cancel show the difference at any size.
     struct Weights {
-        Frag part[PARTS][2];
+        Frag part[2][2];
     };
-    template <int PARTS>
-    static __device__ __forceinline__ Weights<PARTS> pack(const F16x &p, float &sum) {
-        Weights<PARTS> w;
+    static __device__ __forceinline__ Weights pack(const F16x &p, float &sum) {
+        Weights w;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 float a = p[8 * c + j], b = p[8 * c + j + 1];
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     const Vec<T, 2> pair = {static_cast<T>(a), static_cast<T>(b)};
                     const Vec<T, 2> ones = {static_cast<T>(1.0f), static_cast<T>(1.0f)};
                     if constexpr (__is_same(T, __bf16)) {
@@ -106,8 +102,8 @@ struct Of {
         return w;
     }
     // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
-    template <int RB, int PARTS, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights<PARTS> &w, F16x (&out)[N], int lane) {
+    template <int RB, int N>
+    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &w, F16x (&out)[N], int lane) {
         const int h = lane >> 5;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -116,7 +112,7 @@ struct Of {
                 const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
                                                        columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) out[d] = mul(v, w.part[k][c], out[d]);
+                for (int k = 0; k < 2; ++k) out[d] = mul(v, w.part[k][c], out[d]);
             }
     }
 };
@@ -126,9 +122,7 @@ struct Of<float> {
     typedef Vec<float, 4> Frag;
     static constexpr int kFrames = 32;
     static constexpr float kLift = 0.0f, kLag = 8.0f;
-    template <int>
     using Weights = F16x;
-    template <int>
     static __device__ __forceinline__ F16x pack(const F16x &p, float &sum) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += p[i];
@@ -139,7 +133,7 @@ struct Of<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
-    template <int RB, int PARTS, int N>
+    template <int RB, int N>
     static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -313,17 +307,16 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
         const float shift = most == -__builtin_huge_valf() ? 0.0f : fmaf(most, c, -O::kLift);  // no frame yet: weights of 0
         float add = 0.0f;
-        constexpr int kParts = FEW ? 2 : 1;
-        typename O::template Weights<kParts> weights[kBlocks];
+        typename O::Weights weights[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
-            weights[b] = O::template pack<kParts>(p[b], add);
+            weights[b] = O::pack(p[b], add);
         }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB, kParts>(values, 32 * b, weights[b], out, lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, weights[b], out, lane);
     };
 
     constexpr int kStride = FEW ? kAll * kFrames : kFrames;

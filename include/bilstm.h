@@ -567,8 +567,8 @@ bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stre
  *   s[f] = scale * sum_c q[i][h][c] * k[f][g][c];  y[i][h] = sum_f softmax(s)[f] * v[f][g]
  * Memory p is the rows memory_starts[p] .. memory_starts[p + 1] - 1 of k and v, of which the first
  * memory_lengths[p] count, without those whose mask is 0. What the others hold is never used, not-a-numbers included.
- * Scores, maxima and sums are held in float32; weights enter their product with the values in the tensors' type, in two
- * parts where sequences have few rows.
+ * Scores, maxima and sums are held in float32; weights enter their product with the values in float32, or in two parts of
+ * the tensors' 16-bit type, which leave at most 2^-16 of a weight.
  * A row without a frame that counts, or with scores of minus infinity alone, gets zeros.
  * Here `places` are the memories and `slots` names the memory that each sequence reads: several may read one, and
  * a slot outside 0 .. places - 1 marks padding. memory_starts hold `places` + 1 non-decreasing row numbers; values
