@@ -4,9 +4,9 @@
 //
 // Many rows: tiles whose operands go straight from memory to two stages of LDS, a step of 128 bytes of K ahead; waves
 // multiply 16 x 16 blocks and pass their sums through LDS to whole lines of y. A step of 256 x 256 outputs takes 1.6 us
-// on all CUs whatever the type (1342 TFLOP/s bfloat16, 2840 e4m3, at 2.2 GHz, the matrix cores half busy), a tile's
-// start and end 18 us. 8192 x 5120 x 5120: bfloat16 with residual 403 us (1070 TFLOP/s; the library's plain product 471),
-// e4m3 with gelu 238 (1810), int8 233, float32 by parts 2270 (189 TFLOP/s; the library 138).
+// on all CUs (1342 TFLOP/s bfloat16, 2840 int8, at 2.2 GHz, the matrix cores half busy; e4m3, whose codes are widened to
+// bf16, 2.5), a tile's start and end 18 us. 8192 x 5120 x 5120: bfloat16 with residual 403 us (1070 TFLOP/s; the library's
+// plain product 471), e4m3 with gelu 329 (1300), int8 233, float32 by parts 2270 (189 TFLOP/s; the library 138).
 // Few rows: bound by the weights' bytes, one row of 5120 x 5120 bfloat16 11.8 us (floor 10.5).
 #include "linear_device.h"
 
@@ -484,14 +484,6 @@ hipError_t by_output(const LinearArgs &a, Elem type, hipStream_t stream) {
     }
 }
 
-hipError_t of_e4m3(const LinearArgs &a, Elem type, hipStream_t stream) {
-    switch (type) {
-        case Elem::f32: return by_alignment<OfE4m3Exact, float>(a, stream);
-        case Elem::bf16: return by_alignment<OfE4m3, __bf16>(a, stream);
-        default: return by_alignment<OfE4m3, _Float16>(a, stream);
-    }
-}
-
 }  // namespace
 
 size_t linear_scratch_bytes(const LinearArgs &a, Elem type, Eight eight) {
@@ -504,7 +496,7 @@ size_t linear_scratch_bytes(const LinearArgs &a, Elem type, Eight eight) {
 hipError_t launch_linear(const LinearArgs &a, Elem type, Eight eight, hipStream_t stream) {
     if (a.rows <= 0) return hipSuccess;
     switch (eight) {
-        case Eight::e4m3: return of_e4m3(a, type, stream);
+        case Eight::e4m3: return by_output<OfE4m3>(a, type, stream);
         case Eight::int8: return by_output<OfInt8>(a, type, stream);
         default: break;
     }
