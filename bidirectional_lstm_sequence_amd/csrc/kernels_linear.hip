@@ -146,7 +146,10 @@ __device__ __forceinline__ void product_of_tile(const LinearArgs &a, const Tile 
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) any |= odd(acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) {
+                    acc[i][j][e] *= P::kBack;
+                    any |= odd(acc[i][j][e]);
+                }
         if (__syncthreads_or(any)) {
             // sixteen outputs at a time, for the registers; sums that are finite stay as they are
 #pragma unroll

@@ -50,9 +50,12 @@ struct OfF32 {
 };
 
 // float32 by three bf16 parts of each operand, which hold its 24 bits: six products of parts (those left out are below
-// 2^-25 of the whole) at sixteen times the rate of float32's. A part of an infinity, or of what bf16 rounds to one, is
-// not a number; a tile with sums that are not finite is computed again by OfF32.
+// 2^-25 of the whole) at sixteen times the rate of float32's. The parts are those of 2^16 times the operand: the last bit of
+// the smallest float32, 2^-149, is then 2^-133, bf16's own (the matrix instructions keep subnormal numbers). Sums come 2^32
+// times too large. A part of an infinity, or of what bf16 rounds to one, is not a number; a tile with sums that are not
+// finite, which those from 2^96 on may be, is computed again by OfF32.
 struct OfF32Split {
+    static constexpr float kTimes = 0x1p16f, kBack = 0x1p-32f;
     typedef float Elem;
     struct Frag {
         Vec<__bf16, 8> part[3];
@@ -65,7 +68,7 @@ struct OfF32Split {
         typedef __bf16 B2 __attribute__((ext_vector_type(2)));
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __int_as_float(chunk[e / 4][e % 4]);
+        for (int e = 0; e < 8; ++e) v[e] = __int_as_float(chunk[e / 4][e % 4]) * kTimes;
         Frag f;
 #pragma unroll
         for (int p = 0; p < 3; ++p) {

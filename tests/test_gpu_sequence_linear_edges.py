@@ -4,6 +4,7 @@ over several steps."""
 import pytest
 import torch
 
+from tests import decoder_plain as plain
 from tests.sequence_plain import TYPES
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +51,17 @@ def test_every_code_of_e4m3(bl, out_type, width):
         assert torch.equal(got.nan_to_num(nan=-1000), want[rows].nan_to_num(nan=-1000))
         back = bl.linear(w.cuda(), x[rows].cuda(), x_scales=_ones(7), weight_scales=_ones(n), out_type=out_type)[2].cpu()
         assert torch.equal(back.nan_to_num(nan=-1000), want[rows].nan_to_num(nan=-1000))
+
+
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("inputs", [64, 77])
+@pytest.mark.parametrize("x_size, w_size", [(1e-33, 1e30), (1e-35, 1e33), (1e-37, 1e35), (1e30, 1e-36), (1e-20, 1e-15), (1e-37, 1.0),
+                                            (1e15, 1e12), (1e20, 1e10), (1e25, 1e10)])
+def test_float32_operands_of_any_size(bl, rows, inputs, x_size, w_size):
+    g = torch.Generator().manual_seed(1)
+    x, w = torch.randn(rows, inputs, generator=g) * x_size, torch.randn(50, inputs, generator=g) * w_size
+    bias, residual = torch.randn(50, generator=g) * x_size * w_size, torch.randn(rows, 50, generator=g) * x_size * w_size
+    x[abs(x) < 2e-38], w[abs(w) < 2e-38] = 0, 0  # normal numbers
+    value, bound = plain.linear(x, w, bias, None, residual, None, None, 0, torch.float32)
+    off = (bl.linear(x.cuda(), w.cuda(), bias=bias.cuda(), residual=residual.cuda()).cpu().double() - value).abs()
+    assert torch.isfinite(off).all() and (off <= bound).all(), f"{((off - bound) / bound).max():.3e} of the bound over it"
