@@ -6,7 +6,8 @@
 // of one tile. Both products run on 32 x 32 matrix instructions with frames as rows of the first result, so that a lane
 // holds weights of its own row alone and hands them to the second product as they lie; values are read from LDS by
 // columns. Tiles of keys and values go straight from memory to two stages of LDS; frames that do not count come as zeros
-// (an offset behind the buffer) and their scores start from minus infinity, so what they hold never enters.
+// (an offset behind the buffer) and their scores become minus infinity, so neither what they hold nor what a query makes of
+// the zeros enters.
 //
 // Few rows are bound by the bytes of keys and values: 256 rows over 589 frames each, 4 key heads of 64, bfloat16, 32-34
 // us (floor 31 at the copy rate of 5.0 TB/s); 64 rows over 4096 frames, 8 key heads of 128, 188 us, 5.7 TB/s. Many rows:
@@ -269,13 +270,6 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         F16x p[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) p[b] = F16x{};
-        if (bits != kWhole) {  // uniform; keys that do not count are zeros and leave their scores at minus infinity
-            const unsigned long long mine = bits >> 4 * half;
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[b][i] = mine >> (32 * b + 8 * (i / 4) + i % 4) & 1 ? 0.0f : -__builtin_huge_valf();
-        }
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i)
 #pragma unroll
@@ -286,6 +280,13 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
                 p[b] = O::mul(__builtin_bit_cast(typename O::Frag, chunk), qf[i], p[b]);
             }
         __builtin_amdgcn_s_setprio(0);
+        if (bits != kWhole) {  // uniform; what came of the zeros of keys that do not count is no number where a query is not
+            const unsigned long long mine = bits >> 4 * half;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[b][i] = mine >> (32 * b + 8 * (i / 4) + i % 4) & 1 ? p[b][i] : -__builtin_huge_valf();
+        }
         float top = -__builtin_huge_valf();
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)

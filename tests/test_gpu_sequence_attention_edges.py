@@ -56,3 +56,27 @@ def test_weights_keep_their_bits(bl, dtype, rows, width):
 def test_weights_keep_their_bits_over_splits(bl, dtype, rows):
     q, k, v = _make(dtype, rows, 3001, 2, 2, 64, rows)
     _within(_run(bl, q, k, v), strict.attention(q, k, v, range(3001), 64 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [64, 13, 200])
+@pytest.mark.parametrize("frames", [1, 32, 50, 64, 130, 3000])
+def test_queries_that_are_no_numbers_read_no_masked_frame(bl, dtype, rows, width, frames):
+    """A row with nothing to read gets zeros, whatever its query holds, and so does one whose scores are all minus
+    infinity, in whole tiles of frames and in tiles with frames that do not count."""
+    q, k, v = _make(dtype, rows, frames, 2, 2, width, frames)
+    q[0, 0, 3], q[1, 1, 0], q[2, 0, 5] = float("nan"), float("inf"), float("-inf")
+    nothing = torch.zeros(frames, dtype=torch.bool)
+    assert (_run(bl, q, k, v, mask=nothing) == 0).all() and (_run(bl, q, k, v, lengths=[0]) == 0).all()
+    q, k, v = _make(dtype, rows, frames, 2, 2, width, frames)
+    q[1, :, 2], k[:, :, 2] = float("inf"), -1.0
+    mask = torch.arange(frames) % 5 != 4
+    k[~mask] = 1.0
+    clean = q.clone()
+    clean[1] = 0
+    keep = torch.arange(rows) != 1
+    for m, lengths in ((mask, None), (None, [min(frames, 4)]), (mask, [max(1, frames - 3)])):
+        got = _run(bl, q, k, v, mask=m, lengths=lengths)
+        assert (got[1] == 0).all()
+        assert torch.equal(got[keep], _run(bl, clean, k, v, mask=m, lengths=lengths)[keep])
