@@ -549,7 +549,8 @@ bilstm_status attention(const char *call, const bilstm_attention_args *args, boo
     BL_CHECK(attention_sizes(call, args, step, &k));
     const bilstm_attention_args &a = *args;
     if (a.reserved[0] != 0 || a.reserved[1] != 0) return fail(BILSTM_INVALID_ARGUMENT, "%s: reserved must be 0", call);
-    if (!(a.scale > 0.0f) || a.scale > 3.0e38f) return fail(BILSTM_INVALID_ARGUMENT, "%s: scale is not a number > 0", call);
+    // its product with log2 e is a float32
+    if (!(a.scale > 0.0f) || a.scale > 0x1p127f) return fail(BILSTM_INVALID_ARGUMENT, "%s: scale is not a number > 0 up to 2^127", call);
     const uint64_t count = step ? a.rows : a.sequences;
     if (a.rows == 0 || count == 0) return BILSTM_OK;
     const uint64_t size = size_of(a.type);

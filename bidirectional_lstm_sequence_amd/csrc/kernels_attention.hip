@@ -150,6 +150,28 @@ struct Of<float> {
 
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
+// e^(scale d) times 2^lift for a difference d of two products' sums: scores of any size, whose product with log2 e need not
+// be a float32, give the exponents that their difference does. float32 tensors carry the rest of the factor and of its
+// product along (as exp_of_minus does), so that the exponent is that of a rounded difference alone.
+struct Power {
+    float high, low;
+    __device__ __forceinline__ explicit Power(float scale) {
+        constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911266175e-8f;
+        high = scale * kLog2e;
+        low = fmaf(scale, kLog2e, -high) + scale * kLog2eLow;
+    }
+    template <typename T>
+    __device__ __forceinline__ float of(float d, float lift = 0.0f) const {
+        if constexpr (sizeof(T) == 4) {
+            const float t = d * high, e = __builtin_amdgcn_exp2f(t);
+            const float rest = fmaf(d, high, -t) + d * low;
+            return e > 0.0f ? fmaf(e, rest * 0.6931471805599453f, e) : e;
+        } else {
+            return __builtin_amdgcn_exp2f(fmaf(d, high, lift));
+        }
+    }
+};
+
 // D: columns of a tile, the width rounded up; columns behind the width are zeros.
 template <typename T, int D, bool FEW, bool ALIGNED>
 __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * sizeof(T) <= 512 ? 2 : 1)) void attention_kernel(AttentionArgs a) {
@@ -258,7 +280,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
     };
 
-    const float c = a.scale * 1.4426950408889634f;
+    const Power power(a.scale);
     float most = -__builtin_huge_valf(), sum = 0.0f;  // sum: this half's frames
     F16x out[kColumns];
 #pragma unroll
@@ -295,10 +317,10 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         top = fmaxf(top, other_half(top));
         // Weights are measured from `most`, which follows a row's maximum only where that is kLag further up: its sums and
         // values then move with it. They rarely have to, and a wave whose rows stay skips it.
-        const bool moves = (top - most) * c > O::kLag;  // also from minus infinity; never where both are
+        const bool moves = (top - most) * power.high > O::kLag;  // also from minus infinity; never where both are
         if (__any(moves)) {
             const float next = moves ? top : most;
-            const float down = !moves ? 1.0f : (most == -__builtin_huge_valf() ? 0.0f : __builtin_amdgcn_exp2f((most - next) * c));
+            const float down = !moves ? 1.0f : (most == -__builtin_huge_valf() ? 0.0f : power.of<T>(most - next));
             most = next;
             sum *= down;
 #pragma unroll
@@ -306,13 +328,13 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
 #pragma unroll
                 for (int i = 0; i < 16; ++i) out[d][i] *= down;
         }
-        const float shift = most == -__builtin_huge_valf() ? 0.0f : fmaf(most, c, -O::kLift);  // no frame yet: weights of 0
+        const float from = most == -__builtin_huge_valf() ? 0.0f : most;  // no frame yet: weights of 0
         float add = 0.0f;
         typename O::Weights weights[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[b][i] = __builtin_amdgcn_exp2f(fmaf(p[b][i], c, -shift));
+            for (int i = 0; i < 16; ++i) p[b][i] = power.of<T>(p[b][i] - from, O::kLift);
             weights[b] = O::pack(p[b], add);
         }
         sum += add;
@@ -379,7 +401,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
 #pragma unroll
             for (int u = 0; u < kAll; ++u) {
                 const float *const share = shares + u * kShare;
-                const float down = __builtin_amdgcn_exp2f((share[32 * kRow + 2 * r] - from) * c);
+                const float down = power.of<T>(share[32 * kRow + 2 * r] - from);
                 total = fmaf(share[32 * kRow + 2 * r + 1], down, total);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) value[e] = fmaf(share[r * kRow + col + e], down, value[e]);
@@ -388,7 +410,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
             const int head_r = w.group * a.per + static_cast<int>(packed_r % a.per);
             if (a.splits > 1) {
                 *reinterpret_cast<Vec<float, 4> *>(part_values(a, w.split, row_r, head_r) + col) = value;
-                if (col == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row_r, head_r)) = {fmaf(top, c, -O::kLift), total};
+                if (col == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row_r, head_r)) = {top, total};
             } else {
                 const float inverse = total == 0.0f ? 0.0f : 1.0f / total;  // no frame: zeros
                 Vec<T, 4> four;
@@ -410,7 +432,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
                 const int col = 32 * d + 2 * i + 4 * half;
                 if (col < a.padded) *reinterpret_cast<Vec<float, 4> *>(part + col) = {out[d][i], out[d][i + 1], out[d][i + 2], out[d][i + 3]};
             }
-        if (half == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row, head)) = {fmaf(most, c, -O::kLift), sum};
+        if (half == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row, head)) = {most, sum};
         return;
     }
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;  // no frame: zeros
@@ -427,13 +449,14 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
 }
 
-// The parts of up to kJoinRows packed rows of one group, moved to the largest exponent of all, and their quotients. Four
+// The parts of up to kJoinRows packed rows of one group, moved to the largest score of all, and their quotients. Four
 // columns a lane.
 constexpr int kJoinRows = 16;
 
 template <typename T>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     const int splits = a.splits;
+    const Power power(a.scale);
     AttentionArgs whole = a;
     whole.splits = 1;
     const Work w = work_of(whole, kJoinRows, 1);
@@ -453,7 +476,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
         for (int s = 0; s < splits; ++s) {
             const Vec<float, 2> part = *reinterpret_cast<const Vec<float, 2> *>(part_sums(a, s, row, head));
             const Vec<float, 4> add = *reinterpret_cast<const Vec<float, 4> *>(part_values(a, s, row, head) + col);
-            const float down = __builtin_amdgcn_exp2f(part[0] - from);
+            const float down = power.of<T>(part[0] - from);
             sum = fmaf(part[1], down, sum);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = fmaf(add[e], down, v[e]);

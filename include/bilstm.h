@@ -584,7 +584,7 @@ typedef struct {
     uint32_t width;       /* 1 .. 256 elements a head */
     uint32_t sequences;   /* bilstm_cross_attention: number of sequences; the step form ignores it */
     uint32_t places;      /* memories */
-    float scale;          /* > 0 */
+    float scale;          /* > 0, at most 2^127 */
     int32_t reserved[2];  /* 0 */
     bilstm_rows q;        /* [rows][heads * width] */
     bilstm_rows k;        /* [memory_rows][groups * width] */

@@ -1,5 +1,5 @@
 """64-bit definition of cross attention of one sequence to frames of one memory, with bounds that count what the
-kernels promise: weights keep 16 bits and more in every form, float32 exponents are those of exact differences."""
+kernels promise: weights keep 16 bits and more in every form, exponents are those of differences of scores."""
 
 import torch
 
@@ -24,13 +24,11 @@ def attention(q, k, v, chosen, scale, exact_scores=False):
     tiles = (int(chosen.max()) - int(chosen.min())) // 32 + 2
     # A score is a sum of `width` products, a whole step of float32 each.
     off = torch.zeros_like(s) if exact_scores else 2 * U32 * (width + 2) * size
-    if dtype == torch.float32:
-        # An exponent is a rounded difference to a reference up to 2^8 below the maximum, times a factor in two parts; the
-        # moves of the reference add up to the difference once more. Then an exponential and products, with each move too.
-        off = off + U32 * (2 * (top - s + 6) + 8 + 6 * tiles)
-    else:
-        # the factor's rounding, the shift's and the exponent's own
-        off = off + U32 * (6 * s.abs().amax(2, keepdim=True) + 8 + 6 * tiles)
+    # An exponent is a rounded difference to a reference up to 2^8 below the maximum, times a factor: in two parts for
+    # float32 tensors, else one rounded factor and a rounded product; the moves of the reference add up to the difference
+    # once more. Then an exponential and products, with each move too.
+    off = off + U32 * ((2 if dtype == torch.float32 else 6) * (top - s + 6) + 8 + 6 * tiles)
+    if dtype != torch.float32:
         # weights in two parts, each rounded by at most half a step of the rest
         off = off + (torch.finfo(dtype).eps / 2) ** 2
     value, weight = torch.matmul(w, vs), torch.matmul(w, vs.abs())

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import decoder_strict as strict
-from tests.sequence_plain import TYPES
+from tests.sequence_plain import TYPES, U32, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,42 @@ def test_queries_that_are_no_numbers_read_no_masked_frame(bl, dtype, rows, width
         got = _run(bl, q, k, v, mask=m, lengths=lengths)
         assert (got[1] == 0).all()
         assert torch.equal(got[keep], _run(bl, clean, k, v, mask=m, lengths=lengths)[keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("frames", [40, 600, 3000])
+@pytest.mark.parametrize("scale, size", [(1.0, 1.2e19), (1.6e38, 1.0), (1e-3, 1.2e19)])
+def test_scores_at_the_ends_of_the_range(bl, dtype, rows, frames, scale, size):
+    """Scores near the largest float32, and a scale near it: only the largest count."""
+    q, k, v = _make(dtype, rows, frames, 2, 1, 64, frames)
+    q[:], k[:] = 0, 0
+    for sign in (1, -1):
+        q[:, :, 0], k[:, 0, 0] = sign * size, -2 * size
+        k[::7, 0, 0] = -size
+        k[3, 0, 0], k[frames - 1, 0, 0] = 2 * size, 2 * size
+        chosen = [3, frames - 1] if sign > 0 else [f for f in range(frames) if f % 7 and f not in (3, frames - 1)]
+        want = v[chosen, 0].double().mean(0).expand(rows, 2, -1)
+        # equal weights and their sum are exact; a sum of n values is rounded n times, at most at n of the largest, of which
+        # the quotient takes an n-th; then some products, and the output's rounding
+        n = len(chosen)
+        bound = rounded(want, U32 * (n + 64) * v[chosen].double().abs().amax() + 0 * want, dtype)
+        _within(_run(bl, q, k, v, scale=scale), (want, bound))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("frames", [40, 600, 3000])
+@pytest.mark.parametrize("far", [1e3, 1.5e5, 1e7])
+def test_scores_far_from_zero(bl, dtype, rows, frames, far):
+    """Whole numbers far from zero, as sums exact in float32: weights are those of the differences."""
+    q, k, v = _make(dtype, rows, frames, 2, 1, 64, frames)
+    g = torch.Generator().manual_seed(3)
+    q[:], k[:] = 0, 0
+    # far = a b, then differences of 0 .. 7
+    a = 2.0 ** round(torch.log2(torch.tensor(far) / 2).item())
+    q[:, :, 0], q[:, :, 1], k[:, 0, 0] = a, 1, 2
+    k[:, 0, 1] = torch.randint(0, 8, (frames,), generator=g).to(dtype)
+    if a > torch.finfo(dtype).max:
+        pytest.skip("not a number of this type")
+    _within(_run(bl, q, k, v, scale=1.0), strict.attention(q, k, v, range(frames), 1.0, exact_scores=True))
