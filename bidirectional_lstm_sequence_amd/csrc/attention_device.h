@@ -68,7 +68,7 @@ __device__ __forceinline__ Work work_of(const AttentionArgs &a, int size, int fr
     return w;
 }
 
-// Splits' parts: per split, row and head the sums of weights times values, then per split, row and head the
+// Splits' parts: per split, row and head the quotients of its frames alone, then per split, row and head the
 // score that weights are measured from (without the scale) and the sum of weights.
 __device__ __forceinline__ float *part_values(const AttentionArgs &a, int split, long long row, int head) {
     return a.scratch + ((static_cast<size_t>(split) * a.seq.rows + row) * a.heads + head) * a.padded;

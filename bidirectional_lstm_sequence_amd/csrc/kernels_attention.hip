@@ -102,8 +102,17 @@ struct Of {
             }
         return w;
     }
+    // Infinities as zeros, for the second part of weights: it may be zero or below, what the first part gives is right.
+    static __device__ __forceinline__ Frag finite(const Frag &v) {
+        typedef unsigned short U8 __attribute__((ext_vector_type(8)));
+        constexpr unsigned short kInfinity = __is_same(T, __bf16) ? 0x7F80 : 0x7C00;
+        U8 bits = __builtin_bit_cast(U8, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bits[e] = (bits[e] & 0x7FFF) == kInfinity ? 0 : bits[e];
+        return __builtin_bit_cast(Frag, bits);
+    }
     // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
-    template <int RB, int N>
+    template <int RB, bool AGAIN, int N>
     static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &w, F16x (&out)[N], int lane) {
         const int h = lane >> 5;
 #pragma unroll
@@ -113,7 +122,7 @@ struct Of {
                 const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
                                                        columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) out[d] = mul(v, w.part[k][c], out[d]);
+                for (int k = 0; k < 2; ++k) out[d] = mul(AGAIN && k > 0 ? finite(v) : v, w.part[k][c], out[d]);
             }
     }
 };
@@ -134,7 +143,7 @@ struct Of<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
-    template <int RB, int N>
+    template <int RB, bool, int N>
     static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -170,6 +179,13 @@ struct Power {
             return __builtin_amdgcn_exp2f(fmaf(d, high, lift));
         }
     }
+};
+
+struct First {
+    static constexpr bool value = false;
+};
+struct Again {
+    static constexpr bool value = true;
 };
 
 // D: columns of a tile, the width rounded up; columns behind the width are zeros.
@@ -237,7 +253,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
             value_offset[i] = vc < bytes ? static_cast<unsigned>(load_row[i] * a.v_stride * kSize) + vc : kOutOfRange;
         }
     }
-    auto issue = [&](int slot, int f, unsigned long long bits) {
+    auto issue = [&](int slot, int f, unsigned long long bits) __attribute__((always_inline)) {
         if constexpr (ALIGNED) {
             const T *const kt = k + static_cast<size_t>(f) * a.k_stride, *const vt = v + static_cast<size_t>(f) * a.v_stride;
             char *const base = lds + slot * 2 * kTile + sharer * 1024;
@@ -257,7 +273,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
     };
     U4 held_keys[ALIGNED ? 1 : kLoads], held_values[ALIGNED ? 1 : kLoads];
-    auto fetch = [&](int f, unsigned long long bits) {
+    auto fetch = [&](int f, unsigned long long bits) __attribute__((always_inline)) {
         if constexpr (!ALIGNED) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -269,7 +285,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
             }
         }
     };
-    auto put = [&](int slot) {
+    auto put = [&](int slot) __attribute__((always_inline)) {
         if constexpr (!ALIGNED) {
             char *const base = lds + slot * 2 * kTile + sharer * 1024 + lane * 16;
 #pragma unroll
@@ -280,13 +296,18 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
     };
 
+    // Weights up to 2^kLag times values near the end of float32 leave it, and an infinite value times the second part of a
+    // weight is no number: where a sum is not finite, its workgroup (of few rows: its wave) goes over the frames a second
+    // time, AGAIN, with weights times `lower`, so that no sum of the values' type leaves float32 (fp16's never do), and
+    // infinities out of the second part. Sums that were finite come out the same, times `lower`.
     const Power power(a.scale);
-    float most = -__builtin_huge_valf(), sum = 0.0f;  // sum: this half's frames
+    const int room = __is_same(T, _Float16) || w.end <= w.begin ? 0 : static_cast<int>(O::kLag) + 33 - __builtin_clz(w.end - w.begin);
+    const float lower = __builtin_ldexpf(1.0f, -room);
+    float most, sum;  // sum: this half's frames
     F16x out[kColumns];
-#pragma unroll
-    for (int d = 0; d < kColumns; ++d) out[d] = F16x{};
 
-    auto tile = [&](int slot, unsigned long long bits) {
+    auto tile = [&](auto again, int slot, unsigned long long bits) __attribute__((always_inline)) {
+        constexpr bool AGAIN = decltype(again)::value;
         const char *const keys = lds + slot * 2 * kTile, *const values = keys + kTile;
         __builtin_amdgcn_s_setprio(1);
         F16x p[kBlocks];
@@ -334,46 +355,84 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[b][i] = power.of<T>(p[b][i] - from, O::kLift);
+            for (int i = 0; i < 16; ++i) {
+                p[b][i] = power.of<T>(p[b][i] - from, O::kLift);
+                if constexpr (AGAIN) p[b][i] *= lower;
+            }
             weights[b] = O::pack(p[b], add);
         }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB>(values, 32 * b, weights[b], out, lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB, AGAIN>(values, 32 * b, weights[b], out, lane);
     };
 
     constexpr int kStride = FEW ? kAll * kFrames : kFrames;
     const int begin = w.begin + (FEW ? wave * kFrames : 0);
-    if (begin < w.end) {  // uniform where waves meet
-        unsigned long long bits = counted(begin, mask_byte(begin));
-        int next_byte = mask_byte(begin + kStride);
-        if constexpr (ALIGNED) {
-            issue(0, begin, bits);
-        } else {
-            fetch(begin, bits);
-        }
-        for (int f = begin, slot = 0; f < w.end; f += kStride, slot ^= 1) {
-            const bool more = w.end - f > kStride;
-            const unsigned long long next = more ? counted(f + kStride, next_byte) : 0;
+    auto pass = [&](auto again) __attribute__((always_inline)) {
+        most = -__builtin_huge_valf(), sum = 0.0f;
+#pragma unroll
+        for (int d = 0; d < kColumns; ++d) out[d] = F16x{};
+        if (begin < w.end) {  // uniform where waves meet
+            unsigned long long bits = counted(begin, mask_byte(begin));
+            int next_byte = mask_byte(begin + kStride);
             if constexpr (ALIGNED) {
-                meet<0, !FEW>();  // the tile has landed, and every wave is done with the other one
-                if (more) issue(slot ^ 1, f + kStride, next);
+                issue(0, begin, bits);
             } else {
-                put(slot);
-                if constexpr (FEW) {
-                    own_lds();
-                } else {
-                    __syncthreads();
-                }
-                if (more) fetch(f + kStride, next);
+                fetch(begin, bits);
             }
-            if (w.end - f > 2 * kStride) next_byte = mask_byte(f + 2 * kStride);
-            tile(slot, bits);
-            bits = next;
+            for (int f = begin, slot = 0; f < w.end; f += kStride, slot ^= 1) {
+                const bool more = w.end - f > kStride;
+                const unsigned long long next = more ? counted(f + kStride, next_byte) : 0;
+                if constexpr (ALIGNED) {
+                    meet<0, !FEW>();  // the tile has landed, and every wave is done with the other one
+                    if (more) issue(slot ^ 1, f + kStride, next);
+                } else {
+                    put(slot);
+                    if constexpr (FEW) {
+                        own_lds();
+                    } else {
+                        __syncthreads();
+                    }
+                    if (more) fetch(f + kStride, next);
+                }
+                if (w.end - f > 2 * kStride) next_byte = mask_byte(f + 2 * kStride);
+                tile(again, slot, bits);
+                bits = next;
+            }
         }
+        sum += other_half(sum);
+    };
+    pass(First{});
+    bool odd = !(sum < __builtin_huge_valf());
+#pragma unroll
+    for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= !(fabsf(out[d][i]) < __builtin_huge_valf());
+    float back = 1.0f;
+    bool again = __any(odd);
+    if constexpr (!FEW) {  // by floats in LDS: with __syncthreads_or the compiler lets each tile's reads wait for the next one's loads
+        float *const odds = reinterpret_cast<float *>(lds_of_all);
+        meet<0>();  // every wave is done with the tiles
+        if (lane == 0) odds[wave] = again ? 1.0f : 0.0f;
+        meet<0>();
+        float any = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kAll; ++u) any += odds[u];
+        again = any > 0.0f;
+    }
+    if (again) {
+        if constexpr (!FEW) meet<0>();
+        pass(Again{});
+        back = __builtin_ldexpf(1.0f, room);
     }
 
-    sum += other_half(sum);
+    // from here on `out` is the quotient: parts are joined by their shares, and no share passes a value
+    const float inverse = 1.0f / sum;
+#pragma unroll
+    for (int d = 0; d < kColumns; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[d][i] = sum == 0.0f ? 0.0f : out[d][i] * inverse;  // no frame: zeros
+    sum *= back;
     if constexpr (FEW) {
         // every wave's share of the rows to its own LDS, and from there to whole lines
         constexpr int kRow = D + 4;  // floats: the padding spreads rows over the banks
@@ -393,29 +452,31 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         for (int item = threadIdx.x; item < w.count * (D / 4); item += 64 * kAll) {
             const int r = item / (D / 4), col = item % (D / 4) * 4;
             if (col >= a.width) continue;
-            float top = -__builtin_huge_valf(), total = 0.0f;
+            float top = -__builtin_huge_valf(), total = 0.0f, part[kAll];
 #pragma unroll
             for (int u = 0; u < kAll; ++u) top = fmaxf(top, shares[u * kShare + 32 * kRow + 2 * r]);
             const float from = top == -__builtin_huge_valf() ? 0.0f : top;
-            Vec<float, 4> value = {};
 #pragma unroll
             for (int u = 0; u < kAll; ++u) {
-                const float *const share = shares + u * kShare;
-                const float down = power.of<T>(share[32 * kRow + 2 * r] - from);
-                total = fmaf(share[32 * kRow + 2 * r + 1], down, total);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) value[e] = fmaf(share[r * kRow + col + e], down, value[e]);
+                const float *const mine_of = shares + u * kShare + 32 * kRow + 2 * r;
+                part[u] = mine_of[1] * power.of<T>(mine_of[0] - from);
+                total += part[u];
             }
+            const float inverse_total = total == 0.0f ? 0.0f : 1.0f / total;
+            Vec<float, 4> value = {};
+#pragma unroll
+            for (int u = 0; u < kAll; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) value[e] = fmaf(shares[u * kShare + r * kRow + col + e], part[u] * inverse_total, value[e]);
             const long long packed_r = w.first + r, row_r = w.row + packed_r / a.per;
             const int head_r = w.group * a.per + static_cast<int>(packed_r % a.per);
             if (a.splits > 1) {
                 *reinterpret_cast<Vec<float, 4> *>(part_values(a, w.split, row_r, head_r) + col) = value;
                 if (col == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row_r, head_r)) = {top, total};
             } else {
-                const float inverse = total == 0.0f ? 0.0f : 1.0f / total;  // no frame: zeros
                 Vec<T, 4> four;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(value[e] * inverse);
+                for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(value[e]);
                 T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row_r) * a.y_stride + static_cast<size_t>(head_r) * a.width;
                 store_vector<false, T, 4>(y + col, four, a.width - col);
             }
@@ -435,7 +496,6 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         if (half == 0) *reinterpret_cast<Vec<float, 2> *>(part_sums(a, w.split, row, head)) = {most, sum};
         return;
     }
-    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;  // no frame: zeros
     T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
 #pragma unroll
     for (int d = 0; d < kColumns; ++d)
@@ -444,13 +504,12 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
             const int col = 32 * d + 2 * i + 4 * half;
             Vec<T, 4> four;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(out[d][i + e] * inverse);
+            for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(out[d][i + e]);
             if (col < a.width) store_vector<false, T, 4>(y + col, four, a.width - col);
         }
 }
 
-// The parts of up to kJoinRows packed rows of one group, moved to the largest score of all, and their quotients. Four
-// columns a lane.
+// The parts of up to kJoinRows packed rows of one group, by their shares of all weights. Four columns a lane.
 constexpr int kJoinRows = 16;
 
 template <typename T>
@@ -470,22 +529,26 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 #pragma unroll 4
         for (int s = 0; s < splits; ++s) top = fmaxf(top, part_sums(a, s, row, head)[0]);
         const float from = top == -__builtin_huge_valf() ? 0.0f : top;
-        float sum = 0.0f;
+        auto share = [&](int s) {
+            const Vec<float, 2> part = *reinterpret_cast<const Vec<float, 2> *>(part_sums(a, s, row, head));
+            return part[1] * power.of<T>(part[0] - from);
+        };
+        float total = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) total += share(s);
+        const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
         Vec<float, 4> v = {};
 #pragma unroll 4
         for (int s = 0; s < splits; ++s) {
-            const Vec<float, 2> part = *reinterpret_cast<const Vec<float, 2> *>(part_sums(a, s, row, head));
             const Vec<float, 4> add = *reinterpret_cast<const Vec<float, 4> *>(part_values(a, s, row, head) + col);
-            const float down = power.of<T>(part[0] - from);
-            sum = fmaf(part[1], down, sum);
+            const float weight = share(s) * inverse;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = fmaf(add[e], down, v[e]);
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(add[e], weight, v[e]);
         }
-        const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
         T *const y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.y_stride + static_cast<size_t>(head) * a.width;
         Vec<T, 4> four;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(v[e] * inverse);
+        for (int e = 0; e < 4; ++e) four[e] = static_cast<T>(v[e]);
         store_vector<false, T, 4>(y + col, four, a.width - col);
     }
 }

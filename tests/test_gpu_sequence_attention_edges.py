@@ -119,3 +119,38 @@ def test_scores_far_from_zero(bl, dtype, rows, frames, far):
     if a > torch.finfo(dtype).max:
         pytest.skip("not a number of this type")
     _within(_run(bl, q, k, v, scale=1.0), strict.attention(q, k, v, range(frames), 1.0, exact_scores=True))
+
+
+@pytest.mark.parametrize("dtype, size", [(torch.float32, 1e35), (torch.float32, 3e36), (torch.float32, 3e38), (torch.float32, 1e-30),
+                                         (torch.float32, 1e-36), (torch.bfloat16, 1e35), (torch.bfloat16, 3e36), (torch.bfloat16, 3e38),
+                                         (torch.bfloat16, 1e-30), (torch.bfloat16, 1e-36), (torch.float16, 6e4), (torch.float16, 1e-7)],
+                         ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [64, 200])
+def test_values_of_any_size(bl, dtype, size, rows, width):
+    """Weights are measured from a reference that the maximum may pass, and many add up: the quotient is a value's size."""
+    for frames in (64, 300, 3000):
+        q, k, v = _make(dtype, rows, frames, 2, 1, width, frames, scale=0.5)
+        q[:, :, 0], k[:, 0, 0] = 1.0, (torch.arange(frames) // 32 % 4 * 1.5 * width ** 0.5).to(dtype)  # rises from tile to tile
+        v = ((0.5 + torch.rand(frames, 1, width, generator=torch.Generator().manual_seed(1)) / 2) * size).to(dtype)
+        v[:, :, 1::2] *= -1
+        value, bound = strict.attention(q, k, v, range(frames), width ** -0.5)
+        _within(_run(bl, q, k, v), (value, bound + frames * 2.0 ** -149))  # products may be subnormal numbers
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [64, 13])
+@pytest.mark.parametrize("frames", [1, 40, 600, 3000])
+def test_infinite_values_give_infinities(bl, dtype, rows, width, frames):
+    q, k, v = _make(dtype, rows, frames, 2, 1, width, frames, scale=0.3)
+    v[:, :, 2], v[:, :, 5], v[:, :, 9] = 0, 0, 0
+    clean = _run(bl, q, k, v)
+    inf = float("inf")
+    v[frames // 2, 0, 2], v[frames - 1, 0, 5] = inf, -inf
+    v[0, 0, 9], v[frames - 1, 0, 9] = inf, -inf
+    got = _run(bl, q, k, v)
+    assert (got[:, :, 2] == inf).all() and (got[:, :, 5] == -inf).all()
+    assert torch.isnan(got[:, :, 9]).all() if frames > 1 else (got[:, :, 9] == -inf).all()
+    rest = [c for c in range(width) if c not in (2, 5, 9)]
+    assert torch.equal(got[:, :, rest], clean[:, :, rest])
