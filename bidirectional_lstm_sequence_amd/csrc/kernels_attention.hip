@@ -43,6 +43,22 @@ __device__ __forceinline__ int value_place(int r, int c) {
     return RB >= 256 ? c ^ (r & 3) << 2 : (RB == 128 ? c ^ (r & 2) << 1 : c);
 }
 
+// The same places from a lane's first one: chunk c of a row whose chunk `half` is at `at`, for even c - half, and a lane's
+// values 32 d columns further than `at`. What places exchange is a few bits of the chunk, so one exclusive or of a constant
+// finds them.
+template <int RB>
+__device__ __forceinline__ int key_at(int at, int c) {
+    constexpr int kTurns = RB >= 256 ? 15 : (RB == 128 ? 7 : 3);
+    return (at ^ (c & kTurns) * 16) + (c & ~kTurns) * 16;
+}
+
+template <typename T, int RB>
+__device__ __forceinline__ int values_at(int at, int d) {
+    constexpr int kTurns = sizeof(T) == 4 ? (RB >= 256 ? 1 : 0) : (RB >= 256 ? 3 : (RB == 128 ? 1 : 0));
+    constexpr int kBytes = 32 * static_cast<int>(sizeof(T));
+    return (at ^ (d & kTurns) * kBytes) + (d & ~kTurns) * kBytes;
+}
+
 // Products of 32 x 32. A fragment of keys or queries: row lane % 32, chunk 2 s + lane / 32 of 16 bytes.
 // The first product gives frames by rows: a lane holds of its row, lane % 32, the frames
 // 8 (i / 4) + 4 (lane / 32) + i % 4 in i = 0 .. 15. That is how the second product takes them, with the values'
@@ -62,13 +78,16 @@ struct Of {
             return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
         }
     }
-    // Four rows from r on by columns: 16 lanes name four elements each of rows r .. r + 3 and receive a column.
+    // Four rows by columns: 16 lanes name four elements each of rows r .. r + 3 and receive a column. Lane's place for the
+    // first 32 columns of the rows 4 (lane / 32) on; 32 columns further it is `values_at`'s.
     template <int RB>
-    static __device__ __forceinline__ Vec<T, 4> columns(const char *values, int r, int d, int lane) {
+    static __device__ __forceinline__ int values_from(int lane) {
+        const int row = 4 * (lane >> 5) + ((lane & 15) >> 2), c = 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+        return row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
+    }
+    static __device__ __forceinline__ Vec<T, 4> columns(const char *p) {
         typedef short S4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) S4 *Lds;
-        const int row = r + ((lane & 15) >> 2), c = d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
-        const char *p = values + row * RB + value_place<T, RB>(row, c >> 3) * 16 + (c & 7) * 2;
         return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
     }
     // 32 frames' weights as the second product takes them, in two parts: rounded, and what the rounding left (2^-16 of a
@@ -111,16 +130,15 @@ struct Of {
         for (int e = 0; e < 8; ++e) bits[e] = (bits[e] & 0x7FFF) == kInfinity ? 0 : bits[e];
         return __builtin_bit_cast(Frag, bits);
     }
-    // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights
+    // out[d] += values' columns 32 d .. 32 d + 31 of 32 frames from r on, times their weights; `at`: values_from's place
     template <int RB, bool AGAIN, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const Weights &w, F16x (&out)[N], int lane) {
-        const int h = lane >> 5;
+    static __device__ __forceinline__ void weigh(const char *values, int at, int r, const Weights &w, F16x (&out)[N]) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int d = 0; d < N; ++d) {
-                const Frag v = __builtin_shufflevector(columns<RB>(values, r + 16 * c + 4 * h, 32 * d, lane),
-                                                       columns<RB>(values, r + 16 * c + 8 + 4 * h, 32 * d, lane), 0, 1, 2, 3, 4, 5, 6, 7);
+                const char *const p = values + values_at<T, RB>(at, d) + (r + 16 * c) * RB;
+                const Frag v = __builtin_shufflevector(columns(p), columns(p + 8 * RB), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) out[d] = mul(AGAIN && k > 0 ? finite(v) : v, w.part[k][c], out[d]);
             }
@@ -143,15 +161,19 @@ struct Of<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
+    template <int RB>
+    static __device__ __forceinline__ int values_from(int lane) {
+        const int row = 4 * (lane >> 5), c = lane & 31;
+        return row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4;
+    }
     template <int RB, bool, int N>
-    static __device__ __forceinline__ void weigh(const char *values, int r, const F16x &p, F16x (&out)[N], int lane) {
+    static __device__ __forceinline__ void weigh(const char *values, int at, int r, const F16x &p, F16x (&out)[N]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
 #pragma unroll
             for (int d = 0; d < N; ++d) {
-                const int row = r + 8 * (i / 4) + 4 * (lane >> 5) + i % 4, c = 32 * d + (lane & 31);
                 const float v = __uint_as_float(
-                    *reinterpret_cast<const unsigned *>(values + row * RB + value_place<float, RB>(row, c >> 2) * 16 + (c & 3) * 4));
+                    *reinterpret_cast<const unsigned *>(values + values_at<float, RB>(at, d) + (r + 8 * (i / 4) + i % 4) * RB));
                 out[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[i], out[d], 0, 0, 0);
             }
     }
@@ -306,9 +328,13 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
     float most, sum;  // sum: this half's frames
     F16x out[kColumns];
 
+    const int key_from = (lane & 31) * RB + key_place<RB>(lane & 31, half) * 16, value_from = O::template values_from<RB>(lane);
     auto tile = [&](auto again, int slot, unsigned long long bits) __attribute__((always_inline)) {
         constexpr bool AGAIN = decltype(again)::value;
-        const char *const keys = lds + slot * 2 * kTile, *const values = keys + kTile;
+        int keys = slot * 2 * kTile + key_from, values = slot * 2 * kTile + kTile + value_from;
+        // Opaque, else there is a register for every place: heads of 256 bfloat16 then spill in the loop, 912 us where these
+        // take 600 (8192 rows, 16 heads). float32 heads up to 128 have the registers (4096 rows of 8 heads 295 us, 311 so).
+        if constexpr (kSize == 2 || D == 256) asm("" : "+v"(keys), "+v"(values));
         __builtin_amdgcn_s_setprio(1);
         F16x p[kBlocks];
 #pragma unroll
@@ -317,9 +343,8 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         for (int i = 0; i < kSlabs; ++i)
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
-                const int r = b * 32 + (lane & 31);
                 // read as integers: before floats from LDS the compiler waits for all loads to LDS under way
-                const U4 chunk = *reinterpret_cast<const U4 *>(keys + r * RB + key_place<RB>(r, 2 * i + half) * 16);
+                const U4 chunk = *reinterpret_cast<const U4 *>(lds + key_at<RB>(keys, 2 * i) + b * 32 * RB);
                 p[b] = O::mul(__builtin_bit_cast(typename O::Frag, chunk), qf[i], p[b]);
             }
         __builtin_amdgcn_s_setprio(0);
@@ -363,7 +388,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
         }
         sum += add;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB, AGAIN>(values, 32 * b, weights[b], out, lane);
+        for (int b = 0; b < kBlocks; ++b) O::template weigh<RB, AGAIN>(lds, values, 32 * b, weights[b], out);
     };
 
     constexpr int kStride = FEW ? kAll * kFrames : kFrames;
