@@ -397,8 +397,9 @@ constexpr int kFewRows = 32;
 
 // Up to 32 rows the few kernel, one launch (one row of 5120 x 5120 bfloat16 11.8 us, tiles of 64 x 64 with split sums 11.7
 // and 4.4 for the join; 64 rows 17.3 where those take 16). Tiles of 256 x 256 where there is one for every CU; float32 in
-// parts does not fit their registers. Tiles of 128 x 128 for four a CU: below that 64 x 64 are as fast or faster (18848 x
-// 256 x 512 bfloat16 19.7 us and 21.8, 2048 x 2048 x 2048 31.5 and 32.4). Sums are split up to three workgroups a CU and
+// parts does not fit their registers, and rows at any element pass through too many: those take tiles of 128 x 128 where
+// there are four for every CU. Else tiles of 64 x 64, which are as fast as 128 x 128 or faster there (18848 x 256 x 512
+// bfloat16 19.7 us and 21.8, 2048 x 2048 x 2048 31.5 and 32.4). Sums are split up to three workgroups a CU and
 // not below eight steps: 128 x 5120 x 5120 24 us with 4 splits, 30 with 2; 1111 x 777 x 999 18 us whole, 22 with 2.
 Form form_of(const LinearArgs &a, int size, bool aligned) {
     const auto tiles = [&](int bm, int bn) {
@@ -410,8 +411,11 @@ Form form_of(const LinearArgs &a, int size, bool aligned) {
         while (f.splits < 16 && tiles(f.bm, f.bn) * f.splits * 2 <= kCus && steps / (f.splits * 2) >= 4 * kFewWaves) f.splits *= 2;
         return f;
     }
-    if (aligned && size < 4 && tiles(256, 256) >= kCus) return {256, 256, 1};
-    if (tiles(128, 128) >= 4 * kCus) return {128, 128, 1};
+    if (aligned && size < 4) {
+        if (tiles(256, 256) >= kCus) return {256, 256, 1};
+    } else if (tiles(128, 128) >= 4 * kCus) {
+        return {128, 128, 1};
+    }
     Form f = {64, 64, 1};
     const long long t = tiles(64, 64);
     while (f.splits < 16 && t * f.splits * 2 <= 3 * kCus && steps / (f.splits * 2) >= 8) f.splits *= 2;
@@ -447,7 +451,7 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
         } else {
             e = launch(linear_few_kernel<Few, Y, 2, 2, ALIGNED ? 4 : 2, ALIGNED>, blocks, kThreads, stream, a);
         }
-    } else if (f.bm == 256) {
+    } else if (f.bm == 256) {  // see form_of: large tiles of rows on 16 bytes, middle ones of others and of float32
         // One tile a CU at a time: where the last round has work for half of the CUs or less, its tiles are halved
         // (8192 x 5120 x 5120, two and a half rounds: 399 us, 446 with whole tiles).
         const unsigned long long rest = blocks % kCus;
@@ -457,7 +461,7 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
         }
         if constexpr (ALIGNED && sizeof(typename P::Elem) < 4) e = launch(linear_kernel<P, Y, 256, 256, 2, 4, 2, ALIGNED>, blocks, 512, stream, a);
     } else if (f.bm == 128) {
-        e = launch(linear_kernel<P, Y, 128, 128, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
+        if constexpr (!ALIGNED || sizeof(typename P::Elem) == 4) e = launch(linear_kernel<P, Y, 128, 128, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
     } else {
         e = launch(linear_kernel<P, Y, 64, 64, 2, 2, 2, ALIGNED>, blocks, 256, stream, a);
     }
@@ -491,7 +495,7 @@ hipError_t by_output(const LinearArgs &a, Elem type, hipStream_t stream) {
 
 size_t linear_scratch_bytes(const LinearArgs &a, Elem type, Eight eight) {
     if (a.rows <= 0) return 0;
-    // either alignment's form splits alike: only the largest tile differs, which has no splits
+    // either alignment's form splits alike: only the larger tiles differ, which have no splits
     const Form f = form_of(a, eight != Eight::none ? 1 : (type == Elem::f32 ? 4 : 2), false);
     return f.splits > 1 ? static_cast<size_t>(f.splits) * a.rows * ((static_cast<size_t>(a.out) + 3) / 4 * 4) * 4 : 0;
 }
