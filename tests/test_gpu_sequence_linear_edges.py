@@ -65,3 +65,44 @@ def test_float32_operands_of_any_size(bl, rows, inputs, x_size, w_size):
     value, bound = plain.linear(x, w, bias, None, residual, None, None, 0, torch.float32)
     off = (bl.linear(x.cuda(), w.cuda(), bias=bias.cuda(), residual=residual.cuda()).cpu().double() - value).abs()
     assert torch.isfinite(off).all() and (off <= bound).all(), f"{((off - bound) / bound).max():.3e} of the bound over it"
+
+
+def _codes(dtype, rows, inputs, g):
+    """Rows of a type, and of 8-bit types their scales."""
+    x = torch.randn(rows, inputs, generator=g, device="cuda")
+    if dtype not in plain.EIGHT:
+        return x.to(dtype), None
+    scale = x.abs().amax(1) / plain.EIGHT[dtype]
+    q = x / scale[:, None]
+    return (torch.round(q) if dtype == torch.int8 else q).to(dtype), scale
+
+
+@pytest.mark.parametrize("out_type", TYPES, ids=str)
+@pytest.mark.parametrize("dtype", TYPES + list(plain.EIGHT), ids=str)
+@pytest.mark.parametrize("rows, outputs", [(4200, 4200), (5100, 5000)])
+@pytest.mark.parametrize("extra", [0, 1])
+def test_large_tiles_over_many_steps(bl, out_type, dtype, rows, outputs, extra):
+    """One tile of 256 x 256 and more for every CU, halved ones in the last round or not, over six steps and a rest, with
+    everything that an epilogue takes; with an element more the rows lie at any element."""
+    if dtype not in plain.EIGHT and dtype != out_type:
+        pytest.skip("y is of x's type")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    inputs = 816 // torch.finfo(dtype).bits * 8 + extra if dtype != torch.int8 else 816 + extra
+    (x, xs), (w, ws) = _codes(dtype, rows, inputs, g), _codes(dtype, outputs, inputs, g)
+    ws = None if ws is None else ws / inputs ** 0.5
+    bias = torch.randn(outputs, generator=g, device="cuda").to(out_type)
+    residual = torch.randn(rows, outputs, generator=g, device="cuda").to(out_type)
+    got = bl.linear(x, w, bias=bias, activation="gelu", residual=residual, x_scales=xs, weight_scales=ws, out_type=out_type)
+    some = torch.cat([torch.arange(0, rows, 137), torch.arange(rows - 9, rows)]).cuda()
+    cpu = lambda t: None if t is None else t.cpu()  # noqa: E731
+    value, bound = plain.linear(cpu(x[some.long()]), cpu(w), cpu(bias), "gelu", cpu(residual[some]), None if xs is None else cpu(xs[some]),
+                                cpu(ws), 0, out_type)
+    off = (got[some].cpu().double() - value).abs()
+    assert torch.isfinite(off).all() and (off <= bound).all(), f"{(off - bound).max():.3e} over the bound"
+    # the other rows: the same product of fewer, in smaller tiles, differs by the order of its sums (below 1e-4 for values of
+    # this size: 2 n steps of 2^-24) and so by a step of y at most
+    half = rows // 2
+    low = bl.linear(x[:half], w[:700], bias=bias[:700], activation="gelu", residual=residual[:half, :700], x_scales=None if xs is None else xs[:half],
+                    weight_scales=None if ws is None else ws[:700], out_type=out_type)
+    near = torch.finfo(out_type).eps * (1 + low.float().abs()) + 1e-4
+    assert ((got[:half, :700].float() - low.float()).abs() <= near).all()
