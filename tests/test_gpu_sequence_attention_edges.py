@@ -154,3 +154,66 @@ def test_infinite_values_give_infinities(bl, dtype, rows, width, frames):
     assert torch.isnan(got[:, :, 9]).all() if frames > 1 else (got[:, :, 9] == -inf).all()
     rest = [c for c in range(width) if c not in (2, 5, 9)]
     assert torch.equal(got[:, :, rest], clean[:, :, rest])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [64, 80, 13, 100, 200, 256])
+def test_masks_over_many_tiles(bl, dtype, rows, width):
+    """Masked frames among others, whole tiles of them, and a memory of them alone; what they hold is nothing."""
+    held = 333
+    g = torch.Generator().manual_seed(width)
+    q, k, v = _make(dtype, 3 * rows, 3 * held, 4, 2, width, 7)
+    mask = torch.rand(3 * held, generator=g) < 0.5
+    mask[20: 20 + 150], mask[held + 256:], mask[2 * held:] = False, False, False
+    lengths, memory_starts, starts = [held - 9, held, held], [3, held, 2 * held, 3 * held], [0, rows, 2 * rows, 3 * rows]
+    run = lambda: _run(bl, q, k, v, mask=mask, lengths=lengths, starts=starts, memory_starts=memory_starts)  # noqa: E731
+    clean = run()
+    for j in range(2):
+        chosen = [f for f in range(memory_starts[j], min(memory_starts[j] + lengths[j], memory_starts[j + 1])) if mask[f]]
+        value, bound = strict.attention(q[j * rows: (j + 1) * rows], k, v, chosen, width ** -0.5)
+        _within(clean[j * rows: (j + 1) * rows], (value, bound))
+    assert (clean[2 * rows:] == 0).all()
+    reads = torch.zeros(3 * held, dtype=torch.bool)
+    for j in range(3):
+        reads[memory_starts[j]: min(memory_starts[j] + lengths[j], memory_starts[j + 1])] = True
+    for t, bad in ((k, float("nan")), (v, float("inf")), (k, float("-inf")), (v, float("nan")), (k, torch.finfo(dtype).max)):
+        t[~(reads & mask)] = bad
+        assert torch.equal(run(), clean)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", [2, 50])
+@pytest.mark.parametrize("width", [64, 100])
+def test_masks_over_splits(bl, dtype, rows, width):
+    frames = 4099
+    q, k, v = _make(dtype, rows, frames, 4, 2, width, rows)
+    mask = torch.rand(frames, generator=torch.Generator().manual_seed(2)) < 0.3
+    mask[500:1800] = False
+    chosen = torch.nonzero(mask[:frames - 40])[:, 0]
+    clean = _run(bl, q, k, v, mask=mask, lengths=[frames - 40])
+    _within(clean, strict.attention(q, k, v, chosen, width ** -0.5))
+    k[~mask], v[~mask] = float("nan"), float("inf")
+    k[frames - 40:], v[frames - 40:] = float("inf"), float("nan")
+    assert torch.equal(_run(bl, q, k, v, mask=mask, lengths=[frames - 40]), clean)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("width", [65, 96, 127, 128, 129, 200, 255, 256])
+@pytest.mark.parametrize("offset", [1, 8])
+def test_wide_heads_at_any_element(bl, dtype, rows, width, offset):
+    """Keys and values side by side in wider rows, at an element or at 16 bytes; single rows too."""
+    held, groups, heads = 150, 2, 4
+    q, k, v = _make(dtype, rows, held, heads, groups, width, width)
+    n = groups * width
+    wide = torch.full((held, 2 * n + 2 * offset), float("nan"), dtype=dtype, device="cuda")
+    kd, vd = wide[:, offset: offset + n].view(held, groups, width), wide[:, offset + n: offset + 2 * n].view(held, groups, width)
+    kd.copy_(k), vd.copy_(v)
+    into = torch.full((rows, heads * width + offset), 3.0, dtype=dtype, device="cuda")
+    yd = into[:, offset:].view(rows, heads, width)
+    got = bl.cross_attention(q.cuda(), kd, vd, _whole([0, rows]), _whole([20, held - 3]), out=yd)
+    ref = strict.attention(q, k, v, range(20, held - 3), width ** -0.5)
+    assert got is yd and (into[:, :offset] == 3).all()
+    _within(yd.cpu(), ref)
+    _within(bl.cross_attention_step(q.cuda(), kd, vd, _whole([20, held - 3]), slots=_whole([0] * rows)).cpu(), ref)
