@@ -9,11 +9,11 @@
 // (an offset behind the buffer) and their scores become minus infinity, so neither what they hold nor what a query makes of
 // the zeros enters.
 //
-// Few rows are bound by the bytes of keys and values: 256 rows over 589 frames each, 4 key heads of 64, bfloat16, 32-34
-// us (floor 31 at the copy rate of 5.0 TB/s); 64 rows over 4096 frames, 8 key heads of 128, 188 us, 5.7 TB/s. Many rows:
-// 16384 over 2048 frames, 32 heads of 128, bfloat16, 707 us, 778 TFLOP/s, where matrix instructions alone, with neither
-// loads nor softmax, take 448-460: the card lowers its clock to 1.9 GHz under this load (2.2 in a plain product), and
-// what is left out in a trial shortens the call by its own share: loads to LDS 125 us, reads from LDS 80, softmax 65.
+// Few rows are bound by the bytes of keys and values: 256 rows over 589 frames each, 4 key heads of 64, bfloat16, 35
+// us (floor 31 at the copy rate of 5.0 TB/s); 64 rows over 4096 frames, 8 key heads of 128, 186 us, 5.8 TB/s. Many rows:
+// 16384 over 2048 frames, 32 heads of 128, bfloat16, 803 us, 685 TFLOP/s, half as many matrix operations again for the
+// weights' second part (610 us without). Matrix instructions alone, with neither loads nor softmax, take 482; of the rest, in
+// trials that leave one out, reads from LDS 217 us, loads to LDS 80, softmax 62.
 // float32 takes the float32 matrix instructions: 4096 rows, 8 heads of 128, 287 us, 120 TFLOP/s of 138.
 #include "attention_device.h"
 
@@ -22,7 +22,7 @@ namespace {
 
 // A workgroup has either 128 or 256 packed rows, 32 a wave, and its waves read tiles of frames together (many); or up
 // to 32 packed rows, and its waves read every fourth tile each, whose sums they join (few). Many with keys of RB = 512
-// bytes take eight waves, so that two share a SIMD: 389 us where four take 611 (8192 rows, 16 heads of 256).
+// bytes take eight waves, so that two share a SIMD: 575 us where four take 667 (8192 rows, 16 heads of 256).
 template <bool FEW, int RB>  // few: as many as have two tiles of 32 frames in 128 KB
 constexpr int kWaves = FEW ? (RB <= 256 ? 4 : (RB == 512 ? 2 : 1)) : (RB == 512 ? 8 : 4);
 
@@ -332,9 +332,9 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
     auto tile = [&](auto again, int slot, unsigned long long bits) __attribute__((always_inline)) {
         constexpr bool AGAIN = decltype(again)::value;
         int keys = slot * 2 * kTile + key_from, values = slot * 2 * kTile + kTile + value_from;
-        // Opaque, else there is a register for every place: heads of 256 bfloat16 then spill in the loop, 912 us where these
-        // take 600 (8192 rows, 16 heads). float32 heads up to 128 have the registers (4096 rows of 8 heads 295 us, 311 so).
-        if constexpr (kSize == 2 || D == 256) asm("" : "+v"(keys), "+v"(values));
+        // opaque, else there is a register for every place: heads of 256 bfloat16 then spill in the loop, 912 us where these
+        // take 600 (8192 rows, 16 heads)
+        asm("" : "+v"(keys), "+v"(values));
         __builtin_amdgcn_s_setprio(1);
         F16x p[kBlocks];
 #pragma unroll
@@ -583,17 +583,18 @@ unsigned long long tiles_of(const AttentionArgs &a, int size) {
     return static_cast<unsigned long long>(a.seq.rows) * a.per / size + a.seq.sequences;
 }
 
-// Whether a sequence has 32 packed rows or less on average: 256 rows of 4 heads over 589 frames take 31 us so and 36
-// with tiles of 128, a row alone has no join. With 64 packed rows the tiles of 128 are ahead where keys are long (512
-// rows over 2048 frames, heads of 128, 62 us and 81). The lengths are on the device: a long sequence among many short
-// ones is read by workgroups of 32: a prompt of 4000 rows adds 94 us to 255 single rows' 378, alone it takes 58.
+// Whether a sequence has 32 packed rows or less on average: 256 rows of 16 heads on 4 over 589 frames take 35 us so and 49
+// with tiles of 128, a row alone 11 and 15. With 64 packed rows the tiles of 128 are ahead (8 x 64 rows over 2048 frames,
+// heads of 128, 31.6 us and 33.5; 32 x 64 rows of float32 over 589 frames 36.5 and 40.8). The lengths are on the device: a
+// long sequence among many short ones is read by workgroups of 32: a prompt of 4000 rows adds 130 us to 255 single rows'
+// 382, alone it takes 73.
 bool few_rows(const AttentionArgs &a) {
     return static_cast<unsigned long long>(a.seq.rows) * a.per <= 32ull * a.seq.sequences;
 }
 
 // Frames are split over workgroups where those are few, by what the average sequence and memory have, up to two
-// workgroups a CU: one prompt of 500 rows over 4096 frames 28 us with 8 splits, 44 with 16 and their larger join; 32 x 4
-// rows over 4096 frames 102 us with 2, 149 with none. A split keeps at least four tiles for each wave of the few, and
+// workgroups a CU: one prompt of 500 rows over 4096 frames 30 us with 8 splits, 36 with 16 and their larger join; 32 x 4
+// rows over 4096 frames 111 us with 2, 141 with none. A split keeps at least four tiles for each wave of the few, and
 // two of the many.
 int splits_of(const AttentionArgs &a) {
     const bool few = few_rows(a);

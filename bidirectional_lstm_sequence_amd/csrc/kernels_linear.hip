@@ -6,8 +6,8 @@
 // multiply 16 x 16 blocks and pass their sums through LDS to whole lines of y. A step of 256 x 256 outputs takes 1.6 us
 // on all CUs (1342 TFLOP/s bfloat16, 2840 int8, at 2.2 GHz, the matrix cores half busy; e4m3, whose codes are widened to
 // bf16, 2.5), a tile's start and end 18 us. 8192 x 5120 x 5120: bfloat16 with residual 403 us (1070 TFLOP/s; the library's
-// plain product 471), e4m3 with gelu 329 (1300), int8 233, float32 by parts 2270 (189 TFLOP/s; the library 138).
-// Few rows: bound by the weights' bytes, one row of 5120 x 5120 bfloat16 11.8 us (floor 10.5).
+// plain product 464), e4m3 with gelu 332 (1290), int8 with gelu 228 (1880), float32 by parts 2370 (181 TFLOP/s; the
+// library 138). Few rows: bound by the weights' bytes, one row of 5120 x 5120 bfloat16 11.3 us (floor 10.5).
 #include "linear_device.h"
 
 namespace bl {
