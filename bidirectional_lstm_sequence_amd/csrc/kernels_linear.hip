@@ -395,12 +395,12 @@ struct Form {
 constexpr long long kCus = 256;
 constexpr int kFewRows = 32;
 
-// Up to 32 rows the few kernel, one launch (one row of 5120 x 5120 bfloat16 11.8 us, tiles of 64 x 64 with split sums 11.7
-// and 4.4 for the join; 64 rows 17.3 where those take 16). Tiles of 256 x 256 where there is one for every CU; float32 in
+// Up to 32 rows the few kernel, one launch (one row of 5120 x 5120 bfloat16 11.8 us in kernels, tiles of 64 x 64 with split
+// sums 11.7 and 4.4 for the join; 64 rows 17.3 where those take 16). Tiles of 256 x 256 where there is one for every CU; float32 in
 // parts does not fit their registers, and rows at any element pass through too many: those take tiles of 128 x 128 where
 // there are four for every CU. Else tiles of 64 x 64, which are as fast as 128 x 128 or faster there (18848 x 256 x 512
-// bfloat16 19.7 us and 21.8, 2048 x 2048 x 2048 31.5 and 32.4). Sums are split up to three workgroups a CU and
-// not below eight steps: 128 x 5120 x 5120 24 us with 4 splits, 30 with 2; 1111 x 777 x 999 18 us whole, 22 with 2.
+// bfloat16 16.2 us and 18.1, 2048 x 2048 x 2048 26.5 and 27.7). Sums are split up to three workgroups a CU and
+// not below eight steps: 128 x 5120 x 5120 20 us with 4 splits, 26 with 2; 1111 x 777 x 999 13.5 us whole, 17.7 with 2.
 Form form_of(const LinearArgs &a, int size, bool aligned) {
     const auto tiles = [&](int bm, int bn) {
         return ((static_cast<long long>(a.rows) + bm - 1) / bm) * ((static_cast<long long>(a.out) + bn - 1) / bn);
@@ -453,7 +453,7 @@ hipError_t by_form(LinearArgs a, hipStream_t stream) {
         }
     } else if (f.bm == 256) {  // see form_of: large tiles of rows on 16 bytes, middle ones of others and of float32
         // One tile a CU at a time: where the last round has work for half of the CUs or less, its tiles are halved
-        // (8192 x 5120 x 5120, two and a half rounds: 399 us, 446 with whole tiles).
+        // (8192 x 5120 x 5120, two and a half rounds: 404 us, 426 with whole tiles; e4m3 339 and 382).
         const unsigned long long rest = blocks % kCus;
         if (rest <= kCus / 2) {
             a.whole = static_cast<int>(blocks - rest);
