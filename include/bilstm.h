@@ -570,7 +570,8 @@ bilstm_status bilstm_token_logprobs(const bilstm_logprobs_args *args, void *stre
  * Scores, maxima and sums are held in float32; weights enter their product with the values in float32, or in two parts of
  * the tensors' 16-bit type, which leave at most 2^-16 of a weight.
  * A row without a frame that counts, or with scores of minus infinity alone, gets zeros. Finite values of any size give a
- * finite quotient; an infinite value that counts gives its infinity, two of opposite signs not-a-numbers.
+ * finite quotient, but for its rounding next to the type's largest number. An infinite value that counts gives its infinity
+ * (float16: where its weight is at least 2^-35 of the row's largest), two of opposite signs not-a-numbers.
  * Here `places` are the memories and `slots` names the memory that each sequence reads: several may read one, and
  * a slot outside 0 .. places - 1 marks padding. memory_starts hold `places` + 1 non-decreasing row numbers; values
  * outside 0 .. memory_rows, and lengths outside the memory, are clamped.

@@ -217,3 +217,29 @@ def test_wide_heads_at_any_element(bl, dtype, rows, width, offset):
     assert got is yd and (into[:, :offset] == 3).all()
     _within(yd.cpu(), ref)
     _within(bl.cross_attention_step(q.cuda(), kd, vd, _whole([20, held - 3]), slots=_whole([0] * rows)).cpu(), ref)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_captured_with_ordinary_values_and_replayed_with_large_ones(bl, rows):
+    """Whether the frames are gone over again is found out on the device, by each replay."""
+    frames, width = 3000, 64
+    q, k, v = (t.cuda() for t in _make(torch.bfloat16, rows, frames, 2, 1, width, 5, scale=0.5))
+    large, infinite = (v.abs() + 1) * 2.5e37, v.clone()  # up to 1.4e38
+    infinite[frames // 2] = float("inf")
+    starts, memory_starts = _whole([0, rows]), _whole([0, frames])
+    call = lambda held: bl.cross_attention(q, k, held, starts, memory_starts)  # noqa: E731
+    expect = [call(t) for t in (v, large, infinite)]
+    held = v.clone()
+    call(held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call(held)
+    for i in (0, 1, 2, 0, 1):
+        held.copy_((v, large, infinite)[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect[i])
+        call(v)
+        torch.cuda.synchronize()
+    assert torch.isfinite(expect[1]).all() and (expect[2] == float("inf")).all()

@@ -106,3 +106,15 @@ def test_large_tiles_over_many_steps(bl, out_type, dtype, rows, outputs, extra):
                     weight_scales=None if ws is None else ws[:700], out_type=out_type)
     near = torch.finfo(out_type).eps * (1 + low.float().abs()) + 1e-4
     assert ((got[:half, :700].float() - low.float()).abs() <= near).all()
+
+
+@pytest.mark.parametrize("rows", [3, 150])
+def test_float32_operands_down_to_the_smallest(bl, rows):
+    """Subnormal numbers count, in any number of rows."""
+    x, w = torch.zeros(rows, 40), torch.zeros(24, 40)
+    for e in range(24):
+        x[:, e], w[e, e] = 2.0 ** -(149 - e) * 3, 2.0 ** 110  # the first is 3 of the smallest
+    got = bl.linear(x.cuda(), w.cuda()).cpu()
+    assert torch.equal(got, torch.tensor([3 * 2.0 ** (e - 39) for e in range(24)]).expand(rows, 24))
+    back = bl.linear(w.cuda(), x.cuda()).cpu()
+    assert torch.equal(back, got.t())
