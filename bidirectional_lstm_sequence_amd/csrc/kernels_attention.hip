@@ -45,7 +45,7 @@ __device__ __forceinline__ int value_place(int r, int c) {
 
 // The same places from a lane's first one: chunk c of a row whose chunk `half` is at `at`, for even c - half, and a lane's
 // values 32 d columns further than `at`. What places exchange is a few bits of the chunk, so one exclusive or of a constant
-// finds them.
+// finds them. (A register for every place made heads of 256 bfloat16 spill in the loop, 1.5 times as long.)
 template <int RB>
 __device__ __forceinline__ int key_at(int at, int c) {
     constexpr int kTurns = RB >= 256 ? 15 : (RB == 128 ? 7 : 3);
@@ -331,10 +331,7 @@ __global__ __launch_bounds__((64 * kWaves<FEW, D * sizeof(T)>), (!FEW && D * siz
     const int key_from = (lane & 31) * RB + key_place<RB>(lane & 31, half) * 16, value_from = O::template values_from<RB>(lane);
     auto tile = [&](auto again, int slot, unsigned long long bits) __attribute__((always_inline)) {
         constexpr bool AGAIN = decltype(again)::value;
-        int keys = slot * 2 * kTile + key_from, values = slot * 2 * kTile + kTile + value_from;
-        // opaque, else there is a register for every place: heads of 256 bfloat16 then spill in the loop, 912 us where these
-        // take 600 (8192 rows, 16 heads)
-        asm("" : "+v"(keys), "+v"(values));
+        const int keys = slot * 2 * kTile + key_from, values = slot * 2 * kTile + kTile + value_from;
         __builtin_amdgcn_s_setprio(1);
         F16x p[kBlocks];
 #pragma unroll
